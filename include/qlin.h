@@ -297,12 +297,180 @@ qlin_status qlin_linear_ex(const void* x, const uint32_t* wq, const void* scales
                            int64_t N, int64_t K, int bits, int group_size, qlin_dtype dtype,
                            qlin_dtype y_dtype, void* stream);
 
+/* ==========================================================================
+ * What stands between a decoder's linears: RMS norm with the residual's
+ * addition, rotary positions with the append to an 8-bit key/value cache,
+ * attention over that cache, and sampling.  None has a counterpart on the
+ * pages, whose decode step is its linears; these are additions of this library.
+ *
+ * flags of the calls below: 0 or QLIN_OVERLAP_PREVIOUS (the launch and what
+ * reads no tensor of the call overlap the preceding kernel on the stream).
+ *
+ * Head dimensions 64 and 128; activations f16 or bf16.
+ * ======================================================================== */
+
+/*
+ * The key/value cache of one layer.  A slot is one sequence.  Tokens are kept
+ * in blocks of QLIN_KV_BLOCK: complete blocks in 8 bits, in pages that the
+ * table names in any order, with one float32 scale for each block, head and
+ * key/value; the incomplete last block (the slot's tail) in dtype.  Every
+ * value is therefore rounded to 8 bits once, when its block completes, and
+ * what the cache holds does not depend on how the tokens were grouped in
+ * calls.  A code c stands for (c - 128) * scale, 1 <= c <= 255.  Value blocks
+ * are held transposed, as the attention's products read them.  Pages may be
+ * shared by slots with a common beginning.
+ *
+ *   pages    uint8 [n_pages][kv_heads][2][64*head_dim]: keys as
+ *            [64 tokens][head_dim], then values as [head_dim][64 tokens]
+ *   scales   float [n_pages][kv_heads][2]
+ *   tail     dtype [slots][kv_heads][2][64*head_dim], same two layouts;
+ *            what stands beyond a slot's last token is never used
+ *   table    int32 [slots][max_blocks]: the page of each block
+ *   lens     int32 [slots]: tokens held before the call (shared by a model's
+ *            layers; the caller advances it once per step)
+ *
+ * pages and tail are 16-byte aligned.  The struct is read during the call
+ * only; the memory it names is used on the stream.
+ */
+#define QLIN_KV_BLOCK 64
+typedef struct {
+  void* pages;
+  float* scales;
+  void* tail;
+  const int32_t* table;
+  const int32_t* lens;
+  int64_t n_pages;
+  int32_t slots, max_blocks, kv_heads, head_dim;
+  int32_t dtype; /* a qlin_dtype: QLIN_F16 or QLIN_BF16 */
+} qlin_kv_cache;
+
+/*
+ * y[m][k] = h * weight[k] / sqrt(mean_k(h*h) + eps),  h = x[m][k] + residual[m][k]
+ *
+ * x, weight and y are dtype; residual and residual_out are rdtype (dtype or
+ * QLIN_F32).  h is a float32 sum: the norm uses it unrounded, residual_out
+ * receives it rounded once to rdtype.  residual may be NULL (h = x), and then
+ * residual_out is NULL too; residual_out may be NULL.  residual_out may be
+ * residual, and y may be x, for use in place.  x_stride and residual_stride
+ * are elements from row to row (>= K); y and residual_out are contiguous, so
+ * use in place wants the same.  1 <= K <= 32768.  Alignment: of the elements
+ * (rows that start 16-byte aligned are the fast path).
+ */
+qlin_status qlin_add_rms_norm(const void* x, int64_t x_stride, const void* weight,
+                              const void* residual, int64_t residual_stride, void* residual_out,
+                              void* y, int64_t M, int64_t K, float eps, qlin_dtype dtype,
+                              qlin_dtype rdtype, unsigned flags, void* stream);
+
+/*
+ * Load time: the table of rotary positions, float [n_positions][rot_dim/2][2],
+ * (cos, sin) of position * f_i, f_i = base^(-2i/rot_dim), computed in 64 bits.
+ * Long contexts: factor > 1 divides the frequencies whose wavelength
+ * 2*pi/f_i is above long_wavelength (0: all of them, plain interpolation) by
+ * factor, leaves those below short_wavelength as they are, and blends between
+ * the two, linearly in 1/wavelength.  factor = 1 scales nothing.
+ * INVALID_ARG: rot_dim not a positive multiple of 2, base <= 1, factor < 1,
+ * negative wavelengths or short_wavelength > long_wavelength.
+ */
+qlin_status qlin_rope_table(float* table, int64_t n_positions, int rot_dim, double base,
+                            double factor, double short_wavelength, double long_wavelength,
+                            void* stream);
+
+/*
+ * Rotates the queries and keys of new tokens and appends keys and values to
+ * the cache.
+ *   qkv      dtype [n_tokens][qkv_stride]: a row holds q_heads queries, then
+ *            kv_heads keys, then kv_heads values of head_dim
+ *   q_out    dtype [n_tokens][q_heads][head_dim]
+ *   table    float [n_positions][rot_dim/2][2] (qlin_rope_table)
+ *   starts   int32 [slots+1]: slot b's new tokens are rows starts[b] ..
+ *            starts[b+1]-1, in order, at positions lens[b], lens[b]+1, ...
+ *            (no rows: the slot is left as it is)
+ * The first rot_dim elements of a head turn in pairs, the rest stays:
+ * interleaved = 0 pairs i with i + rot_dim/2, 1 pairs 2i with 2i + 1;
+ * (a, b) -> (a cos - b sin, b cos + a sin) in float32, rounded once to dtype.
+ * Values and rotated keys enter the cache as dtype; a block that the call
+ * completes gets scale = amax/127 and codes rint(v/scale) + 128 (float32,
+ * ties to even; 128 where the scale is 0).  Finite inputs.
+ * rot_dim: a multiple of 16, 0 .. head_dim.  qkv and q_out 16-byte aligned,
+ * qkv_stride a multiple of 8.  A slot whose blocks pass max_blocks, a page
+ * outside n_pages, a position outside the table or rows outside n_tokens are
+ * left out and set a device status bit (qlin_device_status).
+ */
+qlin_status qlin_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
+                             const float* table, int64_t n_positions, int rot_dim,
+                             int interleaved, const qlin_kv_cache* cache, const int32_t* starts,
+                             int64_t n_tokens, int q_heads, unsigned flags, void* stream);
+
+/* The values that n pages of the cache stand for, out dtype
+ * [n][kv_heads][2][64*head_dim] in the pages' layouts (16-byte aligned):
+ * (c - 128) * scale in float32, rounded once.  page_ids: int32 [n] on the
+ * device; a page outside n_pages gives zeros and sets a device status bit. */
+qlin_status qlin_cache_dequant(const qlin_kv_cache* cache, const int32_t* page_ids, int64_t n,
+                               void* out, void* stream);
+
+/* Bytes of scratch that qlin_cache_attention needs for this head dimension on
+ * the current device (0 for a head dimension it does not take). */
+size_t qlin_cache_attention_workspace_size(int head_dim);
+
+/*
+ * Attention of new tokens over the cache that already holds them
+ * (qlin_rope_append before, with the same lens and starts):
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)
+ * over the positions j <= lens[b] + i of slot b, whose i-th row is t; query
+ * head h reads key/value head h / (q_heads/kv_heads).
+ *   q        dtype [n_tokens][q_stride], heads contiguous in a row
+ *   out      dtype [n_tokens][q_heads][head_dim]
+ *   max_new  the most new tokens of any slot (host side; it chooses kernels
+ *            and may be larger than it needs to be; a slot with more is left
+ *            out, zeros in its rows, and sets a device status bit)
+ *   workspace  qlin_cache_attention_workspace_size(head_dim) bytes of device
+ *            memory, 16-byte aligned, zeroed once by the caller; calls that
+ *            can overlap need workspaces of their own
+ * Scores, softmax statistics and sums are float32; probabilities enter the
+ * products in 16 bits.  q_heads: a multiple of kv_heads, at most 16 times as
+ * many.  q and out 16-byte aligned, q_stride a multiple of 8.  Rows that no
+ * slot owns are not written; blocks whose page is outside n_pages are left out
+ * and set a device status bit.
+ */
+qlin_status qlin_cache_attention(const void* q, int64_t q_stride, void* out,
+                                 const qlin_kv_cache* cache, const int32_t* starts,
+                                 int64_t n_tokens, int q_heads, float scale, int max_new,
+                                 void* workspace, size_t workspace_bytes, unsigned flags,
+                                 void* stream);
+
+/*
+ * One token per row of logits, ldtype [M][V] (QLIN_F32, F16 or BF16; rows
+ * logits_stride elements apart), from a given uniform number u[m] in [0, 1).
+ * All parameters are device arrays of M values.
+ *   w_i = rint(2^36 * exp((x_i - max)/temperature)): whole numbers, so sums
+ *         are exact and a draw does not depend on how the work is split
+ *   order: larger logits first, equal ones by index
+ *   top_k       keeps the first k (<= 0: all)
+ *   top_p       keeps, of those, each whose predecessors hold less than top_p
+ *               of their mass (>= 1: all)
+ *   min_p       keeps what is at least min_p times as likely as the likeliest
+ *   The first of the order is always kept.  The token is the first index, in
+ *   index order, whose cumulated kept weight is above floor(u * total);
+ *   probs[m] is its share of the kept weight.
+ * temperature <= 0: the first of the order, probability 1.  NaN logits count
+ * as -infinity; a row of nothing else gives token -1, probability 0; with
+ * +infinity among the logits only those can be drawn.  u outside [0, 1) is
+ * taken into it.  1 <= V <= 262144.  probs may be NULL.
+ */
+qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t* tokens, float* probs, int64_t M, int64_t V,
+                        qlin_dtype ldtype, unsigned flags, void* stream);
+
 /*
  * Read and clear the device status words of the current device (synchronises
  * the device).  *flags receives 0 when no kernel gave up a bounded wait since
  * the last call, else a bit mask of the waits that gave up (bits 0-7: the
  * tensor-core kernel, bits 8-15: the CUDA-core kernel, bits 16-23: the chain
- * kernel).  Returns QLIN_OK, or
+ * kernel), or of what the cache kernels refused on the device (bit 24: rows
+ * outside n_tokens or a negative length, 25: a page outside n_pages or a slot
+ * past max_blocks, 26: a position outside the table, 27: a slot with more than
+ * max_new rows, 28: a wait of the attention kernel that gave up).  Returns QLIN_OK, or
  * QLIN_ERR_CUDA if the device could not be read.  No counterpart on the pages:
  * an addition of this library (a kernel that gives up a wait reports instead
  * of hanging, the device-side form of failing fast).

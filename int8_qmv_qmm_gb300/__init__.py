@@ -11,6 +11,10 @@ calls raise.
 Layouts (row-major): packed weights ``wq`` uint32 [N, K*bits/32] (codes low
 bits first), ``scales``/``biases`` [N, K/64] in the activation dtype,
 activations ``x`` [M, K], output ``y`` [M, N].
+
+Beside the linears stand what a decoder runs between them: ``add_rms_norm``,
+``rope_table`` / ``rope_append``, ``KVCache`` with ``cache_attention`` and
+``cache_dequant``, and ``sample``.
 """
 
 from __future__ import annotations
@@ -25,13 +29,15 @@ from .build_lib import LIB_PATH
 __all__ = [
     "QlinError", "lib", "quantize_affine", "dequant", "qmv", "qmm", "linear",
     "crossover_m", "device_status", "QLIN_F32", "QLIN_F16", "QLIN_BF16", "Link", "make_links",
-    "chain_workspace", "qmv_chain",
+    "chain_workspace", "qmv_chain", "KVCache", "add_rms_norm", "rope_table", "rope_append",
+    "cache_dequant", "attention_workspace", "cache_attention", "sample", "KV_BLOCK",
 ]
 
 QLIN_F32, QLIN_F16, QLIN_BF16 = 0, 1, 2
 QLIN_OVERLAP_PREVIOUS = 1
 _DTYPE_CODE = {torch.float32: QLIN_F32, torch.float16: QLIN_F16, torch.bfloat16: QLIN_BF16}
 GROUP_SIZE = 64
+KV_BLOCK = 64
 
 _c_i64, _c_int, _c_vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 
@@ -57,6 +63,18 @@ _SIGNATURES = {
                                 ctypes.c_size_t, _c_vp]),
     "qlin_qmv_chain_static": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp]),
     "qlin_device_status": (_c_int, [ctypes.POINTER(_c_int)]),
+    "qlin_add_rms_norm": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64,
+                                   _c_i64, ctypes.c_float, _c_int, _c_int, ctypes.c_uint, _c_vp]),
+    "qlin_rope_table": (_c_int, [_c_vp, _c_i64, _c_int] + [ctypes.c_double] * 4 + [_c_vp]),
+    "qlin_rope_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_int, _c_int, _c_vp,
+                                  _c_vp, _c_i64, _c_int, ctypes.c_uint, _c_vp]),
+    "qlin_cache_dequant": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "qlin_cache_attention_workspace_size": (ctypes.c_size_t, [_c_int]),
+    "qlin_cache_attention": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_int,
+                                      ctypes.c_float, _c_int, _c_vp, ctypes.c_size_t,
+                                      ctypes.c_uint, _c_vp]),
+    "qlin_sample": (_c_int, [_c_vp, _c_i64] + [_c_vp] * 7 + [_c_i64, _c_i64, _c_int,
+                                                             ctypes.c_uint, _c_vp]),
     # include/qlin_testing.h: failure paths and host-side choices, for the
     # library's own tests
     "qlin_testing_qmv_chain_stalled": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int,
@@ -260,6 +278,282 @@ def qmv_chain(x0, link_array, n_links, bits, dtype, workspace, group_size=GROUP_
                                 bits, group_size, _DTYPE_CODE[dtype], _ptr(workspace),
                                 workspace.numel() * 4,
                                 ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+
+
+class _KVCacheStruct(ctypes.Structure):
+    """qlin_kv_cache (include/qlin.h)."""
+    _fields_ = [("pages", _c_vp), ("scales", _c_vp), ("tail", _c_vp), ("table", _c_vp),
+                ("lens", _c_vp), ("n_pages", _c_i64), ("slots", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache:
+    """The 8-bit key/value cache of one layer (qlin_kv_cache in include/qlin.h):
+    a handle on its tensors, which must not be moved or resized.
+
+    pages  uint8 [n_pages, kv_heads, 2, 64*head_dim], scales float32
+    [n_pages, kv_heads, 2]: complete blocks of 64 tokens; tail (the activation
+    dtype) [slots, kv_heads, 2, 64*head_dim]: each slot's incomplete last block;
+    table int32 [slots, max_blocks]: the page of each block; lens int32 [slots]:
+    the tokens held before the call.  table and lens may be shared by the layers
+    of a model; the caller fills the table and advances lens once per step."""
+
+    def __init__(self, pages, scales, tail, table, lens):
+        _need_cuda(pages, scales, tail, table, lens)
+        _need(pages.dtype == torch.uint8 and pages.dim() == 4 and pages.shape[2] == 2
+              and pages.shape[3] % KV_BLOCK == 0,
+              "pages must be uint8 [n_pages, kv_heads, 2, 64*head_dim]")
+        n_pages, kv_heads, _, width = pages.shape
+        slots = lens.numel()
+        _need(scales.dtype == torch.float32 and tuple(scales.shape) == (n_pages, kv_heads, 2),
+              "scales must be float32 [n_pages, kv_heads, 2]")
+        _need(tail.dtype in (torch.float16, torch.bfloat16)
+              and tuple(tail.shape) == (slots, kv_heads, 2, width),
+              "tail must be float16 or bfloat16 [slots, kv_heads, 2, 64*head_dim]")
+        _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == slots,
+              "table must be int32 [slots, max_blocks]")
+        _need(lens.dtype == torch.int32 and lens.dim() == 1, "lens must be int32 [slots]")
+        _need(len({t.device for t in (pages, scales, tail, table, lens)}) == 1,
+              "the cache's tensors must be on one device")
+        self.pages, self.scales, self.tail, self.table, self.lens = (pages, scales, tail, table,
+                                                                     lens)
+        self.kv_heads, self.head_dim, self.dtype = kv_heads, width // KV_BLOCK, tail.dtype
+        self.slots, self.device = slots, pages.device
+        self._struct = _KVCacheStruct(
+            pages.data_ptr(), scales.data_ptr(), tail.data_ptr(), table.data_ptr(),
+            lens.data_ptr(), n_pages, slots, table.shape[1], kv_heads, self.head_dim,
+            _DTYPE_CODE[tail.dtype])
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, slots: int, max_tokens: int, kv_heads: int, head_dim: int,
+              dtype: torch.dtype = torch.float16, device="cuda", n_pages: int | None = None,
+              table=None, lens=None):
+        """A cache without tokens.  Without a table each slot gets pages of its
+        own for max_tokens; with one (shared by a model's layers, or filled page
+        by page) n_pages says how many there are."""
+        blocks = (max_tokens + KV_BLOCK - 1) // KV_BLOCK
+        if n_pages is None:
+            n_pages = slots * blocks
+        if table is None:
+            table = torch.arange(slots * blocks, dtype=torch.int32,
+                                 device=device).view(slots, blocks)
+        if lens is None:
+            lens = torch.zeros(slots, dtype=torch.int32, device=device)
+        width = KV_BLOCK * head_dim
+        return cls(torch.empty((n_pages, kv_heads, 2, width), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, kv_heads, 2), dtype=torch.float32, device=device),
+                   torch.empty((slots, kv_heads, 2, width), dtype=dtype, device=device),
+                   table, lens)
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _flags(overlap_previous: bool) -> int:
+    return QLIN_OVERLAP_PREVIOUS if overlap_previous else 0
+
+
+def _need_rows(t: torch.Tensor, dim: int, what: str):
+    """On a GPU, rows contiguous (the rows themselves may be strided)."""
+    _need(t.is_cuda and t.dim() == dim, f"{what} must be a {dim}-D CUDA tensor")
+    _need(t.stride(-1) == 1, f"{what}'s rows must be contiguous")
+
+
+def _row_stride(t: torch.Tensor, width: int) -> int:
+    """Elements from row to row (a single row has no stride of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _need_starts(starts, cache):
+    _need(starts.dtype == torch.int32 and starts.device == cache.device
+          and starts.is_contiguous() and starts.numel() == cache.slots + 1,
+          "starts must be int32 [slots + 1] on the cache's device")
+
+
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-5, out=None, residual_out=None,
+                 overlap_previous=False):
+    """h = x + residual; out = h * weight / sqrt(mean(h*h) + eps), per row.
+
+    x [M, K] and weight [K] in the activation dtype, residual [M, K] in that or
+    float32.  Returns (out, residual_out), residual_out being h rounded to the
+    residual's dtype (None without a residual); residual_out=residual updates
+    it in place."""
+    _need_rows(x, 2, "x")
+    _need(x.dtype in (torch.float16, torch.bfloat16), "x must be float16 or bfloat16")
+    m, k = x.shape
+    _need(weight.is_cuda and weight.is_contiguous() and weight.dtype == x.dtype
+          and tuple(weight.shape) == (k,), "weight must be [K] in x's dtype")
+    rdt = x.dtype
+    if residual is None:
+        _need(residual_out is None, "residual_out without a residual")
+        rs = 0
+    else:
+        _need_rows(residual, 2, "residual")
+        rdt, rs = residual.dtype, _row_stride(residual, k)
+        _need(residual.shape == x.shape and rdt in (x.dtype, torch.float32),
+              "residual must have x's shape, in its dtype or float32")
+        if residual_out is None:
+            residual_out = torch.empty((m, k), dtype=rdt, device=x.device)
+        else:
+            _need(residual_out.is_cuda and residual_out.is_contiguous()
+                  and residual_out.shape == x.shape and residual_out.dtype == rdt,
+                  "residual_out must be contiguous, of the residual's shape and dtype")
+    if out is None:
+        out = torch.empty((m, k), dtype=x.dtype, device=x.device)
+    else:
+        _need(out.is_cuda and out.is_contiguous() and out.shape == x.shape
+              and out.dtype == x.dtype, "out must be contiguous, of x's shape and dtype")
+    _check(lib().qlin_add_rms_norm(
+        x.data_ptr(), _row_stride(x, k), weight.data_ptr(),
+        residual.data_ptr() if residual is not None else None, rs,
+        residual_out.data_ptr() if residual_out is not None else None, out.data_ptr(), m, k, eps,
+        _DTYPE_CODE[x.dtype], _DTYPE_CODE[rdt], _flags(overlap_previous), _raw_stream(x.device)))
+    return out, residual_out
+
+
+def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0,
+               short_wavelength: float = 0.0, long_wavelength: float = 0.0, device="cuda"):
+    """(cos, sin) of every position and pair, float32 [n_positions, rot_dim/2, 2]
+    (load time; qlin_rope_table has the scaling for long contexts)."""
+    device = torch.device(device)
+    _need(device.type == "cuda", "the table is made on a CUDA device")
+    _need(n_positions >= 0 and rot_dim >= 2, "n_positions and rot_dim must be positive")
+    table = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    _check(lib().qlin_rope_table(table.data_ptr(), n_positions, rot_dim, base, factor,
+                                 short_wavelength, long_wavelength, _raw_stream(table.device)))
+    return table
+
+
+def rope_append(qkv, table, cache: KVCache, starts, q_heads: int, interleaved: bool = False,
+                out=None, overlap_previous=False):
+    """Rotates new tokens' queries and keys and appends keys and values to the cache.
+
+    qkv [T, (q_heads + 2*kv_heads)*head_dim] (a fused linear's output; rows may
+    be strided), table from rope_table (None: no rotation), starts int32
+    [slots+1].  Returns the rotated queries [T, q_heads, head_dim]."""
+    _need_rows(qkv, 2, "qkv")
+    _need(qkv.dtype == cache.dtype and qkv.device == cache.device,
+          "qkv must have the cache's dtype and device")
+    _need_starts(starts, cache)
+    t, d = qkv.shape[0], cache.head_dim
+    _need(qkv.shape[1] == (q_heads + 2 * cache.kv_heads) * d,
+          "qkv must be [T, (q_heads + 2*kv_heads)*head_dim]")
+    n_pos = rot = 0
+    if table is not None:
+        _need(table.dtype == torch.float32 and table.dim() == 3 and table.is_contiguous()
+              and table.shape[2] == 2 and table.device == cache.device,
+              "table must be float32 [n_positions, rot_dim/2, 2] on the cache's device")
+        n_pos, rot = table.shape[0], 2 * table.shape[1]
+    if out is None:
+        out = torch.empty((t, q_heads, d), dtype=qkv.dtype, device=qkv.device)
+    else:
+        _need(out.is_contiguous() and out.dtype == qkv.dtype and out.device == qkv.device
+              and tuple(out.shape) == (t, q_heads, d),
+              "out must be contiguous [T, q_heads, head_dim] in qkv's dtype")
+    _check(lib().qlin_rope_append(
+        qkv.data_ptr(), _row_stride(qkv, qkv.shape[1]), out.data_ptr(),
+        table.data_ptr() if rot else None, n_pos, rot, int(interleaved), cache._ref,
+        starts.data_ptr(), t, q_heads, _flags(overlap_previous), _raw_stream(qkv.device)))
+    return out
+
+
+def cache_dequant(cache: KVCache, page_ids, out=None):
+    """The values that pages of the cache stand for, [n, kv_heads, 2, 64*head_dim]
+    in the activation dtype (value blocks transposed, as in the pages)."""
+    _need(page_ids.dtype == torch.int32 and page_ids.device == cache.device
+          and page_ids.is_contiguous() and page_ids.dim() == 1,
+          "page_ids must be int32 [n] on the cache's device")
+    n = page_ids.shape[0]
+    shape = (n,) + tuple(cache.pages.shape[1:])
+    if out is None:
+        out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+    else:
+        _need(out.is_contiguous() and out.dtype == cache.dtype and out.device == cache.device
+              and tuple(out.shape) == shape, "out must be contiguous, one block for each page")
+    _check(lib().qlin_cache_dequant(cache._ref, page_ids.data_ptr(), n, out.data_ptr(),
+                                    _raw_stream(cache.device)))
+    return out
+
+
+def attention_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    """Device scratch for cache_attention (calls that can overlap need one each)."""
+    with torch.cuda.device(device):
+        nbytes = int(lib().qlin_cache_attention_workspace_size(head_dim))
+    _need(nbytes > 0, f"head_dim {head_dim} is not supported")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def cache_attention(q, cache: KVCache, starts, max_new: int, workspace, scale=None, out=None,
+                    overlap_previous=False):
+    """Causal attention of new tokens over the cache that already holds them.
+
+    q [T, q_heads, head_dim] (rows may be strided), starts int32 [slots+1] as
+    for rope_append, max_new: the most new tokens of any slot; workspace from
+    attention_workspace; scale: 1/sqrt(head_dim) by default.  Returns
+    [T, q_heads, head_dim]; rows that no slot owns are left unwritten."""
+    _need_rows(q, 3, "q")
+    t, heads, d = q.shape
+    _need(q.dtype == cache.dtype and q.device == cache.device and d == cache.head_dim,
+          "q must have the cache's dtype, device and head dimension")
+    _need(q.stride(1) == d or heads == 1, "q's heads must be contiguous in a row")
+    _need_starts(starts, cache)
+    _need(workspace.device == cache.device and workspace.is_contiguous(),
+          "workspace must be on the cache's device")
+    if out is None:
+        out = torch.empty((t, heads, d), dtype=q.dtype, device=q.device)
+    else:
+        _need(out.is_contiguous() and out.dtype == q.dtype and out.device == q.device
+              and out.shape == q.shape, "out must be contiguous, of q's shape and dtype")
+    if scale is None:
+        scale = d ** -0.5
+    _check(lib().qlin_cache_attention(
+        q.data_ptr(), _row_stride(q, heads * d), out.data_ptr(), cache._ref,
+        starts.data_ptr(), t, heads, scale, max_new, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _flags(overlap_previous),
+        _raw_stream(q.device)))
+    return out
+
+
+def sample(logits, u, temperature, top_k, top_p, min_p, tokens=None, probs=None,
+           overlap_previous=False):
+    """One token per row of logits [M, V] (float32, float16 or bfloat16; rows may
+    be strided) from given uniform numbers u [M].
+
+    temperature, top_p, min_p float32 [M] and top_k int32 [M]; <= 0, >= 1 and
+    <= 0 switch top_k, top_p and min_p off, temperature <= 0 takes the largest
+    logit.  Returns (tokens int32 [M], probs float32 [M]): the share of the
+    token among what the filters kept (-1 and 0 for a row without a token)."""
+    _need_rows(logits, 2, "logits")
+    _need(logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16")
+    m, v = logits.shape
+    for t, dt, what in ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
+                        (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
+                        (min_p, torch.float32, "min_p")):
+        if not (t.dtype == dt and t.device == logits.device and t.is_contiguous()
+                and t.numel() == m):
+            raise ValueError(f"{what} must be {dt} [M] on the logits' device")
+    if tokens is None:
+        tokens = torch.empty(m, dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(m, dtype=torch.float32, device=logits.device)
+    _need(tokens.dtype == torch.int32 and tokens.is_contiguous() and tokens.numel() == m
+          and probs.dtype == torch.float32 and probs.is_contiguous() and probs.numel() == m
+          and tokens.device == probs.device == logits.device,
+          "tokens must be int32 [M] and probs float32 [M] on the logits' device")
+    _check(lib().qlin_sample(
+        logits.data_ptr(), _row_stride(logits, v), u.data_ptr(), temperature.data_ptr(),
+        top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), tokens.data_ptr(),
+        probs.data_ptr(), m, v, _DTYPE_CODE[logits.dtype], _flags(overlap_previous),
+        _raw_stream(logits.device)))
+    return tokens, probs
 
 
 def crossover_m(n: int, k: int, bits: int, dtype: torch.dtype = torch.float16) -> int:

@@ -11,6 +11,9 @@ namespace qlin {
 // Records a formatted detail message for qlin_last_error() and returns s.
 qlin_status fail(qlin_status s, const char* fmt, ...);
 
+// Empties the detail message (each entry point's first step).
+void clear_error();
+
 // Maps a CUDA runtime error (if any) from the last launch to a status.
 qlin_status check_launch(const char* what);
 
@@ -56,10 +59,38 @@ int chain_max_links();
 // N x K matrix of `bits`-bit codes on a device with `sms` SMs.
 int qmv_plan_split(int64_t N, int64_t K, int bits, int sms);
 
+// ------------------------------------------- between a decoder's linears
+// (add_rms_norm.cu, rope_append.cu, cache_attention.cu, sample.cu)
+qlin_status launch_add_rms_norm(const void* x, int64_t x_stride, const void* weight,
+                                const void* residual, int64_t residual_stride,
+                                void* residual_out, void* y, int64_t M, int64_t K, float eps,
+                                qlin_dtype dtype, qlin_dtype rdtype, unsigned flags,
+                                cudaStream_t st);
+qlin_status launch_rope_table(float* table, int64_t n_positions, int rot_dim, double base,
+                              double factor, double short_wavelength, double long_wavelength,
+                              cudaStream_t st);
+qlin_status launch_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
+                               const float* table, int64_t n_positions, int rot_dim,
+                               int interleaved, const qlin_kv_cache& c, const int32_t* starts,
+                               int64_t n_tokens, int q_heads, unsigned flags, cudaStream_t st);
+qlin_status launch_cache_dequant(const qlin_kv_cache& c, const int32_t* page_ids, int64_t n,
+                                 void* out, cudaStream_t st);
+size_t cache_attention_workspace_size(int head_dim);
+qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
+                                   const qlin_kv_cache& c, const int32_t* starts,
+                                   int64_t n_tokens, int q_heads, float scale, int max_new,
+                                   void* workspace, unsigned flags, cudaStream_t st);
+qlin_status launch_sample(const void* logits, int64_t logits_stride, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* tokens, float* probs, int64_t M,
+                          int64_t V, qlin_dtype ldtype, unsigned flags, cudaStream_t st);
+
 // Read and clear the kernels' device status words (no synchronisation).
 cudaError_t qmm_take_device_status(unsigned* flags);
 cudaError_t qmv_take_device_status(unsigned* flags);
 cudaError_t chain_take_device_status(unsigned* flags);
+cudaError_t rope_take_device_status(unsigned* flags);
+cudaError_t attention_take_device_status(unsigned* flags);
 
 constexpr int kGroup = 64;
 
