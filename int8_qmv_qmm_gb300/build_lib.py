@@ -23,7 +23,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libqlin.so")
 
 SOURCES = ("api.cu", "quant.cu", "qmv.cu", "qmv_chain.cu", "chain_static.cu", "qmm.cu",
-           "api_decoder.cu", "add_rms_norm.cu", "rope_append.cu", "cache_attention.cu", "sample.cu")
+           "api_decoder.cu", "add_rms_norm.cu", "rope_append.cu", "cache_attention.cu",
+           "attention_split.cu", "attention_tile.cu", "sample.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
