@@ -17,7 +17,6 @@
 namespace qlin {
 namespace attention {
 
-constexpr int kRows = 16;       // rows (new token, query head) of a warp's tile
 constexpr int kSplitRows = 64;  // slots with more rows go to the tile kernel
 
 struct Args {
@@ -68,32 +67,14 @@ __device__ __forceinline__ uint32_t bf162_bits(__nv_bfloat162 v) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Four codes (a word) as two pairs of 16-bit values c - 128, exactly.
-// f16: 0x6400 | c is 1024 + c, minus 1152.  bf16 has 7 fraction bits, so the
-// code's top bit goes to the subtrahend: (128 + c%128) - (c < 128 ? 256 : 128).
-template <typename T>
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t& lo, uint32_t& hi);
-template <>
-__device__ __forceinline__ void widen_codes<__half>(uint32_t w, uint32_t& lo, uint32_t& hi) {
+// Four codes (a word) as two pairs of f16 values c - 128, exactly: 0x6400 | c is
+// 1024 + c, minus 1152.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t bias = 0x64806480u;
   uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
   const __half2 k = *reinterpret_cast<const __half2*>(&bias);
   lo = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&a), k));
   hi = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&b), k));
-}
-template <>
-__device__ __forceinline__ void widen_codes<__nv_bfloat16>(uint32_t w, uint32_t& lo,
-                                                           uint32_t& hi) {
-  const uint32_t p[2] = {__byte_perm(w, 0u, 0x4140), __byte_perm(w, 0u, 0x4342)};
-  uint32_t out[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t a = (p[i] & 0x007f007fu) | 0x43004300u, b = (~p[i] & 0x00800080u) | 0x43004300u;
-    out[i] = bf162_bits(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                *reinterpret_cast<__nv_bfloat162*>(&b)));
-  }
-  lo = out[0];
-  hi = out[1];
 }
 
 template <typename T>
@@ -109,111 +90,165 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 __device__ __forceinline__ float low_f32(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_f32(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// The order of tokens and dimensions inside the products.  A product may sum
-// its k axis in any order, and the columns of the scores may stand for any
-// tokens, so both are chosen to make each thread's share of a block 16
-// consecutive bytes.  Thread (g, t) = (lane/4, lane%4):
-//   dimension of k step s, thread t:        64(s/4) + 16t + 4(s%4) + {0,1,2,3}
-//   token of score tile j = 2s + h, column n: 16(n/2) + 4s + 2h + n%2
-// and so a thread's scores of tiles 2s, 2s+1 are the tokens 16t + 4s + {0,1,2,3},
-// which is k step s of the second product, whose operand it reads as 16
-// consecutive tokens of a value row.
-template <typename T, int D>
+// Transposes an 8x8 matrix of 16-bit values held as rows lane/4, columns
+// 2(lane%4) + {0, 1}.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// One warp's attention of 8*NT rows over blocks of the cache.
+//
+// Tokens (scores) and dimensions (outputs) are the 16 rows of the products and
+// the query rows their 8 columns, so that a decode step's few rows fill the
+// products, and a block's codes are widened once for all of them:
+//   S^T [64 x 8]  = keys [64 x D] . q^T [D x 8]
+//   O^T [D x 8]  += values^T [D x 64] . P^T [64 x 8]
+// A product may sum its k axis in any order, and the rows of S^T may stand for
+// any tokens; both are chosen to make each thread's share of a key or value
+// row 16 consecutive bytes.  Thread (g, t) = (lane/4, lane%4):
+//   dimension of k step s, thread t:   64(s/4) + 16t + 4(s%4) + {0,1,2,3}
+//   token of score tile i, its row r:  16((r%8)/2) + 4i + 2(r/8) + r%2
+// so that k step i of the second product, thread t, is the tokens
+// 16t + 4i + {0,1,2,3} of a value row; S^T's fragments become P^T's by 8x8
+// transposes in registers.
+//
+// Both products take f16 whatever T is: codes are exact in it, and it rounds p
+// to 11 bits where bf16 has 8.  bf16 queries are scaled by a power of two for
+// each row, to a largest magnitude of 2^14 .. 2^15: exact down to 2^-28 of it.
+template <typename T, int D, int NT>
 struct Warp {
-  static constexpr int kQk = D / 16;  // k steps of the scores
-  static constexpr int kPv = D / 8;   // column tiles of the output
-  uint32_t q[kQk][4];
-  float o[kPv][4];
-  float m[2], l[2];  // of rows g and g + 8; scores in units of log2
-  float unit;        // o counts in units of this: the largest value scale so far
+  static constexpr int kQk = D / 16;  // k steps of the scores, row tiles of the output
+  uint32_t q[kQk][NT][2];
+  float o[kQk][NT][4];
+  float factor[NT][2];       // scores to units of log2, without the key scale
+  float m[NT][2], l[NT][2];  // of rows 8n + 2t + {0, 1}; l over this lane's tokens
+  float unit;                // o counts in units of this: the largest value scale so far
 
   __device__ void init() {
 #pragma unroll
-    for (int i = 0; i < kPv; ++i)
+    for (int i = 0; i < kQk; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
     unit = 0.f;
   }
 
-  // rows: [2] row pointers of this thread's two rows (null: zeros)
-  __device__ void load_q(const T* r0, const T* r1, int t) {
+  // A query row's fragments, in T.
+  __device__ static void load_row(const T* src, uint32_t (&w)[D / 8], int t) {
 #pragma unroll
     for (int p = 0; p < D / 64; ++p) {
-      uint4 v[2][2] = {};
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const T* src = r ? r1 : r0;
-        if (src) {
-          v[r][0] = *reinterpret_cast<const uint4*>(src + 64 * p + 16 * t);
-          v[r][1] = *reinterpret_cast<const uint4*>(src + 64 * p + 16 * t + 8);
-        }
+      uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+      if (src) {
+        v0 = *reinterpret_cast<const uint4*>(src + 64 * p + 16 * t);
+        v1 = *reinterpret_cast<const uint4*>(src + 64 * p + 16 * t + 8);
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t w[8] = {v[r][0].x, v[r][0].y, v[r][0].z, v[r][0].w,
-                               v[r][1].x, v[r][1].y, v[r][1].z, v[r][1].w};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          q[4 * p + s][r] = w[2 * s];
-          q[4 * p + s][2 + r] = w[2 * s + 1];
-        }
-      }
+      w[8 * p + 0] = v0.x, w[8 * p + 1] = v0.y, w[8 * p + 2] = v0.z, w[8 * p + 3] = v0.w;
+      w[8 * p + 4] = v1.x, w[8 * p + 5] = v1.y, w[8 * p + 6] = v1.z, w[8 * p + 7] = v1.w;
     }
   }
 
-  // Scores -> weighted probabilities (in place) with the running maximum; the
-  // factors that the rows' sums so far take go to keep.  seen[r]: tokens of the
-  // block that row r sees.  weight: what the probabilities are scaled by.
-  template <int HALVES>
-  __device__ void softmax(float (&s)[8][4], float scale, float weight, const int (&seen)[2],
-                          bool mask, int t, float (&keep)[2]) {
-    float top[2] = {-INFINITY, -INFINITY};
+  // rows[n]: row 8n + g of the tile (null: zeros)
+  __device__ void load_q(const T* const (&rows)[NT], float scale, int lane) {
+    const int t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int n = 0; n < NT; ++n) {
+      uint32_t w[D / 8];
+      load_row(rows[n], w, t);
+      float back = scale;
+      if (std::is_same<T, __nv_bfloat16>::value) {
+        float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2 * HALVES; ++e) s[j][e] *= scale;
+        for (int i = 0; i < D / 8; ++i)
+          top = fmaxf(top, fmaxf(fabsf(low_f32(w[i])), fabsf(high_f32(w[i]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is at most 2^15
+        e = max(-100, min(113, e));
+        const float down = __uint_as_float(uint32_t(127 - e) << 23);
+        back = scale * __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          w[i] = pack2<__half>(low_f32(w[i]) * down, high_f32(w[i]) * down);
+      }
+#pragma unroll
+      for (int s = 0; s < kQk; ++s) {
+        q[s][n][0] = w[2 * s];
+        q[s][n][1] = w[2 * s + 1];
+      }
+      // row g's factor, to the lanes that hold the row's scores
+      factor[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      factor[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+  }
+
+  // Scores (times scale and the rows' factors) -> weighted probabilities, in
+  // place, with the running maximum; the factors that the rows' sums so far take
+  // go to keep.  seen[n][r]: tokens of the block that row 8n + 2t + r sees.
+  // weight: what the probabilities are scaled by.
+  __device__ void softmax(float (&s)[4][NT][4], const float (&scale)[NT][2], float weight,
+                          const int (&seen)[NT][2], bool mask, int g, float (&keep)[NT][2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][n][e] *= scale[n][e & 1];
     if (mask) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 2 * HALVES; ++e)
-          if (16 * t + 2 * j + (e & 1) >= seen[e >> 1]) s[j][e] = -INFINITY;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * (g >> 1) + 4 * i + 2 * (e >> 1) + (g & 1) >= seen[n][e & 1])
+              s[i][n][e] = -INFINITY;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 2 * HALVES; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
     const float shift = log2f(weight), back = 1.f / weight;
 #pragma unroll
-    for (int r = 0; r < HALVES; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      const float next = fmaxf(m[r], top[r]);
-      const float base = next == -INFINITY ? 0.f : next;  // a row that sees nothing yet
-      keep[r] = exp2_fast(m[r] - base);
-      m[r] = next;
-      const float from = base - shift;
-      float sum = 0.f;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int r = 0; r < 2; ++r) {
+        float top = fmaxf(s[0][n][r], s[0][n][2 + r]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p = exp2_fast(s[j][2 * r + e] - from);
-          s[j][2 * r + e] = p;
-          sum += p;
-        }
-      l[r] = l[r] * keep[r] + sum * back;
-    }
+        for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(s[i][n][r], s[i][n][2 + r]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float next = fmaxf(m[n][r], top);
+        const float base = next == -INFINITY ? 0.f : next;  // a row that sees nothing yet
+        keep[n][r] = exp2_fast(m[n][r] - base);
+        m[n][r] = next;
+        const float from = base - shift;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p = exp2_fast(s[i][n][2 * h + r] - from);
+            s[i][n][2 * h + r] = p;
+            sum += p;
+          }
+        l[n][r] = l[n][r] * keep[n][r] + sum * back;
+      }
   }
 
-  template <int HALVES>
-  __device__ void rescale(const float (&keep)[2], float ratio) {
+  __device__ void rescale(const float (&keep)[NT][2], float ratio) {
 #pragma unroll
-    for (int i = 0; i < kPv; ++i)
+    for (int n = 0; n < NT; ++n) {
+      const float f[2] = {keep[n][0] * ratio, keep[n][1] * ratio};
 #pragma unroll
-      for (int e = 0; e < 2 * HALVES; ++e) o[i][e] *= keep[e >> 1] * ratio;
+      for (int i = 0; i < kQk; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] *= f[e & 1];
+    }
   }
 
   // The factor from the old unit to the new, which is at least v.
@@ -225,130 +260,154 @@ struct Warp {
   }
 
   // The scores of a complete block's 64 keys, in units of its key scale.
-  __device__ void scores(const uint8_t* codes, float (&s)[8][4], int lane) {
+  __device__ void scores(const uint8_t* codes, float (&s)[4][NT][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-      const uint8_t* row = codes + (16 * (g >> 1) + 2 * j + (g & 1)) * D + 16 * t;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+      const uint8_t* row = codes + (16 * (g >> 1) + 4 * i + (g & 1)) * D + 16 * t;
 #pragma unroll
       for (int p = 0; p < D / 64; ++p) {
-        const uint4 w = *reinterpret_cast<const uint4*>(row + 64 * p);
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        const uint4 w0 = *reinterpret_cast<const uint4*>(row + 64 * p);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(row + 2 * D + 64 * p);
+        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b0, b1;
-          widen_codes<T>(words[i], b0, b1);
-          mma<T>(s[j], q[4 * p + i], b0, b1);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t a[4];
+          widen_codes(x0[k], a[0], a[2]);
+          widen_codes(x1[k], a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma<__half>(s[i][n], a, q[4 * p + k][n][0], q[4 * p + k][n][1]);
         }
       }
     }
   }
 
-  // Scores -> the second product's operand.  The probabilities enter it in f16
-  // whatever T is: the codes are exact in f16, and it rounds p to 11 bits where
-  // bf16 has 8.  HALVES = 1: rows 8 .. 15 of the tile are empty.
-  template <int HALVES>
-  __device__ void probabilities(float (&s)[8][4], uint32_t (&a)[4][4], float k_scale,
-                                float v_scale, float scale, const int (&seen)[2], bool mask,
-                                int t) {
+  // Scores -> the second product's operand.
+  __device__ void probabilities(float (&s)[4][NT][4], uint32_t (&b)[4][NT][2], float k_scale,
+                                float v_scale, const int (&seen)[NT][2], bool mask, int lane) {
     const float ratio = raise_unit(v_scale);
     // (a block whose values are all zero has scale 0: its codes are zero too; a
     // weight below f16's range makes every probability zero in it)
     const float weight = v_scale > 0.f ? fmaxf(v_scale / unit, 0x1p-60f) : 1.f;
-    float keep[2] = {1.f, 1.f};
-    softmax<HALVES>(s, scale * k_scale, weight, seen, mask, t, keep);
-    rescale<HALVES>(keep, ratio);
+    float keep[NT][2], scale[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      scale[n][0] = factor[n][0] * k_scale, scale[n][1] = factor[n][1] * k_scale;
+    softmax(s, scale, weight, seen, mask, lane >> 2, keep);
+    rescale(keep, ratio);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          a[i][2 * h + r] = r < HALVES ? pack2<__half>(s[2 * i + h][2 * r], s[2 * i + h][2 * r + 1])
-                                       : 0u;
+        for (int h = 0; h < 2; ++h)
+          b[i][n][h] = transpose8(pack2<__half>(s[i][n][2 * h], s[i][n][2 * h + 1]));
   }
 
   // out += probabilities * the block's values (codes of D rows of 64 tokens)
-  __device__ void values(const uint8_t* codes, const uint32_t (&a)[4][4], int lane) {
+  __device__ void values(const uint8_t* codes, const uint32_t (&b)[4][NT][2], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < kPv; ++n) {
-      const uint4 w = *reinterpret_cast<const uint4*>(codes + (8 * n + g) * kBlock + 16 * t);
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < kQk; ++i) {
+      const uint8_t* row = codes + (16 * i + g) * kBlock + 16 * t;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(row);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(row + 8 * kBlock);
+      const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t b0, b1;
-        widen_codes<__half>(words[i], b0, b1);
-        mma<__half>(o[n], a[i], b0, b1);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4];
+        widen_codes(x0[k], a[0], a[2]);
+        widen_codes(x1[k], a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma<__half>(o[i][n], a, b[k][n][0], b[k][n][1]);
       }
     }
   }
 
-  // The tail: `count` tokens of T, the rest of its memory undefined.
-  __device__ void tail(const T* kv, int count, float scale, const int (&seen)[2],
-                                    int lane) {
+  // The tail: `count` tokens of T, the rest of its memory undefined.  Products
+  // in T (the queries come from memory again: q is f16).
+  __device__ void tail(const T* kv, int count, const T* const (&rows)[NT], float scale_log2,
+                       const int (&seen)[NT][2], int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float s[8][4];
+    float s[4][NT][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int n = 0; n < NT; ++n) {
+      uint32_t w[D / 8];
+      load_row(rows[n], w, t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-      const T* row = kv + (16 * (g >> 1) + 2 * j + (g & 1)) * D + 16 * t;
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) {
-        const uint4 w0 = *reinterpret_cast<const uint4*>(row + 64 * p);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(row + 64 * p + 8);
-        const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+        const T* row = kv + (16 * (g >> 1) + 4 * i + (g & 1)) * D + 16 * t;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma<T>(s[j], q[4 * p + i], words[2 * i], words[2 * i + 1]);
+        for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // two k steps to a load
+            const uint4 v0 = *reinterpret_cast<const uint4*>(row + 64 * p + 8 * h);
+            const uint4 v1 = *reinterpret_cast<const uint4*>(row + 2 * D + 64 * p + 8 * h);
+            const uint32_t a0[4] = {v0.x, v1.x, v0.y, v1.y}, a1[4] = {v0.z, v1.z, v0.w, v1.w};
+            mma<T>(s[i][n], a0, w[8 * p + 4 * h], w[8 * p + 4 * h + 1]);
+            mma<T>(s[i][n], a1, w[8 * p + 4 * h + 2], w[8 * p + 4 * h + 3]);
+          }
       }
     }
     const float ratio = raise_unit(1.f);
-    float keep[2];
-    softmax<2>(s, scale, 1.f, seen, true, t, keep);
-    rescale<2>(keep, ratio);
+    float keep[NT][2], scale[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) scale[n][0] = scale[n][1] = scale_log2;
+    softmax(s, scale, 1.f, seen, true, g, keep);
+    rescale(keep, ratio);
     const float weight = 1.f / unit;
-    // Undefined values must not meet the zeros of masked probabilities: 0 * NaN.
-    uint32_t valid[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = 16 * t + 4 * i + 2 * h;
-        valid[i][h] = tok + 1 < count ? 0xffffffffu : tok < count ? 0x0000ffffu : 0u;
-      }
     // bf16 keeps only 8 bits of p, so what it leaves over goes through a second
     // product.
     constexpr bool kTwo = std::is_same<T, __nv_bfloat16>::value;
-    uint32_t a[4][4], rest[4][4];
+    uint32_t b[4][NT][2], rest[4][NT][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float p0 = s[2 * i + h][2 * r] * weight, p1 = s[2 * i + h][2 * r + 1] * weight;
-          a[i][2 * h + r] = pack2<T>(p0, p1);
-          if (kTwo)
-            rest[i][2 * h + r] = pack2<T>(p0 - low_f32(a[i][2 * h + r]),
-                                          p1 - high_f32(a[i][2 * h + r]));
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = s[i][n][2 * h] * weight, p1 = s[i][n][2 * h + 1] * weight;
+          const uint32_t v = pack2<T>(p0, p1);
+          b[i][n][h] = transpose8(v);
+          if (kTwo) rest[i][n][h] = transpose8(pack2<T>(p0 - low_f32(v), p1 - high_f32(v)));
         }
+    // Undefined values must not meet the zeros of masked probabilities: 0 * NaN.
+    uint32_t valid[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tok = 16 * t + 4 * k + 2 * h;
+        valid[k][h] = tok + 1 < count ? 0xffffffffu : tok < count ? 0x0000ffffu : 0u;
+      }
     kv += kBlock * D;
 #pragma unroll
-    for (int n = 0; n < kPv; ++n) {
-      const T* row = kv + (8 * n + g) * kBlock + 16 * t;
-      const uint4 w0 = *reinterpret_cast<const uint4*>(row);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(row + 8);
-      const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    for (int i = 0; i < kQk; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t b0 = words[2 * i] & valid[i][0], b1 = words[2 * i + 1] & valid[i][1];
-        mma<T>(o[n], a[i], b0, b1);
-        if (kTwo) mma<T>(o[n], rest[i], b0, b1);
+      for (int h = 0; h < 2; ++h) {
+        const T* row = kv + (16 * i + g) * kBlock + 16 * t + 8 * h;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(row);
+        const uint4 v1 = *reinterpret_cast<const uint4*>(row + 8 * kBlock);
+        const uint32_t a[2][4] = {{v0.x, v1.x, v0.y, v1.y}, {v0.z, v1.z, v0.w, v1.w}};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int k = 2 * h + c;
+          const uint32_t av[4] = {a[c][0] & valid[k][0], a[c][1] & valid[k][0],
+                                  a[c][2] & valid[k][1], a[c][3] & valid[k][1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma<T>(o[i][n], av, b[k][n][0], b[k][n][1]);
+            if (kTwo) mma<T>(o[i][n], av, rest[k][n][0], rest[k][n][1]);
+          }
+        }
       }
-    }
   }
 };
 

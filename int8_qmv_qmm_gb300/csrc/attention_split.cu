@@ -53,8 +53,10 @@ struct Info {  // of a block that is being copied
 };
 enum { kCodes = 0, kTail = 1, kNone = 2 };
 
-template <int D>
+// NT: tiles of 8 rows that a warp takes at once.
+template <int D, int NT>
 struct Layout {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kChunk = kBlock * D;             // bytes of a block's keys or values
   static constexpr int kRing = kRingBytes / kChunk;     // chunks in a warp's ring
   static constexpr int kOut = D + 4;                    // floats of a joined row
@@ -70,10 +72,11 @@ struct Layout {
   static constexpr int kPart = kRows * (D + 2);  // floats
 };
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float* parts,
                                                             unsigned* counters) {
-  using L = Layout<D>;
+  using L = Layout<D, NT>;
+  constexpr int kRows = L::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_out = reinterpret_cast<float*>(smem + L::kOutAt);
   float* s_m = reinterpret_cast<float*>(smem + L::kStatAt);
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float*
   };
   pump();
 
-  Warp<T, D> w;
+  Warp<T, D, NT> w;
   for (int64_t x = x0; x < x1;) {
     // ---- a piece: blocks x .. end of the tile that x is in
     const int b = slot_at(x);
@@ -255,61 +258,72 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float*
     const int64_t end = last < x1 ? last : x1;
     const bool over = r.n > a.max_new;
     const int here = min(kRows, rows - row0);
-    const T* qp[2];
-    int pos[2];
+    const T* qp[NT];
+    int pos[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + g + 8 * i;
-      qp[i] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + 8 * n + g;
+      qp[n] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
                                (kvh * a.group + row % a.group) * D
                          : nullptr;
-      pos[i] = row < rows ? r.held + row / a.group : -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int mine = row0 + 8 * n + 2 * t + i;
+        pos[n][i] = mine < rows ? r.held + mine / a.group : -1;
+      }
     }
     w.init();
-    w.load_q(qp[0], qp[1], t);
+    w.load_q(qp, a.scale_log2, lane);
     const int first_pos = r.held + row0 / a.group;
     for (; done < count; ++done) {
       const int64_t at = x0 + member + done * team_warps;
       if (at >= end) break;
       const int j = int(at - first);
       const Info f = info[done % kInfo];
-      const int seen[2] = {pos[0] - j * kBlock + 1, pos[1] - j * kBlock + 1};
+      int seen[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        seen[n][0] = pos[n][0] - j * kBlock + 1, seen[n][1] = pos[n][1] - j * kBlock + 1;
       if (f.kind == kCodes) {
         const bool mask = first_pos < j * kBlock + kBlock - 1;
-        float s[8][4];
-        uint32_t p[4][4];
+        float s[4][NT][4];
+        uint32_t p[4][NT][2];
         w.scores(chunk(), s, lane);
         release();
-        if (here <= 8)
-          w.template probabilities<1>(s, p, f.k_scale, f.v_scale, a.scale_log2, seen, mask, t);
-        else
-          w.template probabilities<2>(s, p, f.k_scale, f.v_scale, a.scale_log2, seen, mask, t);
+        w.probabilities(s, p, f.k_scale, f.v_scale, seen, mask, lane);
         w.values(chunk(), p, lane);
         release();
       } else if (f.kind == kTail) {
         w.tail(static_cast<const T*>(a.c.tail) +
                    (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D,
-               r.held + r.n - j * kBlock, a.scale_log2, seen, lane);
+               r.held + r.n - j * kBlock, qp, a.scale_log2, seen, lane);
       }
     }
     pump();  // (blocks without copies at the piece's end)
 
     // ---- join the team's warps
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 1);
-      w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 2);
-      if (t == 0) {
-        s_m[warp * kRows + g + 8 * i] = w.m[i];
-        s_l[warp * kRows + g + 8 * i] = w.l[i];
-      }
-      if (8 * i < here) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<float2*>(s_out + (warp * kRows + g + 8 * i) * L::kOut + 8 * c + 2 * t) =
-              make_float2(w.o[c][2 * i] * w.unit, w.o[c][2 * i + 1] * w.unit);
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * n + 2 * t + i;
+        float l = w.l[n][i];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) {
+          s_m[warp * kRows + row] = w.m[n][i];
+          s_l[warp * kRows + row] = l;
+        }
+        if (row < here) {
+          float* dst = s_out + (warp * kRows + row) * L::kOut + g;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            dst[16 * c] = w.o[c][n][i] * w.unit;
+            dst[16 * c + 8] = w.o[c][n][2 + i] * w.unit;
+          }
+        }
       }
-    }
     team_barrier();
     const bool whole = x == first && end == last;
     const int w0 = warp - member, mine = member * 32 + lane;
@@ -393,11 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float*
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
-  const int bytes = Layout<D>::bytes(a.c.slots);
-  if (cudaFuncSetAttribute(split_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Layout<D>::bytes(kMaxSlots)) != cudaSuccess)
+  using L = Layout<D, NT>;
+  static_assert(L::kListAt + (kMaxSlots + 1) * 8 + kMaxSlots * 4 <= 227 * 1024, "it fits");
+  if (cudaFuncSetAttribute(split_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           L::bytes(kMaxSlots)) != cudaSuccess)
     return;  // (the caller's check of the launch reports it)
   const int sms = sm_count();
   unsigned* counters = static_cast<unsigned*>(workspace);
@@ -405,14 +420,22 @@ void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(bytes);
+  cfg.dynamicSmemBytes = size_t(L::bytes(a.c.slots));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, parts, counters);
+  cudaLaunchKernelEx(&cfg, split_kernel<T, D, NT>, a, parts, counters);
+}
+
+template <typename T, int D>
+void launch_rows(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
+  if (int64_t(a.max_new) * a.group <= 8)
+    launch_t<T, D, 1>(a, workspace, flags, st);
+  else
+    launch_t<T, D, 2>(a, workspace, flags, st);
 }
 
 }  // namespace
@@ -420,17 +443,16 @@ void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
 size_t split_workspace_size(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const size_t teams = size_t(sm_count()) * kWarps;
-  return (teams + 63) / 64 * 64 * 4 + teams * 2 * kRows * (head_dim + 2) * 4;
+  return (teams + 63) / 64 * 64 * 4 + teams * 2 * 16 * (head_dim + 2) * 4;
 }
 
 void launch_split(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
-  static_assert(Layout<128>::kListAt + (kMaxSlots + 1) * 8 + kMaxSlots * 4 <= 227 * 1024, "fits");
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, flags, st)
-                       : launch_t<__half, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_rows<__half, 64>(a, workspace, flags, st)
+                       : launch_rows<__half, 128>(a, workspace, flags, st);
   else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, flags, st)
-                       : launch_t<__nv_bfloat16, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(a, workspace, flags, st)
+                       : launch_rows<__nv_bfloat16, 128>(a, workspace, flags, st);
 }
 
 cudaError_t split_take_status(unsigned* flags) {

@@ -14,6 +14,7 @@ __device__ unsigned int g_tile_status = 0;
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kRows = 16;
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_tile_status, bit); }
 
@@ -36,25 +37,32 @@ __global__ void __launch_bounds__(kWarps * 32) tile_kernel(const Args a) {
   const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
   const int rows = r.n * a.group, r0 = int(tile) * kRows;
   const bool over = r.n > a.max_new;  // (the split kernel reports it)
-  Warp<T, D> w;
+  Warp<T, D, 2> w;
   w.init();
   const T* qp[2];
-  int pos[2];
+  int pos[2][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = r0 + g + 8 * i;
-    qp[i] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
+  for (int n = 0; n < 2; ++n) {
+    const int row = r0 + 8 * n + g;
+    qp[n] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
                              (kvh * a.group + row % a.group) * D
                        : nullptr;
-    pos[i] = row < rows ? r.held + row / a.group : -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int mine = r0 + 8 * n + 2 * t + i;
+      pos[n][i] = mine < rows ? r.held + mine / a.group : -1;
+    }
   }
-  w.load_q(qp[0], qp[1], t);
+  w.load_q(qp, a.scale_log2, lane);
   const int total = r.held + r.n, full = total / kBlock;
   const int last = r.held + (min(r0 + kRows, rows) - 1) / a.group;  // last position seen
   const int first = r.held + r0 / a.group;
   if (!over) {
     for (int j = warp; j <= last / kBlock; j += kWarps) {
-      const int seen[2] = {pos[0] - j * kBlock + 1, pos[1] - j * kBlock + 1};
+      int seen[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        seen[n][0] = pos[n][0] - j * kBlock + 1, seen[n][1] = pos[n][1] - j * kBlock + 1;
       if (j < full) {
         const int64_t page = page_of(a.c, b, j);
         if (page < 0) {
@@ -63,32 +71,38 @@ __global__ void __launch_bounds__(kWarps * 32) tile_kernel(const Args a) {
         }
         const int64_t at = page * a.c.kv_heads + kvh;
         const uint8_t* codes = static_cast<const uint8_t*>(a.c.pages) + at * 2 * kBlock * D;
-        float s[8][4];
-        uint32_t p[4][4];
+        float s[4][2][4];
+        uint32_t p[4][2][2];
         w.scores(codes, s, lane);
-        w.template probabilities<2>(s, p, a.c.scales[2 * at], a.c.scales[2 * at + 1],
-                                    a.scale_log2, seen, first < j * kBlock + kBlock - 1, t);
+        w.probabilities(s, p, a.c.scales[2 * at], a.c.scales[2 * at + 1], seen,
+                        first < j * kBlock + kBlock - 1, lane);
         w.values(codes + kBlock * D, p, lane);
       } else {
         w.tail(static_cast<const T*>(a.c.tail) +
                    (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D,
-               total - j * kBlock, a.scale_log2, seen, lane);
+               total - j * kBlock, qp, a.scale_log2, seen, lane);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 1);
-    w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 2);
-    if (t == 0) {
-      s_m[warp][g + 8 * i] = w.m[i];
-      s_l[warp][g + 8 * i] = w.l[i];
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 8 * n + 2 * t + i;
+      float l = w.l[n][i];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (g == 0) {
+        s_m[warp][row] = w.m[n][i];
+        s_l[warp][row] = l;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        s_o[warp][row][16 * c + g] = w.o[c][n][i] * w.unit;
+        s_o[warp][row][16 * c + 8 + g] = w.o[c][n][2 + i] * w.unit;
+      }
     }
-  }
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s_o[warp][g + 8 * (e >> 1)][8 * n + 2 * t + (e & 1)] = w.o[n][e] * w.unit;
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * D; i += blockDim.x) {
     const int row = i / D, d = i % D;
