@@ -29,7 +29,7 @@ qlin_status check_cache(const char* name, const qlin_kv_cache* c) {
   if (c->slots < 1 || c->kv_heads < 1 || c->max_blocks < 1 || c->n_pages < 1)
     return fail(QLIN_ERR_INVALID_ARG,
                 "%s: slots, kv_heads, max_blocks and n_pages must be positive", name);
-  if (c->kv_heads > 65535 || c->slots > 2048 || c->n_pages > (int64_t(1) << 31))
+  if (c->kv_heads > 65535 || c->slots > 1024 || c->n_pages > (int64_t(1) << 31))
     return fail(QLIN_ERR_UNSUPPORTED, "%s: cache beyond the supported range", name);
   if (!c->pages || !c->scales || !c->tail || !c->table || !c->lens)
     return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer in the cache", name);

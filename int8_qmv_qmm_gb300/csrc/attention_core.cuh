@@ -60,6 +60,12 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp, exact at 0 and 
   return y;
 }
 
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t half2_bits(__half2 v) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
@@ -155,33 +161,44 @@ struct Warp {
     }
   }
 
-  // rows[n]: row 8n + g of the tile (null: zeros)
-  __device__ void load_q(const T* const (&rows)[NT], float scale, int lane) {
-    const int t = lane & 3;
+  // rows[n]: row 8n + g of the tile (null: zeros).  The fragments are T until
+  // prepare_q.
+  __device__ void load_q(const T* const (&rows)[NT], int lane) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       uint32_t w[D / 8];
-      load_row(rows[n], w, t);
-      float back = scale;
-      if (std::is_same<T, __nv_bfloat16>::value) {
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          top = fmaxf(top, fmaxf(fabsf(low_f32(w[i])), fabsf(high_f32(w[i]))));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is at most 2^15
-        e = max(-100, min(113, e));
-        const float down = __uint_as_float(uint32_t(127 - e) << 23);
-        back = scale * __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          w[i] = pack2<__half>(low_f32(w[i]) * down, high_f32(w[i]) * down);
-      }
+      load_row(rows[n], w, lane & 3);
 #pragma unroll
       for (int s = 0; s < kQk; ++s) {
         q[s][n][0] = w[2 * s];
         q[s][n][1] = w[2 * s + 1];
+      }
+    }
+  }
+
+  __device__ void prepare_q(float scale, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float back = scale;
+      if (std::is_same<T, __nv_bfloat16>::value) {
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < kQk; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            top = fmaxf(top, fmaxf(fabsf(low_f32(q[s][n][h])), fabsf(high_f32(q[s][n][h]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is below 2^15
+        e = max(-100, min(113, e));
+        const float down = __uint_as_float(uint32_t(127 - e) << 23);
+        back = scale * __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < kQk; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            q[s][n][h] = pack2<__half>(low_f32(q[s][n][h]) * down, high_f32(q[s][n][h]) * down);
       }
       // row g's factor, to the lanes that hold the row's scores
       factor[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
@@ -211,7 +228,7 @@ struct Warp {
             if (16 * (g >> 1) + 4 * i + 2 * (e >> 1) + (g & 1) >= seen[n][e & 1])
               s[i][n][e] = -INFINITY;
     }
-    const float shift = log2f(weight), back = 1.f / weight;
+    const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -254,7 +271,7 @@ struct Warp {
   // The factor from the old unit to the new, which is at least v.
   __device__ float raise_unit(float v) {
     const float next = fmaxf(unit, v);
-    const float ratio = next > 0.f ? unit / next : 0.f;
+    const float ratio = next > unit ? __fdividef(unit, next) : next > 0.f ? 1.f : 0.f;
     unit = next;
     return ratio;
   }
@@ -293,7 +310,7 @@ struct Warp {
     const float ratio = raise_unit(v_scale);
     // (a block whose values are all zero has scale 0: its codes are zero too; a
     // weight below f16's range makes every probability zero in it)
-    const float weight = v_scale > 0.f ? fmaxf(v_scale / unit, 0x1p-60f) : 1.f;
+    const float weight = v_scale > 0.f ? fmaxf(__fdividef(v_scale, unit), 0x1p-60f) : 1.f;
     float keep[NT][2], scale[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)

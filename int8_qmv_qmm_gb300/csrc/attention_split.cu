@@ -1,18 +1,18 @@
 // Attention of slots with few new rows: single tokens, drafts, short chunks.
 //
 // What bounds it is reading the cache once, so the blocks of all slots, heads
-// and row tiles are put in one list and every team of warps takes an equal,
-// consecutive share of it, however long or short the slots are.  Inside its
-// share a team's warps take the blocks in turn.  Each warp streams its blocks
-// through a ring of its own in shared memory (bulk copies, one for the keys and
-// one for the values of a block), so no barrier stands in its loop; the page
-// numbers and scales of its next 32 blocks are fetched at once, a lane each.
+// and row tiles are put in one list and every warp takes an equal, consecutive
+// share of it, however long or short the slots are.
 //
-// A piece is what a team has of one tile (slot, key/value head, 16 rows).  At
-// its end the warps' sums are joined through shared memory.  A tile that lies
-// in one team's share is written out; else the team leaves its part in the
-// workspace, and the team that finds itself last joins the parts, always in the
-// list's order: the result does not depend on which came last.
+// A warp streams its blocks through a ring of its own in shared memory (bulk
+// copies, one for the keys and one for the values of a block) and shares nothing
+// with the others, so no barrier stands in its way.  The page numbers and scales
+// of its next 32 blocks are looked up at once, a lane each.
+//
+// A piece is what a warp has of one tile (slot, key/value head, 8 rows).  A tile
+// that lies in one warp's share is written out; of the others each warp leaves
+// its part in the workspace, and a second kernel, launched while the first still
+// runs, joins the parts in the list's order.
 
 #include "attention_core.cuh"
 #include "sm100_ptx.cuh"
@@ -26,9 +26,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRingBytes = 16384;  // of a warp
-constexpr int kMaxSlots = 2048;
-constexpr int kInfo = 8;           // blocks that the copies may run ahead
+constexpr int kRingBytes = 24576;             // of a warp: 6 chunks at D = 64, 3 at 128
+constexpr int kInfo = 8;                      // blocks that the copies may run ahead
+constexpr int kRows = 8;
+constexpr int kMaxSlots = 1024;
+constexpr int kTailCost = 4;                  // of a tail, in blocks
+constexpr int kJoinThreads = 512;
+constexpr int kJoinPerSm = 2;
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_split_status, bit); }
 
@@ -43,167 +47,179 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
+enum : unsigned { kCodes = 0, kTail = 1, kNone = 2 };
 
-struct Info {  // of a block that is being copied
-  float k_scale, v_scale;
-  int kind;
+struct alignas(16) Info {  // of a block on its way
+  float2 scales;  // of its keys and its values
+  unsigned x;  // its place in the list
+  unsigned kind;
 };
-enum { kCodes = 0, kTail = 1, kNone = 2 };
 
-// NT: tiles of 8 rows that a warp takes at once.
-template <int D, int NT>
+struct Slot {  // blocks that the list has before it, its tokens with the new ones, its rows
+  int list, total, row0, n;
+};
+
+// A tile whose blocks begin in warp i's share and pass its end: warps i .. last
+// have parts.
+struct alignas(16) Split {
+  int last;      // -1: warp i has none
+  int token0;    // first row of the slot in q and out
+  int row0;      // of the tile in the slot (-1 - row0: a slot with too many rows)
+  int kvh_here;  // 16 * key/value head + rows of the tile
+};
+
+template <int D>
 struct Layout {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kChunk = kBlock * D;             // bytes of a block's keys or values
-  static constexpr int kRing = kRingBytes / kChunk;     // chunks in a warp's ring
-  static constexpr int kOut = D + 4;                    // floats of a joined row
-  static constexpr int kRingAt = 0;
-  static constexpr int kOutAt = kWarps * kRingBytes;
-  static constexpr int kStatAt = kOutAt + kWarps * kRows * kOut * 4;  // m and l
-  static constexpr int kInfoAt = kStatAt + 2 * kWarps * kRows * 4;
+  static constexpr int kChunk = kBlock * D;          // bytes of a block's keys or values
+  static constexpr int kRing = kRingBytes / kChunk;  // chunks in a warp's ring
+  static constexpr int kInfoAt = kWarps * kRingBytes;
   static constexpr int kBarAt = kInfoAt + kWarps * kInfo * int(sizeof(Info));
   static constexpr int kScanAt = (kBarAt + kWarps * kRing * 8 + 15) / 16 * 16;
-  static constexpr int kListAt = kScanAt + 2 * kWarps * 8 + 16;
-  static int bytes(int slots) { return kListAt + (slots + 1) * 8 + slots * 4; }
-  // the workspace: a part is kRows rows of D sums, then their m and l
+  static constexpr int kListAt = kScanAt + kWarps * 8;
+  static int bytes(int slots) { return kListAt + slots * int(sizeof(Slot)); }
+  // a part in the workspace: sums [D][8 rows], then the rows' m and l
   static constexpr int kPart = kRows * (D + 2);  // floats
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float* parts,
-                                                            unsigned* counters) {
-  using L = Layout<D, NT>;
-  constexpr int kRows = L::kRows;
+// Places of a slot in the list: its blocks, a tail counting for kTailCost of them
+// (it is read without the ring, and takes about as long).
+__device__ __forceinline__ unsigned places_of(int tokens) {
+  return unsigned(tokens) / kBlock + (tokens % kBlock ? kTailCost : 0);
+}
+
+// The shares of `blocks` places: warp i has start(i) .. start(i + 1) - 1, the
+// first `longer` warps one more than the others.
+struct Shares {
+  unsigned each, longer;
+  __device__ Shares(unsigned blocks, unsigned warps)
+      : each(blocks / warps), longer(blocks % warps) {}
+  __device__ unsigned start(unsigned i) const { return i * each + min(i, longer); }
+  __device__ unsigned of(unsigned x) const {
+    const unsigned edge = longer * (each + 1);
+    return x < edge ? x / (each + 1) : longer + (x - edge) / each;
+  }
+};
+
+// A tile.
+struct Piece {
+  int slot, kvh, row0, here;    // here: rows of the tile
+  unsigned first, last;         // the tile's blocks in the list
+};
+
+__device__ __forceinline__ Piece piece_at(const Slot* s_slot, int slots, int group, unsigned x) {
+  int lo = 0, hi = slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (unsigned(s_slot[mid].list) <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Slot sl = s_slot[lo];
+  const int rows = sl.n * group;
+  const unsigned n = places_of(sl.total), tile = (x - sl.list) / n;
+  const unsigned row_tiles = unsigned(rows + kRows - 1) / kRows;
+  Piece p;
+  p.slot = lo;
+  p.kvh = int(tile / row_tiles);
+  p.row0 = int(tile % row_tiles) * kRows;
+  p.here = min(kRows, rows - p.row0);
+  p.first = sl.list + tile * n;
+  p.last = p.first + n;
+  return p;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    split_kernel(const Args a, float* parts, Split* splits) {
+  using L = Layout<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_out = reinterpret_cast<float*>(smem + L::kOutAt);
-  float* s_m = reinterpret_cast<float*>(smem + L::kStatAt);
-  float* s_l = s_m + kWarps * kRows;
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::kScanAt);
-  int* s_last = reinterpret_cast<int*>(smem + L::kScanAt + 2 * kWarps * 8);  // of a team: 4
-  int64_t* s_list = reinterpret_cast<int64_t*>(smem + L::kListAt);  // blocks before each slot
-  int32_t* s_total = reinterpret_cast<int32_t*>(s_list + a.c.slots + 1);
+  Slot* s_slot = reinterpret_cast<Slot*>(smem + L::kListAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + L::kRingAt + warp * kRingBytes;
+  uint8_t* ring = smem + warp * kRingBytes;
   Info* info = reinterpret_cast<Info*>(smem + L::kInfoAt) + warp * kInfo;
   const uint32_t bar = ptx::smem_u32(smem + L::kBarAt) + warp * L::kRing * 8;
-  if (lane == 0)
+  if (lane == 0) {
     for (int i = 0; i < L::kRing; ++i) ptx::mbar_init(bar + 8 * i, 1);
-  ptx::fence_mbar_init();
+    ptx::fence_mbar_init();
+  }
   grid_launch_dependents();
   grid_dependency_wait();
 
-  // the list: blocks before each slot, and how many tiles there are in all
-  int64_t blocks = 0, tiles = 0;
+  // the list: blocks before each slot
+  int64_t all_blocks = 0;
   for (int b0 = 0; b0 < a.c.slots; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    int64_t mine = 0, pieces = 0;
+    int64_t here = 0;
+    SlotRows r = {0, 0, 0, false};
     if (b < a.c.slots) {
-      const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
-      const int64_t rows = int64_t(r.n) * a.group;
+      r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
       if (blockIdx.x == 0) {
         if (r.bad) report(kStatusRows);
         if (r.n > a.max_new) report(kStatusMaxNew);
       }
-      s_total[b] = r.held + r.n;
-      if (rows <= kSplitRows) pieces = (rows + kRows - 1) / kRows * a.c.kv_heads;
-      mine = pieces * ((r.held + r.n + kBlock - 1) / kBlock);
+      const int64_t rows = int64_t(r.n) * a.group;
+      if (rows <= kSplitRows)
+        here = (rows + kRows - 1) / kRows * a.c.kv_heads * places_of(r.held + r.n);
     }
-    int64_t upto = mine;
+    int64_t upto = here;
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += v;
     }
-    for (int d = 16; d; d >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, d);
     __syncthreads();
-    if (lane == 31) {
-      s_scan[warp] = upto;
-      s_scan[kWarps + warp] = pieces;
-    }
+    if (lane == 31) s_scan[warp] = upto;
     __syncthreads();
-    int64_t before = blocks;
+    int64_t before = all_blocks;
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) before += s_scan[i];
-      blocks += s_scan[i];
-      tiles += s_scan[kWarps + i];
+      all_blocks += s_scan[i];
     }
-    if (b < a.c.slots) s_list[b] = before + upto - mine;
+    if (b < a.c.slots)
+      s_slot[b] = Slot{int(before + upto - here), r.held + r.n, int(r.row0), r.n};
   }
-  if (threadIdx.x == 0) s_list[a.c.slots] = blocks;
   __syncthreads();
-  if (blocks == 0) return;
+  // a CTA's warps are gridDim.x apart, so that a short list spreads over the CTAs
+  const unsigned me = warp * gridDim.x + blockIdx.x;
+  if (lane == 0) splits[me].last = -1;
+  if (all_blocks > 0x3fffffff) {  // (more than a cache holds)
+    if (threadIdx.x == 0) report(kStatusRows);
+    return;
+  }
+  const unsigned blocks = unsigned(all_blocks);
+  if (me >= blocks) return;
+  const Shares shares(blocks, min(gridDim.x * kWarps, blocks));
+  const unsigned end = shares.start(me + 1);
 
-  // Teams: as many warps to a tile as there are warps for it, so that tiles are
-  // cut only where they have to be; and no team without a block for each warp,
-  // unless that left tiles without a team.
-  const int64_t all_warps = int64_t(gridDim.x) * kWarps;
-  int64_t each = all_warps / tiles;
-  each = each < blocks / tiles ? each : blocks / tiles;
-  const int team_warps = each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
-  int64_t teams = all_warps / team_warps, useful = blocks / team_warps;
-  useful = useful > tiles ? useful : tiles;
-  teams = teams < useful ? teams : useful;
-  teams = teams < blocks ? teams : blocks;
-  // team i of a CTA: spread over the CTAs first
-  const int in_cta = warp / team_warps, member = warp % team_warps;
-  const int64_t team = int64_t(in_cta) * gridDim.x + blockIdx.x;
-  if (team >= teams) return;  // (a team's warps leave together; barriers are the teams')
-  const int team_threads = team_warps * 32;
-  auto team_barrier = [&] {
-    if (team_warps == 1)
-      __syncwarp();
-    else
-      named_barrier(1 + in_cta, team_threads);
-  };
-  auto start_of = [&](int64_t i) { return i * blocks / teams; };
-  auto team_of = [&](int64_t x) { return ((x + 1) * teams - 1) / blocks; };
-  const int64_t x0 = start_of(team), x1 = start_of(team + 1);
-  const int64_t count = x1 - x0 > member ? (x1 - x0 - member + team_warps - 1) / team_warps : 0;
-
-  // where block x of the list lies
-  auto slot_at = [&](int64_t x) {
-    int lo = 0, hi = a.c.slots;  // s_list[lo] <= x < s_list[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_list[mid] <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    return lo;
-  };
-
-  // ---- the copies of this warp's blocks x0 + member, + team_warps, ...
-  int64_t next = 0;      // the next block to copy
-  bool keys_sent = false;
-  unsigned sent = 0, used = 0;  // chunks
-  int64_t done = 0;      // blocks that are through
-  const uint8_t* my_src = nullptr;  // of lane l: block (next / 32 * 32 + l)
+  // ---- the copies
+  unsigned next = shares.start(me);
+  unsigned looked = next, known = next;  // lane l knows block looked + l < known
+  bool keys_sent = false;                // the next block's keys are on the way
+  unsigned sent = 0, used = 0;           // chunks
+  unsigned begun = 0, done = 0;          // blocks
+  const uint8_t* my_src = nullptr;
   float2 my_scales = make_float2(0.f, 0.f);
-  int my_kind = kNone;
+  unsigned my_kind = kNone;
   auto pump = [&] {
-    while (next < count && sent - used < unsigned(L::kRing) && next - done < kInfo) {
-      if (!keys_sent && (next & 31) == 0) {
-        const int64_t i = next + lane;
+    while (next < end && sent - used < unsigned(L::kRing) && begun - done < unsigned(kInfo)) {
+      if (next == known) {
+        looked = next;
+        known = min(next + 32, end);
+        const unsigned x = next + lane;
         my_kind = kNone;
-        if (i < count) {
-          const int64_t x = x0 + member + i * team_warps;
-          const int b = slot_at(x);
-          const int total = s_total[b], n = (total + kBlock - 1) / kBlock;
-          const int64_t in_slot = x - s_list[b];
-          const int j = int(in_slot % n);
-          const int64_t rows = int64_t(a.starts[b + 1] - a.starts[b]) * a.group;
-          const int kvh = int(in_slot / n / ((rows + kRows - 1) / kRows));
-          if (j >= total / kBlock) {
+        if (x < known) {
+          const Piece p = piece_at(s_slot, a.c.slots, a.group, x);
+          const int j = int(x - p.first);
+          const int full = s_slot[p.slot].total / kBlock;
+          if (j == full) {
             my_kind = kTail;
-          } else {
-            const int64_t page = page_of(a.c, b, j);
+          } else if (j < full) {
+            const int64_t page = page_of(a.c, p.slot, j);
             if (page < 0) {
               report(kStatusPage);
             } else {
-              const int64_t at = page * a.c.kv_heads + kvh;
+              const int64_t at = page * a.c.kv_heads + p.kvh;
               my_kind = kCodes;
               my_src = static_cast<const uint8_t*>(a.c.pages) + at * 2 * L::kChunk;
               my_scales = reinterpret_cast<const float2*>(a.c.scales)[at];
@@ -211,212 +227,229 @@ __global__ void __launch_bounds__(kThreads, 1) split_kernel(const Args a, float*
           }
         }
       }
-      const int from = int(next & 31);
-      const int kind = __shfl_sync(0xffffffffu, my_kind, from);
-      const float ks = __shfl_sync(0xffffffffu, my_scales.x, from);
-      const float vs = __shfl_sync(0xffffffffu, my_scales.y, from);
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(my_src), from));
-      if (!keys_sent && lane == 0) info[next % kInfo] = Info{ks, vs, kind};
-      if (kind != kCodes) {
-        ++next;
-        continue;
+      const int from = int(next - looked);
+      const bool codes = __shfl_sync(0xffffffffu, my_kind, from) == kCodes;
+      if (lane == from) {
+        if (!keys_sent) info[begun % kInfo] = Info{my_scales, next, my_kind};
+        const unsigned slot = sent % L::kRing;
+        if (codes)
+          bulk_load(ptx::smem_u32(ring + slot * L::kChunk), my_src + (keys_sent ? L::kChunk : 0),
+                    L::kChunk, bar + 8 * slot);
       }
-      const unsigned slot = sent % L::kRing;
-      if (lane == 0)
-        bulk_load(ptx::smem_u32(ring + slot * L::kChunk), src + (keys_sent ? L::kChunk : 0),
-                  L::kChunk, bar + 8 * slot);
-      ++sent;
-      next += keys_sent;
-      keys_sent = !keys_sent;
+      sent += codes;
+      begun += !keys_sent;
+      next += !codes || keys_sent;
+      keys_sent = codes && !keys_sent;
     }
     __syncwarp();
   };
-  // the next chunk, when it has landed
-  auto chunk = [&]() -> const uint8_t* {
-    const unsigned slot = used % L::kRing;
-    if (!ptx::mbar_wait(bar + 8 * slot, (used / L::kRing) & 1) && lane == 0) report(kStatusWait);
-    return ring + slot * L::kChunk;
-  };
-  auto release = [&] {
-    __syncwarp();  // every lane has read it
-    ++used;
+
+  Warp<T, D, 1> w;
+  Piece p = {};
+  Split split = {-1, 0, 0, 0};
+  unsigned x = 0, x_piece = 0;
+  const T* qp[1] = {nullptr};
+  int pos0 = 0, pos1 = 0, first_pos = 0;
+  bool open = false;         // a piece is under way
+  bool have_scores = false;  // of the block whose values come next
+  float s[4][1][4];
+  // A block takes two turns, its keys and its values, each of which gives a
+  // chunk of the ring back; the copies go on in between.
+  while (true) {
     pump();
-  };
-  pump();
-
-  Warp<T, D, NT> w;
-  for (int64_t x = x0; x < x1;) {
-    // ---- a piece: blocks x .. end of the tile that x is in
-    const int b = slot_at(x);
-    const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
-    const int rows = r.n * a.group, n = (r.held + r.n + kBlock - 1) / kBlock;
-    const int64_t in_slot = x - s_list[b], tile = in_slot / n;
-    const int row_tiles = (rows + kRows - 1) / kRows;
-    const int kvh = int(tile / row_tiles), row0 = int(tile % row_tiles) * kRows;
-    const int64_t first = x - in_slot % n, last = first + n;  // the tile's blocks in the list
-    const int64_t end = last < x1 ? last : x1;
-    const bool over = r.n > a.max_new;
-    const int here = min(kRows, rows - row0);
-    const T* qp[NT];
-    int pos[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = row0 + 8 * n + g;
-      qp[n] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
-                               (kvh * a.group + row % a.group) * D
-                         : nullptr;
+    const bool through = done == begun;
+    const Info f = info[done % kInfo];
+    const bool same = open && !through && f.x < p.last;
+    if (open && !same) {
+      // ---- the piece is through: blocks x_piece .. x - 1 of the list
+      open = false;
+      float l[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int mine = row0 + 8 * n + 2 * t + i;
-        pos[n][i] = mine < rows ? r.held + mine / a.group : -1;
+        l[i] = w.l[0][i];
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
       }
-    }
-    w.init();
-    w.load_q(qp, a.scale_log2, lane);
-    const int first_pos = r.held + row0 / a.group;
-    for (; done < count; ++done) {
-      const int64_t at = x0 + member + done * team_warps;
-      if (at >= end) break;
-      const int j = int(at - first);
-      const Info f = info[done % kInfo];
-      int seen[NT][2];
+      const Slot sl = s_slot[p.slot];
+      const bool over = sl.n > a.max_new;  // (a slot with more rows than the call allows: zeros)
+      if (x_piece == p.first && x == p.last) {
+        const float f0 = l[0] > 0.f && !over ? w.unit / l[0] : 0.f;
+        const float f1 = l[1] > 0.f && !over ? w.unit / l[1] : 0.f;
+        const int row = p.row0 + g;
+        T* dst = static_cast<T*>(a.out) +
+                 (int64_t(sl.row0 + row / a.group) * a.q_heads + p.kvh * a.group +
+                  row % a.group) * D + 2 * t;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        seen[n][0] = pos[n][0] - j * kBlock + 1, seen[n][1] = pos[n][1] - j * kBlock + 1;
-      if (f.kind == kCodes) {
-        const bool mask = first_pos < j * kBlock + kBlock - 1;
-        float s[4][NT][4];
-        uint32_t p[4][NT][2];
-        w.scores(chunk(), s, lane);
-        release();
-        w.probabilities(s, p, f.k_scale, f.v_scale, seen, mask, lane);
-        w.values(chunk(), p, lane);
-        release();
-      } else if (f.kind == kTail) {
-        w.tail(static_cast<const T*>(a.c.tail) +
-                   (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D,
-               r.held + r.n - j * kBlock, qp, a.scale_log2, seen, lane);
-      }
-    }
-    pump();  // (blocks without copies at the piece's end)
-
-    // ---- join the team's warps
+        for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 8 * n + 2 * t + i;
-        float l = w.l[n][i];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) {
-          s_m[warp * kRows + row] = w.m[n][i];
-          s_l[warp * kRows + row] = l;
-        }
-        if (row < here) {
-          float* dst = s_out + (warp * kRows + row) * L::kOut + g;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            dst[16 * c] = w.o[c][n][i] * w.unit;
-            dst[16 * c + 8] = w.o[c][n][2 + i] * w.unit;
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v =
+                transpose8(over ? 0u : pack2<T>(w.o[c][0][2 * h] * f0, w.o[c][0][2 * h + 1] * f1));
+            if (g < p.here) *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 * h) = v;
           }
-        }
-      }
-    team_barrier();
-    const bool whole = x == first && end == last;
-    const int w0 = warp - member, mine = member * 32 + lane;
-    float* part = parts + (2 * team + (x == first ? 1 : 0)) * L::kPart;
-    T* out = static_cast<T*>(a.out);
-    auto store = [&](int row, int d, float4 o, float sum) {
-      const float inv = sum > 0.f && !over ? 1.f / sum : 0.f;
-      const int rr = row0 + row;
-      T* dst = out + ((r.row0 + rr / a.group) * a.q_heads + kvh * a.group + rr % a.group) * D + d;
-      union {
-        T v[4];
-        uint2 bits;
-      } u;
-      u.v[0] = Act<T>::from_f32_rn(over ? 0.f : o.x * inv);
-      u.v[1] = Act<T>::from_f32_rn(over ? 0.f : o.y * inv);
-      u.v[2] = Act<T>::from_f32_rn(over ? 0.f : o.z * inv);
-      u.v[3] = Act<T>::from_f32_rn(over ? 0.f : o.w * inv);
-      *reinterpret_cast<uint2*>(dst) = u.bits;
-    };
-    for (int i = mine; i < here * (D / 4); i += team_threads) {
-      const int row = i / (D / 4), d = i % (D / 4) * 4;
-      float top = -INFINITY;
-      for (int k = w0; k < w0 + team_warps; ++k) top = fmaxf(top, s_m[k * kRows + row]);
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = w0; k < w0 + team_warps; ++k) {
-        const float m = s_m[k * kRows + row];
-        const float f = m == -INFINITY ? 0.f : exp2_fast(m - top);
-        const float4 v = *reinterpret_cast<const float4*>(s_out + (k * kRows + row) * L::kOut + d);
-        sum += s_l[k * kRows + row] * f;
-        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
-      }
-      if (whole) {
-        store(row, d, o, sum);
       } else {
-        __stcg(reinterpret_cast<float4*>(part + row * D + d), o);
-        if (d == 0) {
-          __stcg(part + kRows * D + row, top);
-          __stcg(part + kRows * D + kRows + row, sum);
+        float* part = parts + size_t(2 * me + (x_piece == p.first ? 1 : 0)) * L::kPart;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(part + (16 * c + 8 * h + g) * kRows + 2 * t) =
+                make_float2(w.o[c][0][2 * h] * w.unit, w.o[c][0][2 * h + 1] * w.unit);
+        if (g == 0) {
+          *reinterpret_cast<float2*>(part + kRows * D + 2 * t) = make_float2(w.m[0][0], w.m[0][1]);
+          *reinterpret_cast<float2*>(part + kRows * (D + 1) + 2 * t) = make_float2(l[0], l[1]);
         }
+        if (x_piece == p.first)
+          split = Split{int(shares.of(p.last - 1)), sl.row0, over ? -1 - p.row0 : p.row0,
+                        16 * p.kvh + p.here};
       }
     }
-    if (!whole) {
-      const int64_t t0 = team_of(first), t1 = team_of(last - 1);
-      __threadfence();
-      team_barrier();
-      if (mine == 0) {
-        const unsigned before = atomicAdd(counters + t0, 1u);
-        const bool is_last = before == unsigned(t1 - t0);
-        if (is_last) atomicExch(counters + t0, 0u);  // as it was, for the next call
-        s_last[in_cta] = is_last;
+    if (through) break;
+    if (!same) {
+      // ---- a new piece
+      open = true;
+      x_piece = f.x;
+      p = piece_at(s_slot, a.c.slots, a.group, f.x);
+      const Slot sl = s_slot[p.slot];
+      const int held = sl.total - sl.n, row = p.row0 + g;
+      qp[0] = g < p.here ? static_cast<const T*>(a.q) +
+                               int64_t(sl.row0 + row / a.group) * a.q_stride +
+                               (p.kvh * a.group + row % a.group) * D
+                         : nullptr;
+      // the two rows whose scores this lane holds
+      pos0 = 2 * t < p.here ? held + (p.row0 + 2 * t) / a.group : -1;
+      pos1 = 2 * t + 1 < p.here ? held + (p.row0 + 2 * t + 1) / a.group : -1;
+      first_pos = held + p.row0 / a.group;
+      w.load_q(qp, lane);
+      w.init();
+      w.prepare_q(a.scale_log2, lane);
+    }
+    x = f.x + 1;
+    const int j = int(f.x - p.first);
+    const int seen[1][2] = {{pos0 - j * kBlock + 1, pos1 - j * kBlock + 1}};
+    if (f.kind == kCodes) {
+      const unsigned slot = used % L::kRing;
+      const uint8_t* chunk = ring + slot * L::kChunk;
+      if (!ptx::mbar_wait(bar + 8 * slot, (used / L::kRing) & 1) && lane == 0) report(kStatusWait);
+      if (!have_scores) {
+        w.scores(chunk, s, lane);
+      } else {
+        uint32_t b[4][1][2];
+        w.probabilities(s, b, f.scales.x, f.scales.y, seen, first_pos < j * kBlock + kBlock - 1,
+                        lane);
+        w.values(chunk, b, lane);
       }
-      team_barrier();
-      if (s_last[in_cta]) {
-        __threadfence();
-        for (int i = mine; i < here * (D / 4); i += team_threads) {
-          const int row = i / (D / 4), d = i % (D / 4) * 4;
-          // a running join: parts come in the list's order
-          float top = -INFINITY, sum = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      ++used;
+      done += have_scores;
+      have_scores = !have_scores;
+    } else {
+      if (f.kind == kTail)
+        w.tail(static_cast<const T*>(a.c.tail) +
+                   (int64_t(p.slot) * a.c.kv_heads + p.kvh) * 2 * kBlock * D,
+               s_slot[p.slot].total - j * kBlock, qp, a.scale_log2, seen, lane);
+      ++done;
+    }
+    __syncwarp();  // every lane has read the chunk and the info
+  }
+  if (lane == 0 && split.last >= 0) splits[me] = split;
+}
+
+// Joins the parts of the tiles that pass the end of a warp's share.  Each CTA
+// lists them (the order is that of the warps) and takes every gridDim.x-th of
+// their slices, 16 dimensions of a tile's 8 rows: groups of 32 threads
+// (4 rows of one dimension each) take a part each in turn, and are added up in
+// order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const float* parts,
+                                                            const Split* splits, int warps) {
+  using L = Layout<D>;
+  constexpr int kSlices = D / 16, kGroups = kJoinThreads / 32;
+  __shared__ int s_which[4096], s_count[kGroups + 1];
+  __shared__ float4 s_o[kGroups][32], s_m[kGroups][2], s_l[kGroups][2];
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  int n = 0;
+  for (int i0 = 0; i0 < warps; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool mine = i < warps && __ldcg(&splits[i].last) >= 0;
+    const unsigned ballot = __ballot_sync(0xffffffffu, mine);
+    __syncthreads();
+    if (lane == 0) s_count[group] = __popc(ballot);
+    __syncthreads();
+    int at = n;
+    for (int k = 0; k < kGroups; ++k) {
+      if (k < group) at += s_count[k];
+      n += s_count[k];
+    }
+    if (mine) s_which[at + __popc(ballot & ((1u << lane) - 1))] = i;
+  }
+  __syncthreads();
+  for (int task = blockIdx.x; task < n * kSlices; task += gridDim.x) {
+    const int first = s_which[task / kSlices], d0 = task % kSlices * 16;
+    const Split sp = splits[first];
+    // this thread: dimension d0 + lane/2, rows 4 * (lane%2) ..
+    const int d = d0 + (lane >> 1), half = lane & 1;
+    float m[4], l[4], o[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r] = 0.f;
 #pragma unroll 4
-          for (int64_t k = t0; k <= t1; ++k) {
-            const float* from = parts + (2 * k + (k == t0 ? 1 : 0)) * L::kPart;
-            const float m = __ldcg(from + kRows * D + row);
-            const float l = __ldcg(from + kRows * D + kRows + row);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + row * D + d));
-            const float next_top = fmaxf(top, m);
-            const float base = next_top == -INFINITY ? 0.f : next_top;
-            const float f0 = exp2_fast(top - base), f1 = exp2_fast(m - base);
-            sum = sum * f0 + l * f1;
-            o.x = o.x * f0 + v.x * f1, o.y = o.y * f0 + v.y * f1;
-            o.z = o.z * f0 + v.z * f1, o.w = o.w * f0 + v.w * f1;
-            top = next_top;
-          }
-          store(row, d, o, sum);
-        }
+    for (int k = first + group; k <= sp.last; k += kGroups) {
+      const float* part = parts + size_t(2 * k + (k == first ? 1 : 0)) * L::kPart;
+      const float4 pm = __ldcg(reinterpret_cast<const float4*>(part + kRows * D) + half);
+      const float4 pl = __ldcg(reinterpret_cast<const float4*>(part + kRows * (D + 1)) + half);
+      const float4 po = __ldcg(reinterpret_cast<const float4*>(part + kRows * d) + half);
+      const float vm[4] = {pm.x, pm.y, pm.z, pm.w}, vl[4] = {pl.x, pl.y, pl.z, pl.w},
+                  vo[4] = {po.x, po.y, po.z, po.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float next = fmaxf(m[r], vm[r]), base = next == -INFINITY ? 0.f : next;
+        const float f0 = exp2_fast(m[r] - base), f1 = exp2_fast(vm[r] - base);
+        l[r] = l[r] * f0 + vl[r] * f1;
+        o[r] = o[r] * f0 + vo[r] * f1;
+        m[r] = next;
       }
     }
-    team_barrier();  // the joined rows are read before the next piece writes its own
-    x = end;
+    s_o[group][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane < 2) {
+      s_m[group][lane] = make_float4(m[0], m[1], m[2], m[3]);
+      s_l[group][lane] = make_float4(l[0], l[1], l[2], l[3]);
+    }
+    __syncthreads();
+    // 128 sums: thread i takes row i/16, dimension d0 + i%16
+    const int row = threadIdx.x >> 4, dd = threadIdx.x & 15, here = sp.kvh_here & 15;
+    if (row < here) {
+      auto value = [&](const float4* v) { return reinterpret_cast<const float*>(v)[row & 3]; };
+      float top = -INFINITY, sum = 0.f, out = 0.f;
+      for (int k = 0; k < kGroups; ++k) top = fmaxf(top, value(&s_m[k][row >> 2]));
+      for (int k = 0; k < kGroups; ++k) {
+        const float vm = value(&s_m[k][row >> 2]);
+        const float f = vm == -INFINITY ? 0.f : exp2_fast(vm - top);
+        sum += value(&s_l[k][row >> 2]) * f;
+        out += value(&s_o[k][2 * dd + (row >> 2)]) * f;
+      }
+      if (sp.row0 < 0) out = 0.f;
+      const int rr = (sp.row0 < 0 ? -1 - sp.row0 : sp.row0) + row, kvh = sp.kvh_here >> 4;
+      static_cast<T*>(a.out)[(int64_t(sp.token0 + rr / a.group) * a.q_heads + kvh * a.group +
+                              rr % a.group) *
+                                 D +
+                             d0 + dd] = Act<T>::from_f32_rn(sum > 0.f ? out / sum : 0.f);
+    }
+    __syncthreads();
   }
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D>
 void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
-  using L = Layout<D, NT>;
-  static_assert(L::kListAt + (kMaxSlots + 1) * 8 + kMaxSlots * 4 <= 227 * 1024, "it fits");
-  if (cudaFuncSetAttribute(split_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using L = Layout<D>;
+  static_assert(L::kListAt + kMaxSlots * int(sizeof(Slot)) <= 227 * 1024, "it fits");
+  if (cudaFuncSetAttribute(split_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            L::bytes(kMaxSlots)) != cudaSuccess)
     return;  // (the caller's check of the launch reports it)
-  const int sms = sm_count();
-  unsigned* counters = static_cast<unsigned*>(workspace);
-  float* parts = reinterpret_cast<float*>(counters + (sms * kWarps + 63) / 64 * 64);
+  const int sms = sm_count(), warps = sms * kWarps;
+  Split* splits = static_cast<Split*>(workspace);
+  float* parts = reinterpret_cast<float*>(splits + warps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sms));
   cfg.blockDim = dim3(kThreads);
@@ -427,32 +460,30 @@ void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, split_kernel<T, D, NT>, a, parts, counters);
-}
-
-template <typename T, int D>
-void launch_rows(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
-  if (int64_t(a.max_new) * a.group <= 8)
-    launch_t<T, D, 1>(a, workspace, flags, st);
-  else
-    launch_t<T, D, 2>(a, workspace, flags, st);
+  cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, parts, splits);
+  cfg.gridDim = dim3(unsigned(sms * kJoinPerSm));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts),
+                     static_cast<const Split*>(splits), warps);
 }
 
 }  // namespace
 
 size_t split_workspace_size(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
-  const size_t teams = size_t(sm_count()) * kWarps;
-  return (teams + 63) / 64 * 64 * 4 + teams * 2 * 16 * (head_dim + 2) * 4;
+  const size_t warps = size_t(sm_count()) * kWarps;
+  return warps * (sizeof(Split) + 2 * kRows * (head_dim + 2) * 4);
 }
 
 void launch_split(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_rows<__half, 64>(a, workspace, flags, st)
-                       : launch_rows<__half, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, flags, st)
+                       : launch_t<__half, 128>(a, workspace, flags, st);
   else
-    a.c.head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(a, workspace, flags, st)
-                       : launch_rows<__nv_bfloat16, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, flags, st)
+                       : launch_t<__nv_bfloat16, 128>(a, workspace, flags, st);
 }
 
 cudaError_t split_take_status(unsigned* flags) {

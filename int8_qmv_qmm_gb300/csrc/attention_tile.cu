@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(kWarps * 32) tile_kernel(const Args a) {
       pos[n][i] = mine < rows ? r.held + mine / a.group : -1;
     }
   }
-  w.load_q(qp, a.scale_log2, lane);
+  w.load_q(qp, lane);
+  w.prepare_q(a.scale_log2, lane);
   const int total = r.held + r.n, full = total / kBlock;
   const int last = r.held + (min(r0 + kRows, rows) - 1) / a.group;  // last position seen
   const int first = r.held + r0 / a.group;
