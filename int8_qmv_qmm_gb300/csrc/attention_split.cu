@@ -36,17 +36,6 @@ constexpr int kJoinPerSm = 2;
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_split_status, bit); }
 
-// Copies `bytes` from global memory to dst, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  ptx::mbar_arrive_expect_tx(bar, bytes);
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 enum : unsigned { kCodes = 0, kTail = 1, kNone = 2 };
 
 struct alignas(16) Info {  // of a block on its way
@@ -64,7 +53,7 @@ struct Slot {  // blocks that the list has before it, its tokens with the new on
 struct alignas(16) Split {
   int last;      // -1: warp i has none
   int token0;    // first row of the slot in q and out
-  int row0;      // of the tile in the slot (-1 - row0: a slot with too many rows)
+  int row0;      // of the tile in the slot
   int kvh_here;  // 16 * key/value head + rows of the tile
 };
 
@@ -149,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the list: blocks before each slot
   int64_t all_blocks = 0;
+  bool over = false;  // a slot has more rows than the call allows
   for (int b0 = 0; b0 < a.c.slots; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     int64_t here = 0;
@@ -160,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r.n > a.max_new) report(kStatusMaxNew);
       }
       const int64_t rows = int64_t(r.n) * a.group;
-      if (rows <= kSplitRows)
+      over |= r.n > a.max_new;
+      if (rows <= kSplitRows && r.n <= a.max_new)
         here = (rows + kRows - 1) / kRows * a.c.kv_heads * places_of(r.held + r.n);
     }
     int64_t upto = here;
@@ -179,7 +170,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (b < a.c.slots)
       s_slot[b] = Slot{int(before + upto - here), r.held + r.n, int(r.row0), r.n};
   }
-  __syncthreads();
+  if (__syncthreads_or(over)) {  // such slots are left out: zeros
+    for (int b = 0; b < a.c.slots; ++b) {
+      const Slot sl = s_slot[b];
+      if (sl.n <= a.max_new) continue;
+      for (int row = blockIdx.x; row < sl.n; row += gridDim.x) {
+        T* dst = static_cast<T*>(a.out) + int64_t(sl.row0 + row) * a.q_heads * D;
+        for (int i = threadIdx.x * 8; i < a.q_heads * D; i += kThreads * 8)
+          *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
   // a CTA's warps are gridDim.x apart, so that a short list spreads over the CTAs
   const unsigned me = warp * gridDim.x + blockIdx.x;
   if (lane == 0) splits[me].last = -1;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!keys_sent) info[begun % kInfo] = Info{my_scales, next, my_kind};
         const unsigned slot = sent % L::kRing;
         if (codes)
-          bulk_load(ptx::smem_u32(ring + slot * L::kChunk), my_src + (keys_sent ? L::kChunk : 0),
+          ptx::bulk_load(ptx::smem_u32(ring + slot * L::kChunk), my_src + (keys_sent ? L::kChunk : 0),
                     L::kChunk, bar + 8 * slot);
       }
       sent += codes;
@@ -272,10 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
       }
       const Slot sl = s_slot[p.slot];
-      const bool over = sl.n > a.max_new;  // (a slot with more rows than the call allows: zeros)
       if (x_piece == p.first && x == p.last) {
-        const float f0 = l[0] > 0.f && !over ? w.unit / l[0] : 0.f;
-        const float f1 = l[1] > 0.f && !over ? w.unit / l[1] : 0.f;
+        const float f0 = l[0] > 0.f ? w.unit / l[0] : 0.f;
+        const float f1 = l[1] > 0.f ? w.unit / l[1] : 0.f;
         const int row = p.row0 + g;
         T* dst = static_cast<T*>(a.out) +
                  (int64_t(sl.row0 + row / a.group) * a.q_heads + p.kvh * a.group +
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t v =
-                transpose8(over ? 0u : pack2<T>(w.o[c][0][2 * h] * f0, w.o[c][0][2 * h + 1] * f1));
+                transpose8(pack2<T>(w.o[c][0][2 * h] * f0, w.o[c][0][2 * h + 1] * f1));
             if (g < p.here) *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 * h) = v;
           }
       } else {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(part + kRows * (D + 1) + 2 * t) = make_float2(l[0], l[1]);
         }
         if (x_piece == p.first)
-          split = Split{int(shares.of(p.last - 1)), sl.row0, over ? -1 - p.row0 : p.row0,
+          split = Split{int(shares.of(p.last - 1)), sl.row0, p.row0,
                         16 * p.kvh + p.here};
       }
     }
@@ -429,8 +429,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const 
         sum += value(&s_l[k][row >> 2]) * f;
         out += value(&s_o[k][2 * dd + (row >> 2)]) * f;
       }
-      if (sp.row0 < 0) out = 0.f;
-      const int rr = (sp.row0 < 0 ? -1 - sp.row0 : sp.row0) + row, kvh = sp.kvh_here >> 4;
+      const int rr = sp.row0 + row, kvh = sp.kvh_here >> 4;
       static_cast<T*>(a.out)[(int64_t(sp.token0 + rr / a.group) * a.q_heads + kvh * a.group +
                               rr % a.group) *
                                  D +

@@ -1,10 +1,33 @@
-// Attention of slots with many new rows (prompts and their chunks).
+// Attention of slots with many new rows (prompts and their chunks) on the
+// tcgen05 tensor cores.
 //
-// One CTA for each 16 rows and key/value head.  Its warps take the blocks in
-// turn, each with a running maximum and sum of its own (m16n8k16 products), and
-// are joined at the end.
+// A CTA takes 256 rows (new tokens times the query heads that share a key/value
+// head) of one slot and key/value head, as two tiles of 128, and walks the
+// blocks that they see.  Per block and tile
+//   S [128 x 64] = q [128 x D] . keys^T      (A: q in tensor memory)
+//   P            = exp2(S * scale - max)     (row by row, in registers)
+//   O [128 x D] += P [128 x 64] . values     (A: P in tensor memory, over S)
+// with S, P and O in tensor memory and both operands of every product in f16:
+// the codes are exact in it (a bf16 tail is scaled by a power of two for the
+// block, bf16 queries by one for each row).  The two tiles alternate: while one
+// is in its exponentials the tensor core works for the other.
+//
+//   warps 0..3, 4..7  a tile each, a thread for each row: the row's query to
+//                     tensor memory, then per block S from tensor memory,
+//                     maximum, exponentials and sum (no other thread has a part
+//                     of the row), P back; O is rescaled only when the maximum
+//                     has grown by 2^8 (P stays within f16, and the last
+//                     division makes up for it).
+//   warps 8..11       widen the codes of keys and values to f16 in shared memory
+//                     (128-byte swizzle, K-major), a ring of 3 blocks; the codes
+//                     come through a ring of bulk copies.
+//   warp 12           issues the products (one thread).
+//
+// What bounds it: at D = 128 the products (1024 cycles of the tensor core for a
+// block of both tiles), at D = 64 the exponentials.
 
 #include "attention_core.cuh"
+#include "sm100_ptx.cuh"
 
 namespace qlin {
 namespace attention {
@@ -13,122 +36,478 @@ __device__ unsigned int g_tile_status = 0;
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kRows = 16;
+constexpr int kTileRows = 128;
+constexpr int kTiles = 2;
+constexpr int kCtaRows = kTiles * kTileRows;
+constexpr int kSoftmaxWarps = 4 * kTiles;
+constexpr int kWidenWarps = 4;
+constexpr int kThreads = (kSoftmaxWarps + kWidenWarps + 1) * 32;
+constexpr int kStages = 3;  // blocks of f16 operands
+constexpr int kRaw = 4;     // blocks of codes
+constexpr float kSlack = 8.f;        // log2 of how far a row's maximum may lag
+constexpr float kUnitSlack = 64.f;   // how far a value scale may be above the unit
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_tile_status, bit); }
 
+template <int D>
+struct Layout {
+  static constexpr int kKeys = 64 * D * 2;            // bytes of a block's f16 keys, or values
+  static constexpr int kStage = 2 * kKeys;
+  static constexpr int kCodes = 2 * 64 * D;           // a block's codes
+  static constexpr int kRawAt = kStages * kStage;
+  static constexpr int kBarAt = kRawAt + kRaw * kCodes;
+  // barriers: operands full/empty, codes full, S full, P full, q full, O full
+  static constexpr int kBars = 2 * kStages + kRaw + 2 * kTiles + 2;
+  static constexpr int kScaleAt = kBarAt + kBars * 8;  // float2 of each stage
+  static constexpr int kMiscAt = kScaleAt + kStages * 8;
+  static constexpr int kBytes = kMiscAt + 64 + 1024;   // + alignment to 1024
+  // tensor memory columns
+  static constexpr int kS = 0;                    // 64 a tile (P over the first 32)
+  static constexpr int kQ = kTiles * 64;          // D/2 a tile
+  static constexpr int kO = kQ + kTiles * D / 2;  // D a tile
+  static_assert(kO + kTiles * D <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void widen_barrier() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// 16 codes -> 16 f16 values, 32 bytes
+__device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
+  widen_codes(w.x, lo.x, lo.y);
+  widen_codes(w.y, lo.z, lo.w);
+  widen_codes(w.z, hi.x, hi.y);
+  widen_codes(w.w, hi.z, hi.w);
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, swizzled.
+__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) tile_kernel(const Args a) {
-  __shared__ float s_o[kWarps][kRows][D + 4];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
+  using L = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw_base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = base + L::kBarAt;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto raw_full = [&](int s) { return bars + 8u * (2 * kStages + s); };
+  auto s_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + t); };
+  auto p_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + kTiles + t); };
+  const uint32_t q_full = bars + 8u * (2 * kStages + kRaw + 2 * kTiles), o_full = q_full + 8u;
+  float2* scales = reinterpret_cast<float2*>(smem + L::kScaleAt);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscAt);
+  int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 8);  // slot, tile
+  float* s_top = reinterpret_cast<float*>(smem + L::kMiscAt + 16);  // of the four widening warps
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full(s), kWidenWarps);
+      ptx::mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < kRaw; ++s) ptx::mbar_init(raw_full(s), 1);
+    for (int t = 0; t < kTiles; ++t) {
+      ptx::mbar_init(s_full(t), 1);
+      ptx::mbar_init(p_full(t), 4);
+    }
+    ptx::mbar_init(q_full, kSoftmaxWarps);
+    ptx::mbar_init(o_full, 1);
+    ptx::fence_mbar_init();
+  }
   grid_launch_dependents();
   grid_dependency_wait();
-  const int kvh = blockIdx.y;
-  int b = 0;
-  int64_t tile = 0;
-  if (!find_slot(a.c.slots, blockIdx.x, &b, &tile, [&](int s) -> int64_t {
-        const SlotRows r = slot_rows(a.starts, a.c.lens, s, a.n_tokens);
-        const int64_t rows = int64_t(r.n) * a.group;
-        return rows > kSplitRows ? (rows + kRows - 1) / kRows : 0;
-      }))
-    return;
-  const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
-  const int rows = r.n * a.group, r0 = int(tile) * kRows;
-  const bool over = r.n > a.max_new;  // (the split kernel reports it)
-  Warp<T, D, 2> w;
-  w.init();
-  const T* qp[2];
-  int pos[2][2];
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int row = r0 + 8 * n + g;
-    qp[n] = row < rows ? static_cast<const T*>(a.q) + (r.row0 + row / a.group) * a.q_stride +
-                             (kvh * a.group + row % a.group) * D
-                       : nullptr;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int mine = r0 + 8 * n + 2 * t + i;
-      pos[n][i] = mine < rows ? r.held + mine / a.group : -1;
-    }
+  // which rows this CTA has: the later ones of a slot, which see more, first
+  if (warp == 0) {
+    int b = -1;
+    int64_t at = 0;
+    const bool any = find_slot(a.c.slots, blockIdx.x, &b, &at, [&](int s) -> int64_t {
+      const SlotRows r = slot_rows(a.starts, a.c.lens, s, a.n_tokens);
+      const int64_t rows = int64_t(r.n) * a.group;
+      return rows > kSplitRows && r.n <= a.max_new ? (rows + kCtaRows - 1) / kCtaRows : 0;
+    });
+    if (lane == 0) s_work[0] = any ? b : -1, s_work[1] = int(at);
   }
-  w.load_q(qp, lane);
-  w.prepare_q(a.scale_log2, lane);
-  const int total = r.held + r.n, full = total / kBlock;
-  const int last = r.held + (min(r0 + kRows, rows) - 1) / a.group;  // last position seen
-  const int first = r.held + r0 / a.group;
-  if (!over) {
-    for (int j = warp; j <= last / kBlock; j += kWarps) {
-      int seen[2][2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        seen[n][0] = pos[n][0] - j * kBlock + 1, seen[n][1] = pos[n][1] - j * kBlock + 1;
-      if (j < full) {
-        const int64_t page = page_of(a.c, b, j);
-        if (page < 0) {
-          if (lane == 0) report(kStatusPage);
-          continue;
-        }
-        const int64_t at = page * a.c.kv_heads + kvh;
-        const uint8_t* codes = static_cast<const uint8_t*>(a.c.pages) + at * 2 * kBlock * D;
-        float s[4][2][4];
-        uint32_t p[4][2][2];
-        w.scores(codes, s, lane);
-        w.probabilities(s, p, a.c.scales[2 * at], a.c.scales[2 * at + 1], seen,
-                        first < j * kBlock + kBlock - 1, lane);
-        w.values(codes + kBlock * D, p, lane);
-      } else {
-        w.tail(static_cast<const T*>(a.c.tail) +
-                   (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D,
-               total - j * kBlock, qp, a.scale_log2, seen, lane);
-      }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 8 * n + 2 * t + i;
-      float l = w.l[n][i];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (g == 0) {
-        s_m[warp][row] = w.m[n][i];
-        s_l[warp][row] = l;
-      }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        s_o[warp][row][16 * c + g] = w.o[c][n][i] * w.unit;
-        s_o[warp][row][16 * c + 8 + g] = w.o[c][n][2 + i] * w.unit;
-      }
-    }
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * D; i += blockDim.x) {
-    const int row = i / D, d = i % D;
-    if (r0 + row >= rows) break;
-    float top = -INFINITY;
-    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_m[k][row]);
-    float sum = 0.f, o = 0.f;
-    for (int k = 0; k < kWarps; ++k) {
-      const float f = s_m[k][row] == -INFINITY ? 0.f : exp2f(s_m[k][row] - top);
-      sum += s_l[k][row] * f;
-      o += s_o[k][row][d] * f;
-    }
-    static_cast<T*>(a.out)[((r.row0 + (r0 + row) / a.group) * a.q_heads + kvh * a.group +
-                            (r0 + row) % a.group) *
-                               D +
-                           d] = Act<T>::from_f32_rn(sum > 0.f ? o / sum : 0.f);
+  const int b = s_work[0];
+  if (b < 0) return;
+  if (warp == kSoftmaxWarps + kWidenWarps) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
   }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
+  const int kvh = blockIdx.y, rows = r.n * a.group;
+  const int tiles = (rows + kCtaRows - 1) / kCtaRows;
+  const int row0 = (tiles - 1 - s_work[1]) * kCtaRows;
+  const int total = r.held + r.n;
+  const int last = r.held + (min(row0 + kCtaRows, rows) - 1) / a.group;  // position seen
+  const int n = last / kBlock + 1;                                      // blocks
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ a row each
+    const int tile = warp >> 2, quarter = warp & 3;
+    const int row = row0 + tile * kTileRows + quarter * 32 + lane;
+    const bool mine = row < rows;
+    const int pos = mine ? r.held + row / a.group : 0x7fffffff;
+    const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t ts = at + L::kS + tile * 64, to = at + L::kO + tile * D;
+    float factor = fabsf(a.scale_log2);
+    {
+      const T* src = static_cast<const T*>(a.q) +
+                     (r.row0 + (mine ? row : 0) / a.group) * a.q_stride +
+                     (kvh * a.group + (mine ? row : 0) % a.group) * D;
+      uint32_t w[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (mine) v = *reinterpret_cast<const uint4*>(src + 8 * i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+      if (std::is_same<T, __nv_bfloat16>::value) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          top = fmaxf(top, fmaxf(fabsf(low_f32(w[i])), fabsf(high_f32(w[i]))));
+        int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is below 2^15
+        e = max(-100, min(113, e));
+        const float down = __uint_as_float(uint32_t(127 - e) << 23);
+        factor *= __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          w[i] = pack2<__half>(low_f32(w[i]) * down, high_f32(w[i]) * down);
+      }
+      // a negative scale goes to the query: the maximum is taken before scaling
+      if (a.scale_log2 < 0.f) {
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        ptx::tmem_st_32x32b_x32(at + L::kQ + tile * (D / 2) + 32 * i,
+                                *reinterpret_cast<uint32_t(*)[32]>(w + 32 * i));
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_full);
+    }
+    const int first = r.held + (row0 + tile * kTileRows) / a.group;  // of the tile: all see up to it
+    float m = -INFINITY, l = 0.f, unit = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % kStages;
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile), j & 1)) &&
+           __all_sync(0xffffffffu, ptx::mbar_wait(full(st), (j / kStages) & 1));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float2 ks = scales[st];
+      uint32_t v[64];
+      ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
+      ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      ptx::tmem_wait_ld();
+      if (first < j * kBlock + kBlock - 1) {
+        const int seen = pos - j * kBlock;  // token i is seen where i <= seen
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i > seen) v[i] = 0xff800000u;  // -infinity
+      }
+      // (never zero: a score of -infinity has to stay one)
+      const float scale = fmaxf(factor * ks.x, 1e-30f);
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 64; i += 2)
+        top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+      top *= scale;
+      // O counts in units of `unit`; a block's values in units of ks.y
+      float keep = 1.f;
+      bool turn = false;
+      if (ks.y > unit * kUnitSlack || (unit == 0.f && ks.y > 0.f)) {  // the same for every row
+        keep = unit > 0.f ? __fdividef(unit, ks.y) : 1.f;
+        turn = unit > 0.f;
+        unit = ks.y;
+      }
+      // (a block of zero values has scale 0; a weight below f16's range is none)
+      const float weight = ks.y > 0.f ? fmaxf(__fdividef(ks.y, unit), 0x1p-60f) : 1.f;
+      if (top > m + kSlack || m == -INFINITY) {
+        const float next = fmaxf(top, m);
+        const float f = m == -INFINITY ? 1.f : exp2_fast(m - next);
+        l *= f;
+        keep *= f;
+        m = next;
+      }
+      turn = turn || keep != 1.f;
+      if (j > 0 && __any_sync(0xffffffffu, turn)) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld_32x32b_x32(to + c, o);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+          ptx::tmem_st_32x32b_x32(to + c, o);
+        }
+        ptx::tmem_wait_st();
+      }
+      const float from = (m == -INFINITY ? 0.f : m) - log2_fast(weight);
+      const float2 scale2 = make_float2(scale, scale), from2 = make_float2(-from, -from);
+      float2 sum = make_float2(0.f, 0.f);
+      uint32_t p[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        x = __ffma2_rn(x, scale2, from2);
+        x.x = exp2_fast(x.x);
+        x.y = exp2_fast(x.y);
+        sum = __fadd2_rn(sum, x);
+        p[i] = pack2<__half>(x.x, x.y);
+      }
+      ptx::tmem_st_32x32b_x32(ts, p);
+      l += (sum.x + sum.y) * __fdividef(1.f, weight);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(p_full(tile));
+    }
+    ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full, 0));
+    if (!ok) {
+      if (lane == 0) report(kStatusWait);
+    } else {
+      ptx::tc_fence_after();
+      const float f = l > 0.f ? unit / l : 0.f;
+      T* dst = static_cast<T*>(a.out) +
+               ((r.row0 + row / a.group) * a.q_heads + kvh * a.group + row % a.group) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld_32x32b_x32(to + c, o);
+        ptx::tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack2<T>(__uint_as_float(o[8 * i + 2 * e]) * f,
+                              __uint_as_float(o[8 * i + 2 * e + 1]) * f);
+            *reinterpret_cast<uint4*>(dst + c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  } else if (warp < kSoftmaxWarps + kWidenWarps) {
+    // ------------------------------------------------- codes to f16 operands
+    const int i0 = (warp - kSoftmaxWarps) * 32 + lane;  // 0 .. 127
+    const int full_blocks = min(n, total / kBlock);
+    // thread 0 keeps the ring of codes filled; the pages of the next 32 blocks
+    // are looked up at once, a lane each
+    int sent = 0, looked = -32;
+    int64_t my_page = -1;
+    auto send = [&](int upto) {
+      for (; sent < upto && sent < full_blocks; ++sent) {
+        if (sent >= looked + 32) {
+          looked = sent;
+          my_page = sent + lane < full_blocks ? page_of(a.c, b, sent + lane) : -1;
+        }
+        const int64_t page = __shfl_sync(0xffffffffu, my_page, sent - looked);
+        const int s = sent % kRaw;
+        if (lane == 0) {
+          if (page >= 0) {
+            ptx::bulk_load(base + L::kRawAt + s * L::kCodes,
+                           static_cast<const uint8_t*>(a.c.pages) +
+                               (page * a.c.kv_heads + kvh) * L::kCodes,
+                           L::kCodes, raw_full(s));
+          } else {
+            report(kStatusPage);
+            ptx::mbar_arrive(raw_full(s));
+          }
+        }
+      }
+    };
+    if (i0 < 32) send(kRaw);
+    int looked2 = -32;
+    float2 my_scales = make_float2(0.f, 0.f);
+    bool my_good = false;
+    bool ok = true;
+    // (after a wait that gave up the warps go on without waiting: the others of
+    // the warpgroup count on them at its barrier)
+    for (int j = 0; j < n; ++j) {
+      const int st = j % kStages;
+      uint8_t* keys = smem + st * L::kStage;
+      uint8_t* vals = keys + L::kKeys;
+      if (j >= kStages && ok) ok = ptx::mbar_wait(empty(st), (j / kStages - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (j < full_blocks) {
+        // scales of the next 32 blocks at once, a lane each
+        if (j >= looked2 + 32) {
+          looked2 = j;
+          const int64_t page = j + lane < full_blocks ? page_of(a.c, b, j + lane) : -1;
+          my_good = page >= 0;
+          my_scales = my_good ? reinterpret_cast<const float2*>(
+                                    a.c.scales)[page * a.c.kv_heads + kvh]
+                              : make_float2(0.f, 0.f);
+        }
+        const float sx = __shfl_sync(0xffffffffu, my_scales.x, j - looked2);
+        const float sy = __shfl_sync(0xffffffffu, my_scales.y, j - looked2);
+        const bool good = __shfl_sync(0xffffffffu, int(my_good), j - looked2);
+        if (i0 == 0) scales[st] = make_float2(sx, sy);
+        const int s = j % kRaw;
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(raw_full(s), (j / kRaw) & 1));
+        const uint8_t* raw = smem + L::kRawAt + s * L::kCodes;
+        constexpr int kUnits = D / 16;  // of 16 codes in a key row
+#pragma unroll
+        for (int k = 0; k < 64 * kUnits / 128; ++k) {
+          const int u = k * 128 + i0, tok = u / kUnits, c = u % kUnits;
+          uint4 lo, hi;
+          uint4 w = *reinterpret_cast<const uint4*>(raw + 16 * u);
+          if (!good) w = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          widen16(w, lo, hi);
+          uint8_t* dst = keys + (c / 4) * 8192;
+          *reinterpret_cast<uint4*>(dst + swizzled(tok, 2 * (c % 4))) = lo;
+          *reinterpret_cast<uint4*>(dst + swizzled(tok, 2 * (c % 4) + 1)) = hi;
+        }
+#pragma unroll
+        for (int k = 0; k < D * 4 / 128; ++k) {
+          const int u = k * 128 + i0, d = u / 4, c = u % 4;
+          uint4 lo, hi;
+          uint4 w = *reinterpret_cast<const uint4*>(raw + 64 * D + 16 * u);
+          if (!good) w = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          widen16(w, lo, hi);
+          *reinterpret_cast<uint4*>(vals + swizzled(d, 2 * c)) = lo;
+          *reinterpret_cast<uint4*>(vals + swizzled(d, 2 * c + 1)) = hi;
+        }
+      } else {
+        // the tail: T as it is (f16), or scaled by a power of two (bf16); what
+        // lies beyond its last token is undefined and becomes zero
+        const T* src = static_cast<const T*>(a.c.tail) +
+                       (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D;
+        const int count = total - j * kBlock;
+        float2 sc = make_float2(1.f, 1.f);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const T* from = src + half * kBlock * D;
+          float down = 1.f;
+          if (std::is_same<T, __nv_bfloat16>::value) {
+            float top = 0.f;
+#pragma unroll 1
+            for (int u = i0; u < kBlock * D; u += 128) {
+              const int tok = half ? u % kBlock : u / D;
+              if (tok < count) top = fmaxf(top, fabsf(Act<T>::to_f32(from[u])));
+            }
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            widen_barrier();
+            if (lane == 0) s_top[warp - kSoftmaxWarps] = top;
+            widen_barrier();
+            top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+            int e = int(__float_as_uint(top) >> 23) - 127 - 14;
+            e = max(-100, min(113, e));
+            down = __uint_as_float(uint32_t(127 - e) << 23);
+            (half ? sc.y : sc.x) = __uint_as_float(uint32_t(127 + e) << 23);
+          }
+#pragma unroll 1
+          for (int u = i0; u < kBlock * D / 8; u += 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(from + 8 * u);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint32_t y[4];
+            const int tok = half ? 8 * u % kBlock : 8 * u / D;  // (values: the first of eight)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v = x[e];
+              if (std::is_same<T, __nv_bfloat16>::value)
+                v = pack2<__half>(low_f32(v) * down, high_f32(v) * down);
+              const int t0 = half ? tok + 2 * e : tok, t1 = half ? t0 + 1 : tok;
+              y[e] = (t0 < count ? v & 0xffffu : 0u) | (t1 < count ? v & 0xffff0000u : 0u);
+            }
+            const int at = half ? swizzled(8 * u / kBlock, 8 * u % kBlock / 8)
+                                : (8 * u % D) / 64 * 8192 + swizzled(tok, 8 * u % 64 / 8);
+            *reinterpret_cast<uint4*>((half ? vals : keys) + at) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        if (i0 == 0) scales[st] = sc;
+      }
+      ptx::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full(st));
+      // the codes are read: the slot takes the next block.  The ring's barrier
+      // orders the four warps' reads before the copy.
+      widen_barrier();
+      if (i0 < 32 && ok) send(j + 1 + kRaw);
+    }
+    if (!ok) {
+      if (lane == 0) report(kStatusWait);
+      if (i0 == 0)  // copies under way land before the CTA goes
+        for (int k = max(0, sent - kRaw); k < sent; ++k)
+          ptx::mbar_wait(raw_full(k % kRaw), (k / kRaw) & 1, 100000000ull);
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t id_s = ptx::idesc_f16(0, kTileRows, kBlock);
+    constexpr uint32_t id_o = ptx::idesc_f16(0, kTileRows, D);
+    bool ok = ptx::mbar_wait(q_full, 0);
+    ptx::tc_fence_after();
+    auto scores = [&](int tile, int st) {
+#pragma unroll
+      for (int p = 0; p < D / 64; ++p) {
+        const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + p * 8192);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_f16_ts(tmem + L::kS + tile * 64,
+                          tmem + L::kQ + tile * (D / 2) + 32 * p + 8 * k, desc + 2 * k, id_s,
+                          p + k > 0);
+      }
+      ptx::mma_commit(s_full(tile));
+    };
+    if (ok) ok = ptx::mbar_wait(full(0), 0);
+    if (ok) {
+      ptx::tc_fence_after();
+      for (int t = 0; t < kTiles; ++t) scores(t, 0);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      const int st = j % kStages;
+      const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + L::kKeys);
+      for (int t = 0; t < kTiles && ok; ++t) {
+        ok = ptx::mbar_wait(p_full(t), j & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_f16_ts(tmem + L::kO + t * D, tmem + L::kS + t * 64 + 8 * k, desc + 2 * k, id_o,
+                          j + k > 0);
+        if (t == kTiles - 1) ptx::mma_commit(empty(st));
+        if (j + 1 < n) {
+          if (t == 0) {
+            ok = ptx::mbar_wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
+          scores(t, (j + 1) % kStages);
+        }
+      }
+    }
+    ptx::mma_commit(o_full);
+    // every product has to be through before tensor memory is given back
+    if (!ptx::mbar_wait(o_full, 0) || !ok) report(kStatusWait);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmaxWarps + kWidenWarps) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <typename T, int D>
 void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
+  if (cudaFuncSetAttribute(tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Layout<D>::kBytes) != cudaSuccess)
+    return;  // (the caller's check of the launch reports it)
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = (a.n_tokens * a.group) / kRows + a.c.slots;  // tiles of all slots
+  const int64_t most = a.n_tokens * a.group / kCtaRows + a.c.slots;  // pairs of tiles of all slots
   cfg.gridDim = dim3(unsigned(most), unsigned(a.c.kv_heads));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
