@@ -324,7 +324,7 @@ class KVCache:
         self.pages, self.scales, self.tail, self.table, self.lens = (pages, scales, tail, table,
                                                                      lens)
         self.kv_heads, self.head_dim, self.dtype = kv_heads, width // KV_BLOCK, tail.dtype
-        self.slots, self.device = slots, pages.device
+        self.slots, self.device, self._index = slots, pages.device, pages.get_device()
         self._struct = _KVCacheStruct(
             pages.data_ptr(), scales.data_ptr(), tail.data_ptr(), table.data_ptr(),
             lens.data_ptr(), n_pages, slots, table.shape[1], kv_heads, self.head_dim,
@@ -353,18 +353,18 @@ class KVCache:
                    table, lens)
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# These calls run between a decoder's linears, some microseconds each, so each
+# looks its arguments over in one expression and goes into what is wrong only
+# where something is.
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _flags(overlap_previous: bool) -> int:
-    return QLIN_OVERLAP_PREVIOUS if overlap_previous else 0
-
-
-def _need_rows(t: torch.Tensor, dim: int, what: str):
-    """On a GPU, rows contiguous (the rows themselves may be strided)."""
-    _need(t.is_cuda and t.dim() == dim, f"{what} must be a {dim}-D CUDA tensor")
-    _need(t.stride(-1) == 1, f"{what}'s rows must be contiguous")
+def _refuse(*checks):
+    """Raises for the first check (ok, what) that does not hold."""
+    for ok, what in checks:
+        if not ok:
+            raise ValueError(what)
+    raise ValueError("tensors do not fit together")
 
 
 def _row_stride(t: torch.Tensor, width: int) -> int:
@@ -372,50 +372,67 @@ def _row_stride(t: torch.Tensor, width: int) -> int:
     return t.stride(0) if t.shape[0] > 1 else width
 
 
-def _need_starts(starts, cache):
-    _need(starts.dtype == torch.int32 and starts.device == cache.device
-          and starts.is_contiguous() and starts.numel() == cache.slots + 1,
-          "starts must be int32 [slots + 1] on the cache's device")
-
-
 def add_rms_norm(x, weight, residual=None, eps: float = 1e-5, out=None, residual_out=None,
                  overlap_previous=False):
     """h = x + residual; out = h * weight / sqrt(mean(h*h) + eps), per row.
 
     x [M, K] and weight [K] in the activation dtype, residual [M, K] in that or
-    float32.  Returns (out, residual_out), residual_out being h rounded to the
-    residual's dtype (None without a residual); residual_out=residual updates
-    it in place."""
-    _need_rows(x, 2, "x")
-    _need(x.dtype in (torch.float16, torch.bfloat16), "x must be float16 or bfloat16")
-    m, k = x.shape
-    _need(weight.is_cuda and weight.is_contiguous() and weight.dtype == x.dtype
-          and tuple(weight.shape) == (k,), "weight must be [K] in x's dtype")
-    rdt = x.dtype
-    if residual is None:
-        _need(residual_out is None, "residual_out without a residual")
-        rs = 0
-    else:
-        _need_rows(residual, 2, "residual")
-        rdt, rs = residual.dtype, _row_stride(residual, k)
-        _need(residual.shape == x.shape and rdt in (x.dtype, torch.float32),
-              "residual must have x's shape, in its dtype or float32")
-        if residual_out is None:
-            residual_out = torch.empty((m, k), dtype=rdt, device=x.device)
+    float32; rows may be strided.  Returns (out, residual_out), residual_out
+    being h rounded to the residual's dtype (None without a residual);
+    residual_out=residual updates it in place."""
+    dt, rdt, shape = x.dtype, x.dtype, x.shape
+    ok = (x.is_cuda and len(shape) == 2 and x.stride(1) == 1
+          and (dt is torch.float16 or dt is torch.bfloat16) and weight.is_cuda
+          and weight.dtype is dt and weight.dim() == 1 and weight.is_contiguous()
+          and weight.shape[0] == shape[1])
+    r_ptr = ro_ptr = None
+    rs = 0
+    if ok and residual is not None:
+        rdt = residual.dtype
+        ok = (residual.is_cuda and residual.shape == shape and residual.stride(1) == 1
+              and (rdt is dt or rdt is torch.float32))
+        if ok:
+            rs, r_ptr = _row_stride(residual, shape[1]), residual.data_ptr()
+            if residual_out is None:
+                residual_out = (torch.empty_like(residual) if residual.is_contiguous()
+                                else torch.empty(shape, dtype=rdt, device=x.device))
+            else:
+                ok = (residual_out.is_cuda and residual_out.is_contiguous()
+                      and residual_out.shape == shape and residual_out.dtype is rdt)
+            ro_ptr = residual_out.data_ptr()
+    elif residual_out is not None:
+        ok = False
+    if ok:
+        if out is None:
+            out = (torch.empty_like(x) if x.is_contiguous()
+                   else torch.empty(shape, dtype=dt, device=x.device))
         else:
-            _need(residual_out.is_cuda and residual_out.is_contiguous()
-                  and residual_out.shape == x.shape and residual_out.dtype == rdt,
-                  "residual_out must be contiguous, of the residual's shape and dtype")
-    if out is None:
-        out = torch.empty((m, k), dtype=x.dtype, device=x.device)
-    else:
-        _need(out.is_cuda and out.is_contiguous() and out.shape == x.shape
-              and out.dtype == x.dtype, "out must be contiguous, of x's shape and dtype")
-    _check(lib().qlin_add_rms_norm(
-        x.data_ptr(), _row_stride(x, k), weight.data_ptr(),
-        residual.data_ptr() if residual is not None else None, rs,
-        residual_out.data_ptr() if residual_out is not None else None, out.data_ptr(), m, k, eps,
-        _DTYPE_CODE[x.dtype], _DTYPE_CODE[rdt], _flags(overlap_previous), _raw_stream(x.device)))
+            ok = (out.is_cuda and out.is_contiguous() and out.shape == shape
+                  and out.dtype is dt)
+    if not ok:
+        _refuse((x.is_cuda and x.dim() == 2 and x.stride(1) == 1,
+                 "x must be a 2-D CUDA tensor with contiguous rows"),
+                (dt in (torch.float16, torch.bfloat16), "x must be float16 or bfloat16"),
+                (weight.is_cuda and weight.is_contiguous() and weight.dtype == dt
+                 and tuple(weight.shape) == tuple(shape[1:]), "weight must be [K] in x's dtype"),
+                (residual is not None or residual_out is None,
+                 "residual_out without a residual"),
+                (residual is None or (residual.is_cuda and residual.shape == shape
+                                      and residual.stride(1) == 1
+                                      and residual.dtype in (dt, torch.float32)),
+                 "residual must have x's shape and contiguous rows, in its dtype or float32"),
+                (residual_out is None or (residual_out.is_cuda and residual_out.is_contiguous()
+                                          and residual_out.shape == shape
+                                          and residual_out.dtype == rdt),
+                 "residual_out must be contiguous, of the residual's shape and dtype"),
+                (False, "out must be contiguous, of x's shape and dtype"))
+    m, k = shape
+    status = lib().qlin_add_rms_norm(
+        x.data_ptr(), _row_stride(x, k), weight.data_ptr(), r_ptr, rs, ro_ptr, out.data_ptr(),
+        m, k, eps, _DTYPE_CODE[dt], _DTYPE_CODE[rdt], 1 if overlap_previous else 0,
+        _current_raw_stream(x.get_device()))
+    if status:
+        _check(status)
     return out, residual_out
 
 
@@ -428,7 +445,7 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, factor: fl
     _need(n_positions >= 0 and rot_dim >= 2, "n_positions and rot_dim must be positive")
     table = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
     _check(lib().qlin_rope_table(table.data_ptr(), n_positions, rot_dim, base, factor,
-                                 short_wavelength, long_wavelength, _raw_stream(table.device)))
+                                 short_wavelength, long_wavelength, _stream(table)))
     return table
 
 
@@ -439,47 +456,70 @@ def rope_append(qkv, table, cache: KVCache, starts, q_heads: int, interleaved: b
     qkv [T, (q_heads + 2*kv_heads)*head_dim] (a fused linear's output; rows may
     be strided), table from rope_table (None: no rotation), starts int32
     [slots+1].  Returns the rotated queries [T, q_heads, head_dim]."""
-    _need_rows(qkv, 2, "qkv")
-    _need(qkv.dtype == cache.dtype and qkv.device == cache.device,
-          "qkv must have the cache's dtype and device")
-    _need_starts(starts, cache)
-    t, d = qkv.shape[0], cache.head_dim
-    _need(qkv.shape[1] == (q_heads + 2 * cache.kv_heads) * d,
-          "qkv must be [T, (q_heads + 2*kv_heads)*head_dim]")
+    dt, d, shape, index = cache.dtype, cache.head_dim, qkv.shape, cache._index
     n_pos = rot = 0
-    if table is not None:
-        _need(table.dtype == torch.float32 and table.dim() == 3 and table.is_contiguous()
-              and table.shape[2] == 2 and table.device == cache.device,
-              "table must be float32 [n_positions, rot_dim/2, 2] on the cache's device")
-        n_pos, rot = table.shape[0], 2 * table.shape[1]
-    if out is None:
-        out = torch.empty((t, q_heads, d), dtype=qkv.dtype, device=qkv.device)
-    else:
-        _need(out.is_contiguous() and out.dtype == qkv.dtype and out.device == qkv.device
-              and tuple(out.shape) == (t, q_heads, d),
-              "out must be contiguous [T, q_heads, head_dim] in qkv's dtype")
-    _check(lib().qlin_rope_append(
-        qkv.data_ptr(), _row_stride(qkv, qkv.shape[1]), out.data_ptr(),
-        table.data_ptr() if rot else None, n_pos, rot, int(interleaved), cache._ref,
-        starts.data_ptr(), t, q_heads, _flags(overlap_previous), _raw_stream(qkv.device)))
+    t_ptr = None
+    ok = (qkv.dtype is dt and qkv.get_device() == index and len(shape) == 2
+          and qkv.stride(1) == 1 and shape[1] == (q_heads + 2 * cache.kv_heads) * d
+          and starts.dtype is torch.int32 and starts.get_device() == index
+          and starts.is_contiguous() and starts.numel() == cache.slots + 1)
+    if ok and table is not None:
+        n_pos, pairs, two = table.shape if table.dim() == 3 else (0, 0, 0)
+        ok = (two == 2 and table.dtype is torch.float32 and table.is_contiguous()
+              and table.get_device() == index)
+        rot = 2 * pairs
+        t_ptr = table.data_ptr() if rot else None
+    if ok:
+        if out is None:
+            out = torch.empty((shape[0], q_heads, d), dtype=dt, device=cache.device)
+        else:
+            ok = (out.is_contiguous() and out.dtype is dt and out.get_device() == index
+                  and tuple(out.shape) == (shape[0], q_heads, d))
+    if not ok:
+        _refuse((qkv.dtype == dt and qkv.device == cache.device,
+                 "qkv must have the cache's dtype and device"),
+                (len(shape) == 2 and qkv.stride(1) == 1
+                 and shape[1] == (q_heads + 2 * cache.kv_heads) * d,
+                 "qkv must be [T, (q_heads + 2*kv_heads)*head_dim] with contiguous rows"),
+                (starts.dtype == torch.int32 and starts.device == cache.device
+                 and starts.is_contiguous() and starts.numel() == cache.slots + 1,
+                 "starts must be int32 [slots + 1] on the cache's device"),
+                (table is None or (table.dim() == 3 and table.shape[2] == 2
+                                   and table.dtype == torch.float32 and table.is_contiguous()
+                                   and table.device == cache.device),
+                 "table must be float32 [n_positions, rot_dim/2, 2] on the cache's device"),
+                (False, "out must be contiguous [T, q_heads, head_dim] in qkv's dtype"))
+    status = lib().qlin_rope_append(
+        qkv.data_ptr(), _row_stride(qkv, shape[1]), out.data_ptr(), t_ptr, n_pos, rot,
+        1 if interleaved else 0, cache._ref, starts.data_ptr(), shape[0], q_heads,
+        1 if overlap_previous else 0, _current_raw_stream(index))
+    if status:
+        _check(status)
     return out
 
 
 def cache_dequant(cache: KVCache, page_ids, out=None):
     """The values that pages of the cache stand for, [n, kv_heads, 2, 64*head_dim]
     in the activation dtype (value blocks transposed, as in the pages)."""
-    _need(page_ids.dtype == torch.int32 and page_ids.device == cache.device
-          and page_ids.is_contiguous() and page_ids.dim() == 1,
-          "page_ids must be int32 [n] on the cache's device")
-    n = page_ids.shape[0]
-    shape = (n,) + tuple(cache.pages.shape[1:])
-    if out is None:
-        out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
-    else:
-        _need(out.is_contiguous() and out.dtype == cache.dtype and out.device == cache.device
-              and tuple(out.shape) == shape, "out must be contiguous, one block for each page")
-    _check(lib().qlin_cache_dequant(cache._ref, page_ids.data_ptr(), n, out.data_ptr(),
-                                    _raw_stream(cache.device)))
+    ok = (page_ids.dtype is torch.int32 and page_ids.get_device() == cache._index
+          and page_ids.is_contiguous() and page_ids.dim() == 1)
+    n = page_ids.numel()
+    if ok:
+        shape = (n, cache.kv_heads, 2, KV_BLOCK * cache.head_dim)
+        if out is None:
+            out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        else:
+            ok = (out.is_contiguous() and out.dtype is cache.dtype
+                  and out.get_device() == cache._index and tuple(out.shape) == shape)
+    if not ok:
+        _refuse((page_ids.dtype == torch.int32 and page_ids.device == cache.device
+                 and page_ids.is_contiguous() and page_ids.dim() == 1,
+                 "page_ids must be int32 [n] on the cache's device"),
+                (False, "out must be contiguous, one block for each page"))
+    status = lib().qlin_cache_dequant(cache._ref, page_ids.data_ptr(), n, out.data_ptr(),
+                                      _current_raw_stream(cache._index))
+    if status:
+        _check(status)
     return out
 
 
@@ -499,26 +539,40 @@ def cache_attention(q, cache: KVCache, starts, max_new: int, workspace, scale=No
     for rope_append, max_new: the most new tokens of any slot; workspace from
     attention_workspace; scale: 1/sqrt(head_dim) by default.  Returns
     [T, q_heads, head_dim]; rows that no slot owns are left unwritten."""
-    _need_rows(q, 3, "q")
-    t, heads, d = q.shape
-    _need(q.dtype == cache.dtype and q.device == cache.device and d == cache.head_dim,
-          "q must have the cache's dtype, device and head dimension")
-    _need(q.stride(1) == d or heads == 1, "q's heads must be contiguous in a row")
-    _need_starts(starts, cache)
-    _need(workspace.device == cache.device and workspace.is_contiguous(),
-          "workspace must be on the cache's device")
-    if out is None:
-        out = torch.empty((t, heads, d), dtype=q.dtype, device=q.device)
-    else:
-        _need(out.is_contiguous() and out.dtype == q.dtype and out.device == q.device
-              and out.shape == q.shape, "out must be contiguous, of q's shape and dtype")
-    if scale is None:
-        scale = d ** -0.5
-    _check(lib().qlin_cache_attention(
-        q.data_ptr(), _row_stride(q, heads * d), out.data_ptr(), cache._ref,
-        starts.data_ptr(), t, heads, scale, max_new, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _flags(overlap_previous),
-        _raw_stream(q.device)))
+    shape, dt, index = q.shape, cache.dtype, cache._index
+    ok = (len(shape) == 3 and q.dtype is dt and q.get_device() == index
+          and shape[2] == cache.head_dim and q.stride(2) == 1
+          and (q.stride(1) == shape[2] or shape[1] == 1)
+          and starts.dtype is torch.int32 and starts.get_device() == index
+          and starts.is_contiguous() and starts.numel() == cache.slots + 1
+          and workspace.get_device() == index and workspace.is_contiguous())
+    if ok:
+        if out is None:
+            out = (torch.empty_like(q) if q.is_contiguous()
+                   else torch.empty(shape, dtype=dt, device=q.device))
+        else:
+            ok = (out.is_contiguous() and out.dtype is dt and out.get_device() == index
+                  and out.shape == shape)
+    if not ok:
+        _refuse((q.dim() == 3 and q.dtype == dt and q.device == cache.device
+                 and shape[-1] == cache.head_dim,
+                 "q must be [T, q_heads, head_dim] with the cache's dtype, device and head "
+                 "dimension"),
+                (q.stride(-1) == 1 and (q.stride(-2) == shape[-1] or shape[-2] == 1),
+                 "q's heads must be contiguous in a row"),
+                (starts.dtype == torch.int32 and starts.device == cache.device
+                 and starts.is_contiguous() and starts.numel() == cache.slots + 1,
+                 "starts must be int32 [slots + 1] on the cache's device"),
+                (workspace.device == cache.device and workspace.is_contiguous(),
+                 "workspace must be contiguous on the cache's device"),
+                (False, "out must be contiguous, of q's shape and dtype"))
+    t, heads, d = shape
+    status = lib().qlin_cache_attention(
+        q.data_ptr(), _row_stride(q, heads * d), out.data_ptr(), cache._ref, starts.data_ptr(), t,
+        heads, d ** -0.5 if scale is None else scale, max_new, workspace.data_ptr(),
+        workspace.nbytes, 1 if overlap_previous else 0, _current_raw_stream(index))
+    if status:
+        _check(status)
     return out
 
 
@@ -531,28 +585,42 @@ def sample(logits, u, temperature, top_k, top_p, min_p, tokens=None, probs=None,
     <= 0 switch top_k, top_p and min_p off, temperature <= 0 takes the largest
     logit.  Returns (tokens int32 [M], probs float32 [M]): the share of the
     token among what the filters kept (-1 and 0 for a row without a token)."""
-    _need_rows(logits, 2, "logits")
-    _need(logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16")
-    m, v = logits.shape
-    for t, dt, what in ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
-                        (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
-                        (min_p, torch.float32, "min_p")):
-        if not (t.dtype == dt and t.device == logits.device and t.is_contiguous()
-                and t.numel() == m):
-            raise ValueError(f"{what} must be {dt} [M] on the logits' device")
-    if tokens is None:
-        tokens = torch.empty(m, dtype=torch.int32, device=logits.device)
-    if probs is None:
-        probs = torch.empty(m, dtype=torch.float32, device=logits.device)
-    _need(tokens.dtype == torch.int32 and tokens.is_contiguous() and tokens.numel() == m
-          and probs.dtype == torch.float32 and probs.is_contiguous() and probs.numel() == m
-          and tokens.device == probs.device == logits.device,
-          "tokens must be int32 [M] and probs float32 [M] on the logits' device")
-    _check(lib().qlin_sample(
-        logits.data_ptr(), _row_stride(logits, v), u.data_ptr(), temperature.data_ptr(),
+    shape, index = logits.shape, logits.get_device()
+    m = shape[0] if len(shape) == 2 else -1
+
+    def row_values(t, dt):
+        return (t.dtype is dt and t.get_device() == index and t.is_contiguous()
+                and t.numel() == m)
+
+    f32, i32 = torch.float32, torch.int32
+    ok = (logits.is_cuda and m >= 0 and logits.stride(1) == 1 and logits.dtype in _DTYPE_CODE
+          and row_values(u, f32) and row_values(temperature, f32) and row_values(top_k, i32)
+          and row_values(top_p, f32) and row_values(min_p, f32))
+    if ok:
+        if tokens is None:
+            tokens = torch.empty_like(top_k)
+        else:
+            ok = row_values(tokens, i32)
+        if probs is None:
+            probs = torch.empty_like(u)
+        else:
+            ok = ok and row_values(probs, f32)
+    if not ok:
+        _refuse((logits.is_cuda and m >= 0 and logits.stride(-1) == 1,
+                 "logits must be a 2-D CUDA tensor with contiguous rows"),
+                (logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16"),
+                *((row_values(t, dt), f"{what} must be {dt} [M] on the logits' device")
+                  for t, dt, what in ((u, f32, "u"), (temperature, f32, "temperature"),
+                                      (top_k, i32, "top_k"), (top_p, f32, "top_p"),
+                                      (min_p, f32, "min_p"))),
+                (False, "tokens must be int32 [M] and probs float32 [M] on the logits' device"))
+    status = lib().qlin_sample(
+        logits.data_ptr(), _row_stride(logits, shape[1]), u.data_ptr(), temperature.data_ptr(),
         top_k.data_ptr(), top_p.data_ptr(), min_p.data_ptr(), tokens.data_ptr(),
-        probs.data_ptr(), m, v, _DTYPE_CODE[logits.dtype], _flags(overlap_previous),
-        _raw_stream(logits.device)))
+        probs.data_ptr(), m, shape[1], _DTYPE_CODE[logits.dtype], 1 if overlap_previous else 0,
+        _current_raw_stream(index))
+    if status:
+        _check(status)
     return tokens, probs
 
 

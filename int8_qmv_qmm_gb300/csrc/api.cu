@@ -43,6 +43,18 @@ int sm_count() {
   return cached[dev];
 }
 
+bool allow_shared(const void* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;  // (the caller's check of the launch reports it)
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -443,9 +443,9 @@ template <typename T, int D>
 void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   using L = Layout<D>;
   static_assert(L::kListAt + kMaxSlots * int(sizeof(Slot)) <= 227 * 1024, "it fits");
-  if (cudaFuncSetAttribute(split_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           L::bytes(kMaxSlots)) != cudaSuccess)
-    return;  // (the caller's check of the launch reports it)
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_shared(reinterpret_cast<const void*>(split_kernel<T, D>), L::bytes(kMaxSlots), &done))
+    return;
   const int sms = sm_count(), warps = sms * kWarps;
   Split* splits = static_cast<Split*>(workspace);
   float* parts = reinterpret_cast<float*>(splits + warps);

@@ -500,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
 
 template <typename T, int D>
 void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
-  if (cudaFuncSetAttribute(tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Layout<D>::kBytes) != cudaSuccess)
-    return;  // (the caller's check of the launch reports it)
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_shared(reinterpret_cast<const void*>(tile_kernel<T, D>), Layout<D>::kBytes, &done))
+    return;
   cudaLaunchConfig_t cfg = {};
   const int64_t most = a.n_tokens * a.group / kCtaRows + a.c.slots;  // pairs of tiles of all slots
   cfg.gridDim = dim3(unsigned(most), unsigned(a.c.kv_heads));

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qlin.h"
 
 namespace qlin {
@@ -19,6 +21,10 @@ qlin_status check_launch(const char* what);
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device; a
+// repeated call costs a look at `done` (one per kernel, its bits the devices).
+bool allow_shared(const void* kernel, int bytes, std::atomic<unsigned long long>* done);
 
 // Launchers.  Arguments are already validated by the public entry points.
 qlin_status launch_quantize(const float* w, int64_t N, int64_t K, int bits, qlin_dtype sdtype,
