@@ -432,7 +432,8 @@ struct Warp {
 // status words that they set.
 size_t split_workspace_size(int head_dim);
 void launch_split(const Args& a, void* workspace, unsigned flags, cudaStream_t st);
-void launch_tile(const Args& a, unsigned flags, cudaStream_t st);
+size_t tile_workspace_size(int head_dim);
+void launch_tile(const Args& a, void* workspace, cudaStream_t st);
 cudaError_t split_take_status(unsigned* flags);
 cudaError_t tile_take_status(unsigned* flags);
 

@@ -23,6 +23,11 @@
 //                     come through a ring of bulk copies.
 //   warp 12           issues the products (one thread).
 //
+// Whole tiles leave some SMs idle in the last round.  What is left after the last
+// full round (at most half of the SMs' number) is therefore cut along the cache,
+// one piece for each SM; the pieces' sums go to the workspace, and a second kernel
+// joins them.
+//
 // What bounds it: at D = 128 the products (1024 cycles of the tensor core for a
 // block of both tiles), at D = 64 the exponentials.
 
@@ -44,6 +49,7 @@ constexpr int kWidenWarps = 4;
 constexpr int kThreads = (kSoftmaxWarps + kWidenWarps + 1) * 32;
 constexpr int kStages = 3;  // blocks of f16 operands
 constexpr int kRaw = 4;     // blocks of codes
+constexpr int kMaxCuts = 8;
 constexpr float kSlack = 8.f;        // log2 of how far a row's maximum may lag
 constexpr float kUnitSlack = 64.f;   // how far a value scale may be above the unit
 
@@ -56,8 +62,8 @@ struct Layout {
   static constexpr int kCodes = 2 * 64 * D;           // a block's codes
   static constexpr int kRawAt = kStages * kStage;
   static constexpr int kBarAt = kRawAt + kRaw * kCodes;
-  // barriers: operands full/empty, codes full, S full, P full, q full, O full
-  static constexpr int kBars = 2 * kStages + kRaw + 2 * kTiles + 2;
+  // barriers: operands full/empty, codes full, S full, halves of P full, q, O
+  static constexpr int kBars = 2 * kStages + kRaw + 3 * kTiles + 2;
   static constexpr int kScaleAt = kBarAt + kBars * 8;  // float2 of each stage
   static constexpr int kMiscAt = kScaleAt + kStages * 8;
   static constexpr int kBytes = kMiscAt + 64 + 1024;   // + alignment to 1024
@@ -72,6 +78,54 @@ __device__ __forceinline__ void widen_barrier() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
+// The work: pairs of tiles over all slots and key/value heads, the first `whole`
+// as they are, the others in `cuts` pieces.
+struct Plan {
+  int pairs, whole, cuts;
+};
+
+__device__ __forceinline__ int64_t pairs_of(const Args& a, int b) {
+  const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
+  const int64_t rows = int64_t(r.n) * a.group;
+  return rows > kSplitRows && r.n <= a.max_new
+             ? (rows + kCtaRows - 1) / kCtaRows * a.c.kv_heads
+             : 0;
+}
+
+// One warp; the same answer in every lane.
+__device__ __forceinline__ Plan plan_of(const Args& a, int sms) {
+  int64_t n = 0;
+  for (int b = threadIdx.x & 31; b < a.c.slots; b += 32) n += pairs_of(a, b);
+  for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+  Plan p;
+  p.pairs = int(n);
+  const int rest = p.pairs % sms;
+  p.cuts = rest ? min(sms / rest, kMaxCuts) : 1;
+  p.whole = p.cuts > 1 ? p.pairs - rest : p.pairs;
+  return p;
+}
+
+// A pair of tiles: the later ones of a slot, which see more, come first.
+struct Work {
+  SlotRows r;
+  int slot, kvh, row0, n;  // n: blocks that its rows see
+};
+__device__ __forceinline__ Work work_at(const Args& a, int slot, int64_t place) {
+  Work w;
+  w.slot = slot;
+  w.r = slot_rows(a.starts, a.c.lens, slot, a.n_tokens);
+  const int rows = w.r.n * a.group, pairs = (rows + kCtaRows - 1) / kCtaRows;
+  w.kvh = int(place % a.c.kv_heads);
+  w.row0 = (pairs - 1 - int(place / a.c.kv_heads)) * kCtaRows;
+  const int last = w.r.held + (min(w.row0 + kCtaRows, rows) - 1) / a.group;  // position seen
+  w.n = last / kBlock + 1;
+  return w;
+}
+
+// A piece's part in the workspace: sums [rows][D], then the rows' m and l.
+template <int D>
+constexpr int kPartFloats = kCtaRows * (D + 2);
+
 // 16 codes -> 16 f16 values, 32 bytes
 __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
   widen_codes(w.x, lo.x, lo.y);
@@ -84,7 +138,8 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
 __device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const Args a, float* parts, int sms) {
   using L = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
@@ -96,12 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto raw_full = [&](int s) { return bars + 8u * (2 * kStages + s); };
   auto s_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + t); };
-  auto p_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + kTiles + t); };
-  const uint32_t q_full = bars + 8u * (2 * kStages + kRaw + 2 * kTiles), o_full = q_full + 8u;
+  auto p_full = [&](int t, int half) {
+    return bars + 8u * (2 * kStages + kRaw + kTiles + 2 * t + half);
+  };
+  const uint32_t q_full = bars + 8u * (2 * kStages + kRaw + 3 * kTiles), o_full = q_full + 8u;
   float2* scales = reinterpret_cast<float2*>(smem + L::kScaleAt);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscAt);
-  int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 8);  // slot, tile
-  float* s_top = reinterpret_cast<float*>(smem + L::kMiscAt + 16);  // of the four widening warps
+  int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 32);  // slot, place, cuts, cut
+  float* s_top = reinterpret_cast<float*>(smem + L::kMiscAt + 8);  // of the four widening warps
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -111,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
     for (int s = 0; s < kRaw; ++s) ptx::mbar_init(raw_full(s), 1);
     for (int t = 0; t < kTiles; ++t) {
       ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(p_full(t), 4);
+      for (int h = 0; h < 2; ++h) ptx::mbar_init(p_full(t, h), 4);
     }
     ptx::mbar_init(q_full, kSoftmaxWarps);
     ptx::mbar_init(o_full, 1);
@@ -119,20 +176,26 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  // which rows this CTA has: the later ones of a slot, which see more, first
   if (warp == 0) {
-    int b = -1;
-    int64_t at = 0;
-    const bool any = find_slot(a.c.slots, blockIdx.x, &b, &at, [&](int s) -> int64_t {
-      const SlotRows r = slot_rows(a.starts, a.c.lens, s, a.n_tokens);
-      const int64_t rows = int64_t(r.n) * a.group;
-      return rows > kSplitRows && r.n <= a.max_new ? (rows + kCtaRows - 1) / kCtaRows : 0;
-    });
-    if (lane == 0) s_work[0] = any ? b : -1, s_work[1] = int(at);
+    const Plan plan = plan_of(a, sms);
+    const int id = blockIdx.x;
+    const int pair = id < plan.whole ? id : plan.whole + (id - plan.whole) / plan.cuts;
+    int slot = -1;
+    int64_t place = 0;
+    const bool any = pair < plan.pairs && find_slot(a.c.slots, pair, &slot, &place,
+                                                    [&](int b) { return pairs_of(a, b); });
+    if (lane == 0) {
+      s_work[0] = any ? slot : -1;
+      s_work[1] = int(place);
+      s_work[2] = id < plan.whole ? 1 : plan.cuts;
+      s_work[3] = id < plan.whole ? 0 : (id - plan.whole) % plan.cuts;
+    }
   }
   __syncthreads();
-  const int b = s_work[0];
-  if (b < 0) return;
+  if (s_work[0] < 0) return;
+  const Work work = work_at(a, s_work[0], s_work[1]);
+  const int cuts = min(s_work[2], work.n), cut = s_work[3];
+  if (cut >= cuts) return;
   if (warp == kSoftmaxWarps + kWidenWarps) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -142,13 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
-  const int kvh = blockIdx.y, rows = r.n * a.group;
-  const int tiles = (rows + kCtaRows - 1) / kCtaRows;
-  const int row0 = (tiles - 1 - s_work[1]) * kCtaRows;
+  const SlotRows r = work.r;
+  const int b = work.slot, kvh = work.kvh, row0 = work.row0, rows = r.n * a.group;
   const int total = r.held + r.n;
-  const int last = r.held + (min(row0 + kCtaRows, rows) - 1) / a.group;  // position seen
-  const int n = last / kBlock + 1;                                      // blocks
+  // this piece's blocks
+  const int j0 = work.n * cut / cuts, n = work.n * (cut + 1) / cuts - j0;
 
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ a row each
@@ -201,39 +262,43 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
     float m = -INFINITY, l = 0.f, unit = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const int st = j % kStages;
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile), j & 1)) &&
-           __all_sync(0xffffffffu, ptx::mbar_wait(full(st), (j / kStages) & 1));
+      const int st = j % kStages, at_token = (j0 + j) * kBlock;
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(full(st), (j / kStages) & 1));
       if (!ok) break;
-      ptx::tc_fence_after();
+      // what goes by the scales alone, while the scores are computed
       const float2 ks = scales[st];
-      uint32_t v[64];
-      ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
-      ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-      ptx::tmem_wait_ld();
-      if (first < j * kBlock + kBlock - 1) {
-        const int seen = pos - j * kBlock;  // token i is seen where i <= seen
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (i > seen) v[i] = 0xff800000u;  // -infinity
-      }
       // (never zero: a score of -infinity has to stay one)
       const float scale = fmaxf(factor * ks.x, 1e-30f);
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 64; i += 2)
-        top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-      top *= scale;
       // O counts in units of `unit`; a block's values in units of ks.y
       float keep = 1.f;
-      bool turn = false;
       if (ks.y > unit * kUnitSlack || (unit == 0.f && ks.y > 0.f)) {  // the same for every row
         keep = unit > 0.f ? __fdividef(unit, ks.y) : 1.f;
-        turn = unit > 0.f;
         unit = ks.y;
       }
       // (a block of zero values has scale 0; a weight below f16's range is none)
       const float weight = ks.y > 0.f ? fmaxf(__fdividef(ks.y, unit), 0x1p-60f) : 1.f;
+      const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile), j & 1));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      uint32_t v[64];
+      ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
+      ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      ptx::tmem_wait_ld();
+      if (first < at_token + kBlock - 1) {
+        const int seen = pos - at_token;  // token i is seen where i <= seen
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i > seen) v[i] = 0xff800000u;  // -infinity
+      }
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 64; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tops[e] = fmaxf(tops[e],
+                          fmaxf(__uint_as_float(v[i + 2 * e]), __uint_as_float(v[i + 2 * e + 1])));
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
       if (top > m + kSlack || m == -INFINITY) {
         const float next = fmaxf(top, m);
         const float f = m == -INFINITY ? 1.f : exp2_fast(m - next);
@@ -241,53 +306,65 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
         keep *= f;
         m = next;
       }
-      turn = turn || keep != 1.f;
-      if (j > 0 && __any_sync(0xffffffffu, turn)) {
+      if (j > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(to + c, o);
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          ptx::tmem_ld_32x32b_x16(to + c, o);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-          ptx::tmem_st_32x32b_x32(to + c, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+          ptx::tmem_st_32x32b_x16(to + c, o);
         }
-        ptx::tmem_wait_st();
       }
-      const float from = (m == -INFINITY ? 0.f : m) - log2_fast(weight);
+      const float from = (m == -INFINITY ? 0.f : m) - shift;
       const float2 scale2 = make_float2(scale, scale), from2 = make_float2(-from, -from);
       float2 sum = make_float2(0.f, 0.f);
-      uint32_t p[32];
+      // in halves of 32 tokens: the products on the first go on beside the second
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        x = __ffma2_rn(x, scale2, from2);
-        x.x = exp2_fast(x.x);
-        x.y = exp2_fast(x.y);
-        sum = __fadd2_rn(sum, x);
-        p[i] = pack2<__half>(x.x, x.y);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 x = make_float2(__uint_as_float(v[32 * h + 2 * i]),
+                                 __uint_as_float(v[32 * h + 2 * i + 1]));
+          x = __ffma2_rn(x, scale2, from2);
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          sum = __fadd2_rn(sum, x);
+          p[i] = pack2<__half>(x.x, x.y);
+        }
+        ptx::tmem_st_32x32b_x16(ts + 16 * h, p);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full(tile, h));
       }
-      ptx::tmem_st_32x32b_x32(ts, p);
-      l += (sum.x + sum.y) * __fdividef(1.f, weight);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(p_full(tile));
+      l += (sum.x + sum.y) * back;
     }
     ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full, 0));
     if (!ok) {
       if (lane == 0) report(kStatusWait);
     } else {
       ptx::tc_fence_after();
-      const float f = l > 0.f ? unit / l : 0.f;
+      const bool part = cuts > 1;
+      const float f = part ? unit : l > 0.f ? unit / l : 0.f;
       T* dst = static_cast<T*>(a.out) +
                ((r.row0 + row / a.group) * a.q_heads + kvh * a.group + row % a.group) * D;
+      float* sums = parts + size_t(blockIdx.x % sms) * kPartFloats<D>;
+      const int here = tile * kTileRows + quarter * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         ptx::tmem_ld_32x32b_x32(to + c, o);
         ptx::tmem_wait_ld();
-        if (mine) {
+        if (part) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(sums + here * D + c + 4 * i) = make_float4(
+                __uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+        } else if (mine) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
@@ -299,11 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
           }
         }
       }
+      if (part) {
+        sums[kCtaRows * D + here] = m;
+        sums[kCtaRows * (D + 1) + here] = l;
+      }
     }
   } else if (warp < kSoftmaxWarps + kWidenWarps) {
     // ------------------------------------------------- codes to f16 operands
     const int i0 = (warp - kSoftmaxWarps) * 32 + lane;  // 0 .. 127
-    const int full_blocks = min(n, total / kBlock);
+    const int full_blocks = min(n, total / kBlock - j0);  // of the piece's
     // thread 0 keeps the ring of codes filled; the pages of the next 32 blocks
     // are looked up at once, a lane each
     int sent = 0, looked = -32;
@@ -312,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
       for (; sent < upto && sent < full_blocks; ++sent) {
         if (sent >= looked + 32) {
           looked = sent;
-          my_page = sent + lane < full_blocks ? page_of(a.c, b, sent + lane) : -1;
+          my_page = sent + lane < full_blocks ? page_of(a.c, b, j0 + sent + lane) : -1;
         }
         const int64_t page = __shfl_sync(0xffffffffu, my_page, sent - looked);
         const int s = sent % kRaw;
@@ -346,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
         // scales of the next 32 blocks at once, a lane each
         if (j >= looked2 + 32) {
           looked2 = j;
-          const int64_t page = j + lane < full_blocks ? page_of(a.c, b, j + lane) : -1;
+          const int64_t page = j + lane < full_blocks ? page_of(a.c, b, j0 + j + lane) : -1;
           my_good = page >= 0;
           my_scales = my_good ? reinterpret_cast<const float2*>(
                                     a.c.scales)[page * a.c.kv_heads + kvh]
@@ -386,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
         // lies beyond its last token is undefined and becomes zero
         const T* src = static_cast<const T*>(a.c.tail) +
                        (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D;
-        const int count = total - j * kBlock;
+        const int count = total - (j0 + j) * kBlock;
         float2 sc = make_float2(1.f, 1.f);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -471,13 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
       const int st = j % kStages;
       const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + L::kKeys);
       for (int t = 0; t < kTiles && ok; ++t) {
-        ok = ptx::mbar_wait(p_full(t), j & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
+        for (int h = 0; h < 2 && ok; ++h) {
+          ok = ptx::mbar_wait(p_full(t, h), j & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ptx::mma_f16_ts(tmem + L::kO + t * D, tmem + L::kS + t * 64 + 8 * k, desc + 2 * k, id_o,
-                          j + k > 0);
+          for (int k = 2 * h; k < 2 * h + 2; ++k)
+            ptx::mma_f16_ts(tmem + L::kO + t * D, tmem + L::kS + t * 64 + 8 * k, desc + 2 * k,
+                            id_o, j + k > 0);
+        }
+        if (!ok) break;
         if (t == kTiles - 1) ptx::mma_commit(empty(st));
         if (j + 1 < n) {
           if (t == 0) {
@@ -498,33 +582,92 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const Args a) {
   if (warp == kSoftmaxWarps + kWidenWarps) ptx::tmem_dealloc(tmem, 512);
 }
 
+// Joins the pieces, a warp for each row.
 template <typename T, int D>
-void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
+__global__ void __launch_bounds__(256) join_kernel(const Args a, const float* parts, int sms) {
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const Plan plan = plan_of(a, sms);
+  if (plan.cuts == 1) return;
+  for (int64_t i = warp; i < int64_t(plan.pairs - plan.whole) * kCtaRows; i += gridDim.x * 8) {
+    const int at = int(i / kCtaRows), row = int(i % kCtaRows);
+    int slot = 0;
+    int64_t place = 0;
+    if (!find_slot(a.c.slots, plan.whole + at, &slot, &place,
+                   [&](int b) { return pairs_of(a, b); }))
+      return;
+    const Work w = work_at(a, slot, place);
+    if (w.row0 + row >= w.r.n * a.group) continue;
+    const int cuts = min(plan.cuts, w.n);
+    if (cuts == 1) continue;  // (written out)
+    float m[kMaxCuts], top = -INFINITY, sum = 0.f;
+    float o[D / 32] = {};
+    const float* first = parts;
+    auto part = [&](int k) {
+      return first + size_t((plan.whole + at * plan.cuts + k) % sms) * kPartFloats<D>;
+    };
+#pragma unroll
+    for (int k = 0; k < kMaxCuts; ++k) {
+      m[k] = k < cuts ? __ldcg(part(k) + kCtaRows * D + row) : -INFINITY;
+      top = fmaxf(top, m[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxCuts; ++k) {
+      if (k >= cuts || m[k] == -INFINITY) continue;
+      const float f = exp2_fast(m[k] - top);
+      sum += __ldcg(part(k) + kCtaRows * (D + 1) + row) * f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] += __ldcg(part(k) + row * D + 32 * e + lane) * f;
+    }
+    const int rr = w.row0 + row;
+    T* dst = static_cast<T*>(a.out) +
+             ((w.r.row0 + rr / a.group) * a.q_heads + w.kvh * a.group + rr % a.group) * D;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      dst[32 * e + lane] = Act<T>::from_f32_rn(sum > 0.f ? o[e] / sum : 0.f);
+  }
+}
+
+template <typename T, int D>
+void launch_t(const Args& a, void* workspace, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(tile_kernel<T, D>), Layout<D>::kBytes, &done))
     return;
+  const int sms = sm_count();
+  float* parts = static_cast<float*>(workspace);
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = a.n_tokens * a.group / kCtaRows + a.c.slots;  // pairs of tiles of all slots
-  cfg.gridDim = dim3(unsigned(most), unsigned(a.c.kv_heads));
+  // pairs of tiles of all slots, and the pieces of the last round
+  const int64_t most = (a.n_tokens * a.group / kCtaRows + a.c.slots) * a.c.kv_heads + sms;
+  cfg.gridDim = dim3(unsigned(most));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::kBytes;
   cfg.stream = st;
+  cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a);
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(unsigned(2 * sms));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts), sms);
 }
 
 }  // namespace
 
-void launch_tile(const Args& a, unsigned flags, cudaStream_t st) {
+size_t tile_workspace_size(int head_dim) {
+  return head_dim == 64 || head_dim == 128 ? size_t(sm_count()) * kCtaRows * (head_dim + 2) * 4 : 0;
+}
+
+void launch_tile(const Args& a, void* workspace, cudaStream_t st) {
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, flags, st) : launch_t<__half, 128>(a, flags, st);
+    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, st)
+                       : launch_t<__half, 128>(a, workspace, st);
   else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, flags, st)
-                       : launch_t<__nv_bfloat16, 128>(a, flags, st);
+    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, st)
+                       : launch_t<__nv_bfloat16, 128>(a, workspace, st);
 }
 
 cudaError_t tile_take_status(unsigned* flags) {

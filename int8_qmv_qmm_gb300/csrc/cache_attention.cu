@@ -7,12 +7,16 @@
 // The host only knows the largest count (max_new), so with prompts among the
 // slots it launches both, each for its own.
 
+#include <algorithm>
+
 #include "attention_core.cuh"
 
 namespace qlin {
 
 size_t cache_attention_workspace_size(int head_dim) {
-  return attention::split_workspace_size(head_dim);
+  // the two kernels run one after the other: they share it
+  return std::max(attention::split_workspace_size(head_dim),
+                  attention::tile_workspace_size(head_dim));
 }
 
 qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
@@ -31,7 +35,7 @@ qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
                              max_new};
   attention::launch_split(a, workspace, flags, st);
   // (the second launch waits for the first: nothing that it could overlap)
-  if (int64_t(max_new) * a.group > attention::kSplitRows) attention::launch_tile(a, 0, st);
+  if (int64_t(max_new) * a.group > attention::kSplitRows) attention::launch_tile(a, workspace, st);
   return check_launch("qlin_cache_attention");
 }
 
