@@ -21,7 +21,9 @@
 //   warps 8..11       widen the codes of keys and values to f16 in shared memory
 //                     (128-byte swizzle, K-major), a ring of 3 blocks; the codes
 //                     come through a ring of bulk copies.
-//   warp 12           issues the products (one thread).
+//   warps 12, 13      issue the products of a tile each (one thread): one thread
+//                     for both took 49 cycles for each 128 x 64 x 16 product,
+//                     which the tensor core does in 32.
 //
 // Whole tiles leave some SMs idle in the last round.  What is left after the last
 // full round (at most half of the SMs' number) is therefore cut along the cache,
@@ -46,7 +48,7 @@ constexpr int kTiles = 2;
 constexpr int kCtaRows = kTiles * kTileRows;
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kWidenWarps = 4;
-constexpr int kThreads = (kSoftmaxWarps + kWidenWarps + 1) * 32;
+constexpr int kThreads = (kSoftmaxWarps + kWidenWarps + kTiles) * 32;
 constexpr int kStages = 3;  // blocks of f16 operands
 constexpr int kRaw = 4;     // blocks of codes
 constexpr int kMaxCuts = 8;
@@ -63,7 +65,7 @@ struct Layout {
   static constexpr int kRawAt = kStages * kStage;
   static constexpr int kBarAt = kRawAt + kRaw * kCodes;
   // barriers: operands full/empty, codes full, S full, halves of P full, q, O
-  static constexpr int kBars = 2 * kStages + kRaw + 3 * kTiles + 2;
+  static constexpr int kBars = 2 * kStages + kRaw + 5 * kTiles;
   static constexpr int kScaleAt = kBarAt + kBars * 8;  // float2 of each stage
   static constexpr int kMiscAt = kScaleAt + kStages * 8;
   static constexpr int kBytes = kMiscAt + 64 + 1024;   // + alignment to 1024
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int t, int half) {
     return bars + 8u * (2 * kStages + kRaw + kTiles + 2 * t + half);
   };
-  const uint32_t q_full = bars + 8u * (2 * kStages + kRaw + 3 * kTiles), o_full = q_full + 8u;
+  auto q_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + 3 * kTiles + t); };
+  auto o_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + 4 * kTiles + t); };
   float2* scales = reinterpret_cast<float2*>(smem + L::kScaleAt);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscAt);
   int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 32);  // slot, place, cuts, cut
@@ -163,15 +166,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full(s), kWidenWarps);
-      ptx::mbar_init(empty(s), 1);
+      ptx::mbar_init(empty(s), kTiles);
     }
     for (int s = 0; s < kRaw; ++s) ptx::mbar_init(raw_full(s), 1);
     for (int t = 0; t < kTiles; ++t) {
       ptx::mbar_init(s_full(t), 1);
       for (int h = 0; h < 2; ++h) ptx::mbar_init(p_full(t, h), 4);
+      ptx::mbar_init(q_full(t), 4);
+      ptx::mbar_init(o_full(t), 1);
     }
-    ptx::mbar_init(q_full, kSoftmaxWarps);
-    ptx::mbar_init(o_full, 1);
     ptx::fence_mbar_init();
   }
   grid_launch_dependents();
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(q_full);
+      if (lane == 0) ptx::mbar_arrive(q_full(tile));
     }
     const int first = r.held + (row0 + tile * kTileRows) / a.group;  // of the tile: all see up to it
     float m = -INFINITY, l = 0.f, unit = 0.f;
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       l += (sum.x + sum.y) * back;
     }
-    ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full, 0));
+    ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full(tile), 0));
     if (!ok) {
       if (lane == 0) report(kStatusWait);
     } else {
@@ -526,56 +529,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_wait(raw_full(k % kRaw), (k / kRaw) & 1, 100000000ull);
     }
   } else if (lane == 0) {
-    // ------------------------------------------------------------ products
+    // ------------------------------------------------ the products of a tile
     constexpr uint32_t id_s = ptx::idesc_f16(0, kTileRows, kBlock);
     constexpr uint32_t id_o = ptx::idesc_f16(0, kTileRows, D);
-    bool ok = ptx::mbar_wait(q_full, 0);
-    ptx::tc_fence_after();
-    auto scores = [&](int tile, int st) {
+    const int t = warp - kSoftmaxWarps - kWidenWarps;
+    const uint32_t ts = tmem + L::kS + t * 64, tq = tmem + L::kQ + t * (D / 2);
+    const uint32_t to = tmem + L::kO + t * D;
+    auto scores = [&](int st) {
 #pragma unroll
       for (int p = 0; p < D / 64; ++p) {
         const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + p * 8192);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::mma_f16_ts(tmem + L::kS + tile * 64,
-                          tmem + L::kQ + tile * (D / 2) + 32 * p + 8 * k, desc + 2 * k, id_s,
-                          p + k > 0);
+          ptx::mma_f16_ts(ts, tq + 32 * p + 8 * k, desc + 2 * k, id_s, p + k > 0);
       }
-      ptx::mma_commit(s_full(tile));
+      ptx::mma_commit(s_full(t));
     };
-    if (ok) ok = ptx::mbar_wait(full(0), 0);
-    if (ok) {
-      ptx::tc_fence_after();
-      for (int t = 0; t < kTiles; ++t) scores(t, 0);
-    }
+    bool ok = ptx::mbar_wait(q_full(t), 0) && ptx::mbar_wait(full(0), 0);
+    ptx::tc_fence_after();
+    if (ok) scores(0);
     for (int j = 0; j < n && ok; ++j) {
-      const int st = j % kStages;
+      const int st = j % kStages, next = (j + 1) % kStages;
       const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + L::kKeys);
-      for (int t = 0; t < kTiles && ok; ++t) {
-        for (int h = 0; h < 2 && ok; ++h) {
-          ok = ptx::mbar_wait(p_full(t, h), j & 1);
-          if (!ok) break;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int k = 2 * h; k < 2 * h + 2; ++k)
-            ptx::mma_f16_ts(tmem + L::kO + t * D, tmem + L::kS + t * 64 + 8 * k, desc + 2 * k,
-                            id_o, j + k > 0);
-        }
+      for (int h = 0; h < 2 && ok; ++h) {
+        ok = ptx::mbar_wait(p_full(t, h), j & 1);
         if (!ok) break;
-        if (t == kTiles - 1) ptx::mma_commit(empty(st));
-        if (j + 1 < n) {
-          if (t == 0) {
-            ok = ptx::mbar_wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1);
-            if (!ok) break;
-            ptx::tc_fence_after();
-          }
-          scores(t, (j + 1) % kStages);
-        }
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          ptx::mma_f16_ts(to, ts + 16 * h + 8 * k, desc + 4 * h + 2 * k, id_o, j + h + k > 0);
+      }
+      if (!ok) break;
+      ptx::mma_commit(empty(st));
+      if (j + 1 < n) {
+        ok = ptx::mbar_wait(full(next), ((j + 1) / kStages) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        scores(next);
       }
     }
-    ptx::mma_commit(o_full);
+    ptx::mma_commit(o_full(t));
     // every product has to be through before tensor memory is given back
-    if (!ptx::mbar_wait(o_full, 0) || !ok) report(kStatusWait);
+    if (!ptx::mbar_wait(o_full(t), 0) || !ok) report(kStatusWait);
   }
   ptx::tc_fence_before();
   __syncthreads();
