@@ -4,16 +4,18 @@
 // A CTA takes 256 rows (new tokens times the query heads that share a key/value
 // head) of one slot and key/value head, as two tiles of 128, and walks the
 // blocks that they see.  Per block and tile
-//   S [128 x 64] = q [128 x D] . keys^T      (A: q in tensor memory)
+//   S [128 x 64] = q [128 x D] . keys^T      (q in shared memory)
 //   P            = exp2(S * scale - max)     (row by row, in registers)
 //   O [128 x D] += P [128 x 64] . values     (A: P in tensor memory, over S)
 // with S, P and O in tensor memory and both operands of every product in f16:
 // the codes are exact in it (a bf16 tail is scaled by a power of two for the
-// block, bf16 queries by one for each row).  The two tiles alternate: while one
-// is in its exponentials the tensor core works for the other.
+// block, bf16 queries by one for each row).  S has two buffers a tile, so the
+// scores of the next block are there when the exponentials of this one are done
+// (with one, and q in tensor memory beside it, a tile waited for its products
+// two fifths of the time: 375 us for two chunks of 2048 tokens over 6001).
 //
 //   warps 0..3, 4..7  a tile each, a thread for each row: the row's query to
-//                     tensor memory, then per block S from tensor memory,
+//                     shared memory, then per block S from tensor memory,
 //                     maximum, exponentials and sum (no other thread has a part
 //                     of the row), P back; O is rescaled only when the maximum
 //                     has grown by 2^8 (P stays within f16, and the last
@@ -62,18 +64,22 @@ struct Layout {
   static constexpr int kKeys = 64 * D * 2;            // bytes of a block's f16 keys, or values
   static constexpr int kStage = 2 * kKeys;
   static constexpr int kCodes = 2 * 64 * D;           // a block's codes
-  static constexpr int kRawAt = kStages * kStage;
+  static constexpr int kQuery = kTileRows * D * 2;     // a tile's queries
+  static constexpr int kQueryAt = kStages * kStage;
+  static constexpr int kRawAt = kQueryAt + kTiles * kQuery;
   static constexpr int kBarAt = kRawAt + kRaw * kCodes;
-  // barriers: operands full/empty, codes full, S full, halves of P full, q, O
-  static constexpr int kBars = 2 * kStages + kRaw + 5 * kTiles;
+  // barriers: operands full/empty, codes full; of a tile, for both buffers S full
+  // and P's halves full, and q full, P used, O full
+  static constexpr int kPerTile = 9;
+  static constexpr int kBars = 2 * kStages + kRaw + kPerTile * kTiles;
   static constexpr int kScaleAt = kBarAt + kBars * 8;  // float2 of each stage
   static constexpr int kMiscAt = kScaleAt + kStages * 8;
   static constexpr int kBytes = kMiscAt + 64 + 1024;   // + alignment to 1024
   // tensor memory columns
-  static constexpr int kS = 0;                    // 64 a tile (P over the first 32)
-  static constexpr int kQ = kTiles * 64;          // D/2 a tile
-  static constexpr int kO = kQ + kTiles * D / 2;  // D a tile
+  static constexpr int kS = 0;             // two buffers of 64 a tile (P over the first 32)
+  static constexpr int kO = kTiles * 128;  // D a tile
   static_assert(kO + kTiles * D <= 512, "tensor memory");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void widen_barrier() {
@@ -152,12 +158,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto raw_full = [&](int s) { return bars + 8u * (2 * kStages + s); };
-  auto s_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + t); };
-  auto p_full = [&](int t, int half) {
-    return bars + 8u * (2 * kStages + kRaw + kTiles + 2 * t + half);
+  auto of_tile = [&](int t, int i) {
+    return bars + 8u * (2 * kStages + kRaw + L::kPerTile * t + i);
   };
-  auto q_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + 3 * kTiles + t); };
-  auto o_full = [&](int t) { return bars + 8u * (2 * kStages + kRaw + 4 * kTiles + t); };
+  auto s_full = [&](int t, int buf) { return of_tile(t, buf); };
+  auto p_full = [&](int t, int buf, int half) { return of_tile(t, 2 + 2 * buf + half); };
+  auto q_full = [&](int t) { return of_tile(t, 6); };
+  auto p_used = [&](int t) { return of_tile(t, 7); };
+  auto o_full = [&](int t) { return of_tile(t, 8); };
   float2* scales = reinterpret_cast<float2*>(smem + L::kScaleAt);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscAt);
   int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 32);  // slot, place, cuts, cut
@@ -170,9 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kRaw; ++s) ptx::mbar_init(raw_full(s), 1);
     for (int t = 0; t < kTiles; ++t) {
-      ptx::mbar_init(s_full(t), 1);
-      for (int h = 0; h < 2; ++h) ptx::mbar_init(p_full(t, h), 4);
+      for (int i = 0; i < 2; ++i) {
+        ptx::mbar_init(s_full(t, i), 1);
+        for (int h = 0; h < 2; ++h) ptx::mbar_init(p_full(t, i, h), 4);
+      }
       ptx::mbar_init(q_full(t), 4);
+      ptx::mbar_init(p_used(t), 1);
       ptx::mbar_init(o_full(t), 1);
     }
     ptx::fence_mbar_init();
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = row < rows;
     const int pos = mine ? r.held + row / a.group : 0x7fffffff;
     const uint32_t at = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t ts = at + L::kS + tile * 64, to = at + L::kO + tile * D;
+    const uint32_t ts2 = at + L::kS + tile * 128, to = at + L::kO + tile * D;
     float factor = fabsf(a.scale_log2);
     {
       const T* src = static_cast<const T*>(a.q) +
@@ -252,12 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
       }
+      uint8_t* dst = smem + L::kQueryAt + tile * L::kQuery;
+      const int here = quarter * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        ptx::tmem_st_32x32b_x32(at + L::kQ + tile * (D / 2) + 32 * i,
-                                *reinterpret_cast<uint32_t(*)[32]>(w + 32 * i));
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<uint4*>(dst + i / 8 * (kTileRows * 128) + swizzled(here, i % 8)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      ptx::fence_async_shared();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(q_full(tile));
     }
@@ -281,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a block of zero values has scale 0; a weight below f16's range is none)
       const float weight = ks.y > 0.f ? fmaxf(__fdividef(ks.y, unit), 0x1p-60f) : 1.f;
       const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile), j & 1));
+      const int buf = j & 1;
+      const uint32_t ts = ts2 + 64 * buf;
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile, buf), (j >> 1) & 1));
       if (!ok) break;
       ptx::tc_fence_after();
       uint32_t v[64];
@@ -310,6 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = next;
       }
       if (j > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(p_used(tile), (j - 1) & 1));
+        if (!ok) break;
+        ptx::tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16];
@@ -341,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(p_full(tile, h));
+        if (lane == 0) ptx::mbar_arrive(p_full(tile, buf, h));
       }
       l += (sum.x + sum.y) * back;
     }
@@ -533,26 +550,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_s = ptx::idesc_f16(0, kTileRows, kBlock);
     constexpr uint32_t id_o = ptx::idesc_f16(0, kTileRows, D);
     const int t = warp - kSoftmaxWarps - kWidenWarps;
-    const uint32_t ts = tmem + L::kS + t * 64, tq = tmem + L::kQ + t * (D / 2);
-    const uint32_t to = tmem + L::kO + t * D;
-    auto scores = [&](int st) {
+    const uint32_t ts2 = tmem + L::kS + t * 128, to = tmem + L::kO + t * D;
+    const uint64_t q_desc = ptx::sw128_kmajor_desc(base + L::kQueryAt + t * L::kQuery);
+    // the scores of block j, into its buffer
+    auto scores = [&](int j) {
+      const uint64_t k_desc = ptx::sw128_kmajor_desc(base + j % kStages * L::kStage);
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) {
-        const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + p * 8192);
+      for (int p = 0; p < D / 64; ++p)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::mma_f16_ts(ts, tq + 32 * p + 8 * k, desc + 2 * k, id_s, p + k > 0);
-      }
-      ptx::mma_commit(s_full(t));
+          ptx::mma_f16_ss(ts2 + 64 * (j & 1), q_desc + (p * (kTileRows * 128) >> 4) + 2 * k,
+                          k_desc + (p * 8192 >> 4) + 2 * k, id_s, p + k > 0);
+      ptx::mma_commit(s_full(t, j & 1));
     };
-    bool ok = ptx::mbar_wait(q_full(t), 0) && ptx::mbar_wait(full(0), 0);
-    ptx::tc_fence_after();
-    if (ok) scores(0);
+    bool ok = ptx::mbar_wait(q_full(t), 0);
+    for (int j = 0; j < 2 && j < n && ok; ++j) {
+      ok = ptx::mbar_wait(full(j), 0);
+      ptx::tc_fence_after();
+      if (ok) scores(j);
+    }
     for (int j = 0; j < n && ok; ++j) {
-      const int st = j % kStages, next = (j + 1) % kStages;
+      const int st = j % kStages;
+      const uint32_t ts = ts2 + 64 * (j & 1);
       const uint64_t desc = ptx::sw128_kmajor_desc(base + st * L::kStage + L::kKeys);
       for (int h = 0; h < 2 && ok; ++h) {
-        ok = ptx::mbar_wait(p_full(t, h), j & 1);
+        ok = ptx::mbar_wait(p_full(t, j & 1, h), (j >> 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -561,11 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ptx::mma_commit(empty(st));
-      if (j + 1 < n) {
-        ok = ptx::mbar_wait(full(next), ((j + 1) / kStages) & 1);
+      ptx::mma_commit(p_used(t));
+      if (j + 2 < n) {  // (its buffer is free: products run in the order of their issue)
+        ok = ptx::mbar_wait(full((j + 2) % kStages), ((j + 2) / kStages) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
-        scores(next);
+        scores(j + 2);
       }
     }
     ptx::mma_commit(o_full(t));
