@@ -18,6 +18,7 @@
 // latency a decode step.  Angles come from a table made in 64 bits: at
 // position 100000 a float32 angle would be off by up to 4e-3 radians.
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -29,23 +30,39 @@ __device__ unsigned int g_rope_status = 0;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: one for each 16 elements of a block's keys.  (256 at both head
+// dimensions left a thread at 128 with twice the registers, and an SM with half the
+// loads in flight: 59 us for 4 prompts of 2048.)
+template <int D>
+constexpr int kThreads = kBlock * (D / 16);
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_rope_status, bit); }
 
-template <typename T>
-struct alignas(16) Vec8 {
-  T v[8];
+// Eight elements as four pairs, the first of a pair in the low half.
+struct Vec8 {
+  uint32_t w[4];
 };
-
 template <typename T>
-__device__ __forceinline__ Vec8<T> load8(const T* p) {
-  return *reinterpret_cast<const Vec8<T>*>(p);
+__device__ __forceinline__ Vec8 load8(const T* p) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  return Vec8{{v.x, v.y, v.z, v.w}};
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const Vec8<T>& v) {
-  *reinterpret_cast<Vec8<T>*>(p) = v;
+__device__ __forceinline__ void store8(T* p, const Vec8& v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  using T2 = typename Act<T>::T2;
+  const T2 v = *reinterpret_cast<const T2*>(&w);
+  return make_float2(Act<T>::to_f32(v.x), Act<T>::to_f32(v.y));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float2 v) {
+  typename Act<T>::T2 r;
+  r.x = Act<T>::from_f32_rn(v.x);
+  r.y = Act<T>::from_f32_rn(v.y);
+  return *reinterpret_cast<uint32_t*>(&r);
 }
 
 // A unit is 16 elements of a head, as two runs of 8 that pair up: units below
@@ -69,33 +86,38 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = nb;
 }
 
-// cs: the position's row of the table.
+// A unit's 8 cosines and sines, from the position's row of the table.
+struct Angles {
+  float4 v[4];
+};
+__device__ __forceinline__ Angles angles_of(const float* row, int u, int rot) {
+  Angles t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    t.v[i] = 16 * u < rot ? reinterpret_cast<const float4*>(row + 16 * u)[i]
+                          : make_float4(1.f, 0.f, 1.f, 0.f);
+  return t;
+}
+
 template <typename T>
-__device__ __forceinline__ void rotate_unit(Vec8<T>& x, Vec8<T>& y, int u, int rot,
-                                            bool interleaved, const float* cs) {
+__device__ __forceinline__ void rotate_unit(Vec8& x, Vec8& y, int u, int rot, bool interleaved,
+                                            const Angles& angles) {
   if (16 * u >= rot) return;
-  float t[16];
-  const float4* p = reinterpret_cast<const float4*>(cs + 16 * u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 v = p[i];
-    t[4 * i] = v.x, t[4 * i + 1] = v.y, t[4 * i + 2] = v.z, t[4 * i + 3] = v.w;
-  }
-  float a[8], b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = Act<T>::to_f32(x.v[i]), b[i] = Act<T>::to_f32(y.v[i]);
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      turn(a[2 * i], a[2 * i + 1], t[2 * i], t[2 * i + 1]);
-      turn(b[2 * i], b[2 * i + 1], t[8 + 2 * i], t[8 + 2 * i + 1]);
+    float2 a = unpack<T>(x.w[i]), b = unpack<T>(y.w[i]);
+    if (interleaved) {
+      const float4 t = angles.v[i / 2], z = angles.v[2 + i / 2];
+      turn(a.x, a.y, i % 2 ? t.z : t.x, i % 2 ? t.w : t.y);
+      turn(b.x, b.y, i % 2 ? z.z : z.x, i % 2 ? z.w : z.y);
+    } else {
+      const float4 t = angles.v[i];
+      turn(a.x, b.x, t.x, t.y);
+      turn(a.y, b.y, t.z, t.w);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(a[i], b[i], t[2 * i], t[2 * i + 1]);
+    x.w[i] = pack<T>(a);
+    y.w[i] = pack<T>(b);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x.v[i] = Act<T>::from_f32_rn(a[i]), y.v[i] = Act<T>::from_f32_rn(b[i]);
 }
 
 // The code of v in a block of this scale.
@@ -104,13 +126,48 @@ __device__ __forceinline__ unsigned code_of(float v, float scale) {
   return unsigned(fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f) + 128.f);
 }
 
+template <typename T>
+__device__ __forceinline__ uint2 codes_of(const Vec8& v, float scale) {
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = unpack<T>(v.w[2 * i]), b = unpack<T>(v.w[2 * i + 1]);
+    r[i] = code_of(a.x, scale) | code_of(a.y, scale) << 8 | code_of(b.x, scale) << 16 |
+           code_of(b.y, scale) << 24;
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+template <typename T>
+__device__ __forceinline__ float largest(const Vec8& v) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack<T>(v.w[i]);
+    top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+  }
+  return top;
+}
+
+// 16 elements to a column.
+template <typename T>
+__device__ __forceinline__ void column_to(T* to, int stride, const Vec8& a, const Vec8& b) {
+  uint16_t* p = reinterpret_cast<uint16_t*>(to);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint32_t w = (e < 8 ? a : b).w[e % 8 / 2];
+    p[e * stride] = uint16_t(e % 2 ? w >> 16 : w);
+  }
+}
+
+template <int WARPS>
 __device__ __forceinline__ float block_max(float v, float* partial) {
   for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
   __syncthreads();
   if ((threadIdx.x & 31) == 0) partial[threadIdx.x >> 5] = v;
   __syncthreads();
   v = partial[0];
-  for (int i = 1; i < kWarps; ++i) v = fmaxf(v, partial[i]);
+  for (int i = 1; i < WARPS; ++i) v = fmaxf(v, partial[i]);
   return v;
 }
 
@@ -126,6 +183,7 @@ struct Args {
   int64_t n_tokens;
   int q_heads;
   int64_t block_items;  // room for completed blocks, over all slots
+  int parts;            // warps that share a token
 };
 
 // Whether all of a slot's rows can be taken: its blocks fit and its positions
@@ -135,36 +193,14 @@ __device__ __forceinline__ bool slot_fits(const Args& a, const SlotRows& r) {
   return !r.bad && total / kBlock <= a.c.max_blocks && (a.rot == 0 || total <= a.n_positions);
 }
 
-// One new token's keys and values to the tail.
+// A share of one new token's heads: the queries, and keys and values to the tail
+// where that is this warp's to write.  A lane's units differ by the head alone, so
+// it looks its angles up once.
 template <typename T, int D>
-__device__ void token_to_tail(const Args& a, const T* row, int b, int pos, int unit0, int step) {
-  const float* cs = a.table + int64_t(pos) * a.rot;
-  const int at = pos % kBlock;
-  for (int i = unit0; i < a.c.kv_heads * (D / 16); i += step) {
-    const int h = i / (D / 16), u = i % (D / 16);
-    T* tail = static_cast<T*>(a.c.tail) + (int64_t(b) * a.c.kv_heads + h) * 2 * kBlock * D;
-    const T* k = row + (a.q_heads + h) * D;
-    const T* v = row + (a.q_heads + a.c.kv_heads + h) * D;
-    const Unit un = unit_of(u, a.rot, a.interleaved);
-    Vec8<T> x = load8(k + un.at0), y = load8(k + un.at1);
-    const Vec8<T> v0 = load8(v + 16 * u), v1 = load8(v + 16 * u + 8);
-    rotate_unit(x, y, u, a.rot, a.interleaved, cs);
-    store8(tail + at * D + un.at0, x);
-    store8(tail + at * D + un.at1, y);
-    T* vt = tail + kBlock * D;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      vt[(16 * u + e) * kBlock + at] = v0.v[e];
-      vt[(16 * u + 8 + e) * kBlock + at] = v1.v[e];
-    }
-  }
-}
-
-template <typename T, int D>
-__device__ void token_warp(const Args& a, int64_t t) {
+__device__ void token_warp(const Args& a, int64_t t, int part) {
+  constexpr int kUnits = D / 16, kHeads = 32 / kUnits;  // of a head; heads at a time
   const int lane = threadIdx.x & 31;
-  // the token's slot: the last one that starts at or before it
-  int b = -1;
+  int b = -1;  // the token's slot
   for (int s0 = 0; s0 < a.c.slots; s0 += 32) {
     const int s = s0 + lane;
     const bool mine = s < a.c.slots && a.starts[s] <= t && t < a.starts[s + 1];
@@ -183,30 +219,59 @@ __device__ void token_warp(const Args& a, int64_t t) {
                                                                        : kStatusPosition);
     return;
   }
-  const int pos = r.held + int(t - r.row0);
+  const int pos = r.held + int(t - r.row0), u = lane % kUnits;
   const T* row = static_cast<const T*>(a.qkv) + t * a.qkv_stride;
+  const Angles angles = angles_of(a.table + int64_t(pos) * a.rot, u, a.rot);
+  const Unit un = unit_of(u, a.rot, a.interleaved);
   T* out = static_cast<T*>(a.q_out) + t * a.q_heads * D;
-  const float* cs = a.table + int64_t(pos) * a.rot;
-  for (int i = lane; i < a.q_heads * (D / 16); i += 32) {
-    const int h = i / (D / 16), u = i % (D / 16);
-    const Unit un = unit_of(u, a.rot, a.interleaved);
-    Vec8<T> x = load8(row + h * D + un.at0), y = load8(row + h * D + un.at1);
-    rotate_unit(x, y, u, a.rot, a.interleaved, cs);
-    store8(out + h * D + un.at0, x);
-    store8(out + h * D + un.at1, y);
+  const int q1 = a.q_heads * (part + 1) / a.parts;
+  // two heads' loads before the first store (which could be to the same memory,
+  // for all that the compiler knows)
+  for (int h = a.q_heads * part / a.parts + lane / kUnits; h < q1; h += 2 * kHeads) {
+    const bool two = h + kHeads < q1;
+    const T* from = row + h * D;
+    T* to = out + h * D;
+    Vec8 x0 = load8(from + un.at0), y0 = load8(from + un.at1), x1 = x0, y1 = y0;
+    if (two) {
+      x1 = load8(from + kHeads * D + un.at0);
+      y1 = load8(from + kHeads * D + un.at1);
+    }
+    rotate_unit<T>(x0, y0, u, a.rot, a.interleaved, angles);
+    store8(to + un.at0, x0);
+    store8(to + un.at1, y0);
+    if (two) {
+      rotate_unit<T>(x1, y1, u, a.rot, a.interleaved, angles);
+      store8(to + kHeads * D + un.at0, x1);
+      store8(to + kHeads * D + un.at1, y1);
+    }
   }
   const int total = r.held + r.n;
   const bool stays = pos / kBlock == total / kBlock;
   const bool left_to_block = total / kBlock > r.held / kBlock && r.held % kBlock;
-  if (stays && !left_to_block) token_to_tail<T, D>(a, row, b, pos, lane, 32);
+  if (!stays || left_to_block) return;
+  const int at = pos % kBlock, k1 = a.c.kv_heads * (part + 1) / a.parts;
+  for (int h = a.c.kv_heads * part / a.parts + lane / kUnits; h < k1; h += kHeads) {
+    T* tail = static_cast<T*>(a.c.tail) + (int64_t(b) * a.c.kv_heads + h) * 2 * kBlock * D;
+    const T* k = row + (a.q_heads + h) * D;
+    const T* v = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
+    Vec8 x = load8(k + un.at0), y = load8(k + un.at1);
+    const Vec8 v0 = load8(v), v1 = load8(v + 8);
+    rotate_unit<T>(x, y, u, a.rot, a.interleaved, angles);
+    store8(tail + at * D + un.at0, x);
+    store8(tail + at * D + un.at1, y);
+    column_to(tail + kBlock * D + 16 * u * kBlock + at, kBlock, v0, v1);
+  }
 }
 
 template <typename T, int D>
 __device__ void block_cta(const Args& a, int64_t item, int h) {
+  constexpr int kWarps = kThreads<D> / 32;
   constexpr int kStride = kBlock + 2;  // of a staged value row: spreads the banks
-  __shared__ T staged[D * kStride];
+  __shared__ alignas(16) T staged[D * kStride];
   __shared__ float partial[kWarps];
   __shared__ int s_slot, s_place;
+  __shared__ int64_t s_page;
+  __shared__ SlotRows s_rows;
   if (threadIdx.x < 32) {
     int b = -1;
     int64_t place = 0;
@@ -214,71 +279,66 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
       const SlotRows r = slot_rows(a.starts, a.c.lens, s, a.n_tokens);
       return slot_fits(a, r) ? (int64_t(r.held) + r.n) / kBlock - r.held / kBlock : 0;
     });
-    if (threadIdx.x == 0) s_slot = any ? b : -1, s_place = int(place);
+    if (threadIdx.x == 0) {
+      s_slot = any ? b : -1;
+      if (any) {
+        s_rows = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
+        s_place = int(place);
+        s_page = page_of(a.c, b, s_rows.held / kBlock + int(place));
+      }
+    }
   }
   __syncthreads();
   const int b = s_slot;
   if (b < 0) return;
-  const SlotRows r = slot_rows(a.starts, a.c.lens, b, a.n_tokens);
+  const SlotRows r = s_rows;
   const int j = r.held / kBlock + s_place;
   const int old = j == r.held / kBlock ? r.held % kBlock : 0;  // tokens that the tail holds
-  const int64_t page = page_of(a.c, b, j);
+  const int64_t page = s_page;
   if (page < 0 && threadIdx.x == 0) report(kStatusPage);
   T* tail = static_cast<T*>(a.c.tail) + (int64_t(b) * a.c.kv_heads + h) * 2 * kBlock * D;
   // rows of the block's new tokens: token i of the block is row first + i
   const int64_t first = r.row0 + int64_t(j) * kBlock - r.held;
   const T* qkv = static_cast<const T*>(a.qkv);
 
-  // keys: each thread holds kUnits units of 16 elements
-  constexpr int kUnits = kBlock * (D / 16) / kThreads;
-  static_assert(kUnits * kThreads == kBlock * (D / 16), "units divide evenly");
-  Vec8<T> kx[kUnits], ky[kUnits];
-  float top = 0.f;
+  // keys: a unit a thread
+  const int tok = threadIdx.x / (D / 16), u = threadIdx.x % (D / 16);
+  const Unit un = unit_of(u, a.rot, a.interleaved);
+  const T* k = tok < old ? tail + tok * D
+                         : qkv + (first + tok) * a.qkv_stride + (a.q_heads + h) * D;
+  // all loads first: new values (transposed on their way through shared memory: a
+  // warp's lanes are tokens, so that its stores run along a row), and the tail's,
+  // which stand transposed already: dimension d, tokens t0 ..
+  const int wi = threadIdx.x >> 5, vu = wi % (D / 16);
+  const int vtok = wi / (D / 16) * 32 + (threadIdx.x & 31);
+  const int d = threadIdx.x / 4, t0 = (threadIdx.x % 4) * 16;
+  Vec8 kx = load8(k + un.at0), ky = load8(k + un.at1), nv[2], vv[2];
+  const Angles angles =
+      angles_of(a.table + (int64_t(j) * kBlock + tok) * a.rot, u, tok < old ? 0 : a.rot);
 #pragma unroll
-  for (int n = 0; n < kUnits; ++n) {
-    const int i = n * kThreads + threadIdx.x, tok = i / (D / 16), u = i % (D / 16);
-    const Unit un = unit_of(u, a.rot, a.interleaved);
-    if (tok < old) {
-      kx[n] = load8(tail + tok * D + un.at0);
-      ky[n] = load8(tail + tok * D + un.at1);
-    } else {
-      const T* k = qkv + (first + tok) * a.qkv_stride + (a.q_heads + h) * D;
-      kx[n] = load8(k + un.at0);
-      ky[n] = load8(k + un.at1);
-      rotate_unit(kx[n], ky[n], u, a.rot, a.interleaved,
-                  a.table + (int64_t(j) * kBlock + tok) * a.rot);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      top = fmaxf(top, fmaxf(fabsf(Act<T>::to_f32(kx[n].v[e])), fabsf(Act<T>::to_f32(ky[n].v[e]))));
-    // values, transposed on the way
-    T v[16];
-    if (tok < old) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = tail[kBlock * D + (16 * u + e) * kBlock + tok];
-    } else {
-      const T* p = qkv + (first + tok) * a.qkv_stride + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
-      const Vec8<T> v0 = load8(p), v1 = load8(p + 8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v0.v[e], v[8 + e] = v1.v[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) staged[(16 * u + e) * kStride + tok] = v[e];
+  for (int p = 0; p < 2; ++p) {
+    if (vtok >= old)
+      nv[p] = load8(qkv + (first + vtok) * a.qkv_stride + (a.q_heads + a.c.kv_heads + h) * D +
+                    16 * vu + 8 * p);
+    if (t0 + 8 * p < old) vv[p] = load8(tail + kBlock * D + d * kBlock + t0 + 8 * p);
   }
-  const float k_scale = __fdiv_rn(block_max(top, partial), 127.f);  // (orders `staged` too)
-
-  T vv[kUnits][16];
-  top = 0.f;
+  if (vtok >= old) column_to(staged + 16 * vu * kStride + vtok, kStride, nv[0], nv[1]);
+  if (tok >= old) rotate_unit<T>(kx, ky, u, a.rot, a.interleaved, angles);
+  float top = fmaxf(largest<T>(kx), largest<T>(ky));
+  // (the barriers of block_max order `staged` too)
+  const float k_scale = __fdiv_rn(block_max<kWarps>(top, partial), 127.f);
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(staged + d * kStride + t0);
 #pragma unroll
-  for (int n = 0; n < kUnits; ++n) {
-    const int i = n * kThreads + threadIdx.x, d = i / 4, t0 = (i % 4) * 16;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      vv[n][e] = staged[d * kStride + t0 + e];
-      top = fmaxf(top, fabsf(Act<T>::to_f32(vv[n][e])));
-    }
+  for (int i = 0; i < 8; ++i) {
+    uint32_t& w = vv[i / 4].w[i % 4];
+    const int at = t0 + 2 * i;  // of the pair's first token
+    if (at >= old)
+      w = from[i];
+    else if (at + 1 >= old)
+      w = (w & 0xffffu) | (from[i] & 0xffff0000u);
   }
-  const float v_scale = __fdiv_rn(block_max(top, partial), 127.f);
+  top = fmaxf(largest<T>(vv[0]), largest<T>(vv[1]));
+  const float v_scale = __fdiv_rn(block_max<kWarps>(top, partial), 127.f);
   if (page >= 0) {
     uint8_t* codes = static_cast<uint8_t*>(a.c.pages) + (page * a.c.kv_heads + h) * 2 * kBlock * D;
     if (threadIdx.x == 0) {
@@ -286,52 +346,32 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
       s[0] = k_scale;
       s[1] = v_scale;
     }
-#pragma unroll
-    for (int n = 0; n < kUnits; ++n) {
-      const int i = n * kThreads + threadIdx.x, tok = i / (D / 16), u = i % (D / 16);
-      const Unit un = unit_of(u, a.rot, a.interleaved);
-      uint32_t w[4] = {0, 0, 0, 0}, z[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        w[e / 4] |= code_of(Act<T>::to_f32(kx[n].v[e]), k_scale) << (8 * (e % 4));
-        w[2 + e / 4] |= code_of(Act<T>::to_f32(ky[n].v[e]), k_scale) << (8 * (e % 4));
-      }
-      *reinterpret_cast<uint2*>(codes + tok * D + un.at0) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(codes + tok * D + un.at1) = make_uint2(w[2], w[3]);
-      const int d = i / 4, t0 = (i % 4) * 16;
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        z[e / 4] |= code_of(Act<T>::to_f32(vv[n][e]), v_scale) << (8 * (e % 4));
-      *reinterpret_cast<uint4*>(codes + kBlock * D + d * kBlock + t0) =
-          make_uint4(z[0], z[1], z[2], z[3]);
-    }
+    *reinterpret_cast<uint2*>(codes + tok * D + un.at0) = codes_of<T>(kx, k_scale);
+    *reinterpret_cast<uint2*>(codes + tok * D + un.at1) = codes_of<T>(ky, k_scale);
+    const uint2 lo = codes_of<T>(vv[0], v_scale), hi = codes_of<T>(vv[1], v_scale);
+    *reinterpret_cast<uint4*>(codes + kBlock * D + d * kBlock + t0) =
+        make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
   // the new tail, where the old one had tokens of this block (all read above:
   // the barriers of block_max lie in between)
-  const int total = r.held + r.n;
-  if (old) {
-    for (int tok = threadIdx.x / (D / 16); tok < total % kBlock; tok += kThreads / (D / 16)) {
-      const int u = threadIdx.x % (D / 16), pos = total / kBlock * kBlock + tok;
-      const T* row = qkv + (r.row0 + pos - r.held) * a.qkv_stride;
-      const Unit un = unit_of(u, a.rot, a.interleaved);
-      const T* k = row + (a.q_heads + h) * D;
-      const T* v = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
-      Vec8<T> x = load8(k + un.at0), y = load8(k + un.at1);
-      const Vec8<T> v0 = load8(v), v1 = load8(v + 8);
-      rotate_unit(x, y, u, a.rot, a.interleaved, a.table + int64_t(pos) * a.rot);
-      store8(tail + tok * D + un.at0, x);
-      store8(tail + tok * D + un.at1, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        tail[kBlock * D + (16 * u + e) * kBlock + tok] = v0.v[e];
-        tail[kBlock * D + (16 * u + 8 + e) * kBlock + tok] = v1.v[e];
-      }
-    }
+  const int total = r.held + r.n, pos = total / kBlock * kBlock + tok;
+  if (old && pos < total) {
+    const T* row = qkv + (r.row0 + pos - r.held) * a.qkv_stride;
+    const T* nk = row + (a.q_heads + h) * D;
+    const T* next = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
+    Vec8 x = load8(nk + un.at0), y = load8(nk + un.at1);
+    const Vec8 v0 = load8(next), v1 = load8(next + 8);
+    rotate_unit<T>(x, y, u, a.rot, a.interleaved,
+                   angles_of(a.table + int64_t(pos) * a.rot, u, a.rot));
+    store8(tail + tok * D + un.at0, x);
+    store8(tail + tok * D + un.at1, y);
+    column_to(tail + kBlock * D + 16 * u * kBlock + tok, kBlock, v0, v1);
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads<D>, 1024 / kThreads<D>) rope_append_kernel(const Args a) {
+  constexpr int kWarps = kThreads<D> / 32;
   grid_launch_dependents();
   grid_dependency_wait();
   // block CTAs first: they take longer
@@ -339,8 +379,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
   if (blockIdx.x < blocks) {
     block_cta<T, D>(a, blockIdx.x / a.c.kv_heads, blockIdx.x % a.c.kv_heads);
   } else {
-    const int64_t t = (blockIdx.x - blocks) * kWarps + (threadIdx.x >> 5);
-    if (t < a.n_tokens) token_warp<T, D>(a, t);
+    const int64_t i = (blockIdx.x - blocks) * kWarps + (threadIdx.x >> 5), t = i / a.parts;
+    if (t < a.n_tokens) token_warp<T, D>(a, t, int(i % a.parts));
   }
 }
 
@@ -376,19 +416,18 @@ __global__ void __launch_bounds__(256)
   const int64_t i = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * 16;
   if (i >= per_page) return;
   T* dst = out + blockIdx.y * per_page + i;
-  Vec8<T> v[2];
+  Vec8 v[2] = {};
   if (good) {
     const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.pages) +
                                                     page * per_page + i);
     const float s = c.scales[page * c.kv_heads * 2 + i / (kBlock * c.head_dim)];
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      v[e / 8].v[e % 8] = Act<T>::from_f32_rn(
-          (float((words[e / 4] >> (8 * (e % 4))) & 0xffu) - 128.f) * s);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e / 8].v[e % 8] = Act<T>::from_f32_rn(0.f);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t pair = words[e / 2] >> (16 * (e % 2));
+      v[e / 4].w[e % 4] = pack<T>(make_float2((float(pair & 0xffu) - 128.f) * s,
+                                              (float(pair >> 8 & 0xffu) - 128.f) * s));
+    }
   }
   store8(dst, v[0]);
   store8(dst + 8, v[1]);
@@ -397,8 +436,9 @@ __global__ void __launch_bounds__(256)
 template <typename T, int D>
 void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.block_items * a.c.kv_heads + (a.n_tokens + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kThreads);
+  constexpr int kWarps = kThreads<D> / 32;
+  cfg.gridDim = dim3(unsigned(a.block_items * a.c.kv_heads + (a.n_tokens * a.parts + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kThreads<D>);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -427,7 +467,9 @@ qlin_status launch_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
   const int64_t most = n_tokens / kBlock + c.slots;
   const Args a = {qkv,    qkv_stride, q_out,   table,    n_positions,
                   rot_dim, interleaved, c,      starts,   n_tokens,
-                  q_heads, n_tokens < most ? n_tokens : most};
+                  q_heads, n_tokens < most ? n_tokens : most,
+                  // few heads a warp: their loads come one pair after the other
+                  std::max(n_tokens <= 1024 ? 4 : 1, (q_heads * c.head_dim / 16 + 127) / 128)};
   if (c.dtype == QLIN_F16)
     c.head_dim == 64 ? launch_t<__half, 64>(a, flags, st) : launch_t<__half, 128>(a, flags, st);
   else
