@@ -17,7 +17,15 @@
 namespace qlin {
 namespace attention {
 
-constexpr int kSplitRows = 64;  // slots with more rows go to the tile kernel
+// Slots with more rows go to the tile kernel.  The split kernel's time grows with the
+// rows, 8 of them a pass over the cache, the tile kernel's does not up to 256, but it
+// starts 20 us behind.  By rows, split against tile, us, head dimension 128:
+//     slots x tokens     32 rows      64 rows      96 rows     128 rows
+//     1 x 400           17  / 42     19  / 41     19  / 41     23  / 41
+//     8 x 8000          70  / 120    106 / 127    131 / 127    190 / 128
+//     32 x 8000         258 / 264    303 / 241    504 / 275    485 / 244
+// (at 64: 8 x 8000 56 / 98, 71 / 100, 109 / 102, 126 / 102).
+constexpr int kSplitRows = 64;
 
 struct Args {
   const void* q;

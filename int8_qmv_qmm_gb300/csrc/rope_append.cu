@@ -2,9 +2,9 @@
 // formats), the table of cosines and sines, and the cache's reconstruction.
 //
 // One launch does two kinds of work:
-//   token warps   one warp per new token: turns its queries and, where the
-//                 token's block stays incomplete, its keys, which go with its
-//                 values to the slot's tail;
+//   token warps   four warps per new token: they turn its queries and, where
+//                 the token's block stays incomplete, its keys, which go with
+//                 its values to the slot's tail;
 //   block CTAs    one CTA per block that the call completes and key/value
 //                 head: gathers the block's 64 tokens (the tail's, then new
 //                 ones), takes the largest magnitude of the keys and of the
@@ -15,10 +15,12 @@
 //
 // It moves 2 bytes in and 2 (queries) or 1 (blocks) out per element and does a
 // handful of operations on each: memory bounds long prompts, launch and
-// latency a decode step.  Angles come from a table made in 64 bits: at
+// latency a decode step.  4 prompts of 2048 tokens, 32 + 8 + 8 heads of 128, take
+// 49 us; their token warps alone would take 42, their block CTAs 31, and both wait
+// for loads, with all of an SM's threads in flight.  32 decoded tokens take 7.2 us.
+// Angles come from a table made in 64 bits: at
 // position 100000 a float32 angle would be off by up to 4e-3 radians.
 
-#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -35,6 +37,11 @@ namespace {
 // loads in flight: 59 us for 4 prompts of 2048.)
 template <int D>
 constexpr int kThreads = kBlock * (D / 16);
+
+// Warps that share a token: the heads of one warp come two after two.  (1, 2, 4
+// and 8: 32 decoded tokens in 19, 15, 15 and 15 us, 4 prompts of 2048 in 74, 66,
+// 62 and 68.)
+constexpr int kParts = 4;
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_rope_status, bit); }
 
@@ -183,7 +190,6 @@ struct Args {
   int64_t n_tokens;
   int q_heads;
   int64_t block_items;  // room for completed blocks, over all slots
-  int parts;            // warps that share a token
 };
 
 // Whether all of a slot's rows can be taken: its blocks fit and its positions
@@ -224,10 +230,10 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
   const Angles angles = angles_of(a.table + int64_t(pos) * a.rot, u, a.rot);
   const Unit un = unit_of(u, a.rot, a.interleaved);
   T* out = static_cast<T*>(a.q_out) + t * a.q_heads * D;
-  const int q1 = a.q_heads * (part + 1) / a.parts;
+  const int q1 = a.q_heads * (part + 1) / kParts;
   // two heads' loads before the first store (which could be to the same memory,
   // for all that the compiler knows)
-  for (int h = a.q_heads * part / a.parts + lane / kUnits; h < q1; h += 2 * kHeads) {
+  for (int h = a.q_heads * part / kParts + lane / kUnits; h < q1; h += 2 * kHeads) {
     const bool two = h + kHeads < q1;
     const T* from = row + h * D;
     T* to = out + h * D;
@@ -249,8 +255,8 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
   const bool stays = pos / kBlock == total / kBlock;
   const bool left_to_block = total / kBlock > r.held / kBlock && r.held % kBlock;
   if (!stays || left_to_block) return;
-  const int at = pos % kBlock, k1 = a.c.kv_heads * (part + 1) / a.parts;
-  for (int h = a.c.kv_heads * part / a.parts + lane / kUnits; h < k1; h += kHeads) {
+  const int at = pos % kBlock, k1 = a.c.kv_heads * (part + 1) / kParts;
+  for (int h = a.c.kv_heads * part / kParts + lane / kUnits; h < k1; h += kHeads) {
     T* tail = static_cast<T*>(a.c.tail) + (int64_t(b) * a.c.kv_heads + h) * 2 * kBlock * D;
     const T* k = row + (a.q_heads + h) * D;
     const T* v = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
@@ -379,8 +385,8 @@ __global__ void __launch_bounds__(kThreads<D>, 1024 / kThreads<D>) rope_append_k
   if (blockIdx.x < blocks) {
     block_cta<T, D>(a, blockIdx.x / a.c.kv_heads, blockIdx.x % a.c.kv_heads);
   } else {
-    const int64_t i = (blockIdx.x - blocks) * kWarps + (threadIdx.x >> 5), t = i / a.parts;
-    if (t < a.n_tokens) token_warp<T, D>(a, t, int(i % a.parts));
+    const int64_t i = (blockIdx.x - blocks) * kWarps + (threadIdx.x >> 5), t = i / kParts;
+    if (t < a.n_tokens) token_warp<T, D>(a, t, int(i % kParts));
   }
 }
 
@@ -437,7 +443,7 @@ template <typename T, int D>
 void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   constexpr int kWarps = kThreads<D> / 32;
-  cfg.gridDim = dim3(unsigned(a.block_items * a.c.kv_heads + (a.n_tokens * a.parts + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3(unsigned(a.block_items * a.c.kv_heads + (a.n_tokens * kParts + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kThreads<D>);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -467,9 +473,7 @@ qlin_status launch_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
   const int64_t most = n_tokens / kBlock + c.slots;
   const Args a = {qkv,    qkv_stride, q_out,   table,    n_positions,
                   rot_dim, interleaved, c,      starts,   n_tokens,
-                  q_heads, n_tokens < most ? n_tokens : most,
-                  // few heads a warp: their loads come one pair after the other
-                  std::max(n_tokens <= 1024 ? 4 : 1, (q_heads * c.head_dim / 16 + 127) / 128)};
+                  q_heads, n_tokens < most ? n_tokens : most};
   if (c.dtype == QLIN_F16)
     c.head_dim == 64 ? launch_t<__half, 64>(a, flags, st) : launch_t<__half, 128>(a, flags, st);
   else
