@@ -713,6 +713,32 @@ struct Row {
   }
 };
 
+// The row of a cluster: of 512 rows those first whose bounds take longest, so that
+// the last clusters to start are short ones.  (96 rows of 128256, a third of them
+// with top-p alone: 128 us in the rows' own order, 110 in this.)
+__device__ __forceinline__ int64_t row_of(const Params& a, int64_t y, int few, Shared& s) {
+  const int64_t y0 = y / kThreads * kThreads;
+  const int at = int(y - y0), rows = int(min(int64_t(kThreads), int64_t(gridDim.y) - y0));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the largest or a few threads' maxima: 0; a draw among all: 1; a share of all: 2
+  int cost = -1;
+  if (int(threadIdx.x) < rows) {
+    const int64_t m = y0 + threadIdx.x;
+    const int k = a.top_k[m];
+    cost = !(a.temperature[m] > 0.f) || (k > 0 && k <= few) ? 0 : a.top_p[m] < 1.f ? 2 : 1;
+  }
+  const int twos = __syncthreads_count(cost == 2), ones = __syncthreads_count(cost == 1);
+  const int want = at < twos ? 2 : at < twos + ones ? 1 : 0;
+  int skip = at - (want == 2 ? 0 : want == 1 ? twos : twos + ones);
+  const unsigned mine = __ballot_sync(0xffffffffu, cost == want);
+  if (lane == 0) s.warp_sum[warp] = __popc(mine);
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) skip -= int(s.warp_sum[i]);
+  if (cost == want && __popc(mine & ((1u << lane) - 1)) == skip) s.drawn = threadIdx.x;
+  __syncthreads();
+  return y0 + s.drawn;
+}
+
 // PER_SM: CTAs that an SM is to hold.
 template <typename T, int PER_SM>
 __global__ void __launch_bounds__(kThreads, PER_SM) sample_kernel(const Params a) {
@@ -723,12 +749,13 @@ __global__ void __launch_bounds__(kThreads, PER_SM) sample_kernel(const Params a
   row.view.x = x;
   row.rank = ptx::cluster_ctarank();
   row.ranks = gridDim.x;
-  const int64_t m = blockIdx.y;
   const int base = row.rank * a.part, n = max(0, min(a.part, a.V - base));
   row.view.base = base;
   row.view.n = n;
   grid_launch_dependents();
   grid_dependency_wait();
+  // (one row for each cluster that fits: no order is better than another)
+  const int64_t m = PER_SM == 1 ? blockIdx.y : row_of(a, blockIdx.y, row.ranks * kThreads / 8, s);
   const T* src = static_cast<const T*>(a.logits) + m * a.stride + base;
 
   // the part into shared memory, and the row's largest logit (the first such)
