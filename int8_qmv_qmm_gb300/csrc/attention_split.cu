@@ -14,6 +14,8 @@
 // its part in the workspace, and a second kernel, launched while the first still
 // runs, joins the parts in the list's order.
 
+#include <algorithm>
+
 #include "attention_core.cuh"
 #include "sm100_ptx.cuh"
 
@@ -33,6 +35,7 @@ constexpr int kMaxSlots = 1024;
 constexpr int kTailCost = 4;                  // of a tail, in blocks
 constexpr int kJoinThreads = 512;
 constexpr int kJoinPerSm = 2;
+constexpr int kMaxWarps = 2048;               // of the split kernel's grid
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_split_status, bit); }
 
@@ -356,37 +359,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the tiles that pass the end of a warp's share.  Each CTA
-// lists them (the order is that of the warps) and takes every gridDim.x-th of
-// their slices, 16 dimensions of a tile's 8 rows: groups of 32 threads
-// (4 rows of one dimension each) take a part each in turn, and are added up in
-// order.
+// lists them (the order is that of the warps).  A team of warps takes a slice, 16
+// dimensions of a tile's 8 rows: its warps (4 rows of one dimension a thread) take
+// a part each in turn, and are added up in order.  Teams are a whole CTA where the
+// slices are no more than the CTAs (few, long lists of parts), else four warps.
+// (Whole CTAs alone: 52.8 us for 32 sequences of 8192 tokens with the split kernel,
+// 32.8 for 36 rows of 3000; with both sizes 49.2 and 29.4.  A warp for each slice of
+// up to 8 parts: 49.7 and 33.2, but 16 sequences of mixed lengths 62 for 59.)
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const float* parts,
                                                             const Split* splits, int warps) {
   using L = Layout<D>;
   constexpr int kSlices = D / 16, kGroups = kJoinThreads / 32;
-  __shared__ int s_which[4096], s_count[kGroups + 1];
+  constexpr int kRounds = kMaxWarps / kJoinThreads;
+  __shared__ int s_which[kMaxWarps], s_count[kRounds][kGroups];
   __shared__ float4 s_o[kGroups][32], s_m[kGroups][2], s_l[kGroups][2];
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
   grid_launch_dependents();
   grid_dependency_wait();
-  int n = 0;
-  for (int i0 = 0; i0 < warps; i0 += kJoinThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool mine = i < warps && __ldcg(&splits[i].last) >= 0;
-    const unsigned ballot = __ballot_sync(0xffffffffu, mine);
-    __syncthreads();
-    if (lane == 0) s_count[group] = __popc(ballot);
-    __syncthreads();
-    int at = n;
-    for (int k = 0; k < kGroups; ++k) {
-      if (k < group) at += s_count[k];
-      n += s_count[k];
-    }
-    if (mine) s_which[at + __popc(ballot & ((1u << lane) - 1))] = i;
+  unsigned ballot[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int w = i * kJoinThreads + threadIdx.x;
+    ballot[i] = w < warps && __ldcg(&splits[w].last) >= 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    ballot[i] = __ballot_sync(0xffffffffu, ballot[i]);
+    if (lane == 0) s_count[i][group] = __popc(ballot[i]);
   }
   __syncthreads();
-  for (int task = blockIdx.x; task < n * kSlices; task += gridDim.x) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    int at = n;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      if (k < group) at += s_count[i][k];
+      n += s_count[i][k];
+    }
+    if (ballot[i] >> lane & 1)
+      s_which[at + __popc(ballot[i] & ((1u << lane) - 1))] = i * kJoinThreads + int(threadIdx.x);
+  }
+  __syncthreads();
+  const int size = n * kSlices <= int(gridDim.x) ? kGroups : 4, teams = kGroups / size;
+  const int team = group / size, g0 = team * size;  // and the team's first warp
+  auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * size) : "memory"); };
+  for (int task = blockIdx.x * teams + team; task < n * kSlices; task += gridDim.x * teams) {
     const int first = s_which[task / kSlices], d0 = task % kSlices * 16;
     const Split sp = splits[first];
     // this thread: dimension d0 + lane/2, rows 4 * (lane%2) ..
@@ -395,7 +414,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const 
 #pragma unroll
     for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r] = 0.f;
 #pragma unroll 4
-    for (int k = first + group; k <= sp.last; k += kGroups) {
+    for (int k = first + group - g0; k <= sp.last; k += size) {
       const float* part = parts + size_t(2 * k + (k == first ? 1 : 0)) * L::kPart;
       const float4 pm = __ldcg(reinterpret_cast<const float4*>(part + kRows * D) + half);
       const float4 pl = __ldcg(reinterpret_cast<const float4*>(part + kRows * (D + 1)) + half);
@@ -416,14 +435,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const 
       s_m[group][lane] = make_float4(m[0], m[1], m[2], m[3]);
       s_l[group][lane] = make_float4(l[0], l[1], l[2], l[3]);
     }
-    __syncthreads();
-    // 128 sums: thread i takes row i/16, dimension d0 + i%16
-    const int row = threadIdx.x >> 4, dd = threadIdx.x & 15, here = sp.kvh_here & 15;
+    meet();
+    // 128 sums: thread i of the team takes row i/16, dimension d0 + i%16
+    const int i = threadIdx.x - 32 * g0, row = i >> 4, dd = i & 15, here = sp.kvh_here & 15;
     if (row < here) {
       auto value = [&](const float4* v) { return reinterpret_cast<const float*>(v)[row & 3]; };
       float top = -INFINITY, sum = 0.f, out = 0.f;
-      for (int k = 0; k < kGroups; ++k) top = fmaxf(top, value(&s_m[k][row >> 2]));
-      for (int k = 0; k < kGroups; ++k) {
+#pragma unroll 4
+      for (int k = g0; k < g0 + size; ++k) top = fmaxf(top, value(&s_m[k][row >> 2]));
+#pragma unroll 4
+      for (int k = g0; k < g0 + size; ++k) {
         const float vm = value(&s_m[k][row >> 2]);
         const float f = vm == -INFINITY ? 0.f : exp2_fast(vm - top);
         sum += value(&s_l[k][row >> 2]) * f;
@@ -435,7 +456,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const 
                                  D +
                              d0 + dd] = Act<T>::from_f32_rn(sum > 0.f ? out / sum : 0.f);
     }
-    __syncthreads();
+    meet();
   }
 }
 
@@ -446,7 +467,7 @@ void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(split_kernel<T, D>), L::bytes(kMaxSlots), &done))
     return;
-  const int sms = sm_count(), warps = sms * kWarps;
+  const int sms = std::min(sm_count(), kMaxWarps / kWarps), warps = sms * kWarps;
   Split* splits = static_cast<Split*>(workspace);
   float* parts = reinterpret_cast<float*>(splits + warps);
   cudaLaunchConfig_t cfg = {};
