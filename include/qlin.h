@@ -329,8 +329,8 @@ qlin_status qlin_linear_ex(const void* x, const uint32_t* wq, const void* scales
  *   lens     int32 [slots]: tokens held before the call (shared by a model's
  *            layers; the caller advances it once per step)
  *
- * pages and tail are 16-byte aligned.  The struct is read during the call
- * only; the memory it names is used on the stream.
+ * At most 1024 slots.  pages and tail are 16-byte aligned.  The struct is read
+ * during the call only; the memory it names is used on the stream.
  */
 #define QLIN_KV_BLOCK 64
 typedef struct {
@@ -424,8 +424,8 @@ size_t qlin_cache_attention_workspace_size(int head_dim);
  *            and may be larger than it needs to be; a slot with more is left
  *            out, zeros in its rows, and sets a device status bit)
  *   workspace  qlin_cache_attention_workspace_size(head_dim) bytes of device
- *            memory, 16-byte aligned, zeroed once by the caller; calls that
- *            can overlap need workspaces of their own
+ *            memory, 16-byte aligned, with anything in it; calls that can
+ *            overlap need workspaces of their own
  * Scores, softmax statistics and sums are float32; probabilities enter the
  * products in 16 bits.  q_heads: a multiple of kv_heads, at most 16 times as
  * many.  q and out 16-byte aligned, q_stride a multiple of 8.  Rows that no

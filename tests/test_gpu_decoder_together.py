@@ -1,0 +1,115 @@
+"""The decoder's calls as they are used together: overlapping one another, over many
+slots, shared pages and used workspaces, and sampling of many unlike rows."""
+
+import pytest
+import torch
+
+import int8_qmv_qmm_gb300 as q
+from tests.test_gpu_decoder import BF16, F16, F32, Model, dev, normal, table_for  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_overlapped_calls_give_the_same(dev):  # noqa: F811
+    """norm, linear, append, attention, norm and sampling in a chain, each started
+    while the one before runs: the same bits as one after the other."""
+    hidden, heads, kvh, d, vocab, slots = 512, 8, 2, 64, 5000, 3
+    width = (heads + 2 * kvh) * d
+    packed = [q.quantize_affine((normal(i, n, hidden) * 0.05).float().to(dev), 8)
+              for i, n in ((1, width), (2, hidden), (3, vocab))]
+    weight = torch.ones(hidden, dtype=F16, device=dev)
+    table, ws = table_for(dev, d), q.attention_workspace(d, dev)
+    starts = torch.arange(slots + 1, dtype=torch.int32, device=dev)
+    rows = dict(u=torch.tensor([0.1, 0.5, 0.9]), temperature=torch.tensor([0.9, 1.0, 0.0]),
+                top_k=torch.tensor([40, 0, 0], dtype=torch.int32),
+                top_p=torch.tensor([1.0, 0.9, 1.0]), min_p=torch.tensor([0.0, 0.0, 0.1]))
+    rows = {k: v.to(dev) for k, v in rows.items()}
+    seen = []
+    for overlap in (False, True):
+        m = Model(dev, slots, kvh, d, F16)
+        m.append([200, 63, 1], heads, table, seed=9)
+        got = []
+        x = normal(10, slots, hidden).to(F16).to(dev)
+        r = x.float()
+        for _ in range(8):
+            h, r = q.add_rms_norm(x, weight, r, residual_out=r, overlap_previous=overlap)
+            qkv = q.qmv(h, *packed[0], 8, overlap_previous=overlap)
+            query = q.rope_append(qkv, table, m.cache, starts, heads, overlap_previous=overlap)
+            a = q.cache_attention(query, m.cache, starts, 1, ws, overlap_previous=overlap)
+            x = q.qmv(a.view(slots, -1), *packed[1], 8, overlap_previous=overlap)
+            h, r = q.add_rms_norm(x, weight, r, overlap_previous=overlap)
+            logits = q.qmv(h, *packed[2], 8, overlap_previous=overlap)
+            tokens, probs = q.sample(logits, **rows, overlap_previous=overlap)
+            m.cache.lens += 1
+            got += [x, r.clone(), tokens, probs]
+        seen.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*seen))
+    assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("d,dt", [(64, F16), (128, BF16)])
+def test_many_slots(dev, d, dt):  # noqa: F811
+    """As many slots as a cache takes, a token each and some with none, one prompt."""
+    slots = 1024
+    m = Model(dev, slots, 1, d, dt, blocks=4)
+    held = [(37 * b) % 131 for b in range(slots)]
+    m.append(held, 2, table_for(dev, d, 256), seed=1)
+    new = [0 if b % 7 == 3 else 1 for b in range(slots)]
+    m.append(new, 2, table_for(dev, d, 256), seed=2, advance=False)
+    total = sum(new)
+    m.attend(new, 2, seed=3, only={0, 1, 100, 511, 512, 600, total - 1})
+    m.cache.lens += torch.tensor(new, dtype=torch.int32, device=dev)
+    new = [90 if b == 700 else int(b % 2) for b in range(slots)]
+    m.append(new, 2, table_for(dev, d, 256), seed=4, advance=False)
+    first = sum(new[:700])
+    m.attend(new, 2, seed=5, only={0, 5, first - 1, first, first + 45, first + 89, first + 90,
+                                   sum(new) - 1})
+    m.check()
+    assert q.device_status() == 0
+
+
+def test_too_many_slots(dev):  # noqa: F811
+    c = q.KVCache.empty(1025, 64, 1, 64, F16, dev)
+    starts = torch.zeros(1026, dtype=torch.int32, device=dev)
+    with pytest.raises(q.QlinError):
+        q.rope_append(torch.zeros(1, 192, dtype=F16, device=dev), None, c, starts, 1)
+    with pytest.raises(q.QlinError):
+        q.cache_attention(torch.zeros(1, 1, 64, dtype=F16, device=dev), c, starts, 1,
+                          q.attention_workspace(64, dev))
+
+
+def test_shared_pages_and_a_used_workspace(dev):  # noqa: F811
+    """Two slots whose first blocks are the same pages, and scratch with anything in
+    it: as for slots with pages of their own and zeroed scratch."""
+    out = []
+    for shared in (False, True):
+        m = Model(dev, 2, 2, 64, F16, blocks=6, seed=4)
+        x = normal(5, 300, 8 * 64)
+        m.append([128, 128], 4, None, values=torch.cat((x[:128], x[:128])))
+        if shared:
+            m.cache.table[1, :2] = m.cache.table[0, :2]
+        m.append([40, 9], 4, None, values=x[128:177])
+        m.append([1, 30], 4, None, values=x[177:208], advance=False)
+        ws = q.attention_workspace(64, dev)
+        if shared:
+            ws.fill_(255)
+        out.append(m.attend([1, 30], 4, seed=6, workspace=ws)[0])
+    assert torch.equal(*out)
+    assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("m,v", [(1100, 300), (130, 20000)])
+def test_sample_many_unlike_rows(dev, m, v, dt):  # noqa: F811
+    """Rows with settings of every kind in one call: each as in a call of its own."""
+    logits = (normal(1, m, v) * 2.5).to(dt).to(dev)
+    kind = torch.arange(m) * 7 % 6
+    pick = {"temperature": [1.0, 0.8, 0.7, 0.0, 1.3, 1.0], "top_p": [0.9, 1.0, 0.95, 1.0, 1.0, 0.5],
+            "min_p": [0.0, 0.1, 0.0, 0.0, 0.0, 0.0]}
+    rows = {k: torch.tensor(x, dtype=F32)[kind].to(dev) for k, x in pick.items()}
+    rows["top_k"] = torch.tensor([0, 20, 5, 0, 0, 290], dtype=torch.int32)[kind].to(dev)
+    rows["u"] = ((torch.arange(m) + 0.5) / m).to(dev)
+    tokens, probs = q.sample(logits, **rows)
+    for r in list(range(0, m, 13)) + [m - 1]:
+        t, p = q.sample(logits[r:r + 1], **{k: x[r:r + 1].contiguous() for k, x in rows.items()})
+        assert t.item() == tokens[r].item() and p.item() == probs[r].item(), (r, int(kind[r]))
