@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
-// One warp's attention of 8*NT rows over blocks of the cache.
+// One warp's attention of 8 rows over blocks of the cache.
 //
 // Tokens (scores) and dimensions (outputs) are the 16 rows of the products and
 // the query rows their 8 columns, so that a decode step's few rows fill the
@@ -131,27 +131,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // Both products take f16 whatever T is: codes are exact in it, and it rounds p
 // to 11 bits where bf16 has 8.  bf16 queries are scaled by a power of two for
 // each row, to a largest magnitude of 2^14 .. 2^15: exact down to 2^-28 of it.
-template <typename T, int D, int NT>
+template <typename T, int D>
 struct Warp {
   static constexpr int kQk = D / 16;  // k steps of the scores, row tiles of the output
-  uint32_t q[kQk][NT][2];
-  float o[kQk][NT][4];
-  float factor[NT][2];       // scores to units of log2, without the key scale
-  float m[NT][2], l[NT][2];  // of rows 8n + 2t + {0, 1}; l over this lane's tokens
-  float unit;                // o counts in units of this: the largest value scale so far
+  uint32_t q[kQk][2];
+  float o[kQk][4];
+  float factor[2];  // scores to units of log2, without the key scale
+  float m[2], l[2];  // of rows 2t + {0, 1}; l over this lane's tokens
+  float unit;        // o counts in units of this: the largest value scale so far
 
   __device__ void init() {
 #pragma unroll
     for (int i = 0; i < kQk; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
     unit = 0.f;
   }
 
@@ -169,111 +164,96 @@ struct Warp {
     }
   }
 
-  // rows[n]: row 8n + g of the tile (null: zeros).  The fragments are T until
+  // row: row g of the tile (null: zeros).  The fragments are T until
   // prepare_q.
-  __device__ void load_q(const T* const (&rows)[NT], int lane) {
+  __device__ void load_q(const T* row, int lane) {
+    uint32_t w[D / 8];
+    load_row(row, w, lane & 3);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t w[D / 8];
-      load_row(rows[n], w, lane & 3);
-#pragma unroll
-      for (int s = 0; s < kQk; ++s) {
-        q[s][n][0] = w[2 * s];
-        q[s][n][1] = w[2 * s + 1];
-      }
+    for (int s = 0; s < kQk; ++s) {
+      q[s][0] = w[2 * s];
+      q[s][1] = w[2 * s + 1];
     }
   }
 
   __device__ void prepare_q(float scale, int lane) {
     const int t = lane & 3;
+    float back = scale;
+    if (std::is_same<T, __nv_bfloat16>::value) {
+      float top = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float back = scale;
-      if (std::is_same<T, __nv_bfloat16>::value) {
-        float top = 0.f;
+      for (int s = 0; s < kQk; ++s)
 #pragma unroll
-        for (int s = 0; s < kQk; ++s)
+        for (int h = 0; h < 2; ++h)
+          top = fmaxf(top, fmaxf(fabsf(low_f32(q[s][h])), fabsf(high_f32(q[s][h]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is below 2^15
+      e = max(-100, min(113, e));
+      const float down = __uint_as_float(uint32_t(127 - e) << 23);
+      back = scale * __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            top = fmaxf(top, fmaxf(fabsf(low_f32(q[s][n][h])), fabsf(high_f32(q[s][n][h]))));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = int(__float_as_uint(top) >> 23) - 127 - 14;  // q * 2^-e is below 2^15
-        e = max(-100, min(113, e));
-        const float down = __uint_as_float(uint32_t(127 - e) << 23);
-        back = scale * __uint_as_float(uint32_t(127 + e) << 23);
+      for (int s = 0; s < kQk; ++s)
 #pragma unroll
-        for (int s = 0; s < kQk; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            q[s][n][h] = pack2<__half>(low_f32(q[s][n][h]) * down, high_f32(q[s][n][h]) * down);
-      }
-      // row g's factor, to the lanes that hold the row's scores
-      factor[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-      factor[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        for (int h = 0; h < 2; ++h)
+          q[s][h] = pack2<__half>(low_f32(q[s][h]) * down, high_f32(q[s][h]) * down);
     }
+    // row g's factor, to the lanes that hold the row's scores
+    factor[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+    factor[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
   }
 
   // Scores (times scale and the rows' factors) -> weighted probabilities, in
   // place, with the running maximum; the factors that the rows' sums so far take
-  // go to keep.  seen[n][r]: tokens of the block that row 8n + 2t + r sees.
+  // go to keep.  seen[r]: tokens of the block that row 2t + r sees.
   // weight: what the probabilities are scaled by.
-  __device__ void softmax(float (&s)[4][NT][4], const float (&scale)[NT][2], float weight,
-                          const int (&seen)[NT][2], bool mask, int g, float (&keep)[NT][2]) {
+  __device__ void softmax(float (&s)[4][4], const float (&scale)[2], float weight,
+                          const int (&seen)[2], bool mask, int g, float (&keep)[2]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] *= scale[n][e & 1];
+      for (int e = 0; e < 4; ++e) s[i][e] *= scale[e & 1];
     if (mask) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * (g >> 1) + 4 * i + 2 * (e >> 1) + (g & 1) >= seen[n][e & 1])
-              s[i][n][e] = -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (16 * (g >> 1) + 4 * i + 2 * (e >> 1) + (g & 1) >= seen[e & 1])
+            s[i][e] = -INFINITY;
     }
     const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 2; ++r) {
+      float top = fmaxf(s[0][r], s[0][2 + r]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float top = fmaxf(s[0][n][r], s[0][n][2 + r]);
+      for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(s[i][r], s[i][2 + r]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float next = fmaxf(m[r], top);
+      const float base = next == -INFINITY ? 0.f : next;  // a row that sees nothing yet
+      keep[r] = exp2_fast(m[r] - base);
+      m[r] = next;
+      const float from = base - shift;
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(s[i][n][r], s[i][n][2 + r]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float next = fmaxf(m[n][r], top);
-        const float base = next == -INFINITY ? 0.f : next;  // a row that sees nothing yet
-        keep[n][r] = exp2_fast(m[n][r] - base);
-        m[n][r] = next;
-        const float from = base - shift;
-        float sum = 0.f;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p = exp2_fast(s[i][n][2 * h + r] - from);
-            s[i][n][2 * h + r] = p;
-            sum += p;
-          }
-        l[n][r] = l[n][r] * keep[n][r] + sum * back;
-      }
+        for (int h = 0; h < 2; ++h) {
+          const float p = exp2_fast(s[i][2 * h + r] - from);
+          s[i][2 * h + r] = p;
+          sum += p;
+        }
+      l[r] = l[r] * keep[r] + sum * back;
+    }
   }
 
-  __device__ void rescale(const float (&keep)[NT][2], float ratio) {
+  __device__ void rescale(const float (&keep)[2], float ratio) {
+    const float f[2] = {keep[0] * ratio, keep[1] * ratio};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float f[2] = {keep[n][0] * ratio, keep[n][1] * ratio};
+    for (int i = 0; i < kQk; ++i)
 #pragma unroll
-      for (int i = 0; i < kQk; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][n][e] *= f[e & 1];
-    }
+      for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
   }
 
   // The factor from the old unit to the new, which is at least v.
@@ -285,14 +265,12 @@ struct Warp {
   }
 
   // The scores of a complete block's 64 keys, in units of its key scale.
-  __device__ void scores(const uint8_t* codes, float (&s)[4][NT][4], int lane) {
+  __device__ void scores(const uint8_t* codes, float (&s)[4][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
       const uint8_t* row = codes + (16 * (g >> 1) + 4 * i + (g & 1)) * D + 16 * t;
 #pragma unroll
       for (int p = 0; p < D / 64; ++p) {
@@ -304,38 +282,32 @@ struct Warp {
           uint32_t a[4];
           widen_codes(x0[k], a[0], a[2]);
           widen_codes(x1[k], a[1], a[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma<__half>(s[i][n], a, q[4 * p + k][n][0], q[4 * p + k][n][1]);
+          mma<__half>(s[i], a, q[4 * p + k][0], q[4 * p + k][1]);
         }
       }
     }
   }
 
   // Scores -> the second product's operand.
-  __device__ void probabilities(float (&s)[4][NT][4], uint32_t (&b)[4][NT][2], float k_scale,
-                                float v_scale, const int (&seen)[NT][2], bool mask, int lane) {
+  __device__ void probabilities(float (&s)[4][4], uint32_t (&b)[4][2], float k_scale,
+                                float v_scale, const int (&seen)[2], bool mask, int lane) {
     const float ratio = raise_unit(v_scale);
     // (a block whose values are all zero has scale 0: its codes are zero too; a
     // weight below f16's range makes every probability zero in it)
     const float weight = v_scale > 0.f ? fmaxf(__fdividef(v_scale, unit), 0x1p-60f) : 1.f;
-    float keep[NT][2], scale[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      scale[n][0] = factor[n][0] * k_scale, scale[n][1] = factor[n][1] * k_scale;
+    float keep[2], scale[2];
+    scale[0] = factor[0] * k_scale, scale[1] = factor[1] * k_scale;
     softmax(s, scale, weight, seen, mask, lane >> 2, keep);
     rescale(keep, ratio);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b[i][n][h] = transpose8(pack2<__half>(s[i][n][2 * h], s[i][n][2 * h + 1]));
+      for (int h = 0; h < 2; ++h)
+        b[i][h] = transpose8(pack2<__half>(s[i][2 * h], s[i][2 * h + 1]));
   }
 
   // out += probabilities * the block's values (codes of D rows of 64 tokens)
-  __device__ void values(const uint8_t* codes, const uint32_t (&b)[4][NT][2], int lane) {
+  __device__ void values(const uint8_t* codes, const uint32_t (&b)[4][2], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < kQk; ++i) {
@@ -348,61 +320,54 @@ struct Warp {
         uint32_t a[4];
         widen_codes(x0[k], a[0], a[2]);
         widen_codes(x1[k], a[1], a[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma<__half>(o[i][n], a, b[k][n][0], b[k][n][1]);
+        mma<__half>(o[i], a, b[k][0], b[k][1]);
       }
     }
   }
 
   // The tail: `count` tokens of T, the rest of its memory undefined.  Products
   // in T (the queries come from memory again: q is f16).
-  __device__ void tail(const T* kv, int count, const T* const (&rows)[NT], float scale_log2,
-                       const int (&seen)[NT][2], int lane) {
+  __device__ void tail(const T* kv, int count, const T* q_row, float scale_log2,
+                       const int (&seen)[2], int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float s[4][NT][4];
+    float s[4][4];
+    uint32_t w[D / 8];
+    load_row(q_row, w, t);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t w[D / 8];
-      load_row(rows[n], w, t);
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+      const T* row = kv + (16 * (g >> 1) + 4 * i + (g & 1)) * D + 16 * t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-        const T* row = kv + (16 * (g >> 1) + 4 * i + (g & 1)) * D + 16 * t;
+      for (int p = 0; p < D / 64; ++p)
 #pragma unroll
-        for (int p = 0; p < D / 64; ++p)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // two k steps to a load
-            const uint4 v0 = *reinterpret_cast<const uint4*>(row + 64 * p + 8 * h);
-            const uint4 v1 = *reinterpret_cast<const uint4*>(row + 2 * D + 64 * p + 8 * h);
-            const uint32_t a0[4] = {v0.x, v1.x, v0.y, v1.y}, a1[4] = {v0.z, v1.z, v0.w, v1.w};
-            mma<T>(s[i][n], a0, w[8 * p + 4 * h], w[8 * p + 4 * h + 1]);
-            mma<T>(s[i][n], a1, w[8 * p + 4 * h + 2], w[8 * p + 4 * h + 3]);
-          }
-      }
+        for (int h = 0; h < 2; ++h) {  // two k steps to a load
+          const uint4 v0 = *reinterpret_cast<const uint4*>(row + 64 * p + 8 * h);
+          const uint4 v1 = *reinterpret_cast<const uint4*>(row + 2 * D + 64 * p + 8 * h);
+          const uint32_t a0[4] = {v0.x, v1.x, v0.y, v1.y}, a1[4] = {v0.z, v1.z, v0.w, v1.w};
+          mma<T>(s[i], a0, w[8 * p + 4 * h], w[8 * p + 4 * h + 1]);
+          mma<T>(s[i], a1, w[8 * p + 4 * h + 2], w[8 * p + 4 * h + 3]);
+        }
     }
     const float ratio = raise_unit(1.f);
-    float keep[NT][2], scale[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) scale[n][0] = scale[n][1] = scale_log2;
+    float keep[2], scale[2];
+    scale[0] = scale[1] = scale_log2;
     softmax(s, scale, 1.f, seen, true, g, keep);
     rescale(keep, ratio);
     const float weight = 1.f / unit;
     // bf16 keeps only 8 bits of p, so what it leaves over goes through a second
     // product.
     constexpr bool kTwo = std::is_same<T, __nv_bfloat16>::value;
-    uint32_t b[4][NT][2], rest[4][NT][2];
+    uint32_t b[4][2], rest[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float p0 = s[i][n][2 * h] * weight, p1 = s[i][n][2 * h + 1] * weight;
-          const uint32_t v = pack2<T>(p0, p1);
-          b[i][n][h] = transpose8(v);
-          if (kTwo) rest[i][n][h] = transpose8(pack2<T>(p0 - low_f32(v), p1 - high_f32(v)));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = s[i][2 * h] * weight, p1 = s[i][2 * h + 1] * weight;
+        const uint32_t v = pack2<T>(p0, p1);
+        b[i][h] = transpose8(v);
+        if (kTwo) rest[i][h] = transpose8(pack2<T>(p0 - low_f32(v), p1 - high_f32(v)));
+      }
     // Undefined values must not meet the zeros of masked probabilities: 0 * NaN.
     uint32_t valid[4][2];
 #pragma unroll
@@ -426,11 +391,8 @@ struct Warp {
           const int k = 2 * h + c;
           const uint32_t av[4] = {a[c][0] & valid[k][0], a[c][1] & valid[k][0],
                                   a[c][2] & valid[k][1], a[c][3] & valid[k][1]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma<T>(o[i][n], av, b[k][n][0], b[k][n][1]);
-            if (kTwo) mma<T>(o[i][n], av, rest[k][n][0], rest[k][n][1]);
-          }
+          mma<T>(o[i], av, b[k][0], b[k][1]);
+          if (kTwo) mma<T>(o[i], av, rest[k][0], rest[k][1]);
         }
       }
   }

@@ -248,15 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   };
 
-  Warp<T, D, 1> w;
+  Warp<T, D> w;
   Piece p = {};
   Split split = {-1, 0, 0, 0};
   unsigned x = 0, x_piece = 0;
-  const T* qp[1] = {nullptr};
+  const T* qp = nullptr;
   int pos0 = 0, pos1 = 0, first_pos = 0;
   bool open = false;         // a piece is under way
   bool have_scores = false;  // of the block whose values come next
-  float s[4][1][4];
+  float s[4][4];
   // A block takes two turns, its keys and its values, each of which gives a
   // chunk of the ring back; the copies go on in between.
   while (true) {
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        l[i] = w.l[0][i];
+        l[i] = w.l[i];
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t v =
-                transpose8(pack2<T>(w.o[c][0][2 * h] * f0, w.o[c][0][2 * h + 1] * f1));
+                transpose8(pack2<T>(w.o[c][2 * h] * f0, w.o[c][2 * h + 1] * f1));
             if (g < p.here) *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 * h) = v;
           }
       } else {
@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<float2*>(part + (16 * c + 8 * h + g) * kRows + 2 * t) =
-                make_float2(w.o[c][0][2 * h] * w.unit, w.o[c][0][2 * h + 1] * w.unit);
+                make_float2(w.o[c][2 * h] * w.unit, w.o[c][2 * h + 1] * w.unit);
         if (g == 0) {
-          *reinterpret_cast<float2*>(part + kRows * D + 2 * t) = make_float2(w.m[0][0], w.m[0][1]);
+          *reinterpret_cast<float2*>(part + kRows * D + 2 * t) = make_float2(w.m[0], w.m[1]);
           *reinterpret_cast<float2*>(part + kRows * (D + 1) + 2 * t) = make_float2(l[0], l[1]);
         }
         if (x_piece == p.first)
@@ -316,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       p = piece_at(s_slot, a.c.slots, a.group, f.x);
       const Slot sl = s_slot[p.slot];
       const int held = sl.total - sl.n, row = p.row0 + g;
-      qp[0] = g < p.here ? static_cast<const T*>(a.q) +
-                               int64_t(sl.row0 + row / a.group) * a.q_stride +
-                               (p.kvh * a.group + row % a.group) * D
-                         : nullptr;
+      qp = g < p.here ? static_cast<const T*>(a.q) +
+                            int64_t(sl.row0 + row / a.group) * a.q_stride +
+                            (p.kvh * a.group + row % a.group) * D
+                      : nullptr;
       // the two rows whose scores this lane holds
       pos0 = 2 * t < p.here ? held + (p.row0 + 2 * t) / a.group : -1;
       pos1 = 2 * t + 1 < p.here ? held + (p.row0 + 2 * t + 1) / a.group : -1;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     x = f.x + 1;
     const int j = int(f.x - p.first);
-    const int seen[1][2] = {{pos0 - j * kBlock + 1, pos1 - j * kBlock + 1}};
+    const int seen[2] = {pos0 - j * kBlock + 1, pos1 - j * kBlock + 1};
     if (f.kind == kCodes) {
       const unsigned slot = used % L::kRing;
       const uint8_t* chunk = ring + slot * L::kChunk;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!have_scores) {
         w.scores(chunk, s, lane);
       } else {
-        uint32_t b[4][1][2];
+        uint32_t b[4][2];
         w.probabilities(s, b, f.scales.x, f.scales.y, seen, first_pos < j * kBlock + kBlock - 1,
                         lane);
         w.values(chunk, b, lane);
