@@ -2,7 +2,11 @@
 //
 // What bounds it is reading the cache once, so the blocks of all slots, heads
 // and row tiles are put in one list and every warp takes an equal, consecutive
-// share of it, however long or short the slots are.
+// share of it, however long or short the slots are.  One sequence of 131071
+// tokens, 8 heads of 128 (269 MB): 51 us, 5.3 TB/s, and 59 with the join; 32 of up
+// to 8192, 8 heads of 64 (185 MB): 43 us, 4.4 TB/s, and 49.  There a block's
+// instructions (the widening of its codes, the softmax of 64 tokens) take longer
+// than its bytes.
 //
 // A warp streams its blocks through a ring of its own in shared memory (bulk
 // copies, one for the keys and one for the values of a block) and shares nothing
@@ -17,7 +21,7 @@
 #include <algorithm>
 
 #include "attention_core.cuh"
-#include "sm100_ptx.cuh"
+#include "attention_ptx.cuh"
 
 namespace qlin {
 namespace attention {
