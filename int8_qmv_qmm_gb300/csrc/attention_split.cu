@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::kRing; ++i) ptx::mbar_init(bar + 8 * i, 1);
     ptx::fence_mbar_init();
   }
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();  // (after the wait: cache_attention.cu says why)
 
   // the list: blocks before each slot
   int64_t all_blocks = 0;

@@ -148,6 +148,12 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
 // Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, swizzled.
 __device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
+// The kernel is through when the split kernel's are, so that what follows it is
+// behind all of the call: one CTA sees to that, at its end.
+__device__ __forceinline__ void last_wait() {
+  if (blockIdx.x == 0) grid_dependency_wait();
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const Args a, float* parts, int sms) {
@@ -191,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
+  // (what the call reads is there: cache_attention.cu)
   grid_launch_dependents();
-  grid_dependency_wait();
   if (warp == 0) {
     const Plan plan = plan_of(a, sms);
     const int id = blockIdx.x;
@@ -209,10 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (s_work[0] < 0) return;
-  const Work work = work_at(a, s_work[0], s_work[1]);
+  const Work work = work_at(a, max(s_work[0], 0), s_work[1]);
   const int cuts = min(s_work[2], work.n), cut = s_work[3];
-  if (cut >= cuts) return;
+  if (s_work[0] < 0 || cut >= cuts) {
+    last_wait();
+    return;
+  }
   if (warp == kSoftmaxWarps + kWidenWarps) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -601,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + kWidenWarps) ptx::tmem_dealloc(tmem, 512);
+  last_wait();
 }
 
 // Joins the pieces, a warp for each row.
@@ -664,12 +673,12 @@ void launch_t(const Args& a, void* workspace, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::kBytes;
   cfg.stream = st;
-  cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
   cfg.gridDim = dim3(unsigned(2 * sms));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -113,3 +113,34 @@ def test_sample_many_unlike_rows(dev, m, v, dt):  # noqa: F811
     for r in list(range(0, m, 13)) + [m - 1]:
         t, p = q.sample(logits[r:r + 1], **{k: x[r:r + 1].contiguous() for k, x in rows.items()})
         assert t.item() == tokens[r].item() and p.item() == probs[r].item(), (r, int(kind[r]))
+
+
+@pytest.mark.parametrize("d,dt", [(64, F16), (128, BF16)])
+def test_mixed_batches_back_to_back(dev, d, dt):  # noqa: F811
+    """Prompts beside decoding sequences, call after call without a pause: the same
+    bits as with the device idle before each call."""
+    heads, kvh, new = 8, 2, [150, 1, 1, 40, 1, 200, 1]
+    total, weight = sum(new), torch.ones(heads * d, dtype=dt, device=dev)
+    table, ws = table_for(dev, d, 2048), q.attention_workspace(d, dev)
+    x = [normal(i, total, (heads + 2 * kvh) * d).to(dt).to(dev) for i in range(6)]
+    seen = []
+    for pause in (True, False):
+        m = Model(dev, len(new), kvh, d, dt, blocks=24)
+        m.append([300, 700, 63, 0, 64, 10, 1], heads, table, seed=9)
+        starts, got = m.starts(new), []
+        counts = starts.diff()
+        for qkv in x:
+            query = q.rope_append(qkv, table, m.cache, starts, heads, overlap_previous=not pause)
+            if pause:
+                torch.cuda.synchronize()
+            a = q.cache_attention(query, m.cache, starts, 200, ws, overlap_previous=not pause)
+            if pause:
+                torch.cuda.synchronize()
+            h, _ = q.add_rms_norm(a.view(total, -1), weight, overlap_previous=not pause)
+            if pause:
+                torch.cuda.synchronize()
+            got += [a, h]
+            m.cache.lens += counts
+        seen.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*seen))
+    assert q.device_status() == 0
