@@ -144,3 +144,25 @@ def test_mixed_batches_back_to_back(dev, d, dt):  # noqa: F811
         seen.append(got)
     assert all(torch.equal(a, b) for a, b in zip(*seen))
     assert q.device_status() == 0
+
+
+def test_calls_without_rows(dev):  # noqa: F811
+    """No token in any slot, no page, no row of logits: nothing happens."""
+    m = Model(dev, 3, 2, 64, F16)
+    m.append([70, 0, 5], 4, None, seed=1)
+    before = [t.clone() for t in (m.cache.pages, m.cache.tail)]
+    starts = m.starts([0, 0, 0])
+    out = q.rope_append(torch.empty(0, 8 * 64, dtype=F16, device=dev), table_for(dev, 64),
+                        m.cache, starts, 4)
+    assert out.shape == (0, 4, 64)
+    a = q.cache_attention(out, m.cache, starts, 0, q.attention_workspace(64, dev))
+    assert a.shape == (0, 4, 64)
+    assert q.cache_dequant(m.cache, starts[:0]).shape == (0, 2, 2, 64 * 64)
+    none = torch.empty(0, device=dev)
+    tokens, probs = q.sample(torch.empty(0, 100, device=dev), none, none,
+                             torch.empty(0, dtype=torch.int32, device=dev), none, none)
+    assert tokens.numel() == probs.numel() == 0
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+               for x, y in zip(before, (m.cache.pages, m.cache.tail)))
+    m.check()
+    assert q.device_status() == 0
