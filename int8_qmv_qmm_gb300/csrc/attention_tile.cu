@@ -33,8 +33,10 @@
 // joins them.
 //
 // What bounds it: at D = 128 the products (1024 cycles of the tensor core for a
-// block of both tiles), at D = 64 the exponentials.  Two chunks of 2048 over 6001,
-// 32 query heads of 128: 351 us, 895 TFLOP/s, of which the products alone would be
+// block of both tiles), at D = 64 the way of a block through a tile's four warps
+// (1660 cycles, of which the exponentials of both tiles take 1024; a quarter or an
+// eighth of them by polynomial on the multiply-add pipe made it 10% longer).  Two chunks of 2048 over 6001,
+// 32 query heads of 128: 351 us, 900 TFLOP/s, of which the products alone would be
 // 163 us at the library's rate; a 128 x 64 x 16 product takes 49 to 55 cycles here,
 // not 32, and the widening, the exponentials and their hand-overs hide behind it.
 

@@ -878,15 +878,17 @@ qlin_status launch_t(Params a, int64_t M, unsigned flags, cudaStream_t st) {
   const int64_t header = (sizeof(Shared) + 15) / 16 * 16;
   auto bytes = [&](int r) { return header + ((a.V + r - 1) / r + 7) / 8 * 8 * int64_t(sizeof(T)); };
   // CTAs that share a row: enough to fill the SMs twice, with 4096 elements or
-  // more each; and below 16384 each, where weights take two atomics for three
+  // more each; and below 16384 each, where weights take two atomics for three (96
+  // rows of 128256 by 8 CTAs each 110 us, by 4 109: what is saved in exchanges goes
+  // into the third)
   const int sms = sm_count();
   int n = 1;
   while (n < kMaxCluster && ((a.V + n - 1) / n + 7 >= 16384 || (M * n < 2 * sms && a.V > 4096 * 2 * n)))
     n *= 2;
   a.part = ((a.V + n - 1) / n + 7) / 8 * 8;
   // Where the clusters do not fill the SMs, all registers for one CTA (one row of
-  // 128256: 19.4 us, 22.5 with room for two); else room for two (96 rows: 128 us,
-  // 194 with one).
+  // 128256: 19.4 us, 22.5 with room for two); else room for two (96 rows, in their
+  // own order: 128 us, 194 with one).
   return M * n <= sms ? launch_per_sm<T, 1>(a, M, n, size_t(bytes(n)), flags, st)
                       : launch_per_sm<T, 2>(a, M, n, size_t(bytes(n)), flags, st);
 }
