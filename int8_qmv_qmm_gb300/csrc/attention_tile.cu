@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
       ptx::tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
       ptx::tmem_wait_ld();
-      if (first < at_token + kBlock - 1) {
-        const int seen = pos - at_token;  // token i is seen where i <= seen
+      if (first < at_token + kBlock - 1 || ks.x < 0.f) {
+        // token i is seen where i <= seen (none of a block without a page)
+        const int seen = ks.x < 0.f ? -1 : pos - at_token;
 #pragma unroll
         for (int i = 0; i < 64; ++i)
           if (i > seen) v[i] = 0xff800000u;  // -infinity
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sx = __shfl_sync(0xffffffffu, my_scales.x, j - looked2);
         const float sy = __shfl_sync(0xffffffffu, my_scales.y, j - looked2);
         const bool good = __shfl_sync(0xffffffffu, int(my_good), j - looked2);
-        if (i0 == 0) scales[st] = make_float2(sx, sy);
+        if (i0 == 0) scales[st] = make_float2(good ? sx : -1.f, sy);
         const int s = j % kRaw;
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(raw_full(s), (j / kRaw) & 1));
         const uint8_t* raw = smem + L::kRawAt + s * L::kCodes;

@@ -1,11 +1,14 @@
 """The decoder's calls as they are used together: overlapping one another, over many
 slots, shared pages and used workspaces, and sampling of many unlike rows."""
 
+import numpy as np
 import pytest
 import torch
 
 import int8_qmv_qmm_gb300 as q
-from tests.test_gpu_decoder import BF16, F16, F32, Model, dev, normal, table_for  # noqa: F401
+from oracle import decoder_oracle as O
+from tests.test_gpu_decoder import (BF16, F16, F32, TINY, U, Model, dev, f64, normal,  # noqa: F401
+                                    table_for)
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +169,30 @@ def test_calls_without_rows(dev):  # noqa: F811
                for x, y in zip(before, (m.cache.pages, m.cache.tail)))
     m.check()
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 5, 100])
+def test_a_block_without_a_page_is_left_out(dev, new):  # noqa: F811
+    """As if its tokens were not there, in both kernels."""
+    heads, kvh, d, held = 4, 2, 64, 250
+    group = heads // kvh
+    m = Model(dev, 1, kvh, d, F16, blocks=8)
+    m.append([held], heads, None, seed=1)
+    m.append([new], heads, None, seed=2, advance=False)
+    m.cache.table[0, 1] = m.cache.pages.shape[0]
+    x = (normal(3, new, heads, d) * 1.5).to(F16).to(dev)
+    out = f64(q.cache_attention(x, m.cache, m.starts([new]), new, q.attention_workspace(d, dev)))
+    assert q.device_status() == 2 << 24
+    there = np.r_[0:64, 128:held + new]
+    for h in range(kvh):
+        k, v = (t[there] for t in m.values(0, h))
+        for i in sorted({0, new // 2, new - 1}):
+            for g in range(h * group, (h + 1) * group):
+                ref, size, total, most = O.attention(f64(x)[i, g], k, v, held + i - 64, d ** -0.5)
+                # the bound of Model.attend
+                seen = held + i - 63
+                e = (d + 8) * 2.0 ** -23 * (most + 1)
+                bound = size * (2.0 ** -11 + 2 * e + (seen / 16 + 8) * 2.0 ** -22)
+                bound += seen * 2.0 ** -25 * np.abs(v).max() / total
+                bound += U[F16] * np.abs(ref) + TINY[F16]
+                assert (np.abs(out[i, g] - ref) <= bound).all(), (h, i, g)
