@@ -412,31 +412,46 @@ __global__ void rope_table_kernel(float* table, int64_t n, int pairs, double bas
 }
 
 // --------------------------------------------------------------- reconstruction
+// 8192 codes of a page a CTA (a page has a multiple of them), eight at a time a thread,
+// so that a warp's stores run on without gaps: 103 pages of 8 heads of 128 (13.5 MB to
+// 27) in 8.6 us (16 at a time, in two stores apart: 10.3).
+constexpr int kDequantThreads = 256, kDequantCodes = 8192;
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kDequantThreads)
     cache_dequant_kernel(const qlin_kv_cache c, const int32_t* __restrict__ ids, T* out) {
+  constexpr int kTurns = kDequantCodes / (8 * kDequantThreads);
   const int64_t per_page = int64_t(c.kv_heads) * 2 * kBlock * c.head_dim;
   const int64_t page = ids[blockIdx.y];
   const bool good = page >= 0 && page < c.n_pages;
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) report(kStatusPage);
-  const int64_t i = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * 16;
-  if (i >= per_page) return;
-  T* dst = out + blockIdx.y * per_page + i;
-  Vec8 v[2] = {};
-  if (good) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.pages) +
-                                                    page * per_page + i);
-    const float s = c.scales[page * c.kv_heads * 2 + i / (kBlock * c.head_dim)];
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  const int64_t at = int64_t(blockIdx.x) * kDequantCodes + threadIdx.x * 8;
+  T* dst = out + blockIdx.y * per_page + at;
+  uint2 w[kTurns];
+  float s[kTurns];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t pair = words[e / 2] >> (16 * (e % 2));
-      v[e / 4].w[e % 4] = pack<T>(make_float2((float(pair & 0xffu) - 128.f) * s,
-                                              (float(pair >> 8 & 0xffu) - 128.f) * s));
+  for (int i = 0; i < kTurns; ++i) {
+    const int64_t j = at + i * 8 * kDequantThreads;
+    w[i] = make_uint2(0, 0);
+    s[i] = 0.f;
+    if (good) {
+      w[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.pages) +
+                                             page * per_page + j);
+      s[i] = c.scales[page * c.kv_heads * 2 + j / (kBlock * c.head_dim)];
     }
   }
-  store8(dst, v[0]);
-  store8(dst + 8, v[1]);
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    Vec8 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t pair = (e < 2 ? w[i].x : w[i].y) >> (16 * (e % 2));
+      v.w[e] = pack<T>(make_float2((float(pair & 0xffu) - 128.f) * s[i],
+                                   (float(pair >> 8 & 0xffu) - 128.f) * s[i]));
+    }
+    if (!good) v = Vec8{};
+    store8(dst + i * 8 * kDequantThreads, v);
+  }
 }
 
 template <typename T, int D>
@@ -487,14 +502,15 @@ qlin_status launch_cache_dequant(const qlin_kv_cache& c, const int32_t* page_ids
   const int64_t per_page = int64_t(c.kv_heads) * 2 * kBlock * c.head_dim;
   const int64_t elem = 2;
   for (int64_t at = 0; at < n; at += 32768) {  // the grid's second axis ends at 65535
-    const dim3 grid(unsigned((per_page / 16 + 255) / 256),
+    const dim3 grid(unsigned(per_page / kDequantCodes),
                     unsigned(n - at < 32768 ? n - at : 32768));
     void* dst = static_cast<uint8_t*>(out) + at * per_page * elem;
     if (c.dtype == QLIN_F16)
-      cache_dequant_kernel<<<grid, 256, 0, st>>>(c, page_ids + at, static_cast<__half*>(dst));
+      cache_dequant_kernel<<<grid, kDequantThreads, 0, st>>>(c, page_ids + at,
+                                                             static_cast<__half*>(dst));
     else
-      cache_dequant_kernel<<<grid, 256, 0, st>>>(c, page_ids + at,
-                                                 static_cast<__nv_bfloat16*>(dst));
+      cache_dequant_kernel<<<grid, kDequantThreads, 0, st>>>(c, page_ids + at,
+                                                             static_cast<__nv_bfloat16*>(dst));
   }
   return check_launch("qlin_cache_dequant");
 }
