@@ -94,10 +94,11 @@ class Decoder:
                 r = y.float()
                 h, _ = add_rms_norm(y, layer["norm1"])
             else:
-                h, _ = add_rms_norm(y, layer["norm1"], r, residual_out=r)
+                h, _ = add_rms_norm(y, layer["norm1"], r, residual_out=r, overlap_previous=True)
             q = rope_append(self._linear(h, layer["qkv"]), self.rope, layer["cache"], starts,
-                            self.q_heads)
-            a = cache_attention(q, layer["cache"], starts, max_new, self.workspace)
+                            self.q_heads, overlap_previous=True)
+            a = cache_attention(q, layer["cache"], starts, max_new, self.workspace,
+                                overlap_previous=True)
             y = self._linear(a.view(len(tokens), -1), layer["o"])
             h, _ = add_rms_norm(y, layer["norm2"], r, residual_out=r, overlap_previous=True)
             gate_up = self._linear(h, layer["gate_up"])
