@@ -878,9 +878,9 @@ qlin_status launch_t(Params a, int64_t M, unsigned flags, cudaStream_t st) {
   const int64_t header = (sizeof(Shared) + 15) / 16 * 16;
   auto bytes = [&](int r) { return header + ((a.V + r - 1) / r + 7) / 8 * 8 * int64_t(sizeof(T)); };
   // CTAs that share a row: enough to fill the SMs twice, with 4096 elements or
-  // more each; and below 16384 each, where weights take two atomics for three (96
-  // rows of 128256 by 8 CTAs each 110 us, by 4 109: what is saved in exchanges goes
-  // into the third)
+  // more each; and below 16384 each, where weights take two atomics for three.  (Rows
+  // of 128256, by this rule, by one that fills the SMs once, and by one that keeps to
+  // one CTA an SM, us: 32 rows 70, 70, 99; 64 rows 89, 111, 169; 256 rows 281, 310, 310.)
   const int sms = sm_count();
   int n = 1;
   while (n < kMaxCluster && ((a.V + n - 1) / n + 7 >= 16384 || (M * n < 2 * sms && a.V > 4096 * 2 * n)))
