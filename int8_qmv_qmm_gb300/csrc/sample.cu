@@ -752,6 +752,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) sample_kernel(const Params a
   const int base = row.rank * a.part, n = max(0, min(a.part, a.V - base));
   row.view.base = base;
   row.view.n = n;
+  // a peer's shared memory may be written to once the peer is known to have started;
+  // the wait stands before the first exchange, behind the row's loads
+  ptx::cluster_arrive_relaxed();
   grid_launch_dependents();
   grid_dependency_wait();
   // (one row for each cluster that fits: no order is better than another)
@@ -800,6 +803,7 @@ __global__ void __launch_bounds__(kThreads, PER_SM) sample_kernel(const Params a
   if ((threadIdx.x & 31) == 0) s.warp_sum[threadIdx.x >> 5] = best;
   __syncthreads();
   for (int i = 0; i < kWarps; ++i) best = s.warp_sum[i] > best ? s.warp_sum[i] : best;
+  ptx::cluster_wait();  // every CTA of the cluster has started
   const u64* all = row.exchange(best);
   for (int i = 0; i < row.ranks; ++i) best = all[i] > best ? all[i] : best;
   const int first = int(~uint32_t(best));

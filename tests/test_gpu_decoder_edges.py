@@ -1,0 +1,23 @@
+"""GPU parity of the calls between a decoder's linears where their work splits unevenly
+or their values are far apart, infinite or NaN, against the float64 oracle."""
+
+import pytest
+import torch
+
+import int8_qmv_qmm_gb300 as q
+from tests.test_gpu_decoder import (F16, F32, check_sample, dev, normal,  # noqa: F401
+                                    settings)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ sampling
+@pytest.mark.parametrize("v", [8200, 16392, 33000])
+def test_sample_small_parts_of_a_row(dev, v):  # noqa: F811
+    """Clusters of 2, 4 and 8 CTAs whose first exchange comes soon after their start:
+    the same token every time, and the oracle's."""
+    row = (2.5 * normal(v, v)).to(F32)
+    check_sample(dev, row, m=8, p=0.9)
+    x, u = row.to(dev).view(1, v), torch.tensor([0.37], device=dev)
+    got = [q.sample(x, u, *settings(dev, 1, p=0.9)) for _ in range(300)]
+    assert len({(t.item(), p.item()) for t, p in got}) == 1
