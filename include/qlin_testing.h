@@ -43,6 +43,17 @@ qlin_status qlin_testing_qmv_chain_stalled(const void* x0, const qlin_link* link
  */
 int qlin_testing_qmv_split(int64_t N, int64_t K, int bits, int sm_count);
 
+/*
+ * How qlin_sample cuts each of M rows of V logits on a device with `sm_count`
+ * SMs: *ranks CTAs (a thread-block cluster) share a row, each takes *part
+ * consecutive elements (the last ones what is left of them), and all sum
+ * weights in limbs of *limb_bits bits.  Host logic only; touches no device.
+ * Returns QLIN_ERR_INVALID_ARG for M < 1, V outside 1 .. 262144, sm_count < 1
+ * or a null pointer.
+ */
+qlin_status qlin_testing_sample_plan(int64_t M, int64_t V, int sm_count, int* ranks, int* part,
+                                     int* limb_bits);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,6 +81,8 @@ _SIGNATURES = {
                                                 _c_vp, ctypes.c_size_t, _c_int, ctypes.c_uint,
                                                 _c_vp]),
     "qlin_testing_qmv_split": (_c_int, [_c_i64, _c_i64, _c_int, _c_int]),
+    "qlin_testing_sample_plan": (_c_int, [_c_i64, _c_i64, _c_int]
+                                 + [ctypes.POINTER(_c_int)] * 3),
 }
 
 _LIB = None

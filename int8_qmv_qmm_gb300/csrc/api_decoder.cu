@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "qlin_internal.h"
+#include "qlin_testing.h"
 
 namespace qlin {
 namespace {
@@ -217,6 +218,19 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
     return fail(QLIN_ERR_MISALIGNED, "%s: a pointer is not aligned to its elements", name);
   return launch_sample(logits, logits_stride, u, temperature, top_k, top_p, min_p, tokens, probs,
                        M, V, ldtype, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_testing_sample_plan(int64_t M, int64_t V, int sm_count, int* ranks, int* part,
+                                     int* limb_bits) {
+  clear_error();
+  if (M < 1 || V < 1 || V > 262144 || sm_count < 1 || !ranks || !part || !limb_bits)
+    return fail(QLIN_ERR_INVALID_ARG, "qlin_testing_sample_plan: M=%lld V=%lld sm_count=%d",
+                (long long)M, (long long)V, sm_count);
+  const SamplePlan p = sample_plan(M, V, sm_count);
+  *ranks = p.ranks;
+  *part = p.part;
+  *limb_bits = p.limb;
+  return QLIN_OK;
 }
 
 }  // extern "C"

@@ -86,6 +86,12 @@ qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
                                    const qlin_kv_cache& c, const int32_t* starts,
                                    int64_t n_tokens, int q_heads, float scale, int max_new,
                                    void* workspace, unsigned flags, cudaStream_t st);
+// How a row of V logits, of M, is cut: CTAs that share it, elements of each one's
+// part, and bits of the limbs that its weights are summed in.
+struct SamplePlan {
+  int ranks, part, limb;
+};
+SamplePlan sample_plan(int64_t M, int64_t V, int sms);
 qlin_status launch_sample(const void* logits, int64_t logits_stride, const float* u,
                           const float* temperature, const int32_t* top_k, const float* top_p,
                           const float* min_p, int32_t* tokens, float* probs, int64_t M,

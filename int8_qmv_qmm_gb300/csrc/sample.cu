@@ -92,6 +92,7 @@ struct Params {
   int32_t* tokens;
   float* probs;
   int V, part;  // elements of a row, and of a CTA's part
+  int limb;     // bits of the weights' limbs in a histogram
 };
 
 struct Shared {
@@ -187,6 +188,7 @@ struct Row {
   Shared& s;
   View<T> view;
   int rank, ranks;
+  int limb;  // of every CTA of the cluster: they read each other's histograms
   float my_top;  // this thread's largest
   float u, min_p, below;
   int first_of_all;  // of the order
@@ -407,8 +409,7 @@ struct Row {
                                              double* mass, const Digits& digits) {
     const View<T>& r = view;
     const int n = r.n;
-    // limbs whose sums over a part stay below 2^32
-    const int limb = n < 16384 ? 18 : 12, arrays = by_count ? 1 : n < 16384 ? 2 : 3;
+    const int arrays = by_count ? 1 : limb == 18 ? 2 : 3;
     const int count = what == kDigits ? 1 << digits.bits : kBins;
     for (int i = threadIdx.x; i < count; i += kThreads)
       for (int a = 0; a < arrays; ++a) s.hist[a][i] = 0;
@@ -749,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, PER_SM) sample_kernel(const Params a
   row.view.x = x;
   row.rank = ptx::cluster_ctarank();
   row.ranks = gridDim.x;
+  row.limb = a.limb;
   const int base = row.rank * a.part, n = max(0, min(a.part, a.V - base));
   row.view.base = base;
   row.view.n = n;
@@ -879,25 +881,34 @@ qlin_status launch_per_sm(const Params& a, int64_t M, int n, size_t bytes, unsig
 
 template <typename T>
 qlin_status launch_t(Params a, int64_t M, unsigned flags, cudaStream_t st) {
-  const int64_t header = (sizeof(Shared) + 15) / 16 * 16;
-  auto bytes = [&](int r) { return header + ((a.V + r - 1) / r + 7) / 8 * 8 * int64_t(sizeof(T)); };
+  const int sms = sm_count();
+  const SamplePlan p = sample_plan(M, a.V, sms);
+  a.part = p.part;
+  a.limb = p.limb;
+  const size_t bytes = (sizeof(Shared) + 15) / 16 * 16 + size_t(p.part) * sizeof(T);
+  // Where the clusters do not fill the SMs, all registers for one CTA (one row of
+  // 128256: 19.4 us, 22.5 with room for two); else room for two (96 rows, in their
+  // own order: 128 us, 194 with one).
+  return M * p.ranks <= sms ? launch_per_sm<T, 1>(a, M, p.ranks, bytes, flags, st)
+                            : launch_per_sm<T, 2>(a, M, p.ranks, bytes, flags, st);
+}
+
+}  // namespace
+
+SamplePlan sample_plan(int64_t M, int64_t V, int sms) {
   // CTAs that share a row: enough to fill the SMs twice, with 4096 elements or
   // more each; and below 16384 each, where weights take two atomics for three.  (Rows
   // of 128256, by this rule, by one that fills the SMs once, and by one that keeps to
   // one CTA an SM, us: 32 rows 70, 70, 99; 64 rows 89, 111, 169; 256 rows 281, 310, 310.)
-  const int sms = sm_count();
-  int n = 1;
-  while (n < kMaxCluster && ((a.V + n - 1) / n + 7 >= 16384 || (M * n < 2 * sms && a.V > 4096 * 2 * n)))
+  int64_t n = 1;
+  while (n < kMaxCluster &&
+         ((V + n - 1) / n + 7 >= 16384 || (M * n < 2 * sms && V > 4096 * 2 * n)))
     n *= 2;
-  a.part = ((a.V + n - 1) / n + 7) / 8 * 8;
-  // Where the clusters do not fill the SMs, all registers for one CTA (one row of
-  // 128256: 19.4 us, 22.5 with room for two); else room for two (96 rows, in their
-  // own order: 128 us, 194 with one).
-  return M * n <= sms ? launch_per_sm<T, 1>(a, M, n, size_t(bytes(n)), flags, st)
-                      : launch_per_sm<T, 2>(a, M, n, size_t(bytes(n)), flags, st);
+  const int part = int(((V + n - 1) / n + 7) / 8 * 8);
+  // Limbs whose sums over a part stay below 2^32.  It goes by the part's size, which
+  // the row's CTAs have in common, not by how much of it the row fills.
+  return SamplePlan{int(n), part, part < 16384 ? 18 : 12};
 }
-
-}  // namespace
 
 qlin_status launch_sample(const void* logits, int64_t logits_stride, const float* u,
                           const float* temperature, const int32_t* top_k, const float* top_p,
@@ -905,7 +916,7 @@ qlin_status launch_sample(const void* logits, int64_t logits_stride, const float
                           int64_t V, qlin_dtype ldtype, unsigned flags, cudaStream_t st) {
   static_assert(kMaxVocab / kMaxCluster * 4 + sizeof(Shared) + 16 <= 200 * 1024, "a row fits");
   const Params a = {logits, logits_stride, u,      temperature, top_k, top_p,
-                    min_p,  tokens,        probs,  int(V),      0};
+                    min_p,  tokens,        probs,  int(V),      0,     0};
   switch (ldtype) {
     case QLIN_F16: return launch_t<__half>(a, M, flags, st);
     case QLIN_BF16: return launch_t<__nv_bfloat16>(a, M, flags, st);

@@ -21,3 +21,14 @@ def test_sample_small_parts_of_a_row(dev, v):  # noqa: F811
     x, u = row.to(dev).view(1, v), torch.tensor([0.37], device=dev)
     got = [q.sample(x, u, *settings(dev, 1, p=0.9)) for _ in range(300)]
     assert len({(t.item(), p.item()) for t, p in got}) == 1
+
+
+@pytest.mark.parametrize("dt", [F32, F16])
+@pytest.mark.parametrize("v", [131009, 131071, 131073, 131463, 131464])
+def test_sample_where_the_last_part_is_short(dev, v, dt):  # noqa: F811
+    """Eight CTAs share a row, the last with fewer than 16384 logits, the others with
+    16384 or more: a bound by weight, alone and after top-k."""
+    row = (3.0 * normal(v, v)).to(dt)
+    for kw in (dict(p=0.9), dict(p=0.3, tau=2.0), dict(k=v // 2, p=0.95), dict(p=0.7, mp=0.01),
+               dict(k=50, p=0.9), dict(p=0.999, tau=0.5)):
+        check_sample(dev, row, m=16, **kw)
