@@ -470,7 +470,8 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
  * kernel), or of what the cache kernels refused on the device (bit 24: rows
  * outside n_tokens or a negative length, 25: a page outside n_pages or a slot
  * past max_blocks, 26: a position outside the table, 27: a slot with more than
- * max_new rows, 28: a wait of the attention kernel that gave up).  Returns QLIN_OK, or
+ * max_new rows, 28: a wait of the attention kernel that gave up), or in sampling
+ * (bit 29: a bound that no bin passed was left out).  Returns QLIN_OK, or
  * QLIN_ERR_CUDA if the device could not be read.  No counterpart on the pages:
  * an addition of this library (a kernel that gives up a wait reports instead
  * of hanging, the device-side form of failing fast).

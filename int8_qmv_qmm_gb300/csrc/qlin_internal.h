@@ -103,6 +103,7 @@ cudaError_t qmv_take_device_status(unsigned* flags);
 cudaError_t chain_take_device_status(unsigned* flags);
 cudaError_t rope_take_device_status(unsigned* flags);
 cudaError_t attention_take_device_status(unsigned* flags);
+cudaError_t sample_take_device_status(unsigned* flags);
 
 constexpr int kGroup = 64;
 

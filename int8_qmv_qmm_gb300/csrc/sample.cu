@@ -25,6 +25,9 @@
 #include "sm100_ptx.cuh"
 
 namespace qlin {
+
+__device__ unsigned int g_sample_status = 0;  // 1: a bound that no bin passes
+
 namespace {
 
 constexpr int kThreads = 512;
@@ -586,12 +589,18 @@ struct Row {
     // down to some distances, in registers, tell the band in which the bound lies,
     // and only its elements go through the histogram's atomics.
     What what = by_count && k <= u64(ranks * kThreads / 8) ? kTops : kBands;
-    bool banded = !by_count, list = true;
-    if (banded) mass = fmax(double(p) * double(band(p)), 0.5);
+    bool all_bins = by_count, list = true;
+    if (!by_count) mass = fmax(double(p) * double(band(p)), 0.5);
     Digits digits = {0, 0, 21, 11, false};
     Cross c = {-1, 0, 0};
     while (true) {
       const Cross d = histogram(what, by_count, what == kDigits ? c.above : 0, k, p, &mass, digits);
+      // (the sums are exact, so that over all bins, and over a bin's digits, one passes
+      // the bound; if none did, the bound would be left out, not looked for again)
+      if (d.bin < 0 && (what == kDigits || (what == kBands && all_bins))) {
+        if (rank == 0 && threadIdx.x == 0) atomicOr(&g_sample_status, 1u);
+        return kOne;
+      }
       if (what == kDigits) {
         // too many for the list: digit by digit, of the elements of the bin
         digits.prefix =
@@ -607,6 +616,7 @@ struct Row {
       c = d;
       if (c.bin < 0) {  // fewer threads have elements than k; or the band, which goes by
         what = kBands;  // rounded sums, was not the one
+        all_bins = true;
         view.all_bins();
         continue;
       }
@@ -922,6 +932,16 @@ qlin_status launch_sample(const void* logits, int64_t logits_stride, const float
     case QLIN_BF16: return launch_t<__nv_bfloat16>(a, M, flags, st);
     default: return launch_t<float>(a, M, flags, st);
   }
+}
+
+cudaError_t sample_take_device_status(unsigned* flags) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_sample_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  e = cudaMemcpyToSymbol(g_sample_status, &zero, sizeof(zero));
+  *flags = v;
+  return e;
 }
 
 }  // namespace qlin
