@@ -399,11 +399,12 @@ struct Warp {
 };
 
 // Launchers of the two kernels (attention_split.cu, attention_tile.cu), and the
-// status words that they set.
+// status words that they set.  The split kernel's parts are joined by its own launch
+// (`join`) or by the tile kernel's, with its pieces.
 size_t split_workspace_size(int head_dim);
-void launch_split(const Args& a, void* workspace, unsigned flags, cudaStream_t st);
+void launch_split(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st);
 size_t tile_workspace_size(int head_dim);
-void launch_tile(const Args& a, void* workspace, cudaStream_t st);
+void launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st);
 cudaError_t split_take_status(unsigned* flags);
 cudaError_t tile_take_status(unsigned* flags);
 

@@ -18,9 +18,7 @@
 // its part in the workspace, and a second kernel, launched while the first still
 // runs, joins the parts in the list's order.
 
-#include <algorithm>
-
-#include "attention_core.cuh"
+#include "attention_join.cuh"
 #include "attention_ptx.cuh"
 
 namespace qlin {
@@ -30,16 +28,11 @@ __device__ unsigned int g_split_status = 0;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = kSplitWarps * 32;
 constexpr int kRingBytes = 24576;             // of a warp: 6 chunks at D = 64, 3 at 128
 constexpr int kInfo = 8;                      // blocks that the copies may run ahead
-constexpr int kRows = 8;
 constexpr int kMaxSlots = 1024;
 constexpr int kTailCost = 4;                  // of a tail, in blocks
-constexpr int kJoinThreads = 512;
-constexpr int kJoinPerSm = 2;
-constexpr int kMaxWarps = 2048;               // of the split kernel's grid
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_split_status, bit); }
 
@@ -55,26 +48,15 @@ struct Slot {  // blocks that the list has before it, its tokens with the new on
   int list, total, row0, n;
 };
 
-// A tile whose blocks begin in warp i's share and pass its end: warps i .. last
-// have parts.
-struct alignas(16) Split {
-  int last;      // -1: warp i has none
-  int token0;    // first row of the slot in q and out
-  int row0;      // of the tile in the slot
-  int kvh_here;  // 16 * key/value head + rows of the tile
-};
-
 template <int D>
 struct Layout {
   static constexpr int kChunk = kBlock * D;          // bytes of a block's keys or values
   static constexpr int kRing = kRingBytes / kChunk;  // chunks in a warp's ring
-  static constexpr int kInfoAt = kWarps * kRingBytes;
-  static constexpr int kBarAt = kInfoAt + kWarps * kInfo * int(sizeof(Info));
-  static constexpr int kScanAt = (kBarAt + kWarps * kRing * 8 + 15) / 16 * 16;
-  static constexpr int kListAt = kScanAt + kWarps * 8;
+  static constexpr int kInfoAt = kSplitWarps * kRingBytes;
+  static constexpr int kBarAt = kInfoAt + kSplitWarps * kInfo * int(sizeof(Info));
+  static constexpr int kScanAt = (kBarAt + kSplitWarps * kRing * 8 + 15) / 16 * 16;
+  static constexpr int kListAt = kScanAt + kSplitWarps * 8;
   static int bytes(int slots) { return kListAt + slots * int(sizeof(Slot)); }
-  // a part in the workspace: sums [D][8 rows], then the rows' m and l
-  static constexpr int kPart = kRows * (D + 2);  // floats
 };
 
 // Places of a slot in the list: its blocks, a tail counting for kTailCost of them
@@ -114,12 +96,12 @@ __device__ __forceinline__ Piece piece_at(const Slot* s_slot, int slots, int gro
   const Slot sl = s_slot[lo];
   const int rows = sl.n * group;
   const unsigned n = places_of(sl.total), tile = (x - sl.list) / n;
-  const unsigned row_tiles = unsigned(rows + kRows - 1) / kRows;
+  const unsigned row_tiles = unsigned(rows + kSplitTile - 1) / kSplitTile;
   Piece p;
   p.slot = lo;
   p.kvh = int(tile / row_tiles);
-  p.row0 = int(tile % row_tiles) * kRows;
-  p.here = min(kRows, rows - p.row0);
+  p.row0 = int(tile % row_tiles) * kSplitTile;
+  p.here = min(kSplitTile, rows - p.row0);
   p.first = sl.list + tile * n;
   p.last = p.first + n;
   return p;
@@ -141,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
   }
   grid_dependency_wait();
-  grid_launch_dependents();  // (after the wait: cache_attention.cu says why)
+  grid_launch_dependents();
 
   // the list: blocks before each slot
   int64_t all_blocks = 0;
@@ -159,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t rows = int64_t(r.n) * a.group;
       over |= r.n > a.max_new;
       if (rows <= kSplitRows && r.n <= a.max_new)
-        here = (rows + kRows - 1) / kRows * a.c.kv_heads * places_of(r.held + r.n);
+        here = (rows + kSplitTile - 1) / kSplitTile * a.c.kv_heads * places_of(r.held + r.n);
     }
     int64_t upto = here;
     for (int d = 1; d < 32; d <<= 1) {
@@ -170,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) s_scan[warp] = upto;
     __syncthreads();
     int64_t before = all_blocks;
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kSplitWarps; ++i) {
       if (i < warp) before += s_scan[i];
       all_blocks += s_scan[i];
     }
@@ -197,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const unsigned blocks = unsigned(all_blocks);
   if (me >= blocks) return;
-  const Shares shares(blocks, min(gridDim.x * kWarps, blocks));
+  const Shares shares(blocks, min(gridDim.x * kSplitWarps, blocks));
   const unsigned end = shares.start(me + 1);
 
   // ---- the copies
@@ -296,16 +278,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g < p.here) *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 * h) = v;
           }
       } else {
-        float* part = parts + size_t(2 * me + (x_piece == p.first ? 1 : 0)) * L::kPart;
+        float* part = parts + size_t(2 * me + (x_piece == p.first ? 1 : 0)) * kSplitPart<D>;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(part + (16 * c + 8 * h + g) * kRows + 2 * t) =
+            *reinterpret_cast<float2*>(part + (16 * c + 8 * h + g) * kSplitTile + 2 * t) =
                 make_float2(w.o[c][2 * h] * w.unit, w.o[c][2 * h + 1] * w.unit);
         if (g == 0) {
-          *reinterpret_cast<float2*>(part + kRows * D + 2 * t) = make_float2(w.m[0], w.m[1]);
-          *reinterpret_cast<float2*>(part + kRows * (D + 1) + 2 * t) = make_float2(l[0], l[1]);
+          *reinterpret_cast<float2*>(part + kSplitTile * D + 2 * t) = make_float2(w.m[0], w.m[1]);
+          *reinterpret_cast<float2*>(part + kSplitTile * (D + 1) + 2 * t) = make_float2(l[0], l[1]);
         }
         if (x_piece == p.first)
           split = Split{int(shares.of(p.last - 1)), sl.row0, p.row0,
@@ -362,120 +344,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 0 && split.last >= 0) splits[me] = split;
 }
 
-// Joins the parts of the tiles that pass the end of a warp's share.  Each CTA
-// lists them (the order is that of the warps).  A team of warps takes a slice, 16
-// dimensions of a tile's 8 rows: its warps (4 rows of one dimension a thread) take
-// a part each in turn, and are added up in order.  Teams are a whole CTA where the
-// slices are no more than the CTAs (few, long lists of parts), else four warps.
-// (Whole CTAs alone: 52.8 us for 32 sequences of 8192 tokens with the split kernel,
-// 32.8 for 36 rows of 3000; with both sizes 49.2 and 29.4.  A warp for each slice of
-// up to 8 parts: 49.7 and 33.2, but 16 sequences of mixed lengths 62 for 59.)
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const float* parts,
-                                                            const Split* splits, int warps) {
-  using L = Layout<D>;
-  constexpr int kSlices = D / 16, kGroups = kJoinThreads / 32;
-  constexpr int kRounds = kMaxWarps / kJoinThreads;
-  __shared__ int s_which[kMaxWarps], s_count[kRounds][kGroups];
-  __shared__ float4 s_o[kGroups][32], s_m[kGroups][2], s_l[kGroups][2];
-  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const SplitScratch sc) {
   grid_launch_dependents();
   grid_dependency_wait();
-  unsigned ballot[kRounds];
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int w = i * kJoinThreads + threadIdx.x;
-    ballot[i] = w < warps && __ldcg(&splits[w].last) >= 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    ballot[i] = __ballot_sync(0xffffffffu, ballot[i]);
-    if (lane == 0) s_count[i][group] = __popc(ballot[i]);
-  }
-  __syncthreads();
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    int at = n;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      if (k < group) at += s_count[i][k];
-      n += s_count[i][k];
-    }
-    if (ballot[i] >> lane & 1)
-      s_which[at + __popc(ballot[i] & ((1u << lane) - 1))] = i * kJoinThreads + int(threadIdx.x);
-  }
-  __syncthreads();
-  const int size = n * kSlices <= int(gridDim.x) ? kGroups : 4, teams = kGroups / size;
-  const int team = group / size, g0 = team * size;  // and the team's first warp
-  auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * size) : "memory"); };
-  for (int task = blockIdx.x * teams + team; task < n * kSlices; task += gridDim.x * teams) {
-    const int first = s_which[task / kSlices], d0 = task % kSlices * 16;
-    const Split sp = splits[first];
-    // this thread: dimension d0 + lane/2, rows 4 * (lane%2) ..
-    const int d = d0 + (lane >> 1), half = lane & 1;
-    float m[4], l[4], o[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = o[r] = 0.f;
-#pragma unroll 4
-    for (int k = first + group - g0; k <= sp.last; k += size) {
-      const float* part = parts + size_t(2 * k + (k == first ? 1 : 0)) * L::kPart;
-      const float4 pm = __ldcg(reinterpret_cast<const float4*>(part + kRows * D) + half);
-      const float4 pl = __ldcg(reinterpret_cast<const float4*>(part + kRows * (D + 1)) + half);
-      const float4 po = __ldcg(reinterpret_cast<const float4*>(part + kRows * d) + half);
-      const float vm[4] = {pm.x, pm.y, pm.z, pm.w}, vl[4] = {pl.x, pl.y, pl.z, pl.w},
-                  vo[4] = {po.x, po.y, po.z, po.w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float next = fmaxf(m[r], vm[r]), base = next == -INFINITY ? 0.f : next;
-        const float f0 = exp2_fast(m[r] - base), f1 = exp2_fast(vm[r] - base);
-        l[r] = l[r] * f0 + vl[r] * f1;
-        o[r] = o[r] * f0 + vo[r] * f1;
-        m[r] = next;
-      }
-    }
-    s_o[group][lane] = make_float4(o[0], o[1], o[2], o[3]);
-    if (lane < 2) {
-      s_m[group][lane] = make_float4(m[0], m[1], m[2], m[3]);
-      s_l[group][lane] = make_float4(l[0], l[1], l[2], l[3]);
-    }
-    meet();
-    // 128 sums: thread i of the team takes row i/16, dimension d0 + i%16
-    const int i = threadIdx.x - 32 * g0, row = i >> 4, dd = i & 15, here = sp.kvh_here & 15;
-    if (row < here) {
-      auto value = [&](const float4* v) { return reinterpret_cast<const float*>(v)[row & 3]; };
-      float top = -INFINITY, sum = 0.f, out = 0.f;
-#pragma unroll 4
-      for (int k = g0; k < g0 + size; ++k) top = fmaxf(top, value(&s_m[k][row >> 2]));
-#pragma unroll 4
-      for (int k = g0; k < g0 + size; ++k) {
-        const float vm = value(&s_m[k][row >> 2]);
-        const float f = vm == -INFINITY ? 0.f : exp2_fast(vm - top);
-        sum += value(&s_l[k][row >> 2]) * f;
-        out += value(&s_o[k][2 * dd + (row >> 2)]) * f;
-      }
-      const int rr = sp.row0 + row, kvh = sp.kvh_here >> 4;
-      static_cast<T*>(a.out)[(int64_t(sp.token0 + rr / a.group) * a.q_heads + kvh * a.group +
-                              rr % a.group) *
-                                 D +
-                             d0 + dd] = Act<T>::from_f32_rn(sum > 0.f ? out / sum : 0.f);
-    }
-    meet();
-  }
+  join_split<T, D>(a, sc, blockIdx.x, gridDim.x);
 }
 
 template <typename T, int D>
-void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
+void launch_t(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st) {
   using L = Layout<D>;
   static_assert(L::kListAt + kMaxSlots * int(sizeof(Slot)) <= 227 * 1024, "it fits");
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(split_kernel<T, D>), L::bytes(kMaxSlots), &done))
     return;
-  const int sms = std::min(sm_count(), kMaxWarps / kWarps), warps = sms * kWarps;
-  Split* splits = static_cast<Split*>(workspace);
-  float* parts = reinterpret_cast<float*>(splits + warps);
+  const SplitScratch sc = split_scratch(workspace, sm_count());
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(sms));
+  cfg.gridDim = dim3(unsigned(sc.warps / kSplitWarps));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = size_t(L::bytes(a.c.slots));
   cfg.stream = st;
@@ -484,30 +369,30 @@ void launch_t(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, parts, splits);
-  cfg.gridDim = dim3(unsigned(sms * kJoinPerSm));
+  cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, sc.parts, sc.splits);
+  if (!join) return;
+  cfg.gridDim = dim3(unsigned(sm_count() * kSplitJoinPerSm));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts),
-                     static_cast<const Split*>(splits), warps);
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, sc);
 }
 
 }  // namespace
 
 size_t split_workspace_size(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
-  const size_t warps = size_t(sm_count()) * kWarps;
-  return warps * (sizeof(Split) + 2 * kRows * (head_dim + 2) * 4);
+  const size_t warps = size_t(split_scratch(nullptr, sm_count()).warps);
+  return warps * (sizeof(Split) + 2 * kSplitTile * (head_dim + 2) * 4);
 }
 
-void launch_split(const Args& a, void* workspace, unsigned flags, cudaStream_t st) {
+void launch_split(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st) {
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, flags, st)
-                       : launch_t<__half, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, join, flags, st)
+                       : launch_t<__half, 128>(a, workspace, join, flags, st);
   else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, flags, st)
-                       : launch_t<__nv_bfloat16, 128>(a, workspace, flags, st);
+    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, join, flags, st)
+                       : launch_t<__nv_bfloat16, 128>(a, workspace, join, flags, st);
 }
 
 cudaError_t split_take_status(unsigned* flags) {

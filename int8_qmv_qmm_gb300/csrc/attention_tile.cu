@@ -40,7 +40,7 @@
 // 163 us at the library's rate; a 128 x 64 x 16 product takes 49 to 55 cycles here,
 // not 32, and the widening, the exponentials and their hand-overs hide behind it.
 
-#include "attention_core.cuh"
+#include "attention_join.cuh"
 #include "attention_ptx.cuh"
 
 namespace qlin {
@@ -150,12 +150,6 @@ __device__ __forceinline__ void widen16(const uint4& w, uint4& lo, uint4& hi) {
 // Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, swizzled.
 __device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-// The kernel is through when the split kernel's are, so that what follows it is
-// behind all of the call: one CTA sees to that, at its end.
-__device__ __forceinline__ void last_wait() {
-  if (blockIdx.x == 0) grid_dependency_wait();
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const Args a, float* parts, int sms) {
@@ -199,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
-  // (what the call reads is there: cache_attention.cu)
   grid_launch_dependents();
+  grid_dependency_wait();
   if (warp == 0) {
     const Plan plan = plan_of(a, sms);
     const int id = blockIdx.x;
@@ -219,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const Work work = work_at(a, max(s_work[0], 0), s_work[1]);
   const int cuts = min(s_work[2], work.n), cut = s_work[3];
-  if (s_work[0] < 0 || cut >= cuts) {
-    last_wait();
-    return;
-  }
+  if (s_work[0] < 0 || cut >= cuts) return;
   if (warp == kSoftmaxWarps + kWidenWarps) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
@@ -612,18 +603,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + kWidenWarps) ptx::tmem_dealloc(tmem, 512);
-  last_wait();
 }
 
-// Joins the pieces, a warp for each row.
+// Joins the pieces, a warp for each row.  The CTA is `block` of `blocks`.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const Args a, const float* parts, int sms) {
-  const int lane = threadIdx.x & 31, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
-  grid_launch_dependents();
-  grid_dependency_wait();
+__device__ void join_pieces(const Args& a, const float* parts, int sms, int block, int blocks) {
+  constexpr int kWarps = kJoinThreads / 32;
+  const int lane = threadIdx.x & 31, warp = block * kWarps + (threadIdx.x >> 5);
   const Plan plan = plan_of(a, sms);
   if (plan.cuts == 1) return;
-  for (int64_t i = warp; i < int64_t(plan.pairs - plan.whole) * kCtaRows; i += gridDim.x * 8) {
+  for (int64_t i = warp; i < int64_t(plan.pairs - plan.whole) * kCtaRows; i += blocks * kWarps) {
     const int at = int(i / kCtaRows), row = int(i % kCtaRows);
     int slot = 0;
     int64_t place = 0;
@@ -662,8 +651,24 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, const float* pa
   }
 }
 
+// After both kernels, what both left: the pieces by the first kTileJoinPerSm * sms
+// CTAs, the split kernel's parts by the others.
+constexpr int kTileJoinPerSm = 1;
+
 template <typename T, int D>
-void launch_t(const Args& a, void* workspace, cudaStream_t st) {
+__global__ void __launch_bounds__(kJoinThreads)
+    join_kernel(const Args a, const float* parts, const SplitScratch sc, int sms) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int pieces = kTileJoinPerSm * sms;
+  if (int(blockIdx.x) < pieces)
+    join_pieces<T, D>(a, parts, sms, blockIdx.x, pieces);
+  else
+    join_split<T, D>(a, sc, blockIdx.x - pieces, gridDim.x - pieces);
+}
+
+template <typename T, int D>
+void launch_t(const Args& a, void* workspace, const SplitScratch& sc, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(tile_kernel<T, D>), Layout<D>::kBytes, &done))
     return;
@@ -682,10 +687,10 @@ void launch_t(const Args& a, void* workspace, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
-  cfg.gridDim = dim3(unsigned(2 * sms));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(unsigned((kTileJoinPerSm + kSplitJoinPerSm) * sms));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts), sms);
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts), sc, sms);
 }
 
 }  // namespace
@@ -694,13 +699,14 @@ size_t tile_workspace_size(int head_dim) {
   return head_dim == 64 || head_dim == 128 ? size_t(sm_count()) * kCtaRows * (head_dim + 2) * 4 : 0;
 }
 
-void launch_tile(const Args& a, void* workspace, cudaStream_t st) {
+void launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st) {
+  const SplitScratch sc = split_scratch(split_workspace, sm_count());
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, st)
-                       : launch_t<__half, 128>(a, workspace, st);
+    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, sc, st)
+                       : launch_t<__half, 128>(a, workspace, sc, st);
   else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, st)
-                       : launch_t<__nv_bfloat16, 128>(a, workspace, st);
+    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, sc, st)
+                       : launch_t<__nv_bfloat16, 128>(a, workspace, sc, st);
 }
 
 cudaError_t tile_take_status(unsigned* flags) {

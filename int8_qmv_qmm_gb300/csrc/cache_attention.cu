@@ -5,12 +5,9 @@
 //                      all SMs along its length
 //   more               attention_tile.cu: products of 128 rows
 // The host only knows the largest count (max_new), so with prompts among the
-// slots it launches both, each for its own.  They share neither outputs nor scratch,
-// and the tile kernel begins while the split kernel's parts are being joined (one
-// after the other, 16 sequences of mixed lengths took 59.6 us, now 54.9).  It does
-// not wait for them before it reads: that its launch was allowed says that every CTA
-// of the split kernel is past its own wait, and so that what came before the call is
-// done.
+// slots it launches both, each for its own, and then one kernel that joins what both
+// have left in parts.  Each starts while the one before it ends and waits for it
+// before it reads anything: only that wait makes what came before the call visible.
 
 #include "attention_core.cuh"
 
@@ -34,10 +31,12 @@ qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
                              q_heads / c.kv_heads,
                              scale * 1.4426950408889634f,
                              max_new};
-  attention::launch_split(a, workspace, flags, st);
-  if (int64_t(max_new) * a.group > attention::kSplitRows)
+  const bool tile = int64_t(max_new) * a.group > attention::kSplitRows;
+  attention::launch_split(a, workspace, !tile, flags, st);
+  if (tile)
     attention::launch_tile(
-        a, static_cast<uint8_t*>(workspace) + attention::split_workspace_size(c.head_dim), st);
+        a, static_cast<uint8_t*>(workspace) + attention::split_workspace_size(c.head_dim),
+        workspace, st);
   return check_launch("qlin_cache_attention");
 }
 
