@@ -5,8 +5,15 @@
 //
 // With k_j = s_k c_j and v_j = s_v c_j inside a block (c: whole numbers, -127 ..
 // 127, exact in 16-bit floating point), the scales leave the products:
-//   score = (scale * s_k) * (q . c_j)         out += s_v * sum_j p_j c_j
-// so both products run on codes, with float32 sums, and only p is rounded.
+//   score = (scale * s_k) * (q . c_j)         out += sum_j (s_v p_j) c_j
+// so both products run on codes, with float32 sums, and only s_v p is rounded (to
+// f16).  s_v goes into the exponent and into the running maximum,
+//   s_v p_j = exp2(score + log2 s_v - m),  m the largest score + log2 s_v so far
+// so that a rounding is 2^-11 of a token's own weight, or 2^-25 of the largest so
+// far, whatever the blocks' scales are: a block of large values that gets no
+// probability takes nothing from the others.  (With the values' scales relative to
+// the largest of them, blocks 2^26 apart lost the smaller one.)  The denominator
+// takes the weights back.
 #pragma once
 
 #include <cmath>
@@ -112,6 +119,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
+// The logarithm of a block's value scale, for the exponents; the denominator takes it
+// back by exp2(-it).  A block whose values are all zero has scale 0, and any weight will
+// do: its codes are zero too.  Scales below 2^-100 weigh as that (the sums of values
+// below 2^-93 are off by as much).
+__device__ __forceinline__ float weight_log2(float v_scale) {
+  return log2_fast(v_scale > 0.f ? fmaxf(v_scale, 0x1p-100f) : 0x1p-60f);
+}
+
 // One warp's attention of 8 rows over blocks of the cache.
 //
 // Tokens (scores) and dimensions (outputs) are the 16 rows of the products and
@@ -138,7 +153,6 @@ struct Warp {
   float o[kQk][4];
   float factor[2];  // scores to units of log2, without the key scale
   float m[2], l[2];  // of rows 2t + {0, 1}; l over this lane's tokens
-  float unit;        // o counts in units of this: the largest value scale so far
 
   __device__ void init() {
 #pragma unroll
@@ -147,7 +161,6 @@ struct Warp {
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    unit = 0.f;
   }
 
   // A query row's fragments, in T.
@@ -205,14 +218,14 @@ struct Warp {
 
   // Scores (times scale and the rows' factors) -> weighted probabilities, in
   // place, with the running maximum; the factors that the rows' sums so far take
-  // go to keep.  seen[r]: tokens of the block that row 2t + r sees.
-  // weight: what the probabilities are scaled by.
-  __device__ void softmax(float (&s)[4][4], const float (&scale)[2], float weight,
+  // go to keep.  shift: the logarithm of the block's weight.  seen[r]: tokens of the
+  // block that row 2t + r sees.
+  __device__ void softmax(float (&s)[4][4], const float (&scale)[2], float shift,
                           const int (&seen)[2], bool mask, int g, float (&keep)[2]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] *= scale[e & 1];
+      for (int e = 0; e < 4; ++e) s[i][e] = fmaf(s[i][e], scale[e & 1], shift);
     if (mask) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -221,7 +234,6 @@ struct Warp {
           if (16 * (g >> 1) + 4 * i + 2 * (e >> 1) + (g & 1) >= seen[e & 1])
             s[i][e] = -INFINITY;
     }
-    const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float top = fmaxf(s[0][r], s[0][2 + r]);
@@ -234,34 +246,24 @@ struct Warp {
       const float base = next == -INFINITY ? 0.f : next;  // a row that sees nothing yet
       keep[r] = exp2_fast(m[r] - base);
       m[r] = next;
-      const float from = base - shift;
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float p = exp2_fast(s[i][2 * h + r] - from);
+          const float p = exp2_fast(s[i][2 * h + r] - base);
           s[i][2 * h + r] = p;
           sum += p;
         }
-      l[r] = l[r] * keep[r] + sum * back;
+      l[r] = l[r] * keep[r] + sum * exp2_fast(-shift);
     }
   }
 
-  __device__ void rescale(const float (&keep)[2], float ratio) {
-    const float f[2] = {keep[0] * ratio, keep[1] * ratio};
+  __device__ void rescale(const float (&keep)[2]) {
 #pragma unroll
     for (int i = 0; i < kQk; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
-  }
-
-  // The factor from the old unit to the new, which is at least v.
-  __device__ float raise_unit(float v) {
-    const float next = fmaxf(unit, v);
-    const float ratio = next > unit ? __fdividef(unit, next) : next > 0.f ? 1.f : 0.f;
-    unit = next;
-    return ratio;
+      for (int e = 0; e < 4; ++e) o[i][e] *= keep[e & 1];
   }
 
   // The scores of a complete block's 64 keys, in units of its key scale.
@@ -291,14 +293,10 @@ struct Warp {
   // Scores -> the second product's operand.
   __device__ void probabilities(float (&s)[4][4], uint32_t (&b)[4][2], float k_scale,
                                 float v_scale, const int (&seen)[2], bool mask, int lane) {
-    const float ratio = raise_unit(v_scale);
-    // (a block whose values are all zero has scale 0: its codes are zero too; a
-    // weight below f16's range makes every probability zero in it)
-    const float weight = v_scale > 0.f ? fmaxf(__fdividef(v_scale, unit), 0x1p-60f) : 1.f;
     float keep[2], scale[2];
     scale[0] = factor[0] * k_scale, scale[1] = factor[1] * k_scale;
-    softmax(s, scale, weight, seen, mask, lane >> 2, keep);
-    rescale(keep, ratio);
+    softmax(s, scale, weight_log2(v_scale), seen, mask, lane >> 2, keep);
+    rescale(keep);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -349,12 +347,10 @@ struct Warp {
           mma<T>(s[i], a1, w[8 * p + 4 * h + 2], w[8 * p + 4 * h + 3]);
         }
     }
-    const float ratio = raise_unit(1.f);
     float keep[2], scale[2];
     scale[0] = scale[1] = scale_log2;
-    softmax(s, scale, 1.f, seen, true, g, keep);
-    rescale(keep, ratio);
-    const float weight = 1.f / unit;
+    softmax(s, scale, 0.f, seen, true, g, keep);
+    rescale(keep);
     // bf16 keeps only 8 bits of p, so what it leaves over goes through a second
     // product.
     constexpr bool kTwo = std::is_same<T, __nv_bfloat16>::value;
@@ -363,7 +359,7 @@ struct Warp {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float p0 = s[i][2 * h] * weight, p1 = s[i][2 * h + 1] * weight;
+        const float p0 = s[i][2 * h], p1 = s[i][2 * h + 1];
         const uint32_t v = pack2<T>(p0, p1);
         b[i][h] = transpose8(v);
         if (kTwo) rest[i][h] = transpose8(pack2<T>(p0 - low_f32(v), p1 - high_f32(v)));

@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Slot sl = s_slot[p.slot];
       if (x_piece == p.first && x == p.last) {
-        const float f0 = l[0] > 0.f ? w.unit / l[0] : 0.f;
-        const float f1 = l[1] > 0.f ? w.unit / l[1] : 0.f;
+        const float f0 = l[0] > 0.f ? 1.f / l[0] : 0.f;
+        const float f1 = l[1] > 0.f ? 1.f / l[1] : 0.f;
         const int row = p.row0 + g;
         T* dst = static_cast<T*>(a.out) +
                  (int64_t(sl.row0 + row / a.group) * a.q_heads + p.kvh * a.group +
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<float2*>(part + (16 * c + 8 * h + g) * kSplitTile + 2 * t) =
-                make_float2(w.o[c][2 * h] * w.unit, w.o[c][2 * h + 1] * w.unit);
+                make_float2(w.o[c][2 * h], w.o[c][2 * h + 1]);
         if (g == 0) {
           *reinterpret_cast<float2*>(part + kSplitTile * D + 2 * t) = make_float2(w.m[0], w.m[1]);
           *reinterpret_cast<float2*>(part + kSplitTile * (D + 1) + 2 * t) = make_float2(l[0], l[1]);

@@ -60,7 +60,6 @@ constexpr int kStages = 3;  // blocks of f16 operands
 constexpr int kRaw = 4;     // blocks of codes
 constexpr int kMaxCuts = 8;
 constexpr float kSlack = 8.f;        // log2 of how far a row's maximum may lag
-constexpr float kUnitSlack = 64.f;   // how far a value scale may be above the unit
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_tile_status, bit); }
 
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(q_full(tile));
     }
     const int first = r.held + (row0 + tile * kTileRows) / a.group;  // of the tile: all see up to it
-    float m = -INFINITY, l = 0.f, unit = 0.f;
+    float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int st = j % kStages, at_token = (j0 + j) * kBlock;
@@ -288,15 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 ks = scales[st];
       // (never zero: a score of -infinity has to stay one)
       const float scale = fmaxf(factor * ks.x, 1e-30f);
-      // O counts in units of `unit`; a block's values in units of ks.y
-      float keep = 1.f;
-      if (ks.y > unit * kUnitSlack || (unit == 0.f && ks.y > 0.f)) {  // the same for every row
-        keep = unit > 0.f ? __fdividef(unit, ks.y) : 1.f;
-        unit = ks.y;
-      }
-      // (a block of zero values has scale 0; a weight below f16's range is none)
-      const float weight = ks.y > 0.f ? fmaxf(__fdividef(ks.y, unit), 0x1p-60f) : 1.f;
-      const float shift = log2_fast(weight), back = __fdividef(1.f, weight);
+      const float shift = weight_log2(ks.y);
       const int buf = j & 1;
       const uint32_t ts = ts2 + 64 * buf;
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile, buf), (j >> 1) & 1));
@@ -320,12 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e)
           tops[e] = fmaxf(tops[e],
                           fmaxf(__uint_as_float(v[i + 2 * e]), __uint_as_float(v[i + 2 * e + 1])));
-      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale + shift;
+      float keep = 1.f;
       if (top > m + kSlack || m == -INFINITY) {
         const float next = fmaxf(top, m);
         const float f = m == -INFINITY ? 1.f : exp2_fast(m - next);
         l *= f;
-        keep *= f;
+        keep = f;
         m = next;
       }
       if (j > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
@@ -365,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_full(tile, buf, h));
       }
-      l += (sum.x + sum.y) * back;
+      l += (sum.x + sum.y) * exp2_fast(-shift);
     }
     ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full(tile), 0));
     if (!ok) {
@@ -373,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       ptx::tc_fence_after();
       const bool part = cuts > 1;
-      const float f = part ? unit : l > 0.f ? unit / l : 0.f;
+      const float f = l > 0.f ? 1.f / l : 0.f;
       T* dst = static_cast<T*>(a.out) +
                ((r.row0 + row / a.group) * a.q_heads + kvh * a.group + row % a.group) * D;
       float* sums = parts + size_t(blockIdx.x % sms) * kPartFloats<D>;
@@ -386,9 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(sums + here * D + c + 4 * i) = make_float4(
-                __uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
-                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            *reinterpret_cast<uint4*>(sums + here * D + c + 4 * i) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else if (mine) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -510,8 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) s_top[warp - kSoftmaxWarps] = top;
             widen_barrier();
             top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-            int e = int(__float_as_uint(top) >> 23) - 127 - 14;
-            e = max(-100, min(113, e));
+            // keys to below 2^15; values to below 2^7, as codes are, for a weight like theirs
+            int e = int(__float_as_uint(top) >> 23) - 127 - (half ? 6 : 14);
+            e = max(-100, min(121, e));
             down = __uint_as_float(uint32_t(127 - e) << 23);
             (half ? sc.y : sc.x) = __uint_as_float(uint32_t(127 + e) << 23);
           }

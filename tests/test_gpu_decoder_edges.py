@@ -1,12 +1,16 @@
 """GPU parity of the calls between a decoder's linears where their work splits unevenly
 or their values are far apart, infinite or NaN, against the float64 oracle."""
 
+import math
+
+import numpy as np
 import pytest
 import torch
 
 import int8_qmv_qmm_gb300 as q
-from tests.test_gpu_decoder import (F16, F32, Model, check_sample, dev, normal,  # noqa: F401
-                                    settings)
+from oracle import decoder_oracle as O
+from tests.test_gpu_decoder import (BF16, BLOCK, F16, F32, TINY, U, Model,  # noqa: F401
+                                    check_sample, close, dev, f64, normal, settings)
 
 pytestmark = pytest.mark.gpu
 
@@ -43,4 +47,71 @@ def test_parts_of_both_kernels_joined_in_one_call(dev):  # noqa: F811
     new = [1, 2, 150, 1, 90]
     m.append(new, 8, None, seed=2, advance=False)
     m.attend(new, 8, seed=3, q_scale=1.5, only={0, 1, 2, 3, 80, 152, 153, 154, 200, 243})
+    assert q.device_status() == 0
+
+
+def attend_copies(m, n, copies, x, max_new=None, scale=None):
+    """cache_attention over `copies` sequences that are all slot 0 of m (shared pages),
+    so that warps and CTAs walk over several blocks, with the n last tokens of each as
+    the rows of x.  For rows of the first and the last sequence, what the float64 oracle
+    and the definition's roundings need: (out, [(row, head, ref, size, total, most, seen,
+    largest)]), largest being the largest p_j * max|v of j's block|."""
+    c, heads = m.cache, x.shape[1]
+    many = q.KVCache(c.pages, c.scales, *(t[:1].repeat(copies, *[1] * (t.dim() - 1))
+                                          for t in (c.tail, c.table, c.lens)))
+    out = q.cache_attention(x, many, m.starts([n] * copies), max_new or n,
+                            q.attention_workspace(m.d, m.dev), scale=scale)
+    s = m.d ** -0.5 if scale is None else scale
+    rows, held, group = [], len(m.k[0]) - n, heads // m.kvh
+    for h in range(m.kvh):
+        k, v = m.values(0, h)
+        tops = np.repeat([np.abs(v[j:j + BLOCK]).max() for j in range(0, len(v), BLOCK)],
+                         BLOCK)[:len(v)]
+        for first in sorted({0, (copies - 1) * n}):
+            for i in sorted({0, n // 2, n - 1}):
+                seen = held + i + 1
+                for g in range(h * group, (h + 1) * group):
+                    xn = f64(x[first + i, g])
+                    ref, size, total, most = O.attention(xn, k, v, held + i, s)
+                    p = k[:seen] @ xn * s
+                    p = np.exp(p - p.max()) / total
+                    rows.append((first + i, g, ref, size, total, most, seen,
+                                 (p * tops[:seen]).max()))
+    return out, rows
+
+
+@pytest.mark.parametrize("d,dt,small,large", [(64, F16, 2.0 ** -13, 2.0 ** 13),
+                                              (128, F16, 2.0 ** -13, 2.0 ** 13),
+                                              (64, BF16, 2.0 ** -20, 2.0 ** 20),
+                                              (128, BF16, 1.0, 2.0 ** 40)])
+@pytest.mark.parametrize("n,copies", [(1, 200), (3, 100), (100, 40)])
+@pytest.mark.parametrize("at", [0, 3])
+def test_attention_beside_a_block_of_large_values(dev, d, dt, small, large, n, copies,  # noqa: F811
+                                                  at):
+    """One block's values are far larger than all others', and its keys leave it no
+    probability: the small values' sums keep their precision.
+
+    Bound: probabilities enter the second product in f16 in units of the largest
+    p * (value scale) so far, so that a token is off by 2^-11 of itself or 2^-25 of that
+    unit (2^-24 here, since a bf16 tail's unit is a power of two), times its block's
+    largest code; the rest as in Model.attend."""
+    heads, kvh, held = 16, 4, 700
+    m = Model(dev, 1, kvh, d, dt, blocks=13)
+    x = normal(1, held + n, (heads + 2 * kvh) * d)
+    parts = x.view(held + n, heads + 2 * kvh, d)
+    big = slice(at * BLOCK, (at + 1) * BLOCK)
+    parts[:, heads:heads + kvh, 0] = 0.0
+    parts[big, heads:heads + kvh, 0] = -60.0  # against sqrt(d) in every query: exp(-60)
+    parts[:, heads + kvh:] *= small
+    parts[big, heads + kvh:] *= large / small
+    m.append([held], heads, None, values=x[:held])
+    m.append([n], heads, None, values=x[held:], advance=False)
+    qx = normal(2, n * copies, heads, d)
+    qx[..., 0] = math.sqrt(d)
+    out, rows = attend_copies(m, n, copies, qx.to(dt).to(dev))
+    for row, g, ref, size, total, most, seen, largest in rows:
+        e = (d + 8) * 2.0 ** -23 * (most + 1)
+        bound = size * (2.0 ** -11 + 2 * e + (seen / 16 + 8) * 2.0 ** -22)
+        bound += seen * 2.0 ** -24 * largest + U[dt] * np.abs(ref) + TINY[dt]
+        close(out[row, g], ref, bound, f"row {row} head {g}")
     assert q.device_status() == 0
