@@ -81,6 +81,10 @@ __device__ __forceinline__ float log2_fast(float x) {
   return y;
 }
 
+// What a row's sums are multiplied by at the end: 1 over its denominator; 0 for a row
+// that saw nothing.  A NaN stays one, however the work was cut.
+__device__ __forceinline__ float share_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 __device__ __forceinline__ uint32_t half2_bits(__half2 v) {
   return *reinterpret_cast<uint32_t*>(&v);
 }

@@ -136,7 +136,7 @@ __device__ void join_split(const Args& a, const SplitScratch& sc, int block, int
       static_cast<T*>(a.out)[(int64_t(sp.token0 + rr / a.group) * a.q_heads + kvh * a.group +
                               rr % a.group) *
                                  D +
-                             d0 + dd] = Act<T>::from_f32_rn(sum > 0.f ? out / sum : 0.f);
+                             d0 + dd] = Act<T>::from_f32_rn(out * share_of(sum));
     }
     meet();
   }

@@ -263,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Slot sl = s_slot[p.slot];
       if (x_piece == p.first && x == p.last) {
-        const float f0 = l[0] > 0.f ? 1.f / l[0] : 0.f;
-        const float f1 = l[1] > 0.f ? 1.f / l[1] : 0.f;
+        const float f0 = share_of(l[0]), f1 = share_of(l[1]);
         const int row = p.row0 + g;
         T* dst = static_cast<T*>(a.out) +
                  (int64_t(sl.row0 + row / a.group) * a.q_heads + p.kvh * a.group +

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       ptx::tc_fence_after();
       const bool part = cuts > 1;
-      const float f = l > 0.f ? 1.f / l : 0.f;
+      const float f = share_of(l);
       T* dst = static_cast<T*>(a.out) +
                ((r.row0 + row / a.group) * a.q_heads + kvh * a.group + row % a.group) * D;
       float* sums = parts + size_t(blockIdx.x % sms) * kPartFloats<D>;
@@ -615,7 +615,7 @@ __device__ void join_pieces(const Args& a, const float* parts, int sms, int bloc
     if (w.row0 + row >= w.r.n * a.group) continue;
     const int cuts = min(plan.cuts, w.n);
     if (cuts == 1) continue;  // (written out)
-    float m[kMaxCuts], top = -INFINITY, sum = 0.f;
+    float m[kMaxCuts], l[kMaxCuts], top = -INFINITY, sum = 0.f;
     float o[D / 32] = {};
     const float* first = parts;
     auto part = [&](int k) {
@@ -624,22 +624,24 @@ __device__ void join_pieces(const Args& a, const float* parts, int sms, int bloc
 #pragma unroll
     for (int k = 0; k < kMaxCuts; ++k) {
       m[k] = k < cuts ? __ldcg(part(k) + kCtaRows * D + row) : -INFINITY;
+      l[k] = k < cuts ? __ldcg(part(k) + kCtaRows * (D + 1) + row) : 0.f;
       top = fmaxf(top, m[k]);
     }
 #pragma unroll
     for (int k = 0; k < kMaxCuts; ++k) {
-      if (k >= cuts || m[k] == -INFINITY) continue;
-      const float f = exp2_fast(m[k] - top);
-      sum += __ldcg(part(k) + kCtaRows * (D + 1) + row) * f;
+      if (l[k] == 0.f) continue;  // (no such piece, or none of its blocks is seen)
+      const float f = m[k] == -INFINITY ? 0.f : exp2_fast(m[k] - top);
+      sum += l[k] * f;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) o[e] += __ldcg(part(k) + row * D + 32 * e + lane) * f;
     }
     const int rr = w.row0 + row;
     T* dst = static_cast<T*>(a.out) +
              ((w.r.row0 + rr / a.group) * a.q_heads + w.kvh * a.group + rr % a.group) * D;
+    const float f = share_of(sum);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)
-      dst[32 * e + lane] = Act<T>::from_f32_rn(sum > 0.f ? o[e] / sum : 0.f);
+      dst[32 * e + lane] = Act<T>::from_f32_rn(o[e] * f);
   }
 }
 

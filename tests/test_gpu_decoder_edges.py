@@ -50,7 +50,7 @@ def test_parts_of_both_kernels_joined_in_one_call(dev):  # noqa: F811
     assert q.device_status() == 0
 
 
-def attend_copies(m, n, copies, x, max_new=None, scale=None):
+def attend_copies(m, n, copies, x, max_new=None, scale=None, check=True):
     """cache_attention over `copies` sequences that are all slot 0 of m (shared pages),
     so that warps and CTAs walk over several blocks, with the n last tokens of each as
     the rows of x.  For rows of the first and the last sequence, what the float64 oracle
@@ -63,7 +63,7 @@ def attend_copies(m, n, copies, x, max_new=None, scale=None):
                             q.attention_workspace(m.d, m.dev), scale=scale)
     s = m.d ** -0.5 if scale is None else scale
     rows, held, group = [], len(m.k[0]) - n, heads // m.kvh
-    for h in range(m.kvh):
+    for h in range(m.kvh if check else 0):
         k, v = m.values(0, h)
         tops = np.repeat([np.abs(v[j:j + BLOCK]).max() for j in range(0, len(v), BLOCK)],
                          BLOCK)[:len(v)]
@@ -114,4 +114,34 @@ def test_attention_beside_a_block_of_large_values(dev, d, dt, small, large, n, c
         bound = size * (2.0 ** -11 + 2 * e + (seen / 16 + 8) * 2.0 ** -22)
         bound += seen * 2.0 ** -24 * largest + U[dt] * np.abs(ref) + TINY[dt]
         close(out[row, g], ref, bound, f"row {row} head {g}")
+    assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("d,dt", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("n,copies", [(1, 1), (1, 200), (3, 1), (3, 100), (100, 1), (100, 40)])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_attention_of_nan(dev, d, dt, n, copies, where):  # noqa: F811
+    """A row whose query, or whose own key, is NaN is NaN, whether one warp or CTA
+    finishes it or its parts are joined; all other rows keep their bits."""
+    heads, kvh, held = 16, 4, 700
+    m = Model(dev, 1, kvh, d, dt, blocks=13)
+    m.append([held], heads, None, seed=1)
+    x = normal(2, n, (heads + 2 * kvh) * d)
+    m.append([n], heads, None, values=x, advance=False)
+    qx = normal(3, n * copies, heads, d).to(dt).to(dev)
+    clean, _ = attend_copies(m, n, copies, qx, check=False)
+    bad = torch.zeros(n * copies, heads, dtype=torch.bool, device=dev)
+    if where == "query":
+        for row, g in ((0, 1), (n * copies - 1, 14)):
+            qx[row, g, d // 3] = math.nan
+            bad[row, g] = True
+    else:  # of the last token, which only the last row of each sequence sees
+        x.view(n, -1, d)[n - 1, heads + 2, 5] = math.nan
+        m = Model(dev, 1, kvh, d, dt, blocks=13)
+        m.append([held], heads, None, seed=1)
+        q.rope_append(x.to(dt).to(dev), None, m.cache, m.starts([n]), heads)
+        bad[n - 1::n, 8:12] = True
+    out, _ = attend_copies(m, n, copies, qx, check=False)
+    assert out[bad].isnan().all()
+    assert torch.equal(out[~bad], clean[~bad])
     assert q.device_status() == 0
