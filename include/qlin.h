@@ -390,7 +390,10 @@ qlin_status qlin_rope_table(float* table, int64_t n_positions, int rot_dim, doub
  * (a, b) -> (a cos - b sin, b cos + a sin) in float32, rounded once to dtype.
  * Values and rotated keys enter the cache as dtype; a block that the call
  * completes gets scale = amax/127 and codes rint(v/scale) + 128 (float32,
- * ties to even; 128 where the scale is 0).  Finite inputs.
+ * ties to even; 128 where the scale is 0).  A block with an element that is
+ * not finite (in dtype: the rotation can pass f16's range) gets the scale
+ * infinity and codes 128: it stands for NaN, and so does the output of every
+ * row that sees it.
  * rot_dim: a multiple of 16, 0 .. head_dim.  qkv and q_out 16-byte aligned,
  * qkv_stride a multiple of 8.  A slot whose blocks pass max_blocks, a page
  * outside n_pages, a position outside the table or rows outside n_tokens are

@@ -126,9 +126,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // The logarithm of a block's value scale, for the exponents; the denominator takes it
 // back by exp2(-it).  A block whose values are all zero has scale 0, and any weight will
 // do: its codes are zero too.  Scales below 2^-100 weigh as that (the sums of values
-// below 2^-93 are off by as much).
+// below 2^-93 are off by as much).  Infinity, of a block that is not finite, makes the
+// rows that see it NaN: infinite scores less an infinite maximum.
 __device__ __forceinline__ float weight_log2(float v_scale) {
-  return log2_fast(v_scale > 0.f ? fmaxf(v_scale, 0x1p-100f) : 0x1p-60f);
+  const float w = v_scale > 0.f ? fmaxf(v_scale, 0x1p-100f) : 0x1p-60f;
+  return log2_fast(v_scale == v_scale ? w : INFINITY);
 }
 
 // One warp's attention of 8 rows over blocks of the cache.

@@ -286,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what goes by the scales alone, while the scores are computed
       const float2 ks = scales[st];
       // (never zero: a score of -infinity has to stay one)
-      const float scale = fmaxf(factor * ks.x, 1e-30f);
-      const float shift = weight_log2(ks.y);
+      const float scale = ks.x < INFINITY ? fmaxf(factor * ks.x, 1e-30f) : INFINITY;
+      // values that are not finite: the rows that see them are NaN, no other
+      const bool lost = !(ks.y < INFINITY);
+      const float shift = lost ? 0.f : weight_log2(ks.y);
       const int buf = j & 1;
       const uint32_t ts = ts2 + 64 * buf;
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile, buf), (j >> 1) & 1));
@@ -358,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(p_full(tile, buf, h));
       }
       l += (sum.x + sum.y) * exp2_fast(-shift);
+      if (lost && pos >= at_token) l = NAN;
     }
     ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full(tile), 0));
     if (!ok) {

@@ -127,9 +127,10 @@ __device__ __forceinline__ void rotate_unit(Vec8& x, Vec8& y, int u, int rot, bo
   }
 }
 
-// The code of v in a block of this scale.
+// The code of v in a block of this scale; 128 throughout where the scale is 0, or
+// infinite (an element was not finite: the block stands for 0 times infinity, NaN).
 __device__ __forceinline__ unsigned code_of(float v, float scale) {
-  if (!(scale > 0.f)) return 128u;
+  if (!(scale > 0.f && scale < INFINITY)) return 128u;
   return unsigned(fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f) + 128.f);
 }
 
@@ -145,13 +146,15 @@ __device__ __forceinline__ uint2 codes_of(const Vec8& v, float scale) {
   return make_uint2(r[0], r[1]);
 }
 
+// The largest magnitude, as bits: they order as the magnitudes do, with infinity above
+// all numbers and NaN above that, where fmaxf would drop it.
 template <typename T>
-__device__ __forceinline__ float largest(const Vec8& v) {
-  float top = 0.f;
+__device__ __forceinline__ uint32_t largest(const Vec8& v) {
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = unpack<T>(v.w[i]);
-    top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+    top = max(top, max(__float_as_uint(fabsf(a.x)), __float_as_uint(fabsf(a.y))));
   }
   return top;
 }
@@ -168,14 +171,14 @@ __device__ __forceinline__ void column_to(T* to, int stride, const Vec8& a, cons
 }
 
 template <int WARPS>
-__device__ __forceinline__ float block_max(float v, float* partial) {
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+__device__ __forceinline__ float block_max(uint32_t v, uint32_t* partial) {
+  for (int d = 16; d; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
   __syncthreads();
   if ((threadIdx.x & 31) == 0) partial[threadIdx.x >> 5] = v;
   __syncthreads();
   v = partial[0];
-  for (int i = 1; i < WARPS; ++i) v = fmaxf(v, partial[i]);
-  return v;
+  for (int i = 1; i < WARPS; ++i) v = max(v, partial[i]);
+  return __uint_as_float(min(v, 0x7f800000u));  // (infinity for NaN)
 }
 
 struct Args {
@@ -274,7 +277,7 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
   constexpr int kWarps = kThreads<D> / 32;
   constexpr int kStride = kBlock + 2;  // of a staged value row: spreads the banks
   __shared__ alignas(16) T staged[D * kStride];
-  __shared__ float partial[kWarps];
+  __shared__ uint32_t partial[kWarps];
   __shared__ int s_slot, s_place;
   __shared__ int64_t s_page;
   __shared__ SlotRows s_rows;
@@ -330,7 +333,7 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
   }
   if (vtok >= old) column_to(staged + 16 * vu * kStride + vtok, kStride, nv[0], nv[1]);
   if (tok >= old) rotate_unit<T>(kx, ky, u, a.rot, a.interleaved, angles);
-  float top = fmaxf(largest<T>(kx), largest<T>(ky));
+  uint32_t top = max(largest<T>(kx), largest<T>(ky));
   // (the barriers of block_max order `staged` too)
   const float k_scale = __fdiv_rn(block_max<kWarps>(top, partial), 127.f);
   const uint32_t* from = reinterpret_cast<const uint32_t*>(staged + d * kStride + t0);
@@ -343,7 +346,7 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
     else if (at + 1 >= old)
       w = (w & 0xffffu) | (from[i] & 0xffff0000u);
   }
-  top = fmaxf(largest<T>(vv[0]), largest<T>(vv[1]));
+  top = max(largest<T>(vv[0]), largest<T>(vv[1]));
   const float v_scale = __fdiv_rn(block_max<kWarps>(top, partial), 127.f);
   if (page >= 0) {
     uint8_t* codes = static_cast<uint8_t*>(a.c.pages) + (page * a.c.kv_heads + h) * 2 * kBlock * D;

@@ -145,3 +145,41 @@ def test_attention_of_nan(dev, d, dt, n, copies, where):  # noqa: F811
     assert out[bad].isnan().all()
     assert torch.equal(out[~bad], clean[~bad])
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("d,dt", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("which", ["key", "value"])
+def test_a_completed_block_that_is_not_finite(dev, d, dt, value, which):  # noqa: F811
+    """Its scale is infinite, it stands for NaN, and so do the rows that see it, in both
+    kernels; the blocks, heads and rows beside it keep their bits."""
+    heads, kvh, held = 16, 4, 100
+    out = []
+    for bad in (False, True):
+        m = Model(dev, 1, kvh, d, dt, blocks=13)
+        x = normal(4, held + 150, (heads + 2 * kvh) * d).to(dt)
+        if bad:  # token 130, of head 2, in block 2: rows 30 - .. see it
+            at = heads + 2 if which == "key" else heads + kvh + 2
+            x.view(held + 150, -1, d)[130, at, 7] = value
+        q.rope_append(x[:held].to(dev), None, m.cache, m.starts([held]), heads)
+        m.cache.lens += held
+        q.rope_append(x[held:].to(dev), None, m.cache, m.starts([150]), heads)
+        ids = m.cache.table[0, :3].contiguous()
+        back = q.cache_dequant(m.cache, ids)
+        qx = normal(5, 150, heads, d).to(dt).to(dev)
+        ws = q.attention_workspace(d, dev)
+        tile = q.cache_attention(qx, m.cache, m.starts([150]), 150, ws)
+        m.cache.lens += 146  # the same with the last four tokens alone
+        few = q.cache_attention(qx[146:], m.cache, m.starts([4]), 4, ws)
+        out.append((back, m.cache.scales[ids.long()].clone(), tile, few))
+    (back0, scales0, tile0, few0), (back, scales, tile, few) = out
+    here = torch.zeros(3, kvh, 2, dtype=torch.bool, device=dev)
+    here[2, 2, 0 if which == "key" else 1] = True
+    assert torch.equal(scales[~here], scales0[~here]) and (scales[here] == math.inf).all()
+    assert torch.equal(back[~here], back0[~here]) and back[here].isnan().all()
+    rows = torch.zeros(150, heads, dtype=torch.bool, device=dev)
+    # the whole block is NaN, so a row that sees its first token, 128, does
+    rows[128 - held:, 8:12] = True
+    assert tile[rows].isnan().all() and torch.equal(tile[~rows], tile0[~rows])
+    assert few[rows[146:]].isnan().all() and torch.equal(few[~rows[146:]], few0[~rows[146:]])
+    assert q.device_status() == 0
