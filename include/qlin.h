@@ -392,8 +392,7 @@ qlin_status qlin_rope_table(float* table, int64_t n_positions, int rot_dim, doub
  * completes gets scale = amax/127 and codes rint(v/scale) + 128 (float32,
  * ties to even; 128 where the scale is 0).  A block with an element that is
  * not finite (in dtype: the rotation can pass f16's range) gets the scale
- * infinity and codes 128: it stands for NaN, and so does the output of every
- * row that sees it.
+ * infinity and codes 128: it stands for NaN.
  * rot_dim: a multiple of 16, 0 .. head_dim.  qkv and q_out 16-byte aligned,
  * qkv_stride a multiple of 8.  A slot whose blocks pass max_blocks, a page
  * outside n_pages, a position outside the table or rows outside n_tokens are
@@ -429,6 +428,8 @@ size_t qlin_cache_attention_workspace_size(int head_dim);
  *   workspace  qlin_cache_attention_workspace_size(head_dim) bytes of device
  *            memory, 16-byte aligned, with anything in it; calls that can
  *            overlap need workspaces of their own
+ * What a row does not see does not reach it, whether it is finite or not; a
+ * value that it sees and that is not finite makes it so.
  * Scores, softmax statistics and sums are float32; probabilities enter the
  * products in 16 bits.  q_heads: a multiple of kv_heads, at most 16 times as
  * many.  q and out 16-byte aligned, q_stride a multiple of 8.  Rows that no

@@ -329,10 +329,36 @@ struct Warp {
     }
   }
 
+  // The first of the tail's `count` tokens with a value that is not finite, else count.
+  __device__ static int first_lost(const T* values, int count, int lane) {
+    constexpr uint32_t kExponent = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    constexpr uint32_t kOne = kExponent & -kExponent;  // carries out of a full exponent
+    int lost = count;
+#pragma unroll 8
+    for (int u = lane; u < kBlock * D / 8; u += 32) {
+      const uint4 v = *reinterpret_cast<const uint4*>(values + 8 * u);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t any = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) any |= (w[e] & kExponent * 0x10001u) + kOne * 0x10001u;
+      if (any & 0x80008000u) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e)
+          if ((reinterpret_cast<const uint16_t*>(values)[8 * u + e] & kExponent) == kExponent)
+            lost = min(lost, 8 * u % kBlock + e);
+      }
+    }
+    return __reduce_min_sync(0xffffffffu, lost);
+  }
+
   // The tail: `count` tokens of T, the rest of its memory undefined.  Products
-  // in T (the queries come from memory again: q is f16).
+  // in T (the queries come from memory again: q is f16).  `uneven`: not every row
+  // sees all of them, and a value that is not finite must not reach, as 0 times it,
+  // the rows that do not.  Then values from its token on are left out, and the rows
+  // that see it are NaN.  (Looking first: 12 x 3 drafts 30.1 -> 31.0 us; beside each
+  // product, 33.0.)
   __device__ void tail(const T* kv, int count, const T* q_row, float scale_log2,
-                       const int (&seen)[2], int lane) {
+                       const int (&seen)[2], bool uneven, int lane) {
     const int g = lane >> 2, t = lane & 3;
     float s[4][4];
     uint32_t w[D / 8];
@@ -357,6 +383,12 @@ struct Warp {
     scale[0] = scale[1] = scale_log2;
     softmax(s, scale, 0.f, seen, true, g, keep);
     rescale(keep);
+    const int lost = uneven ? first_lost(kv + kBlock * D, count, lane) : count;
+    if (lost < count) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (seen[r] > lost) l[r] = NAN;
+    }
     // bf16 keeps only 8 bits of p, so what it leaves over goes through a second
     // product.
     constexpr bool kTwo = std::is_same<T, __nv_bfloat16>::value;
@@ -377,7 +409,7 @@ struct Warp {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int tok = 16 * t + 4 * k + 2 * h;
-        valid[k][h] = tok + 1 < count ? 0xffffffffu : tok < count ? 0x0000ffffu : 0u;
+        valid[k][h] = tok + 1 < lost ? 0xffffffffu : tok < lost ? 0x0000ffffu : 0u;
       }
     kv += kBlock * D;
 #pragma unroll

@@ -174,8 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscAt);
   int* s_work = reinterpret_cast<int*>(smem + L::kMiscAt + 32);  // slot, place, cuts, cut
   float* s_top = reinterpret_cast<float*>(smem + L::kMiscAt + 8);  // of the four widening warps
+  // the first of the tail's tokens with a value that is not finite, else kBlock
+  int* s_lost = reinterpret_cast<int*>(smem + L::kMiscAt + 48);
 
   if (threadIdx.x == 0) {
+    *s_lost = kBlock;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full(s), kWidenWarps);
       ptx::mbar_init(empty(s), kTiles);
@@ -288,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (never zero: a score of -infinity has to stay one)
       const float scale = ks.x < INFINITY ? fmaxf(factor * ks.x, 1e-30f) : INFINITY;
       // values that are not finite: the rows that see them are NaN, no other
-      const bool lost = !(ks.y < INFINITY);
-      const float shift = lost ? 0.f : weight_log2(ks.y);
+      int lost = ks.y < INFINITY ? kBlock : 0;
+      const float shift = lost ? weight_log2(ks.y) : 0.f;
+      if (at_token + kBlock > total) lost = *s_lost;
       const int buf = j & 1;
       const uint32_t ts = ts2 + 64 * buf;
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(tile, buf), (j >> 1) & 1));
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(p_full(tile, buf, h));
       }
       l += (sum.x + sum.y) * exp2_fast(-shift);
-      if (lost && pos >= at_token) l = NAN;
+      if (lost < kBlock && pos - at_token >= lost) l = NAN;
     }
     ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(o_full(tile), 0));
     if (!ok) {
@@ -483,7 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // the tail: T as it is (f16), or scaled by a power of two (bf16); what
-        // lies beyond its last token is undefined and becomes zero
+        // lies beyond its last token is undefined and becomes zero, as do values
+        // that are not finite (0 times them would be NaN in the rows that do not see
+        // their token)
         const T* src = static_cast<const T*>(a.c.tail) +
                        (int64_t(b) * a.c.kv_heads + kvh) * 2 * kBlock * D;
         const int count = total - (j0 + j) * kBlock;
@@ -497,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int u = i0; u < kBlock * D; u += 128) {
               const int tok = half ? u % kBlock : u / D;
-              if (tok < count) top = fmaxf(top, fabsf(Act<T>::to_f32(from[u])));
+              const float v = fabsf(Act<T>::to_f32(from[u]));
+              if (tok < count && v < INFINITY) top = fmaxf(top, v);
             }
             for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             widen_barrier();
@@ -522,7 +529,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (std::is_same<T, __nv_bfloat16>::value)
                 v = pack2<__half>(low_f32(v) * down, high_f32(v) * down);
               const int t0 = half ? tok + 2 * e : tok, t1 = half ? t0 + 1 : tok;
-              y[e] = (t0 < count ? v & 0xffffu : 0u) | (t1 < count ? v & 0xffff0000u : 0u);
+              uint32_t lo = t0 < count ? v & 0xffffu : 0u, hi = t1 < count ? v & 0xffff0000u : 0u;
+              if (half && (lo & 0x7c00u) == 0x7c00u) {
+                atomicMin(s_lost, t0);
+                lo = 0;
+              }
+              if (half && (hi & 0x7c000000u) == 0x7c000000u) {
+                atomicMin(s_lost, t1);
+                hi = 0;
+              }
+              y[e] = lo | hi;
             }
             const int at = half ? swizzled(8 * u / kBlock, 8 * u % kBlock / 8)
                                 : (8 * u % D) / 64 * 8192 + swizzled(tok, 8 * u % 64 / 8);

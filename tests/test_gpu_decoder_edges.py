@@ -183,3 +183,35 @@ def test_a_completed_block_that_is_not_finite(dev, d, dt, value, which):  # noqa
     assert tile[rows].isnan().all() and torch.equal(tile[~rows], tile0[~rows])
     assert few[rows[146:]].isnan().all() and torch.equal(few[~rows[146:]], few0[~rows[146:]])
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("d,dt", [(64, F16), (128, F16), (64, BF16), (128, BF16)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("which", ["key", "value"])
+@pytest.mark.parametrize("n", [3, 13, 50])
+def test_a_tail_that_is_not_finite(dev, d, dt, value, which, n):  # noqa: F811
+    """A token of the incomplete block, one that the first rows of the call do not see:
+    those keep their bits, the others are not finite."""
+    heads, kvh, held, at = 16, 4, 201, 2 if n < 50 else 30
+    out = []
+    for bad in (False, True):
+        m = Model(dev, 1, kvh, d, dt, blocks=13)
+        x = normal(6, held + n, (heads + 2 * kvh) * d).to(dt)
+        if bad:
+            head = heads + 1 if which == "key" else heads + kvh + 1
+            x.view(held + n, -1, d)[held + at, head, 3] = value
+        q.rope_append(x[:held].to(dev), None, m.cache, m.starts([held]), heads)
+        m.cache.lens += held
+        q.rope_append(x[held:].to(dev), None, m.cache, m.starts([n]), heads)
+        qx = normal(7, n, heads, d).to(dt)
+        qx[..., 3] = 0.5  # (no product of zero and infinity)
+        ws = q.attention_workspace(d, dev)
+        out.append(q.cache_attention(qx.to(dev), m.cache, m.starts([n]), n, ws))
+    rows = torch.zeros(n, heads, dtype=torch.bool, device=dev)
+    rows[at:, 4:8] = True
+    if which == "key" and value == -math.inf:  # no probability for that token, and no harm
+        assert out[1][rows].isfinite().all()
+    else:
+        assert (~out[1][rows].isfinite()).any(-1).all()
+    assert torch.equal(out[1][~rows], out[0][~rows])
+    assert q.device_status() == 0
