@@ -319,7 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (f.kind == kCodes) {
       const unsigned slot = used % L::kRing;
       const uint8_t* chunk = ring + slot * L::kChunk;
-      if (!ptx::mbar_wait(bar + 8 * slot, (used / L::kRing) & 1) && lane == 0) report(kStatusWait);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar + 8 * slot, (used / L::kRing) & 1))) {
+        // the warp's other waits would run out one by one: it reports and goes, once the
+        // copies under way have landed
+        if (lane == 0) report(kStatusWait);
+        for (; used < sent; ++used)
+          ptx::mbar_wait(bar + 8 * (used % L::kRing), (used / L::kRing) & 1, 100000000ull);
+        break;
+      }
       if (!have_scores) {
         w.scores(chunk, s, lane);
       } else {
