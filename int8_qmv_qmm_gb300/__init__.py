@@ -382,24 +382,24 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-5, out=None, residual
     float32; rows may be strided.  Returns (out, residual_out), residual_out
     being h rounded to the residual's dtype (None without a residual);
     residual_out=residual updates it in place."""
-    dt, rdt, shape = x.dtype, x.dtype, x.shape
-    ok = (x.is_cuda and len(shape) == 2 and x.stride(1) == 1
-          and (dt is torch.float16 or dt is torch.bfloat16) and weight.is_cuda
+    dt, rdt, shape, index = x.dtype, x.dtype, x.shape, x.get_device()
+    ok = (index >= 0 and len(shape) == 2 and x.stride(1) == 1
+          and (dt is torch.float16 or dt is torch.bfloat16) and weight.get_device() == index
           and weight.dtype is dt and weight.dim() == 1 and weight.is_contiguous()
           and weight.shape[0] == shape[1])
     r_ptr = ro_ptr = None
     rs = 0
     if ok and residual is not None:
         rdt = residual.dtype
-        ok = (residual.is_cuda and residual.shape == shape and residual.stride(1) == 1
-              and (rdt is dt or rdt is torch.float32))
+        ok = (residual.get_device() == index and residual.shape == shape
+              and residual.stride(1) == 1 and (rdt is dt or rdt is torch.float32))
         if ok:
             rs, r_ptr = _row_stride(residual, shape[1]), residual.data_ptr()
             if residual_out is None:
                 residual_out = (torch.empty_like(residual) if residual.is_contiguous()
                                 else torch.empty(shape, dtype=rdt, device=x.device))
             else:
-                ok = (residual_out.is_cuda and residual_out.is_contiguous()
+                ok = (residual_out.get_device() == index and residual_out.is_contiguous()
                       and residual_out.shape == shape and residual_out.dtype is rdt)
             ro_ptr = residual_out.data_ptr()
     elif residual_out is not None:
@@ -409,30 +409,33 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-5, out=None, residual
             out = (torch.empty_like(x) if x.is_contiguous()
                    else torch.empty(shape, dtype=dt, device=x.device))
         else:
-            ok = (out.is_cuda and out.is_contiguous() and out.shape == shape
+            ok = (out.get_device() == index and out.is_contiguous() and out.shape == shape
                   and out.dtype is dt)
     if not ok:
         _refuse((x.is_cuda and x.dim() == 2 and x.stride(1) == 1,
                  "x must be a 2-D CUDA tensor with contiguous rows"),
                 (dt in (torch.float16, torch.bfloat16), "x must be float16 or bfloat16"),
-                (weight.is_cuda and weight.is_contiguous() and weight.dtype == dt
-                 and tuple(weight.shape) == tuple(shape[1:]), "weight must be [K] in x's dtype"),
+                (weight.device == x.device and weight.is_contiguous() and weight.dtype == dt
+                 and tuple(weight.shape) == tuple(shape[1:]),
+                 "weight must be [K] in x's dtype, on its device"),
                 (residual is not None or residual_out is None,
                  "residual_out without a residual"),
-                (residual is None or (residual.is_cuda and residual.shape == shape
+                (residual is None or (residual.device == x.device and residual.shape == shape
                                       and residual.stride(1) == 1
                                       and residual.dtype in (dt, torch.float32)),
-                 "residual must have x's shape and contiguous rows, in its dtype or float32"),
-                (residual_out is None or (residual_out.is_cuda and residual_out.is_contiguous()
+                 "residual must have x's device, shape and contiguous rows, in its dtype or "
+                 "float32"),
+                (residual_out is None or (residual_out.device == x.device
+                                          and residual_out.is_contiguous()
                                           and residual_out.shape == shape
                                           and residual_out.dtype == rdt),
-                 "residual_out must be contiguous, of the residual's shape and dtype"),
-                (False, "out must be contiguous, of x's shape and dtype"))
+                 "residual_out must be contiguous, of the residual's device, shape and dtype"),
+                (False, "out must be contiguous, of x's device, shape and dtype"))
     m, k = shape
     status = lib().qlin_add_rms_norm(
         x.data_ptr(), _row_stride(x, k), weight.data_ptr(), r_ptr, rs, ro_ptr, out.data_ptr(),
         m, k, eps, _DTYPE_CODE[dt], _DTYPE_CODE[rdt], 1 if overlap_previous else 0,
-        _current_raw_stream(x.get_device()))
+        _current_raw_stream(index))
     if status:
         _check(status)
     return out, residual_out

@@ -4,6 +4,7 @@ work is cut, and what the bindings do before anything is launched."""
 import ctypes
 
 import pytest
+import torch
 
 import int8_qmv_qmm_gb300 as q
 from int8_qmv_qmm_gb300 import build_lib
@@ -46,3 +47,41 @@ def test_sample_plan_refusals(L):
     assert sample_plan(L, 1, 262145)[0] == 1
     assert sample_plan(L, 1, 10, 0)[0] == 1
     assert L.qlin_testing_sample_plan(1, 10, 152, None, None, None) == 1
+
+
+# ------------------------------------------------------------------ the bindings
+class OnDevice:
+    """A tensor's face, on a CUDA device that need not be there."""
+
+    def __init__(self, shape, dtype, index=0):
+        self.t = torch.zeros(shape, dtype=dtype)
+        self.index, self.device, self.is_cuda = index, torch.device("cuda", index), True
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class NoLaunch:
+    """A library whose calls all launch: none may be reached."""
+
+    def __getattr__(self, name):
+        def call(*args):
+            raise AssertionError(f"{name} was called")
+        return call
+
+
+@pytest.mark.parametrize("which", ["weight", "residual", "residual_out", "out"])
+def test_norm_refuses_tensors_on_another_device(monkeypatch, which):
+    monkeypatch.setattr(q, "lib", NoLaunch)
+    monkeypatch.setattr(q, "_current_raw_stream", lambda index: 0)
+    f16, f32 = torch.float16, torch.float32
+    tensors = dict(x=((3, 64), f16), weight=((64,), f16), residual=((3, 64), f32),
+                   residual_out=((3, 64), f32), out=((3, 64), f16))
+    good = {name: OnDevice(*v) for name, v in tensors.items()}
+    with pytest.raises(AssertionError, match="qlin_add_rms_norm was called"):
+        q.add_rms_norm(**good)
+    with pytest.raises(ValueError, match=f"^{which} must"):
+        q.add_rms_norm(**{**good, which: OnDevice(*tensors[which], index=1)})
