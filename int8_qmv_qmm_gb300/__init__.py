@@ -304,7 +304,11 @@ class KVCache:
     dtype) [slots, kv_heads, 2, 64*head_dim]: each slot's incomplete last block;
     table int32 [slots, max_blocks]: the page of each block; lens int32 [slots]:
     the tokens held before the call.  table and lens may be shared by the layers
-    of a model; the caller fills the table and advances lens once per step."""
+    of a model; the caller fills the table and advances lens once per step, in place
+    (the calls use the memory that the handle was made with, so its tensors cannot
+    be replaced)."""
+
+    _TENSORS = ("pages", "scales", "tail", "table", "lens")
 
     def __init__(self, pages, scales, tail, table, lens):
         _need_cuda(pages, scales, tail, table, lens)
@@ -332,6 +336,13 @@ class KVCache:
             lens.data_ptr(), n_pages, slots, table.shape[1], kv_heads, self.head_dim,
             _DTYPE_CODE[tail.dtype])
         self._ref = ctypes.byref(self._struct)
+
+    def __setattr__(self, name, value):
+        # (cache.lens += n assigns the tensor that it has changed in place)
+        if name in self._TENSORS and getattr(self, name, value) is not value:
+            raise AttributeError(f"the cache's {name} cannot be replaced: write into it "
+                                 f"(cache.{name}.copy_(...)), or make another KVCache")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, slots: int, max_tokens: int, kv_heads: int, head_dim: int,

@@ -85,3 +85,21 @@ def test_norm_refuses_tensors_on_another_device(monkeypatch, which):
         q.add_rms_norm(**good)
     with pytest.raises(ValueError, match=f"^{which} must"):
         q.add_rms_norm(**{**good, which: OnDevice(*tensors[which], index=1)})
+
+
+def test_a_cache_keeps_its_tensors(monkeypatch):
+    """The handle holds their addresses: replacing one would be silently ignored."""
+    monkeypatch.setattr(q, "_need_cuda", lambda *ts: None)
+    c = q.KVCache.empty(2, 128, 1, 64, device="cpu")
+    lens, at = c.lens, c.lens.data_ptr()
+    c.lens += 3
+    c.lens.copy_(c.lens + 1)
+    c.table[1] = 5
+    c.table = c.table
+    assert c.lens is lens and c.lens.tolist() == [4, 4] and c._struct.lens == at
+    for name in ("pages", "scales", "tail", "table", "lens"):
+        with pytest.raises(AttributeError, match=f"cache's {name} cannot be replaced"):
+            setattr(c, name, getattr(c, name) + 1)
+        with pytest.raises(AttributeError, match="cannot be replaced"):
+            setattr(c, name, getattr(c, name).clone())
+    assert c.lens is lens and c.table.tolist() == [[0, 1], [5, 5]]
