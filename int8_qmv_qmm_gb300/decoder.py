@@ -34,7 +34,10 @@ from . import synthetic as S
 class Decoder:
     """Sampling settings are the tensors temperature, top_k, top_p and min_p
     [slots], as sample() takes them (the largest logit by default); write to
-    them at any time, also after capture()."""
+    them at any time, also after capture().
+
+    A slot whose logits have no token (all NaN or -infinity, as after an overflow) gets -1,
+    and goes on from token 0; its neighbours are not affected."""
 
     def __init__(self, device="cuda", slots: int = 4, max_tokens: int = 4096, layers: int = 2,
                  hidden: int = 256, q_heads: int = 4, kv_heads: int = 2, head_dim: int = 64,
@@ -143,7 +146,8 @@ class Decoder:
         return self.tokens
 
     def _step(self):
-        self.logits = self._forward(self.tokens, self._one_each, 1)
+        # (a row of logits without a token gives -1, which has no embedding)
+        self.logits = self._forward(self.tokens.clamp(min=0), self._one_each, 1)
         self._sample(self.logits, self.tokens)
 
     def capture(self):

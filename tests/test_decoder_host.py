@@ -5,9 +5,11 @@ import ctypes
 
 import pytest
 import torch
+import torch.nn.functional as F
 
 import int8_qmv_qmm_gb300 as q
 from int8_qmv_qmm_gb300 import build_lib
+from int8_qmv_qmm_gb300.decoder import Decoder
 
 
 @pytest.fixture(scope="module")
@@ -103,3 +105,17 @@ def test_a_cache_keeps_its_tensors(monkeypatch):
         with pytest.raises(AttributeError, match="cannot be replaced"):
             setattr(c, name, getattr(c, name).clone())
     assert c.lens is lens and c.table.tolist() == [[0, 1], [5, 5]]
+
+
+# ------------------------------------------------------------------ the decoder
+def test_a_decode_step_after_a_row_without_a_token():
+    """sample() gives -1 for such a row; looking its embedding up would fault."""
+    d = object.__new__(Decoder)
+    d.embed = torch.arange(12.0).view(4, 3)
+    d.tokens = torch.tensor([2, -1, 3], dtype=torch.int32)
+    d._one_each = torch.arange(4, dtype=torch.int32)
+    d._forward = lambda tokens, starts, max_new: F.embedding(tokens, d.embed)
+    d._sample = lambda logits, tokens: None
+    d._step()
+    assert torch.equal(d.logits, d.embed[[2, 0, 3]])
+    assert d.tokens.tolist() == [2, -1, 3]
