@@ -155,7 +155,7 @@ class Decoder:
         (A warm-up step runs first and is undone: the next step writes its token to
         the same place of the caches.)"""
         self._check_room([1] * self.slots)
-        tokens, lens = self.tokens.clone(), self.lens.clone()
+        tokens, lens, logits = self.tokens.clone(), self.lens.clone(), self.logits
         side = torch.cuda.Stream(self.device)
         side.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(side):
@@ -166,15 +166,18 @@ class Decoder:
         self._graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self._graph):
             self._step()
+        self._graph_logits, self.logits = self.logits, logits
 
     def decode(self):
-        """One decode step of every slot.  Returns the new tokens [slots]."""
+        """One decode step of every slot.  Returns the new tokens [slots] (one tensor,
+        written to by every call; after capture() logits is one too)."""
         self._check_room([1] * self.slots)
         self.u.uniform_()
         if self._graph is None:
             self._step()
         else:
             self._graph.replay()
+            self.logits = self._graph_logits
         self.held = [h + 1 for h in self.held]
         return self.tokens
 

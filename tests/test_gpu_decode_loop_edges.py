@@ -36,3 +36,34 @@ def test_a_slot_without_a_token(dev, captured):  # noqa: F811
     assert all(7 not in (t[0], t[2]) for t in clean)
     assert [(t[0], t[2]) for t in bad] == [(t[0], t[2]) for t in clean]
     assert q.device_status() == 0
+
+
+def test_logits_are_the_last_calls(dev):  # noqa: F811
+    """Around a capture, and where prompts come between replays."""
+    seen = []
+    for captured in (False, True):
+        d = Decoder(dev, **SHAPE)
+        ids = prompts((63, 5, 120))
+        got = []
+
+        def keep():
+            got.append((d.tokens.clone(), d.logits.clone()))
+
+        d.prefill(ids)
+        keep()
+        if captured:
+            d.capture()
+            keep()
+        else:
+            got.append(got[-1])
+        for more in ([], [[], ids[0][:9], []], [ids[1], [], [3]]):
+            if more:
+                d.prefill(more)
+                keep()
+            for _ in range(2):
+                d.decode()
+                keep()
+        seen.append(got)
+    for i, ((t0, l0), (t1, l1)) in enumerate(zip(*seen)):
+        assert torch.equal(t0, t1) and torch.equal(l0, l1), i
+    assert q.device_status() == 0
