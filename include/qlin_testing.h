@@ -54,6 +54,13 @@ int qlin_testing_qmv_split(int64_t N, int64_t K, int bits, int sm_count);
 qlin_status qlin_testing_sample_plan(int64_t M, int64_t V, int sm_count, int* ranks, int* part,
                                      int* limb_bits);
 
+/*
+ * q[i] = a[i]/tau[i] by the steps that qlin_sample takes in place of a division
+ * (same fused multiply-adds, on the host; a, tau and q are HOST pointers), for
+ * i < n.  Returns QLIN_ERR_INVALID_ARG for n < 0 or a null pointer.
+ */
+qlin_status qlin_testing_sample_quotient(const float* a, const float* tau, float* q, int64_t n);
+
 #ifdef __cplusplus
 }
 #endif

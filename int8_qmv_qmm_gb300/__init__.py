@@ -83,6 +83,7 @@ _SIGNATURES = {
     "qlin_testing_qmv_split": (_c_int, [_c_i64, _c_i64, _c_int, _c_int]),
     "qlin_testing_sample_plan": (_c_int, [_c_i64, _c_i64, _c_int]
                                  + [ctypes.POINTER(_c_int)] * 3),
+    "qlin_testing_sample_quotient": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64]),
 }
 
 _LIB = None

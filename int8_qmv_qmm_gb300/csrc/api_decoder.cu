@@ -233,4 +233,12 @@ qlin_status qlin_testing_sample_plan(int64_t M, int64_t V, int sm_count, int* ra
   return QLIN_OK;
 }
 
+qlin_status qlin_testing_sample_quotient(const float* a, const float* tau, float* q, int64_t n) {
+  clear_error();
+  if (n < 0 || (n && (!a || !tau || !q)))
+    return fail(QLIN_ERR_INVALID_ARG, "qlin_testing_sample_quotient: n=%lld", (long long)n);
+  for (int64_t i = 0; i < n; ++i) q[i] = sample_quotient(a[i], tau[i]);
+  return QLIN_OK;
+}
+
 }  // extern "C"

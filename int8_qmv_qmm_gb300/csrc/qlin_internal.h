@@ -92,6 +92,8 @@ struct SamplePlan {
   int ranks, part, limb;
 };
 SamplePlan sample_plan(int64_t M, int64_t V, int sms);
+// a/tau as the kernel computes it, on the host.
+float sample_quotient(float a, float tau);
 qlin_status launch_sample(const void* logits, int64_t logits_stride, const float* u,
                           const float* temperature, const int32_t* top_k, const float* top_p,
                           const float* min_p, int32_t* tokens, float* probs, int64_t M,

@@ -20,6 +20,8 @@
 // Weights are whole numbers of 2^-36, summed in limbs of 18 or 12 bits: the sums
 // are exact, and the order of the atomic additions does not show.
 
+#include <cmath>
+
 #include "device_common.cuh"
 #include "qlin_internal.h"
 #include "sm100_ptx.cuh"
@@ -110,12 +112,21 @@ struct Shared {
   u64 found[2][3];
 };
 
-// exp((x - top)/tau), rounded as the division and expf round.  The quotient is
-// Markstein's (IBM J. Res. Dev. 34, 1990): with the reciprocal correctly
-// rounded, a step that makes the quotient faithful and one that makes it
-// correctly rounded, each on the exact remainder of a fused multiply-add.
-// What weighs less than 2^-37 (quotients below -26) is 0, which also keeps
-// infinities out of the steps.
+// a/tau, rounded as the division rounds, for 1e-30 < tau < 1e30, |a| < 26 tau and
+// quotients of 2^-30 or more (where a is subnormal, smaller ones can be off in their
+// last bit; exp of them is 1).
+// Markstein's (IBM J. Res. Dev. 34, 1990): with the reciprocal correctly rounded, a
+// step that makes the quotient faithful and one that makes it correctly rounded,
+// each on the exact remainder of a fused multiply-add.
+__host__ __device__ inline float quotient(float a, float tau, float inverse) {
+  float q = a * inverse;
+  q = fmaf(fmaf(-q, tau, a), inverse, q);
+  return fmaf(fmaf(-q, tau, a), inverse, q);
+}
+
+// exp((x - top)/tau), rounded as the division and expf round.  What weighs less
+// than 2^-37 (quotients below -26) is 0, which also keeps infinities out of the
+// quotient's steps.
 struct Weigh {
   float top, tau, inverse, least;
   __device__ void set(float top_, float tau_) {
@@ -130,10 +141,7 @@ struct Weigh {
     if (!(a > least)) return 0.0f;
     if (tau == 1.0f) return expf(a);
     if (!(tau > 1e-30f && tau < 1e30f)) return expf(__fdiv_rn(a, tau));  // the steps' range
-    float q = a * inverse;
-    q = fmaf(fmaf(-q, tau, a), inverse, q);
-    q = fmaf(fmaf(-q, tau, a), inverse, q);
-    return expf(q);
+    return expf(quotient(a, tau, inverse));
   }
 };
 // rint(2^36 e), 0 <= e <= 1, as hi * 2^18 + lo with -2^17 <= lo <= 2^17.  Adding
@@ -904,6 +912,8 @@ qlin_status launch_t(Params a, int64_t M, unsigned flags, cudaStream_t st) {
 }
 
 }  // namespace
+
+float sample_quotient(float a, float tau) { return quotient(a, tau, 1.0f / tau); }
 
 SamplePlan sample_plan(int64_t M, int64_t V, int sms) {
   // CTAs that share a row: enough to fill the SMs twice, with 4096 elements or

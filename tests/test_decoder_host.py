@@ -3,6 +3,7 @@ work is cut, and what the bindings do before anything is launched."""
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 import torch.nn.functional as F
@@ -49,6 +50,32 @@ def test_sample_plan_refusals(L):
     assert sample_plan(L, 1, 262145)[0] == 1
     assert sample_plan(L, 1, 10, 0)[0] == 1
     assert L.qlin_testing_sample_plan(1, 10, 152, None, None, None) == 1
+
+
+def test_sample_quotient_rounds_as_the_division(L):
+    """Over temperatures of every size, distances up to 26 of them, and quotients next to
+    the middle between two numbers, where a faithful but not correct step shows.  (A
+    distance that is subnormal leaves no exact remainder: quotients below 2^-30, whose
+    exponential is 1, only have to stay below it.)"""
+    rng = np.random.default_rng(3)
+    f32 = np.float32
+    n = 200000
+    tau = np.concatenate([np.exp(rng.uniform(np.log(1e-2), np.log(1e2), n)),
+                          np.exp(rng.uniform(np.log(1.1e-30), np.log(0.9e30), n)),
+                          2.0 ** rng.integers(-90, 90, n) * (2 - 2.0 ** -23)]).astype(f32)
+    share = np.concatenate([rng.uniform(1e-9, 25.9, 2 * n), 2.0 ** rng.uniform(-60, 4, n)])
+    a = -(tau.astype(np.float64) * share).astype(f32)
+    # numbers nearest to tau times a middle
+    mid = (1 + (2 * rng.integers(0, 2 ** 23, n) + 1) * 2.0 ** -24) * 2.0 ** rng.integers(-8, 4, n)
+    a = np.concatenate([a, -(tau[:n].astype(np.float64) * mid).astype(f32)])
+    tau = np.concatenate([tau, tau[:n]])
+    q = np.empty_like(a)
+    assert L.qlin_testing_sample_quotient(a.ctypes.data, tau.ctypes.data, q.ctypes.data, len(a)) == 0
+    true = a / tau
+    matters = np.abs(true) >= 2.0 ** -30
+    assert matters.sum() > 3.4 * n and np.array_equal(q[matters], true[matters])
+    assert (np.abs(q[~matters]) <= 2.0 ** -30).all()
+    assert L.qlin_testing_sample_quotient(None, None, None, 1) == 1
 
 
 # ------------------------------------------------------------------ the bindings

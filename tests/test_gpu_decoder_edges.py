@@ -215,3 +215,55 @@ def test_a_tail_that_is_not_finite(dev, d, dt, value, which, n):  # noqa: F811
         assert (~out[1][rows].isfinite()).any(-1).all()
     assert torch.equal(out[1][~rows], out[0][~rows])
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("n,copies", [(1, 60), (3, 40), (100, 2), (100, 40)])
+@pytest.mark.parametrize("dt,scale", [(F16, 0.0), (F16, -0.2), (BF16, -0.05), (F16, 2.0)])
+def test_attention_scales_of_both_kernels(dev, n, copies, dt, scale):  # noqa: F811
+    """Negative and zero scales among them; from few rows to whole rounds of tiles."""
+    heads, kvh, d, held = 16, 4, 64, 500
+    m = Model(dev, 1, kvh, d, dt, blocks=13)
+    m.append([held], heads, None, seed=1)
+    m.append([n], heads, None, seed=2, advance=False)
+    x = normal(3, n * copies, heads, d).to(dt).to(dev)
+    out, rows = attend_copies(m, n, copies, x, scale=scale)
+    for row, g, ref, size, total, most, seen, largest in rows:  # (as beside large values)
+        e = (d + 8) * 2.0 ** -23 * (abs(most) + 1)
+        bound = size * (2.0 ** -11 + 2 * e + (seen / 16 + 8) * 2.0 ** -22)
+        bound += seen * 2.0 ** -24 * largest + U[dt] * np.abs(ref) + TINY[dt]
+        close(out[row, g], ref, bound, f"row {row} head {g}")
+    assert q.device_status() == 0
+
+
+def test_prompts_with_offsets_beyond_32_bits(dev):  # noqa: F811
+    """Pages whose byte offsets pass 2^32, read for more rows than single tokens."""
+    kvh, d, n_pages = 8, 128, 33000  # 128 KB a page
+    c = q.KVCache(torch.empty((n_pages, kvh, 2, 64 * d), dtype=torch.uint8, device=dev),
+                  torch.zeros((n_pages, kvh, 2), device=dev),
+                  torch.zeros((1, kvh, 2, 64 * d), dtype=BF16, device=dev),
+                  torch.tensor([[32999, 3, 16500, 32000, 32768]], dtype=torch.int32, device=dev),
+                  torch.zeros(1, dtype=torch.int32, device=dev))
+    m = Model(dev, 1, kvh, d, BF16, blocks=5)
+    m.cache = c
+    m.append([200], 8, None, seed=51)
+    m.append([100], 8, None, seed=52, advance=False)
+    m.attend([100], 8, seed=53, only={0, 50, 99})
+    assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("n,copies", [(1, 1), (3, 60), (100, 40)])
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_attention_of_an_infinite_query(dev, dt, n, copies):  # noqa: F811
+    """The row is not finite; the others keep their bits."""
+    heads, kvh, d = 16, 4, 64
+    m = Model(dev, 1, kvh, d, dt, blocks=13)
+    m.append([300], heads, None, seed=1)
+    m.append([n], heads, None, seed=2, advance=False)
+    x = normal(3, n * copies, heads, d).to(dt).to(dev)
+    clean, _ = attend_copies(m, n, copies, x, check=False)
+    x[0, 3, 5] = math.inf
+    out, _ = attend_copies(m, n, copies, x, check=False)
+    assert not out[0, 3].isfinite().any()
+    out[0, 3] = clean[0, 3]
+    assert torch.equal(out, clean)
+    assert q.device_status() == 0
