@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::fence_mbar_init();
   }
-  grid_launch_dependents();
   grid_dependency_wait();
   if (warp == 0) {
     const Plan plan = plan_of(a, sms);
@@ -224,6 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (not before: a later kernel of the stream that takes tensor memory, and then waits
+  // for this one, could stand on this SM first)
+  grid_launch_dependents();
 
   const SlotRows r = work.r;
   const int b = work.slot, kvh = work.kvh, row0 = work.row0, rows = r.n * a.group;

@@ -267,3 +267,32 @@ def test_attention_of_an_infinite_query(dev, dt, n, copies):  # noqa: F811
     out[0, 3] = clean[0, 3]
     assert torch.equal(out, clean)
     assert q.device_status() == 0
+
+
+def test_prompts_between_products_of_the_tensor_cores(dev):  # noqa: F811
+    """Both kinds of kernel take tensor memory, and each starts while the one before it
+    runs: small products after prompts, call after call, the same bits as with pauses."""
+    heads, kvh, d, slots, n = 8, 2, 64, 12, 60
+    rows, width = slots * n, (heads + 2 * kvh) * d
+    packed = q.quantize_affine((normal(1, width, heads * d) * 0.05).float().to(dev), 8)
+    starts = torch.arange(slots + 1, dtype=torch.int32, device=dev) * n
+    ws, table = q.attention_workspace(d, dev), q.rope_table(512, d, device=dev)
+    seen = []
+    for pause in (True, False):
+        m = Model(dev, slots, kvh, d, F16)
+        x, got = normal(2, rows, heads * d).to(F16).to(dev), []
+        for _ in range(6):
+            qkv = q.qmm(x, *packed, 8, overlap_previous=not pause)
+            if pause:
+                torch.cuda.synchronize()
+            query = q.rope_append(qkv, table, m.cache, starts, heads, overlap_previous=not pause)
+            a = q.cache_attention(query, m.cache, starts, n, ws, overlap_previous=not pause)
+            if pause:
+                torch.cuda.synchronize()
+            x = q.qmm(a.view(rows, -1), *packed, 8,
+                      overlap_previous=not pause)[:, :heads * d].contiguous()
+            m.cache.lens += n
+            got.append(x)
+        seen.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*seen))
+    assert q.device_status() == 0
