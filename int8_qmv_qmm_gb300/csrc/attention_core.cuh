@@ -436,9 +436,10 @@ struct Warp {
 // status words that they set.  The split kernel's parts are joined by its own launch
 // (`join`) or by the tile kernel's, with its pieces.
 size_t split_workspace_size(int head_dim);
-void launch_split(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st);
+cudaError_t launch_split(const Args& a, void* workspace, bool join, unsigned flags,
+                         cudaStream_t st);
 size_t tile_workspace_size(int head_dim);
-void launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st);
+cudaError_t launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st);
 cudaError_t split_take_status(unsigned* flags);
 cudaError_t tile_take_status(unsigned* flags);
 

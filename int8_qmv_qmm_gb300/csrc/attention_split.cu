@@ -359,12 +359,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, const 
 }
 
 template <typename T, int D>
-void launch_t(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st) {
+cudaError_t launch_t(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st) {
   using L = Layout<D>;
   static_assert(L::kListAt + kMaxSlots * int(sizeof(Slot)) <= 227 * 1024, "it fits");
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(split_kernel<T, D>), L::bytes(kMaxSlots), &done))
-    return;
+    return cudaGetLastError();
   const SplitScratch sc = split_scratch(workspace, sm_count());
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sc.warps / kSplitWarps));
@@ -376,13 +376,13 @@ void launch_t(const Args& a, void* workspace, bool join, unsigned flags, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, sc.parts, sc.splits);
-  if (!join) return;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, split_kernel<T, D>, a, sc.parts, sc.splits);
+  if (e != cudaSuccess || !join) return e;
   cfg.gridDim = dim3(unsigned(sm_count() * kSplitJoinPerSm));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, sc);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, sc);
 }
 
 }  // namespace
@@ -393,13 +393,13 @@ size_t split_workspace_size(int head_dim) {
   return warps * (sizeof(Split) + 2 * kSplitTile * (head_dim + 2) * 4);
 }
 
-void launch_split(const Args& a, void* workspace, bool join, unsigned flags, cudaStream_t st) {
+cudaError_t launch_split(const Args& a, void* workspace, bool join, unsigned flags,
+                         cudaStream_t st) {
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, join, flags, st)
-                       : launch_t<__half, 128>(a, workspace, join, flags, st);
-  else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, join, flags, st)
-                       : launch_t<__nv_bfloat16, 128>(a, workspace, join, flags, st);
+    return a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, join, flags, st)
+                              : launch_t<__half, 128>(a, workspace, join, flags, st);
+  return a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, join, flags, st)
+                            : launch_t<__nv_bfloat16, 128>(a, workspace, join, flags, st);
 }
 
 cudaError_t split_take_status(unsigned* flags) {

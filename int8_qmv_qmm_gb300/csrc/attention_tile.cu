@@ -683,10 +683,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <typename T, int D>
-void launch_t(const Args& a, void* workspace, const SplitScratch& sc, cudaStream_t st) {
+cudaError_t launch_t(const Args& a, void* workspace, const SplitScratch& sc, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(tile_kernel<T, D>), Layout<D>::kBytes, &done))
-    return;
+    return cudaGetLastError();
   const int sms = sm_count();
   float* parts = static_cast<float*>(workspace);
   cudaLaunchConfig_t cfg = {};
@@ -701,11 +701,12 @@ void launch_t(const Args& a, void* workspace, const SplitScratch& sc, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<T, D>, a, parts, sms);
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(unsigned((kTileJoinPerSm + kSplitJoinPerSm) * sms));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts), sc, sms);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, static_cast<const float*>(parts), sc, sms);
 }
 
 }  // namespace
@@ -714,14 +715,13 @@ size_t tile_workspace_size(int head_dim) {
   return head_dim == 64 || head_dim == 128 ? size_t(sm_count()) * kCtaRows * (head_dim + 2) * 4 : 0;
 }
 
-void launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st) {
+cudaError_t launch_tile(const Args& a, void* workspace, void* split_workspace, cudaStream_t st) {
   const SplitScratch sc = split_scratch(split_workspace, sm_count());
   if (a.c.dtype == QLIN_F16)
-    a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, sc, st)
-                       : launch_t<__half, 128>(a, workspace, sc, st);
-  else
-    a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, sc, st)
-                       : launch_t<__nv_bfloat16, 128>(a, workspace, sc, st);
+    return a.c.head_dim == 64 ? launch_t<__half, 64>(a, workspace, sc, st)
+                              : launch_t<__half, 128>(a, workspace, sc, st);
+  return a.c.head_dim == 64 ? launch_t<__nv_bfloat16, 64>(a, workspace, sc, st)
+                            : launch_t<__nv_bfloat16, 128>(a, workspace, sc, st);
 }
 
 cudaError_t tile_take_status(unsigned* flags) {

@@ -32,12 +32,16 @@ qlin_status launch_cache_attention(const void* q, int64_t q_stride, void* out,
                              scale * 1.4426950408889634f,
                              max_new};
   const bool tile = int64_t(max_new) * a.group > attention::kSplitRows;
-  attention::launch_split(a, workspace, !tile, flags, st);
-  if (tile)
-    attention::launch_tile(
+  // (a kernel whose predecessor was not launched would read what it never wrote)
+  cudaError_t e = attention::launch_split(a, workspace, !tile, flags, st);
+  if (e == cudaSuccess && tile)
+    e = attention::launch_tile(
         a, static_cast<uint8_t*>(workspace) + attention::split_workspace_size(c.head_dim),
         workspace, st);
-  return check_launch("qlin_cache_attention");
+  const qlin_status s = check_launch("qlin_cache_attention");
+  return e == cudaSuccess || s != QLIN_OK
+             ? s
+             : fail(QLIN_ERR_CUDA, "qlin_cache_attention: %s", cudaGetErrorString(e));
 }
 
 cudaError_t attention_take_device_status(unsigned* flags) {
