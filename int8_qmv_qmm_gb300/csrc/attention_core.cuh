@@ -329,14 +329,18 @@ struct Warp {
     }
   }
 
-  // The first of the tail's `count` tokens with a value that is not finite, else count.
-  __device__ static int first_lost(const T* values, int count, int lane) {
+  // The first of the tail's tokens from about `from` on with a value that is not
+  // finite, else count.
+  __device__ static int first_lost(const T* values, int from, int count, int lane) {
     constexpr uint32_t kExponent = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
     constexpr uint32_t kOne = kExponent & -kExponent;  // carries out of a full exponent
+    const unsigned g0 = unsigned(from) / 8, groups = unsigned(count - 1) / 8 - g0 + 1;
     int lost = count;
-#pragma unroll 8
-    for (int u = lane; u < kBlock * D / 8; u += 32) {
-      const uint4 v = *reinterpret_cast<const uint4*>(values + 8 * u);
+#pragma unroll 4
+    for (unsigned u = lane; u < D * groups; u += 32) {  // 8 tokens of a dimension each
+      const unsigned t0 = 8 * (g0 + u % groups);
+      const T* at = values + u / groups * kBlock + t0;
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t any = 0;
 #pragma unroll
@@ -344,21 +348,21 @@ struct Warp {
       if (any & 0x80008000u) {
 #pragma unroll 1
         for (int e = 0; e < 8; ++e)
-          if ((reinterpret_cast<const uint16_t*>(values)[8 * u + e] & kExponent) == kExponent)
-            lost = min(lost, 8 * u % kBlock + e);
+          if ((reinterpret_cast<const uint16_t*>(at)[e] & kExponent) == kExponent)
+            lost = min(lost, int(t0) + e);
       }
     }
     return __reduce_min_sync(0xffffffffu, lost);
   }
 
   // The tail: `count` tokens of T, the rest of its memory undefined.  Products
-  // in T (the queries come from memory again: q is f16).  `uneven`: not every row
-  // sees all of them, and a value that is not finite must not reach, as 0 times it,
-  // the rows that do not.  Then values from its token on are left out, and the rows
-  // that see it are NaN.  (Looking first: 12 x 3 drafts 30.1 -> 31.0 us; beside each
-  // product, 33.0.)
+  // in T (the queries come from memory again: q is f16).  All rows see its first
+  // `common` tokens.  A value of the others that is not finite must not reach, as 0
+  // times it, the rows that do not see it: values from its token on are left out, and
+  // the rows that see it are NaN.  (Looking for one in the whole tail took 31.0 us for
+  // 12 x 3 drafts, beside each product 33.0; 30.1 without.)
   __device__ void tail(const T* kv, int count, const T* q_row, float scale_log2,
-                       const int (&seen)[2], bool uneven, int lane) {
+                       const int (&seen)[2], int common, int lane) {
     const int g = lane >> 2, t = lane & 3;
     float s[4][4];
     uint32_t w[D / 8];
@@ -383,7 +387,8 @@ struct Warp {
     scale[0] = scale[1] = scale_log2;
     softmax(s, scale, 0.f, seen, true, g, keep);
     rescale(keep);
-    const int lost = uneven ? first_lost(kv + kBlock * D, count, lane) : count;
+    const int lost =
+        common < count ? first_lost(kv + kBlock * D, max(common, 0), count, lane) : count;
     if (lost < count) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)

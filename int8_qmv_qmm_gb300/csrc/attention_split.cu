@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.tail(static_cast<const T*>(a.c.tail) +
                    (int64_t(p.slot) * a.c.kv_heads + p.kvh) * 2 * kBlock * D,
                s_slot[p.slot].total - j * kBlock, qp, a.scale_log2, seen,
-               first_pos < s_slot[p.slot].total - 1, lane);
+               first_pos + 1 - j * kBlock, lane);
       ++done;
     }
     __syncwarp();  // every lane has read the chunk and the info
