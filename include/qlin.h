@@ -393,8 +393,8 @@ qlin_status qlin_rope_table(float* table, int64_t n_positions, int rot_dim, doub
  * ties to even; 128 where the scale is 0).  A block with an element that is
  * not finite (in dtype: the rotation can pass f16's range) gets the scale
  * infinity and codes 128: it stands for NaN.
- * rot_dim: a multiple of 16, 0 .. head_dim.  qkv and q_out 16-byte aligned,
- * qkv_stride a multiple of 8.  A slot whose blocks pass max_blocks, a page
+ * rot_dim: a multiple of 16, 0 .. head_dim.  qkv and q_out 16-byte aligned
+ * and apart, qkv_stride a multiple of 8.  A slot whose blocks pass max_blocks, a page
  * outside n_pages, a position outside the table or rows outside n_tokens are
  * left out and set a device status bit (qlin_device_status).
  */
@@ -430,11 +430,18 @@ size_t qlin_cache_attention_workspace_size(int head_dim);
  *            overlap need workspaces of their own
  * What a row does not see does not reach it, whether it is finite or not; a
  * value that it sees and that is not finite makes it so.
- * Scores, softmax statistics and sums are float32; probabilities enter the
- * products in 16 bits.  q_heads: a multiple of kv_heads, at most 16 times as
- * many.  q and out 16-byte aligned, q_stride a multiple of 8.  Rows that no
- * slot owns are not written; blocks whose page is outside n_pages are left out
- * and set a device status bit.
+ * Scores, softmax statistics and sums are float32; exponentials are the
+ * hardware's (2 ulp).  Rounded to 16 bits on the way: probabilities, to f16 in
+ * units of the largest product of a probability and its block's value scale so
+ * far (2^-11 of each, or 2^-25 of that unit; a bf16 tail of few rows keeps 16
+ * bits of them); bf16 queries, to f16 after a power of two for each row (exact
+ * down to 2^-28 of the row's largest); with many rows a bf16 tail in the same
+ * way.  f16 outputs are up to 30% further from the exact ones than by their own
+ * rounding alone, bf16 ones 1%.
+ * q_heads: a multiple of kv_heads, at most 16 times as many.  q and out 16-byte
+ * aligned and apart, q_stride a multiple of 8.  Rows that no slot owns are not
+ * written; blocks whose page is outside n_pages are left out and set a device
+ * status bit.
  */
 qlin_status qlin_cache_attention(const void* q, int64_t q_stride, void* out,
                                  const qlin_kv_cache* cache, const int32_t* starts,

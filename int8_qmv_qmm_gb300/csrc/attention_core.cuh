@@ -26,12 +26,23 @@ namespace attention {
 
 // Slots with more rows go to the tile kernel.  The split kernel's time grows with the
 // rows, 8 of them a pass over the cache, the tile kernel's does not up to 256, but it
-// starts 20 us behind.  By rows, split against tile, us, head dimension 128:
-//     slots x tokens     32 rows      64 rows      96 rows     128 rows
-//     1 x 400           17  / 42     19  / 41     19  / 41     23  / 41
-//     8 x 8000          70  / 120    106 / 127    131 / 127    190 / 128
-//     32 x 8000         258 / 264    303 / 241    504 / 275    485 / 244
-// (at 64: 8 x 8000 56 / 98, 71 / 100, 109 / 102, 126 / 102).
+// starts behind: by 13 to 20 us with f16, 40 to 70 with a bf16 tail, which its widening
+// warps go over twice.  Split against tile, us, 8 key/value heads, caches flushed:
+//     slots x tokens        32 rows     64 rows     96 rows    128 rows
+//     1 x 400,  f16 64     15 / 28     15 / 28     17 / 29     19 / 28
+//               f16 128    17 / 39     19 / 39     19 / 38     20 / 39
+//               bf16 64    17 / 55     17 / 54     19 / 55     19 / 55
+//               bf16 128   17 / 90     19 / 92     21 / 90     21 / 90
+//     8 x 8000, f16 64     66 / 92    113 / 92    160 / 92    207 / 92
+//               f16 128   100 / 114   151 / 114   213 / 116   277 / 114
+//               bf16 64    67 / 120   115 / 120   163 / 120   210 / 120
+//               bf16 128  101 / 169   153 / 170   218 / 170   283 / 172
+//     32 x 8000, f16 64   216 / 247   394 / 247   572 / 247   765 / 250
+//               f16 128   370 / 314   568 / 315   791 / 317  1234 / 317
+//               bf16 64   218 / 299   399 / 299   584 / 299   773 / 300
+//               bf16 128  369 / 420   573 / 424   799 / 425  1221 / 425
+// The rule goes by rows alone, since the lengths are on the device only: 64 serves short
+// caches and bf16; many long f16 caches would want 32.
 constexpr int kSplitRows = 64;
 
 struct Args {

@@ -3,8 +3,8 @@
 // What bounds it is reading the cache once, so the blocks of all slots, heads
 // and row tiles are put in one list and every warp takes an equal, consecutive
 // share of it, however long or short the slots are.  One sequence of 131071
-// tokens, 8 heads of 128 (269 MB): 51 us, 5.3 TB/s, and 59 with the join; 32 of up
-// to 8192, 8 heads of 64 (185 MB): 43 us, 4.4 TB/s, and 49.  There a block's
+// tokens, 8 heads of 128 (269 MB): 50 us, 5.4 TB/s, and 60 with the join; 32 of up
+// to 8192, 8 heads of 64 (185 MB): 42 us, 4.4 TB/s, and 49.  There a block's
 // instructions (the widening of its codes, the softmax of 64 tokens) take longer
 // than its bytes.
 //
@@ -15,8 +15,8 @@
 //
 // A piece is what a warp has of one tile (slot, key/value head, 8 rows).  A tile
 // that lies in one warp's share is written out; of the others each warp leaves
-// its part in the workspace, and a second kernel, launched while the first still
-// runs, joins the parts in the list's order.
+// its part in the workspace, and another kernel (attention_join.cuh), launched while
+// this one still runs, joins the parts in the list's order.
 
 #include "attention_join.cuh"
 #include "attention_ptx.cuh"

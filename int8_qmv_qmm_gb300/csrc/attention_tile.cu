@@ -8,8 +8,9 @@
 //   P            = exp2(S * scale - max)     (row by row, in registers)
 //   O [128 x D] += P [128 x 64] . values     (A: P in tensor memory, over S)
 // with S, P and O in tensor memory and both operands of every product in f16:
-// the codes are exact in it (a bf16 tail is scaled by a power of two for the
-// block, bf16 queries by one for each row).  S has two buffers a tile, so the
+// the codes are exact in it (a bf16 tail is scaled by a power of two for its keys and
+// one for its values, exact down to 2^-28 and 2^-23 of the largest and rounded at 2^-31
+// below; bf16 queries by one for each row, exact down to 2^-28).  S has two buffers a tile, so the
 // scores of the next block are there when the exponentials of this one are done
 // (with one, and q in tensor memory beside it, a tile waited for its products
 // two fifths of the time: 375 us for two chunks of 2048 tokens over 6001).
@@ -29,16 +30,19 @@
 //
 // Whole tiles leave some SMs idle in the last round.  What is left after the last
 // full round (at most half of the SMs' number) is therefore cut along the cache,
-// one piece for each SM; the pieces' sums go to the workspace, and a second kernel
-// joins them.
+// one piece for each SM; the pieces' sums go to the workspace, and the last kernel
+// of the call joins them.
 //
-// What bounds it: at D = 128 the products (1024 cycles of the tensor core for a
-// block of both tiles), at D = 64 the way of a block through a tile's four warps
-// (1660 cycles, of which the exponentials of both tiles take 1024; a quarter or an
-// eighth of them by polynomial on the multiply-add pipe made it 10% longer).  Two chunks of 2048 over 6001,
-// 32 query heads of 128: 351 us, 900 TFLOP/s, of which the products alone would be
-// 163 us at the library's rate; a 128 x 64 x 16 product takes 49 to 55 cycles here,
-// not 32, and the widening, the exponentials and their hand-overs hide behind it.
+// What bounds it: at D = 128 a block of both tiles takes about 2650 cycles, and no
+// unit is busy that long.  Its 32 products take 49 to 55 cycles each (1570 to 1760;
+// the tensor core needs 32, but a product of the scores reads 6 KB of operands from
+// shared memory, 48 cycles), all shared-memory traffic 192 KB (1536), the exponentials
+// 1024; the last third is hand-overs between them.  bf16 spills 216 bytes there: 14
+// warps leave 128 registers.  At D = 64 it is the way of a block through a tile's four
+// warps (1660 cycles, of which the exponentials of both tiles take 1024; a quarter or
+// an eighth of them by polynomial on the multiply-add pipe made it 10% longer).  Two
+// chunks of 2048 over 6001, 32 query heads of 128: 351 us, 900 TFLOP/s; the products
+// alone would be 163 us at the library's rate.
 
 #include "attention_join.cuh"
 #include "attention_ptx.cuh"

@@ -67,7 +67,9 @@ class Decoder:
         self.workspace = attention_workspace(head_dim, self.device)
         self.lens = lens
         self.held = [0] * slots  # the same on the host
-        self.logits = None       # of the last call, float32 [slots, vocab]
+        # of the last call, float32 [slots, vocab] (rows of slots that got no tokens in it
+        # are not theirs)
+        self.logits = None
 
         def row(value, dt=torch.float32):
             return torch.full((slots,), value, dtype=dt, device=self.device)
