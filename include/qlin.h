@@ -403,6 +403,19 @@ qlin_status qlin_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
                              int interleaved, const qlin_kv_cache* cache, const int32_t* starts,
                              int64_t n_tokens, int q_heads, unsigned flags, void* stream);
 
+/*
+ * qlin_rope_append with a norm of each query and key head before the rotation:
+ *   x[i] * w[i] / sqrt(mean_i(x[i]*x[i]) + eps)   over the head's elements,
+ * in float32, not rounded before the rotation.  q_norm and k_norm: dtype
+ * [head_dim], 16-byte aligned; eps finite, >= 0.  Values are not normed, nor
+ * what the cache holds already.  All else as qlin_rope_append.
+ */
+qlin_status qlin_norm_rope_append(const void* qkv, int64_t qkv_stride, const void* q_norm,
+                                  const void* k_norm, float eps, void* q_out, const float* table,
+                                  int64_t n_positions, int rot_dim, int interleaved,
+                                  const qlin_kv_cache* cache, const int32_t* starts,
+                                  int64_t n_tokens, int q_heads, unsigned flags, void* stream);
+
 /* The values that n pages of the cache stand for, out dtype
  * [n][kv_heads][2][64*head_dim] in the pages' layouts (16-byte aligned):
  * (c - 128) * scale in float32, rounded once.  page_ids: int32 [n] on the
@@ -474,6 +487,106 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
                         qlin_dtype ldtype, unsigned flags, void* stream);
 
 /*
+ * Log probabilities of rows of logits, ldtype [M][V] (QLIN_F32, F16 or BF16;
+ * rows logits_stride elements apart), in float32:
+ *   logprobs[m]  x[tokens[m]] - log sum_i exp(x[i]); -infinity for a token
+ *                outside 0 .. V-1
+ *   entropy[m]   -sum_i p_i log p_i
+ *   top_tokens, top_logprobs   [M][top]: the likeliest tokens, larger logits
+ *                first, equal ones by index (0 <= top <= 32; may be NULL with 0)
+ * NaN logits count as -infinity; a row of nothing else has logprob -infinity
+ * and entropy 0; with +infinity among the logits only those have a share, equal
+ * ones.  Where fewer than top logits are above -infinity the rest of top_tokens
+ * is -1, of top_logprobs -infinity.  1 <= V <= 262144.
+ */
+qlin_status qlin_token_logprobs(const void* logits, int64_t logits_stride, const int32_t* tokens,
+                                float* logprobs, float* entropy, int top, int32_t* top_tokens,
+                                float* top_logprobs, int64_t M, int64_t V, qlin_dtype ldtype,
+                                unsigned flags, void* stream);
+
+/* ==========================================================================
+ * Experts: routing, the packed products of each token's experts, and their
+ * weighted sum (additions of this library, like the calls above).
+ *
+ * Token t's j-th expert is pair t*top_k + j.  A routing is
+ *   experts  int32 [T][top_k]: -1 for none
+ *   weights  float [T][top_k]
+ *   order    int32 [T*top_k]: the pairs by expert, those of one expert in their
+ *            own order, pairs without an expert after all others
+ *   offsets  int32 [E+1]: where each expert's pairs start in order;
+ *            offsets[E] is the number of pairs that have an expert
+ * At most 512 experts, 32 of them for a token.
+ * ======================================================================== */
+#define QLIN_SOFTMAX 0
+#define QLIN_SIGMOID 1
+#define QLIN_GROUP_MAX 0
+#define QLIN_GROUP_TOP2 1
+
+/* Bytes of device scratch that qlin_route_experts needs (0 for few tokens). */
+size_t qlin_route_experts_workspace_size(int64_t T, int E);
+
+/*
+ * Chooses top_k of E experts for each of T rows of logits (ldtype; rows
+ * logits_stride elements apart), in float32:
+ *   scores   QLIN_SOFTMAX: exp(x - max) / sum, QLIN_SIGMOID: 1 / (1 + exp(-x))
+ *   choice   scores + bias (float [E]: it chooses, and does not weigh); without
+ *            a bias (NULL) the order of choice is that of the logits
+ *   groups   E/groups neighbours make a group; its value is its largest choice
+ *            (QLIN_GROUP_MAX) or the sum of its two largest (QLIN_GROUP_TOP2;
+ *            without a bias, of the scores, for QLIN_SOFTMAX before the division
+ *            by their sum); only the top_groups groups of the largest values
+ *            take part
+ *   experts  the top_k largest choices in descending order
+ *   weights  their scores, with renormalise divided by their sum, times scale
+ * Equal choices and groups go to the lowest index.  A logit of -infinity (or
+ * NaN, which counts as that) is never chosen: where fewer than top_k remain the
+ * rest of the row is expert -1, weight 0.  With T = 0 offsets is still written.
+ * groups: 1 .. 32, a divisor of E.  workspace: qlin_route_experts_workspace_size
+ * bytes with anything in them (NULL where that is 0); calls that can overlap
+ * need one each.
+ */
+qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const float* bias,
+                               int scoring, int groups, int top_groups, int group_score, int top_k,
+                               int renormalise, float scale, int32_t* experts, float* weights,
+                               int32_t* order, int32_t* offsets, int64_t T, int E,
+                               qlin_dtype ldtype, void* workspace, size_t workspace_bytes,
+                               unsigned flags, void* stream);
+
+/*
+ * y[p] = x[p / pairs_per_row] . W_hat[e]^T for every pair p of each expert e of
+ * a plan (order, offsets), from packed weights as above with E in front:
+ *   wq       uint32 [E][N][K*bits/32]
+ *   scales, biases   dtype [E][N][K/group_size]
+ *   x        dtype [n_pairs / pairs_per_row][x_stride]: pairs_per_row = top_k
+ *            for a row for each token, 1 for a row for each pair
+ *   y        y_dtype [n_pairs][N] (dtype, one rounding, or QLIN_F32); rows of
+ *            pairs without an expert are not written
+ * float32 sums; accuracy as qlin_linear.  x and wq 16-byte aligned, x_stride a
+ * multiple of 8; y apart from all else.  Experts whose offsets are not a plan's
+ * and pairs outside n_pairs are left out and set a device status bit.
+ * QLIN_OVERLAP_PREVIOUS: as for qlin_qmv_ex (weights may be read before the
+ * preceding kernel has completed; x, order and offsets are not).
+ */
+qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_row,
+                               const int32_t* order, const int32_t* offsets, int64_t n_pairs,
+                               const uint32_t* wq, const void* scales, const void* biases, void* y,
+                               int E, int64_t N, int64_t K, int bits, int group_size,
+                               qlin_dtype dtype, qlin_dtype y_dtype, unsigned flags,
+                               void* stream);
+
+/*
+ * out[t] = add[t] + sum_j weights[t][j] * y[t*top_k + j]  over the j with
+ * experts[t][j] >= 0 (the rows of the others are not read), float32 sums in the
+ * order of j, one rounding.  y: y_dtype [T*top_k][N] (dtype or QLIN_F32); add:
+ * dtype, rows add_stride elements apart, or NULL; out: dtype [T][N], may be add
+ * with add_stride = N.  top_k at most 32.
+ */
+qlin_status qlin_combine_experts(const void* y, const int32_t* experts, const float* weights,
+                                 const void* add, int64_t add_stride, void* out, int64_t T,
+                                 int top_k, int64_t N, qlin_dtype dtype, qlin_dtype y_dtype,
+                                 unsigned flags, void* stream);
+
+/*
  * Read and clear the device status words of the current device (synchronises
  * the device).  *flags receives 0 when no kernel gave up a bounded wait since
  * the last call, else a bit mask of the waits that gave up (bits 0-7: the
@@ -482,7 +595,8 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
  * outside n_tokens or a negative length, 25: a page outside n_pages or a slot
  * past max_blocks, 26: a position outside the table, 27: a slot with more than
  * max_new rows, 28: a wait of the attention kernel that gave up), or in sampling
- * (bit 29: a bound that no bin passed was left out).  Returns QLIN_OK, or
+ * (bit 29: a bound that no bin passed was left out), or in the experts' products
+ * (bit 30: a plan that is none was left out, or a wait gave up).  Returns QLIN_OK, or
  * QLIN_ERR_CUDA if the device could not be read.  No counterpart on the pages:
  * an addition of this library (a kernel that gives up a wait reports instead
  * of hanging, the device-side form of failing fast).

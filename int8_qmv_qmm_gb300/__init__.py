@@ -14,7 +14,8 @@ activations ``x`` [M, K], output ``y`` [M, N].
 
 Beside the linears stand what a decoder runs between them: ``add_rms_norm``,
 ``rope_table`` / ``rope_append``, ``KVCache`` with ``cache_attention`` and
-``cache_dequant``, and ``sample``.
+``cache_dequant``, ``sample`` and ``token_logprobs``; and for layers of experts
+``route_experts`` (a ``Routing``), ``expert_linear`` and ``combine_experts``.
 """
 
 from __future__ import annotations
@@ -31,6 +32,7 @@ __all__ = [
     "crossover_m", "device_status", "QLIN_F32", "QLIN_F16", "QLIN_BF16", "Link", "make_links",
     "chain_workspace", "qmv_chain", "KVCache", "add_rms_norm", "rope_table", "rope_append",
     "cache_dequant", "attention_workspace", "cache_attention", "sample", "KV_BLOCK",
+    "token_logprobs", "Routing", "route_experts", "expert_linear", "combine_experts",
 ]
 
 QLIN_F32, QLIN_F16, QLIN_BF16 = 0, 1, 2
@@ -68,6 +70,9 @@ _SIGNATURES = {
     "qlin_rope_table": (_c_int, [_c_vp, _c_i64, _c_int] + [ctypes.c_double] * 4 + [_c_vp]),
     "qlin_rope_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_int, _c_int, _c_vp,
                                   _c_vp, _c_i64, _c_int, ctypes.c_uint, _c_vp]),
+    "qlin_norm_rope_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp,
+                                       _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_i64, _c_int,
+                                       ctypes.c_uint, _c_vp]),
     "qlin_cache_dequant": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
     "qlin_cache_attention_workspace_size": (ctypes.c_size_t, [_c_int]),
     "qlin_cache_attention": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_int,
@@ -75,6 +80,16 @@ _SIGNATURES = {
                                       ctypes.c_uint, _c_vp]),
     "qlin_sample": (_c_int, [_c_vp, _c_i64] + [_c_vp] * 7 + [_c_i64, _c_i64, _c_int,
                                                              ctypes.c_uint, _c_vp]),
+    "qlin_token_logprobs": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp,
+                                     _c_i64, _c_i64, _c_int, ctypes.c_uint, _c_vp]),
+    "qlin_route_experts_workspace_size": (ctypes.c_size_t, [_c_i64, _c_int]),
+    "qlin_route_experts": (_c_int, [_c_vp, _c_i64, _c_vp] + [_c_int] * 6 + [ctypes.c_float]
+                           + [_c_vp] * 4 + [_c_i64, _c_int, _c_int, _c_vp, ctypes.c_size_t,
+                                            ctypes.c_uint, _c_vp]),
+    "qlin_expert_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_i64] + [_c_vp] * 4
+                           + [_c_int, _c_i64, _c_i64] + [_c_int] * 4 + [ctypes.c_uint, _c_vp]),
+    "qlin_combine_experts": (_c_int, [_c_vp] * 4 + [_c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int,
+                                                    _c_int, ctypes.c_uint, _c_vp]),
     # include/qlin_testing.h: failure paths and host-side choices, for the
     # library's own tests
     "qlin_testing_qmv_chain_stalled": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int,
@@ -467,12 +482,14 @@ def rope_table(n_positions: int, rot_dim: int, base: float = 10000.0, factor: fl
 
 
 def rope_append(qkv, table, cache: KVCache, starts, q_heads: int, interleaved: bool = False,
-                out=None, overlap_previous=False):
+                out=None, overlap_previous=False, q_norm=None, k_norm=None, eps: float = 1e-6):
     """Rotates new tokens' queries and keys and appends keys and values to the cache.
 
     qkv [T, (q_heads + 2*kv_heads)*head_dim] (a fused linear's output; rows may
     be strided), table from rope_table (None: no rotation), starts int32
-    [slots+1].  Returns the rotated queries [T, q_heads, head_dim]."""
+    [slots+1].  q_norm and k_norm [head_dim], both or neither: each query and key
+    head is first normed, x * weight / sqrt(mean(x*x) + eps), in the same pass.
+    Returns the rotated queries [T, q_heads, head_dim]."""
     dt, d, shape, index = cache.dtype, cache.head_dim, qkv.shape, cache._index
     n_pos = rot = 0
     t_ptr = None
@@ -486,6 +503,12 @@ def rope_append(qkv, table, cache: KVCache, starts, q_heads: int, interleaved: b
               and table.get_device() == index)
         rot = 2 * pairs
         t_ptr = table.data_ptr() if rot else None
+    normed = q_norm is not None or k_norm is not None
+    if ok and normed:
+        ok = (q_norm is not None and k_norm is not None and q_norm.dtype is dt
+              and k_norm.dtype is dt and q_norm.get_device() == index
+              and k_norm.get_device() == index and q_norm.is_contiguous()
+              and k_norm.is_contiguous() and q_norm.shape == (d,) and k_norm.shape == (d,))
     if ok:
         if out is None:
             out = torch.empty((shape[0], q_heads, d), dtype=dt, device=cache.device)
@@ -505,11 +528,20 @@ def rope_append(qkv, table, cache: KVCache, starts, q_heads: int, interleaved: b
                                    and table.dtype == torch.float32 and table.is_contiguous()
                                    and table.device == cache.device),
                  "table must be float32 [n_positions, rot_dim/2, 2] on the cache's device"),
+                ((q_norm is None) == (k_norm is None), "q_norm and k_norm come together"),
+                (all(w is None or (w.dtype == dt and w.device == cache.device
+                                   and w.is_contiguous() and tuple(w.shape) == (d,))
+                     for w in (q_norm, k_norm)),
+                 "q_norm and k_norm must be [head_dim] in the cache's dtype, on its device"),
                 (False, "out must be contiguous [T, q_heads, head_dim] in qkv's dtype"))
-    status = lib().qlin_rope_append(
-        qkv.data_ptr(), _row_stride(qkv, shape[1]), out.data_ptr(), t_ptr, n_pos, rot,
-        1 if interleaved else 0, cache._ref, starts.data_ptr(), shape[0], q_heads,
-        1 if overlap_previous else 0, _current_raw_stream(index))
+    rest = (out.data_ptr(), t_ptr, n_pos, rot, 1 if interleaved else 0, cache._ref,
+            starts.data_ptr(), shape[0], q_heads, 1 if overlap_previous else 0,
+            _current_raw_stream(index))
+    if normed:
+        status = lib().qlin_norm_rope_append(qkv.data_ptr(), _row_stride(qkv, shape[1]),
+                                             q_norm.data_ptr(), k_norm.data_ptr(), eps, *rest)
+    else:
+        status = lib().qlin_rope_append(qkv.data_ptr(), _row_stride(qkv, shape[1]), *rest)
     if status:
         _check(status)
     return out
@@ -639,6 +671,217 @@ def sample(logits, u, temperature, top_k, top_p, min_p, tokens=None, probs=None,
     if status:
         _check(status)
     return tokens, probs
+
+
+def token_logprobs(logits, tokens, top: int = 0, overlap_previous=False):
+    """Log probabilities of given tokens [M] (int32) under rows of logits [M, V]
+    (float32, float16 or bfloat16; rows may be strided).
+
+    Returns (logprobs [M], entropy [M], top_tokens int32 [M, top], top_logprobs
+    [M, top]), float32 (natural logarithms); the top tokens come in descending
+    order, equal logits by index.  qlin_token_logprobs says what rows with NaN
+    and infinities give."""
+    shape, index = logits.shape, logits.get_device()
+    m = shape[0] if len(shape) == 2 else -1
+    if not (logits.is_cuda and m >= 0 and logits.stride(1) == 1 and logits.dtype in _DTYPE_CODE
+            and tokens.dtype is torch.int32 and tokens.get_device() == index
+            and tokens.is_contiguous() and tokens.numel() == m and 0 <= top <= 32):
+        _refuse((logits.is_cuda and m >= 0 and logits.stride(-1) == 1,
+                 "logits must be a 2-D CUDA tensor with contiguous rows"),
+                (logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16"),
+                (0 <= top <= 32, "top must be 0 .. 32"),
+                (False, "tokens must be int32 [M] on the logits' device"))
+    # one allocation: two values a row, then the top ones and their tokens
+    values = torch.empty(m * (2 + 2 * top), dtype=torch.float32, device=logits.device)
+    logprobs, entropy, top_logprobs, top_tokens = values.split((m, m, m * top, m * top))
+    top_tokens = top_tokens.view(torch.int32)
+    status = lib().qlin_token_logprobs(
+        logits.data_ptr(), _row_stride(logits, shape[1]), tokens.data_ptr(), logprobs.data_ptr(),
+        entropy.data_ptr(), top, top_tokens.data_ptr(), top_logprobs.data_ptr(), m, shape[1],
+        _DTYPE_CODE[logits.dtype], 1 if overlap_previous else 0, _current_raw_stream(index))
+    if status:
+        _check(status)
+    return logprobs, entropy, top_tokens.view(m, top), top_logprobs.view(m, top)
+
+
+class Routing:
+    """Which experts each token goes to, and the plan that groups their rows
+    (include/qlin.h): experts int32 and weights float32 [T, top_k], order int32
+    [T*top_k], offsets int32 [n_experts + 1], on one device.  Token t's j-th
+    expert is pair t*top_k + j; expert -1 is none."""
+
+    def __init__(self, experts, weights, order, offsets):
+        _need_cuda(experts, weights, order, offsets)
+        _need(experts.dim() == 2 and experts.dtype == torch.int32 and experts.shape[1] >= 1,
+              "experts must be int32 [T, top_k]")
+        _need(weights.dtype == torch.float32 and weights.shape == experts.shape,
+              "weights must be float32 [T, top_k]")
+        _need(order.dtype == torch.int32 and tuple(order.shape) == (experts.numel(),),
+              "order must be int32 [T*top_k]")
+        _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.shape[0] >= 2,
+              "offsets must be int32 [n_experts + 1]")
+        _need(len({t.device for t in (experts, weights, order, offsets)}) == 1,
+              "a routing's tensors must be on one device")
+        self._set(experts, weights, order, offsets)
+
+    def _set(self, experts, weights, order, offsets):
+        self.experts, self.weights, self.order, self.offsets = experts, weights, order, offsets
+        self.tokens, self.top_k = experts.shape
+        self.pairs, self.n_experts = self.tokens * self.top_k, offsets.shape[0] - 1
+        self._index = experts.get_device()
+        return self
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORE = {"max": 0, "top2": 1}
+
+
+def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int = 1, group_score: str = "max", renormalise: bool = True,
+                  scale: float = 1.0, overlap_previous=False) -> Routing:
+    """Chooses top_k experts for each row of logits [T, n_experts] (float32,
+    float16 or bfloat16; rows may be strided) and plans their products.
+
+    scoring: "softmax" or "sigmoid"; bias float32 [n_experts] is added to the
+    scores for the choice alone; with groups only the top_groups of them take
+    part, by their largest choice ("max") or the sum of their two largest
+    ("top2"); weights are the chosen scores, divided by their sum with
+    renormalise, times scale (qlin_route_experts has it in full)."""
+    shape, index = logits.shape, logits.get_device()
+    if not (logits.is_cuda and len(shape) == 2 and logits.stride(1) == 1
+            and logits.dtype in _DTYPE_CODE and scoring in _SCORING
+            and group_score in _GROUP_SCORE and top_k >= 1 and shape[1] >= 1
+            and (bias is None or (bias.dtype is torch.float32 and bias.get_device() == index
+                                  and bias.is_contiguous() and bias.shape == shape[1:]))):
+        _refuse((logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1,
+                 "logits must be a 2-D CUDA tensor with contiguous rows"),
+                (logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16"),
+                (scoring in _SCORING, "scoring must be 'softmax' or 'sigmoid'"),
+                (group_score in _GROUP_SCORE, "group_score must be 'max' or 'top2'"),
+                (top_k >= 1 and shape[1] >= 1, "top_k and the number of experts must be positive"),
+                (False, "bias must be float32 [n_experts] on the logits' device"))
+    t, e = shape
+    L = lib()
+    pairs = t * top_k
+    size = int(L.qlin_route_experts_workspace_size(t, e)) // 4
+    # one allocation: experts, order, offsets and the scratch
+    ints = torch.empty(2 * pairs + e + 1 + size, dtype=torch.int32, device=logits.device)
+    weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    at = ints.data_ptr()
+    status = L.qlin_route_experts(
+        logits.data_ptr(), _row_stride(logits, e), None if bias is None else bias.data_ptr(),
+        _SCORING[scoring], groups, top_groups, _GROUP_SCORE[group_score], top_k,
+        1 if renormalise else 0, scale, at, weights.data_ptr(), at + 4 * pairs, at + 8 * pairs, t,
+        e, _DTYPE_CODE[logits.dtype], at + 8 * pairs + 4 * (e + 1) if size else None, 4 * size,
+        1 if overlap_previous else 0, _current_raw_stream(index))
+    if status:
+        _check(status)
+    return Routing.__new__(Routing)._set(ints[:pairs].view(t, top_k), weights,
+                                         ints[pairs:2 * pairs], ints[2 * pairs:2 * pairs + e + 1])
+
+
+def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
+                  group_size: int = GROUP_SIZE, out=None, out_dtype=None, overlap_previous=False):
+    """The products of each token's experts: row p = t*top_k + j of the result is
+    x's row of that pair times the weights of expert routing.experts[t, j].
+
+    x [T, K] (a row for each token) or [T*top_k, K] (a row for each pair), rows
+    strided by a multiple of 8 elements; wq int32 [n_experts, N, K*bits/32],
+    scales and biases [n_experts, N, K/64] in x's dtype.  Returns [T*top_k, N] in
+    x's dtype or float32 (out_dtype); rows of pairs without an expert are left as
+    they are.  overlap_previous: as for qmv."""
+    dt, shape, index = x.dtype, x.shape, x.get_device()
+    out_dtype = out_dtype or (dt if out is None else out.dtype)
+    pairs = routing.pairs
+    ok = (index >= 0 and index == routing._index and len(shape) == 2 and x.stride(1) == 1
+          and (dt is torch.float16 or dt is torch.bfloat16)
+          and (shape[0] == routing.tokens or shape[0] == pairs)
+          and (out_dtype is dt or out_dtype is torch.float32)
+          and wq.dim() == 3 and wq.is_contiguous() and wq.get_device() == index
+          and wq.element_size() == 4 and wq.shape[0] == routing.n_experts
+          and wq.shape[2] * 32 == shape[1] * bits and scales.is_contiguous()
+          and biases.is_contiguous() and scales.dtype is dt and biases.dtype is dt
+          and scales.get_device() == index and biases.get_device() == index
+          and scales.shape == biases.shape
+          and scales.shape == (wq.shape[0], wq.shape[1], shape[1] // group_size))
+    if ok:
+        n = wq.shape[1]
+        if out is None:
+            out = torch.empty((pairs, n), dtype=out_dtype, device=x.device)
+        else:
+            ok = (out.get_device() == index and out.is_contiguous() and out.dtype is out_dtype
+                  and out.shape == (pairs, n))
+    if not ok:
+        _refuse((x.is_cuda and len(shape) == 2 and x.stride(1) == 1
+                 and dt in (torch.float16, torch.bfloat16),
+                 "x must be a 2-D float16 or bfloat16 CUDA tensor with contiguous rows"),
+                (index == routing._index, "x must be on the routing's device"),
+                (shape[0] in (routing.tokens, pairs),
+                 "x must have a row for each token or one for each pair"),
+                (out_dtype in (dt, torch.float32), "out_dtype must be x's dtype or float32"),
+                (wq.dim() == 3 and wq.is_contiguous() and wq.device == x.device
+                 and wq.element_size() == 4 and wq.shape[0] == routing.n_experts
+                 and wq.shape[2] * 32 == shape[1] * bits,
+                 "wq must be contiguous int32 [n_experts, N, K*bits/32] on x's device"),
+                (all(t.is_contiguous() and t.dtype == dt and t.device == x.device
+                     and tuple(t.shape) == (wq.shape[0], wq.shape[1], shape[1] // group_size)
+                     for t in (scales, biases)),
+                 "scales and biases must be contiguous [n_experts, N, K/64] in x's dtype, on its "
+                 "device"),
+                (False, "out must be contiguous [T*top_k, N], on x's device, in out_dtype"))
+    status = lib().qlin_expert_linear(
+        x.data_ptr(), _row_stride(x, shape[1]), 1 if shape[0] == pairs else routing.top_k,
+        routing.order.data_ptr(), routing.offsets.data_ptr(), pairs, wq.data_ptr(),
+        scales.data_ptr(), biases.data_ptr(), out.data_ptr(), routing.n_experts, n, shape[1], bits,
+        group_size, _DTYPE_CODE[dt], _DTYPE_CODE[out_dtype], 1 if overlap_previous else 0,
+        _current_raw_stream(index))
+    if status:
+        _check(status)
+    return out
+
+
+def combine_experts(y, routing: Routing, add=None, out=None, out_dtype=None,
+                    overlap_previous=False):
+    """out[t] = add[t] + sum_j weights[t, j] * y[t*top_k + j] over the experts of
+    token t (rows of pairs without one are not read).
+
+    y [T*top_k, N] from expert_linear (float32 or the activation dtype), add
+    [T, N] in the activation dtype (rows may be strided).  Returns [T, N] in the
+    activation dtype: y's, or for float32 y that of add or out_dtype."""
+    shape, index, ydt = y.shape, y.get_device(), y.dtype
+    dt = (out.dtype if out is not None else out_dtype if out_dtype is not None
+          else add.dtype if add is not None else ydt)
+    t = routing.tokens
+    ok = (index >= 0 and index == routing._index and len(shape) == 2 and y.is_contiguous()
+          and shape[0] == routing.pairs and (dt is torch.float16 or dt is torch.bfloat16)
+          and (ydt is dt or ydt is torch.float32)
+          and (add is None or (add.get_device() == index and add.dtype is dt
+                               and add.shape == (t, shape[1]) and add.stride(1) == 1)))
+    if ok:
+        if out is None:
+            out = torch.empty((t, shape[1]), dtype=dt, device=y.device)
+        else:
+            ok = (out.get_device() == index and out.is_contiguous()
+                  and out.shape == (t, shape[1]))
+    if not ok:
+        _refuse((y.is_cuda and y.is_contiguous() and len(shape) == 2
+                 and shape[0] == routing.pairs and index == routing._index,
+                 "y must be contiguous [T*top_k, N] on the routing's device"),
+                (dt in (torch.float16, torch.bfloat16),
+                 "the result must be float16 or bfloat16 (out_dtype)"),
+                (ydt in (dt, torch.float32), "y must be float32 or in the result's dtype"),
+                (add is None or (add.device == y.device and add.dtype == dt
+                                 and tuple(add.shape) == (t, shape[1]) and add.stride(1) == 1),
+                 "add must be [T, N] with contiguous rows in the result's dtype"),
+                (False, "out must be contiguous [T, N] on y's device"))
+    status = lib().qlin_combine_experts(
+        y.data_ptr(), routing.experts.data_ptr(), routing.weights.data_ptr(),
+        None if add is None else add.data_ptr(), 0 if add is None else _row_stride(add, shape[1]),
+        out.data_ptr(), t, routing.top_k, shape[1], _DTYPE_CODE[dt], _DTYPE_CODE[ydt],
+        1 if overlap_previous else 0, _current_raw_stream(index))
+    if status:
+        _check(status)
+    return out
 
 
 def crossover_m(n: int, k: int, bits: int, dtype: torch.dtype = torch.float16) -> int:

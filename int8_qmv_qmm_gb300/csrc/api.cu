@@ -358,7 +358,7 @@ qlin_status qlin_linear_ex(const void* x, const uint32_t* wq, const void* scales
 qlin_status qlin_device_status(int* flags) {
   g_last_error[0] = 0;
   if (!flags) return fail(QLIN_ERR_INVALID_ARG, "qlin_device_status: null pointer");
-  unsigned fm = 0, fv = 0, fc = 0, fr = 0, fa = 0, fs = 0;
+  unsigned fm = 0, fv = 0, fc = 0, fr = 0, fa = 0, fs = 0, fe = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = qmm_take_device_status(&fm);
   if (e == cudaSuccess) e = qmv_take_device_status(&fv);
@@ -366,12 +366,15 @@ qlin_status qlin_device_status(int* flags) {
   if (e == cudaSuccess) e = rope_take_device_status(&fr);
   if (e == cudaSuccess) e = attention_take_device_status(&fa);
   if (e == cudaSuccess) e = sample_take_device_status(&fs);
+  if (e == cudaSuccess) e = expert_take_device_status(&fe);
   if (e != cudaSuccess)
     return fail(QLIN_ERR_CUDA, "qlin_device_status: %s", cudaGetErrorString(e));
   // qmm waits in the low byte, qmv waits in the next one, the chain above, and
-  // what the cache kernels refused from bit 24, sampling in bit 29
+  // what the cache kernels refused from bit 24, sampling in bit 29, the experts'
+  // products in bit 30
   *flags = static_cast<int>((fm & 0xffu) | ((fv & 0xffu) << 8) | ((fc & 0xffu) << 16) |
-                            (((fr | fa) & 0x1fu) << 24) | ((fs & 1u) << 29));
+                            (((fr | fa) & 0x1fu) << 24) | ((fs & 1u) << 29) |
+                            ((fe ? 1u : 0u) << 30));
   return QLIN_OK;
 }
 

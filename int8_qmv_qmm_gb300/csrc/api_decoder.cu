@@ -115,11 +115,13 @@ qlin_status qlin_rope_table(float* table, int64_t n_positions, int rot_dim, doub
                            long_wavelength, reinterpret_cast<cudaStream_t>(stream));
 }
 
-qlin_status qlin_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
-                             const float* table, int64_t n_positions, int rot_dim,
-                             int interleaved, const qlin_kv_cache* cache, const int32_t* starts,
-                             int64_t n_tokens, int q_heads, unsigned flags, void* stream) {
-  const char* name = "qlin_rope_append";
+namespace {
+
+qlin_status rope_append_entry(const char* name, const void* qkv, int64_t qkv_stride, void* q_out,
+                              const float* table, int64_t n_positions, int rot_dim,
+                              int interleaved, const qlin_kv_cache* cache, const int32_t* starts,
+                              int64_t n_tokens, int q_heads, const HeadNorms& norms,
+                              unsigned flags, void* stream) {
   clear_error();
   qlin_status s = check_flags(name, flags);
   if (s != QLIN_OK) return s;
@@ -142,8 +144,37 @@ qlin_status qlin_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
                 "%s: qkv, q_out and table must be 16-byte aligned, qkv_stride a multiple of 8",
                 name);
   return launch_rope_append(qkv, qkv_stride, q_out, table, n_positions, rot_dim, interleaved,
-                            *cache, starts, n_tokens, q_heads, flags,
+                            *cache, starts, n_tokens, q_heads, norms, flags,
                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+qlin_status qlin_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
+                             const float* table, int64_t n_positions, int rot_dim,
+                             int interleaved, const qlin_kv_cache* cache, const int32_t* starts,
+                             int64_t n_tokens, int q_heads, unsigned flags, void* stream) {
+  return rope_append_entry("qlin_rope_append", qkv, qkv_stride, q_out, table, n_positions, rot_dim,
+                           interleaved, cache, starts, n_tokens, q_heads, HeadNorms{}, flags,
+                           stream);
+}
+
+qlin_status qlin_norm_rope_append(const void* qkv, int64_t qkv_stride, const void* q_norm,
+                                  const void* k_norm, float eps, void* q_out, const float* table,
+                                  int64_t n_positions, int rot_dim, int interleaved,
+                                  const qlin_kv_cache* cache, const int32_t* starts,
+                                  int64_t n_tokens, int q_heads, unsigned flags, void* stream) {
+  const char* name = "qlin_norm_rope_append";
+  clear_error();
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(QLIN_ERR_INVALID_ARG, "%s: eps must be finite and not negative", name);
+  if (n_tokens > 0 && (!q_norm || !k_norm))
+    return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned(q_norm, 16) || !aligned(k_norm, 16))
+    return fail(QLIN_ERR_MISALIGNED, "%s: the norms' weights must be 16-byte aligned", name);
+  return rope_append_entry(name, qkv, qkv_stride, q_out, table, n_positions, rot_dim, interleaved,
+                           cache, starts, n_tokens, q_heads, HeadNorms{q_norm, k_norm, eps}, flags,
+                           stream);
 }
 
 qlin_status qlin_cache_dequant(const qlin_kv_cache* cache, const int32_t* page_ids, int64_t n,
@@ -218,6 +249,35 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
     return fail(QLIN_ERR_MISALIGNED, "%s: a pointer is not aligned to its elements", name);
   return launch_sample(logits, logits_stride, u, temperature, top_k, top_p, min_p, tokens, probs,
                        M, V, ldtype, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_token_logprobs(const void* logits, int64_t logits_stride, const int32_t* tokens,
+                                float* logprobs, float* entropy, int top, int32_t* top_tokens,
+                                float* top_logprobs, int64_t M, int64_t V, qlin_dtype ldtype,
+                                unsigned flags, void* stream) {
+  const char* name = "qlin_token_logprobs";
+  clear_error();
+  qlin_status s = check_flags(name, flags);
+  if (s != QLIN_OK) return s;
+  if (ldtype != QLIN_F32 && ldtype != QLIN_F16 && ldtype != QLIN_BF16)
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: logits dtype %d", name, int(ldtype));
+  if (M < 0 || V < 1) return fail(QLIN_ERR_INVALID_ARG, "%s: M=%lld V=%lld", name, (long long)M, (long long)V);
+  if (V > 262144) return fail(QLIN_ERR_UNSUPPORTED, "%s: V=%lld (at most 262144)", name, (long long)V);
+  if (M > kMaxRows / 32) return fail(QLIN_ERR_UNSUPPORTED, "%s: M too large", name);
+  if (top < 0) return fail(QLIN_ERR_INVALID_ARG, "%s: top=%d", name, top);
+  if (top > 32) return fail(QLIN_ERR_UNSUPPORTED, "%s: top=%d (at most 32)", name, top);
+  if (M == 0) return QLIN_OK;
+  if (!logits || !tokens || !logprobs || !entropy || (top && (!top_tokens || !top_logprobs)))
+    return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (logits_stride < V)
+    return fail(QLIN_ERR_INVALID_ARG, "%s: logits_stride is shorter than V", name);
+  if (!aligned(logits, ldtype == QLIN_F32 ? 4 : 2) || !aligned(tokens, 4) ||
+      !aligned(logprobs, 4) || !aligned(entropy, 4) || !aligned(top_tokens, 4) ||
+      !aligned(top_logprobs, 4))
+    return fail(QLIN_ERR_MISALIGNED, "%s: a pointer is not aligned to its elements", name);
+  return launch_token_logprobs(logits, logits_stride, tokens, logprobs, entropy, top, top_tokens,
+                               top_logprobs, M, V, ldtype, flags,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlin_status qlin_testing_sample_plan(int64_t M, int64_t V, int sm_count, int* ranks, int* part,

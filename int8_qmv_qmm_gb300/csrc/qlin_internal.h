@@ -75,10 +75,18 @@ qlin_status launch_add_rms_norm(const void* x, int64_t x_stride, const void* wei
 qlin_status launch_rope_table(float* table, int64_t n_positions, int rot_dim, double base,
                               double factor, double short_wavelength, double long_wavelength,
                               cudaStream_t st);
+// Norms of the queries and keys of each head before the rotation (weights
+// [head_dim]; both null: none).
+struct HeadNorms {
+  const void* q;
+  const void* k;
+  float eps;
+};
 qlin_status launch_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
                                const float* table, int64_t n_positions, int rot_dim,
                                int interleaved, const qlin_kv_cache& c, const int32_t* starts,
-                               int64_t n_tokens, int q_heads, unsigned flags, cudaStream_t st);
+                               int64_t n_tokens, int q_heads, const HeadNorms& norms,
+                               unsigned flags, cudaStream_t st);
 qlin_status launch_cache_dequant(const qlin_kv_cache& c, const int32_t* page_ids, int64_t n,
                                  void* out, cudaStream_t st);
 size_t cache_attention_workspace_size(int head_dim);
@@ -99,6 +107,54 @@ qlin_status launch_sample(const void* logits, int64_t logits_stride, const float
                           const float* min_p, int32_t* tokens, float* probs, int64_t M,
                           int64_t V, qlin_dtype ldtype, unsigned flags, cudaStream_t st);
 
+qlin_status launch_token_logprobs(const void* logits, int64_t stride, const int32_t* tokens,
+                                  float* logprobs, float* entropy, int top, int32_t* top_tokens,
+                                  float* top_logprobs, int64_t M, int64_t V, qlin_dtype ldtype,
+                                  unsigned flags, cudaStream_t st);
+
+// ------------------------------------------------------------------ experts
+// (route_experts.cu, expert_linear.cu, combine_experts.cu)
+struct RouteArgs {
+  const void* logits;
+  int64_t stride;
+  const float* bias;
+  int scoring, groups, top_groups, group_score, top_k, renormalise;
+  float scale;
+  int32_t* experts;
+  float* weights;
+  int32_t* order;
+  int32_t* offsets;
+  int64_t T;
+  int E;
+  qlin_dtype dtype;
+};
+size_t route_experts_workspace_size(int64_t T, int E);
+qlin_status launch_route_experts(const RouteArgs& r, void* workspace, unsigned flags,
+                                 cudaStream_t st);
+
+// Weights [E][N][K]; pair p's row of x is p / pairs_per_row.
+struct ExpertArgs {
+  const void* x;
+  int64_t x_stride;
+  int pairs_per_row;
+  const int32_t* order;
+  const int32_t* offsets;
+  int64_t n_pairs;
+  const uint32_t* wq;
+  const void* scales;
+  const void* biases;
+  void* y;
+  int y_f32;
+  int E;
+  int64_t N, K;
+};
+qlin_status launch_expert_linear(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
+                                 cudaStream_t st);
+qlin_status launch_combine_experts(const void* y, const int32_t* experts, const float* weights,
+                                   const void* add, int64_t add_stride, void* out, int64_t T,
+                                   int top_k, int64_t N, qlin_dtype dtype, qlin_dtype y_dtype,
+                                   unsigned flags, cudaStream_t st);
+
 // Read and clear the kernels' device status words (no synchronisation).
 cudaError_t qmm_take_device_status(unsigned* flags);
 cudaError_t qmv_take_device_status(unsigned* flags);
@@ -106,6 +162,7 @@ cudaError_t chain_take_device_status(unsigned* flags);
 cudaError_t rope_take_device_status(unsigned* flags);
 cudaError_t attention_take_device_status(unsigned* flags);
 cudaError_t sample_take_device_status(unsigned* flags);
+cudaError_t expert_take_device_status(unsigned* flags);
 
 constexpr int kGroup = 64;
 

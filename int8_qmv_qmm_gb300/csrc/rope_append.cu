@@ -21,6 +21,10 @@
 // 4.8 in a graph.
 // Angles come from a table made in 64 bits: at
 // position 100000 a float32 angle would be off by up to 4e-3 radians.
+//
+// With norms (qlin_norm_rope_append) each query and new key is first divided by its
+// head's root mean square and multiplied by a weight, in float32 and without a
+// rounding before the rotation: the lanes that share a head add up their squares.
 
 #include <cmath>
 #include <type_traits>
@@ -107,14 +111,43 @@ __device__ __forceinline__ Angles angles_of(const float* row, int u, int rot) {
   return t;
 }
 
-template <typename T>
+// A unit's norm weights, and 1/rms of its head.
+struct Norm {
+  Vec8 x, y;
+  float inv;
+};
+
+// 1/rms of the head that a lane's unit is part of: kUnits lanes share it, each calls.
+template <typename T, int D>
+__device__ __forceinline__ float inverse_rms(const Vec8& x, const Vec8& y, float eps) {
+  constexpr int kUnits = D / 16;
+  const unsigned mask = ((1u << kUnits) - 1u) << ((threadIdx.x & 31) / kUnits * kUnits);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack<T>(x.w[i]), b = unpack<T>(y.w[i]);
+    sum += a.x * a.x + a.y * a.y + b.x * b.x + b.y * b.y;
+  }
+#pragma unroll
+  for (int d = 1; d < kUnits; d <<= 1) sum += __shfl_xor_sync(mask, sum, d);
+  return 1.0f / sqrtf(sum * (1.0f / D) + eps);
+}
+
+template <typename T, bool NORM>
 __device__ __forceinline__ void rotate_unit(Vec8& x, Vec8& y, int u, int rot, bool interleaved,
-                                            const Angles& angles) {
-  if (16 * u >= rot) return;
+                                            const Angles& angles, const Norm& norm) {
+  if (!NORM && 16 * u >= rot) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 a = unpack<T>(x.w[i]), b = unpack<T>(y.w[i]);
-    if (interleaved) {
+    if constexpr (NORM) {
+      const float2 p = unpack<T>(norm.x.w[i]), q = unpack<T>(norm.y.w[i]);
+      a = make_float2(a.x * norm.inv * p.x, a.y * norm.inv * p.y);
+      b = make_float2(b.x * norm.inv * q.x, b.y * norm.inv * q.y);
+    }
+    if (NORM && 16 * u >= rot) {
+      // (normed only)
+    } else if (interleaved) {
       const float4 t = angles.v[i / 2], z = angles.v[2 + i / 2];
       turn(a.x, a.y, i % 2 ? t.z : t.x, i % 2 ? t.w : t.y);
       turn(b.x, b.y, i % 2 ? z.z : z.x, i % 2 ? z.w : z.y);
@@ -194,7 +227,21 @@ struct Args {
   int64_t n_tokens;
   int q_heads;
   int64_t block_items;  // room for completed blocks, over all slots
+  const void* q_norm;   // weights [head_dim] (with norms)
+  const void* k_norm;
+  float eps;
 };
+
+// The weights of a unit.
+template <typename T, bool NORM>
+__device__ __forceinline__ Norm norm_of(const void* weight, const Unit& un) {
+  Norm n{};
+  if constexpr (NORM) {
+    n.x = load8(static_cast<const T*>(weight) + un.at0);
+    n.y = load8(static_cast<const T*>(weight) + un.at1);
+  }
+  return n;
+}
 
 // Whether all of a slot's rows can be taken: its blocks fit and its positions
 // are in the table.
@@ -206,7 +253,7 @@ __device__ __forceinline__ bool slot_fits(const Args& a, const SlotRows& r) {
 // A share of one new token's heads: the queries, and keys and values to the tail
 // where that is this warp's to write.  A lane's units differ by the head alone, so
 // it looks its angles up once.
-template <typename T, int D>
+template <typename T, int D, bool NORM>
 __device__ void token_warp(const Args& a, int64_t t, int part) {
   constexpr int kUnits = D / 16, kHeads = 32 / kUnits;  // of a head; heads at a time
   const int lane = threadIdx.x & 31;
@@ -233,6 +280,7 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
   const T* row = static_cast<const T*>(a.qkv) + t * a.qkv_stride;
   const Angles angles = angles_of(a.table + int64_t(pos) * a.rot, u, a.rot);
   const Unit un = unit_of(u, a.rot, a.interleaved);
+  Norm norm = norm_of<T, NORM>(a.q_norm, un);
   T* out = static_cast<T*>(a.q_out) + t * a.q_heads * D;
   const int q1 = a.q_heads * (part + 1) / kParts;
   // two heads' loads before the first store (which could be to the same memory,
@@ -246,11 +294,13 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
       x1 = load8(from + kHeads * D + un.at0);
       y1 = load8(from + kHeads * D + un.at1);
     }
-    rotate_unit<T>(x0, y0, u, a.rot, a.interleaved, angles);
+    if constexpr (NORM) norm.inv = inverse_rms<T, D>(x0, y0, a.eps);
+    rotate_unit<T, NORM>(x0, y0, u, a.rot, a.interleaved, angles, norm);
     store8(to + un.at0, x0);
     store8(to + un.at1, y0);
     if (two) {
-      rotate_unit<T>(x1, y1, u, a.rot, a.interleaved, angles);
+      if constexpr (NORM) norm.inv = inverse_rms<T, D>(x1, y1, a.eps);
+      rotate_unit<T, NORM>(x1, y1, u, a.rot, a.interleaved, angles, norm);
       store8(to + kHeads * D + un.at0, x1);
       store8(to + kHeads * D + un.at1, y1);
     }
@@ -260,20 +310,22 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
   const bool left_to_block = total / kBlock > r.held / kBlock && r.held % kBlock;
   if (!stays || left_to_block) return;
   const int at = pos % kBlock, k1 = a.c.kv_heads * (part + 1) / kParts;
+  norm = norm_of<T, NORM>(a.k_norm, un);
   for (int h = a.c.kv_heads * part / kParts + lane / kUnits; h < k1; h += kHeads) {
     T* tail = static_cast<T*>(a.c.tail) + (int64_t(b) * a.c.kv_heads + h) * 2 * kBlock * D;
     const T* k = row + (a.q_heads + h) * D;
     const T* v = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
     Vec8 x = load8(k + un.at0), y = load8(k + un.at1);
     const Vec8 v0 = load8(v), v1 = load8(v + 8);
-    rotate_unit<T>(x, y, u, a.rot, a.interleaved, angles);
+    if constexpr (NORM) norm.inv = inverse_rms<T, D>(x, y, a.eps);
+    rotate_unit<T, NORM>(x, y, u, a.rot, a.interleaved, angles, norm);
     store8(tail + at * D + un.at0, x);
     store8(tail + at * D + un.at1, y);
     column_to(tail + kBlock * D + 16 * u * kBlock + at, kBlock, v0, v1);
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool NORM>
 __device__ void block_cta(const Args& a, int64_t item, int h) {
   constexpr int kWarps = kThreads<D> / 32;
   constexpr int kStride = kBlock + 2;  // of a staged value row: spreads the banks
@@ -333,7 +385,11 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
     if (t0 + 8 * p < old) vv[p] = load8(tail + kBlock * D + d * kBlock + t0 + 8 * p);
   }
   if (vtok >= old) column_to(staged + 16 * vu * kStride + vtok, kStride, nv[0], nv[1]);
-  if (tok >= old) rotate_unit<T>(kx, ky, u, a.rot, a.interleaved, angles);
+  Norm norm = norm_of<T, NORM>(a.k_norm, un);
+  if (tok >= old) {  // (all lanes of a head, or none)
+    if constexpr (NORM) norm.inv = inverse_rms<T, D>(kx, ky, a.eps);
+    rotate_unit<T, NORM>(kx, ky, u, a.rot, a.interleaved, angles, norm);
+  }
   uint32_t top = max(largest<T>(kx), largest<T>(ky));
   // (the barriers of block_max order `staged` too)
   const float k_scale = __fdiv_rn(block_max<kWarps>(top, partial), 127.f);
@@ -371,15 +427,16 @@ __device__ void block_cta(const Args& a, int64_t item, int h) {
     const T* next = row + (a.q_heads + a.c.kv_heads + h) * D + 16 * u;
     Vec8 x = load8(nk + un.at0), y = load8(nk + un.at1);
     const Vec8 v0 = load8(next), v1 = load8(next + 8);
-    rotate_unit<T>(x, y, u, a.rot, a.interleaved,
-                   angles_of(a.table + int64_t(pos) * a.rot, u, a.rot));
+    if constexpr (NORM) norm.inv = inverse_rms<T, D>(x, y, a.eps);
+    rotate_unit<T, NORM>(x, y, u, a.rot, a.interleaved,
+                         angles_of(a.table + int64_t(pos) * a.rot, u, a.rot), norm);
     store8(tail + tok * D + un.at0, x);
     store8(tail + tok * D + un.at1, y);
     column_to(tail + kBlock * D + 16 * u * kBlock + tok, kBlock, v0, v1);
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool NORM>
 __global__ void __launch_bounds__(kThreads<D>, 1024 / kThreads<D>) rope_append_kernel(const Args a) {
   constexpr int kWarps = kThreads<D> / 32;
   grid_launch_dependents();
@@ -387,10 +444,10 @@ __global__ void __launch_bounds__(kThreads<D>, 1024 / kThreads<D>) rope_append_k
   // block CTAs first: they take longer
   const int64_t blocks = a.block_items * a.c.kv_heads;
   if (blockIdx.x < blocks) {
-    block_cta<T, D>(a, blockIdx.x / a.c.kv_heads, blockIdx.x % a.c.kv_heads);
+    block_cta<T, D, NORM>(a, blockIdx.x / a.c.kv_heads, blockIdx.x % a.c.kv_heads);
   } else {
     const int64_t i = (blockIdx.x - blocks) * kWarps + (threadIdx.x >> 5), t = i / kParts;
-    if (t < a.n_tokens) token_warp<T, D>(a, t, int(i % kParts));
+    if (t < a.n_tokens) token_warp<T, D, NORM>(a, t, int(i % kParts));
   }
 }
 
@@ -470,7 +527,10 @@ void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D>, a);
+  if (a.q_norm)
+    cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, true>, a);
+  else
+    cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, false>, a);
 }
 
 }  // namespace
@@ -487,12 +547,14 @@ qlin_status launch_rope_table(float* table, int64_t n_positions, int rot_dim, do
 qlin_status launch_rope_append(const void* qkv, int64_t qkv_stride, void* q_out,
                                const float* table, int64_t n_positions, int rot_dim,
                                int interleaved, const qlin_kv_cache& c, const int32_t* starts,
-                               int64_t n_tokens, int q_heads, unsigned flags, cudaStream_t st) {
+                               int64_t n_tokens, int q_heads, const HeadNorms& norms,
+                               unsigned flags, cudaStream_t st) {
   // a slot with n new tokens completes at most (63 + n)/64 blocks, and at most n
   const int64_t most = n_tokens / kBlock + c.slots;
   const Args a = {qkv,    qkv_stride, q_out,   table,    n_positions,
                   rot_dim, interleaved, c,      starts,   n_tokens,
-                  q_heads, n_tokens < most ? n_tokens : most};
+                  q_heads, n_tokens < most ? n_tokens : most,
+                  norms.q, norms.k, norms.eps};
   if (c.dtype == QLIN_F16)
     c.head_dim == 64 ? launch_t<__half, 64>(a, flags, st) : launch_t<__half, 128>(a, flags, st);
   else
