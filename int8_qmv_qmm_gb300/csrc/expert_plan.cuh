@@ -8,6 +8,12 @@
 
 namespace qlin {
 
+// Bits of the experts' status words.
+enum : unsigned {
+  kStatusPlan = 1u,  // offsets that are no plan's, or a pair outside n_pairs
+  kStatusWait = 2u,  // a wait that gave up
+};
+
 struct ExpertRows {
   int first;  // in order
   int n;
@@ -22,5 +28,12 @@ __device__ __forceinline__ ExpertRows expert_rows(const ExpertArgs& a, int exper
   r.n = r.bad ? 0 : end - first;
   return r;
 }
+
+// Tiles of 8 tokens (1, 2 or 4; 0: none fits) that the streaming kernel takes at a
+// time for experts of `rows` rows.
+int expert_stream_tiles(int64_t K, double rows);
+qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, int tiles,
+                                 unsigned flags, cudaStream_t st);
+cudaError_t expert_stream_take_status(unsigned* flags);
 
 }  // namespace qlin
