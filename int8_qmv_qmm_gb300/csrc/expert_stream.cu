@@ -2,22 +2,26 @@
 // the tokens, and memory bounds it.
 //
 // mma.sync takes 16 weight rows as its rows and 8 of the expert's tokens as its
-// columns, and works on the codes themselves: placed under the exponent of a 16-bit
-// unit (f16 1024 + q, bfloat16 128 + q; 8-bit codes in bfloat16 by halves of 4 bits,
-// 128 + low and 2048 + 16 high) a code costs one byte permute or mask, and is exact.
-// Over a group of 64, with X = sum_k x_k and P = sum_k x_k (unit + q_k),
-//     sum_k x_k w_k = scale * P + (bias - unit * scale) * X,
-// in float32: no weight is rounded.  (The unit costs P seven of its 24 bits at most,
-// far below the output's rounding.)
+// columns, and works on the codes themselves: placed under the exponent of f16's 1024
+// a code costs a byte permute (8 bits) or a mask (4 bits), and 1024 + q is exact.  Over
+// a group of 64, with X = sum_k x_k and P = sum_k x_k (1024 + q_k),
+//     sum_k x_k w_k = scale * P + (bias - 1024 * scale) * X,
+// in float32: no weight is rounded.  (The 1024 costs P seven of its 24 bits at most, far
+// below the output's rounding.)  Tokens in bfloat16 become f16 after a power of two for
+// each group, which brings its largest element to 2^14: exact down to 2^-31 of that
+// element, below which 2^-38 of it is lost at most.  (bfloat16 products on 8-bit codes
+// need two halves of each code, and took 70 us where f16 codes take 60.)
 //
-// A CTA takes a run of (expert, tile of tokens, 16 or more rows) items; its eight warps
-// share an item's K and, where K is short, 16 rows each of several.  The tile's tokens
-// lie in shared memory in the order of the products' fragments, with the X of every
-// group, for all items of the run that use them.  Each warp keeps a ring of stages of
-// four groups in flight by its own cp.async, on through items and experts, so that the
-// stream does not stop where a tile of tokens is fetched or sums are joined.
+// A CTA, one on an SM, takes a run of items, each 16 rows for a tile of an expert's
+// tokens.  Its 16 warps form teams that take items in turn, the warps of a team a share
+// of K each.  The tile's tokens lie in shared memory in the order of the products'
+// fragments, with the X of every group, for all items of the run that use them.  Each
+// warp keeps a ring of stages in flight by its own cp.async, on through items and
+// experts, so that the stream does not stop where a tile of tokens is fetched or sums
+// are joined.
 
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -33,19 +37,21 @@ namespace {
 
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_stream_status, bit); }
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGroups = 4;            // of a stage
-constexpr int kRows = 16;             // weight rows of a warp
-constexpr int kRingBytes = 8 * 1024;  // of a warp
+constexpr int kRows = 16;  // of an item
+constexpr int kGroups = 4;               // of a stage
+constexpr int kRingBytes = 8 * 1024;     // of a warp
+constexpr int kScaleStride = kRows + 4;  // of a group's (scale, rest): spreads the banks
+constexpr int kSumStride = kRows + 4;  // of a token's sums: spreads the banks
 constexpr int kMaxExperts = 512;
+constexpr int kCtasForJob = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int BITS>
-struct Ring {
-  static constexpr int kStageBytes = kGroups * kRows * 8 * BITS;
-  static constexpr int kStages = kRingBytes / kStageBytes;  // 4 (4-bit) or 2
-};
+constexpr int kStageBytes = kGroups * kRows * 8 * BITS;
+template <int BITS>
+constexpr int kStages = kRingBytes / kStageBytes<BITS>;  // 4 (4-bit) or 2
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -59,107 +65,115 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // d += a (16 x 16) b (16 x 8)
-template <typename AT>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<AT, __half>::value)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What a code is placed in, and how a lane's 16 codes of a group become the A operands
-// of four products (two of each for 8 bits in bfloat16), two pairs of codes to each.
-// kOrder: how tokens' elements pair up to match: 0 neighbours, 1 (0,2)(1,3) of four,
-// 2 (0,4)(1,5)(2,6)(3,7) of eight.
-template <int BITS, typename AT>
-struct Codes;
-
-template <>
-struct Codes<8, __half> {
-  static constexpr float kUnit = 1024.f;
-  static constexpr int kOrder = 0, kParts = 1;
-  static __device__ __forceinline__ void pairs(const uint32_t (&w)[4], int s, int,
-                                               uint32_t& p0, uint32_t& p1) {
-    p0 = __byte_perm(w[s], 0x64646464u, 0x4140u);
-    p1 = __byte_perm(w[s], 0x64646464u, 0x4342u);
+// A lane's 16 codes of a group (of rows g and g + 8) as the A operands of four products.
+// Within a product's 16 elements of k the order is free, as long as the tokens' is the
+// same: 8-bit codes pair up with their neighbours, 4-bit ones (a word at a time) as
+// (0,4)(1,5) and (2,6)(3,7).
+__device__ __forceinline__ void codes8(const uint4& w, int row, uint32_t (&a)[4][4]) {
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    a[s][row] = __byte_perm(words[s], 0x64646464u, 0x4140u);
+    a[s][row + 2] = __byte_perm(words[s], 0x64646464u, 0x4342u);
   }
-};
-template <>
-struct Codes<8, __nv_bfloat16> {
-  static constexpr float kUnit = 128.f + 2048.f;
-  static constexpr int kOrder = 1, kParts = 2;
-  static __device__ __forceinline__ void pairs(const uint32_t (&w)[4], int s, int part,
-                                               uint32_t& p0, uint32_t& p1) {
-    const uint32_t unit = part ? 0x45004500u : 0x43004300u;
-    p0 = ((w[s] >> (4 * part)) & 0x000f000fu) | unit;
-    p1 = ((w[s] >> (4 * part + 8)) & 0x000f000fu) | unit;
+}
+__device__ __forceinline__ void codes4(const uint2& w, int row, uint32_t (&a)[4][4]) {
+  const uint32_t words[2] = {w.x, w.y};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t v = words[s / 2] >> (8 * (s % 2));
+    a[s][row] = (v & 0x000f000fu) | 0x64006400u;
+    a[s][row + 2] = ((v >> 4) & 0x000f000fu) | 0x64006400u;
   }
-};
-template <typename AT>
-struct Codes<4, AT> {
-  static constexpr float kUnit = std::is_same<AT, __half>::value ? 1024.f : 128.f;
-  static constexpr int kOrder = 2, kParts = 1;
-  static __device__ __forceinline__ void pairs(const uint32_t (&w)[2], int s, int,
-                                               uint32_t& p0, uint32_t& p1) {
-    p0 = ((w[s / 2] >> (8 * (s % 2))) & 0x000f000fu) | Act<AT>::kMagic2;
-    p1 = ((w[s / 2] >> (8 * (s % 2) + 4)) & 0x000f000fu) | Act<AT>::kMagic2;
-  }
-};
+}
 
 // Eight neighbours (four words of two) in the order of the products' B operands.
-template <int ORDER>
+template <int BITS>
 __device__ __forceinline__ uint4 in_order(uint4 v) {
-  if constexpr (ORDER == 0) return v;
+  if constexpr (BITS == 8) return v;
   constexpr uint32_t kLow = 0x5410u, kHigh = 0x7632u;  // both low halves, both high ones
-  if constexpr (ORDER == 1)
-    return make_uint4(__byte_perm(v.x, v.y, kLow), __byte_perm(v.x, v.y, kHigh),
-                      __byte_perm(v.z, v.w, kLow), __byte_perm(v.z, v.w, kHigh));
   return make_uint4(__byte_perm(v.x, v.z, kLow), __byte_perm(v.x, v.z, kHigh),
                     __byte_perm(v.y, v.w, kLow), __byte_perm(v.y, v.w, kHigh));
 }
 
 template <typename AT>
-__device__ __forceinline__ float sum8(uint4 v) {
-  using T2 = typename Act<AT>::T2;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const T2 p = *reinterpret_cast<const T2*>(&w[i]);
-    s += Act<AT>::to_f32(p.x) + Act<AT>::to_f32(p.y);
-  }
-  return s;
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  const typename Act<AT>::T2 p = *reinterpret_cast<const typename Act<AT>::T2*>(&w);
+  return make_float2(Act<AT>::to_f32(p.x), Act<AT>::to_f32(p.y));
 }
 
-// NT: tiles of 8 tokens; WK: warps that share a row's K (8 / WK blocks of 16 rows an
-// item).
+// Of a token's group: X, and what its products are to be multiplied by (1 for f16).
+struct TokenGroup {
+  float x, back;
+};
+
+// Turns a quarter (16 elements) of a token's group, as loaded, into f16; the four lanes
+// of the group call together.
+template <typename AT>
+__device__ __forceinline__ TokenGroup token_quarter(uint4& v0, uint4& v1) {
+  uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  float sum = 0.f;
+  uint32_t most = 0u;  // the bits of magnitudes order as they do
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = widen2<AT>(w[i]);
+    sum += f.x + f.y;
+    most = max(most, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    sum += __shfl_xor_sync(kAll, sum, d);
+    most = max(most, __shfl_xor_sync(kAll, most, d));
+  }
+  if constexpr (std::is_same<AT, __half>::value) return TokenGroup{sum, 1.f};
+  // exponents of the largest: 14 after the factor; not where that passes float32's (the
+  // element is then below 2^-100, or not finite)
+  const int e = int(most >> 23);
+  const int up = e < 27 ? 127 + 14 + 100 : e == 255 ? 127 : 127 + 14 + 127 - e;
+  const float factor = __uint_as_float(uint32_t(up) << 23);
+  const float back = __uint_as_float(uint32_t(254 - up) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = widen2<AT>(w[i]);
+    const __half2 h = __floats2half2_rn(f.x * factor, f.y * factor);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  v0 = make_uint4(w[0], w[1], w[2], w[3]);
+  v1 = make_uint4(w[4], w[5], w[6], w[7]);
+  return TokenGroup{sum, back};
+}
+
+// NT: tiles of 8 tokens that an item can have; WK: warps of a team.
 template <int BITS, typename AT, int NT, int WK>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2) stream_kernel(const ExpertArgs a) {
-  using C = Codes<BITS, AT>;
-  using R = Ring<BITS>;
-  constexpr int kTokens = 8 * NT, WN = kWarps / WK, kItemRows = kRows * WN;
-  constexpr int kSumStride = kItemRows + 4;  // (of a token: spreads the banks)
-  constexpr int kLaneBytes = 2 * BITS;       // of a lane's 16 codes of a group
+__global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a) {
+  constexpr int kTokens = 8 * NT, kTeams = kWarps / WK, kAhead = kStages<BITS> - 1;
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int first_job[kMaxExperts + 1];  // the tiles of the experts before each
-  __shared__ int pair_of[2][kTokens];         // of the tile's tokens (-1: none)
+  __shared__ int pair_of[kTokens];            // of the tile's tokens (-1: none)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wk = warp % WK, wn = warp / WK;
+  const int wk = warp % WK, team = warp / WK;
   const int g = lane >> 2, c = lane & 3;
-  const int n_groups = int(a.K) / kGroup;
-  // rings | sums [2][WK][kTokens][kSumStride] | X [n_groups][kTokens] | tokens
-  float* sums = reinterpret_cast<float*>(shared + kWarps * kRingBytes);
-  float* xsum = sums + 2 * WK * kTokens * kSumStride;
+  const int n_groups = int(a.K) / kGroup, N = int(a.N);
+  // rings | scales [kWarps][kGroups][kScaleStride] | sums [kWarps][kTokens][kSumStride] |
+  // X and factors [n_groups][kTokens] | tokens
+  float2* scales = reinterpret_cast<float2*>(shared + kWarps * kRingBytes) +
+                   warp * kGroups * kScaleStride;
+  float* sums = reinterpret_cast<float*>(shared + kWarps * (kRingBytes + kGroups * kScaleStride * 8));
+  TokenGroup* xsum = reinterpret_cast<TokenGroup*>(sums + kWarps * kTokens * kSumStride);
   uint4* xs = reinterpret_cast<uint4*>(xsum + n_groups * kTokens);
   const uint8_t* ring = shared + warp * kRingBytes;
-  const uint32_t ring_u32 = ptx::smem_u32(ring);
+  // where this lane's copies go (4-bit: two groups of a row are 64 bytes, chunk c of row g
+  // at chunk c ^ 2 * (g / 2 % 2), so that the reads below meet no bank twice)
+  const uint32_t ring_to =
+      ptx::smem_u32(ring) + uint32_t(BITS == 8 ? lane * 16 : g * 64 + (c ^ (g & 2)) * 16);
 
   grid_launch_dependents();
   grid_dependency_wait();
@@ -183,239 +197,260 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2) stream_kernel(const
     }
   }
   __syncthreads();
-  const int blocks = int((a.N + kItemRows - 1) / kItemRows);
-  const int64_t items = int64_t(first_job[a.E]) * blocks;
-  const int64_t item0 = items * blockIdx.x / gridDim.x;
-  const int n_items = int(items * (blockIdx.x + 1) / gridDim.x - item0);
+  const int blocks = (N + kRows - 1) / kRows;
+  // The CTA's run of items: an equal share of all; where there are CTAs enough for each
+  // job, one of a single job, whose tokens are then all that it fetches.
+  const int jobs = first_job[a.E], ctas = int(gridDim.x), cta = int(blockIdx.x);
+  int64_t item0 = int64_t(jobs) * blocks * cta / ctas;
+  int64_t item1 = int64_t(jobs) * blocks * (cta + 1) / ctas;
+  if (jobs > 0 && kCtasForJob * jobs <= ctas) {
+    const int job = cta * jobs / ctas;
+    const int first = (job * ctas + jobs - 1) / jobs;  // of the job's CTAs
+    const int n = ((job + 1) * ctas + jobs - 1) / jobs - first;
+    item0 = int64_t(job) * blocks + int64_t(blocks) * (cta - first) / n;
+    item1 = int64_t(job) * blocks + int64_t(blocks) * (cta - first + 1) / n;
+  }
+  const int n_items = int(item1 - item0);
   if (n_items == 0) return;
 
-  // this warp's groups, and the stages that every warp takes for an item
+  // this warp's groups, and the stages that every warp of a team takes for an item
   const int g0 = wk * n_groups / WK, g1 = (wk + 1) * n_groups / WK;
   const int per_item = ((n_groups + WK - 1) / WK + kGroups - 1) / kGroups;
+  const int64_t row_bytes = a.K * BITS / 8;
 
-  // where a stage is: an item and a stage of it
-  struct Cursor {
-    int job, expert, block, stage, left;  // left: stages to the end of the run
+  // The team's items: a tile of an expert's tokens (job) and a block of rows.
+  struct Place {
+    int job, block, stage, left;  // left: items to come, this one too
   };
-  auto at_expert = [&](Cursor& q) {
-    while (first_job[q.expert + 1] <= q.job) ++q.expert;
-  };
-  auto next = [&](Cursor& q) {
-    --q.left;
-    if (++q.stage < per_item) return;
-    q.stage = 0;
-    if (++q.block < blocks) return;
-    q.block = 0;
-    ++q.job;
-    if (q.left > 0) at_expert(q);
-  };
-  Cursor now;
+  Place now;
   now.job = int(item0 / blocks);
-  now.block = int(item0 % blocks);
-  now.expert = now.stage = 0;
-  now.left = n_items * per_item;
-  at_expert(now);
-  Cursor ahead = now;
-
-  const int row_bytes = int(a.K) * BITS / 8;
-  // row r of the item (past the end: the last one, whose sums are not stored)
-  auto row_of = [&](const Cursor& q, int half) {
-    const int64_t n = int64_t(q.block) * kItemRows + wn * kRows + 8 * half + g;
-    return int64_t(q.expert) * a.N + min(n, a.N - 1);
+  now.block = int(item0 % blocks) + team;
+  now.stage = 0;
+  now.left = (n_items - team + kTeams - 1) / kTeams;
+  auto settle = [&](Place& q) {
+    while (q.block >= blocks) {
+      q.block -= blocks;
+      ++q.job;
+    }
   };
+  if (now.left > 0) settle(now);
+  // Where the copies are, ahead of the products: this lane's chunk of rows g and g + 8,
+  // and the scale and bias of its group (c) there.
+  Place ahead = now;
+  int expert = 0;  // ahead's
+  const uint8_t* from[2];
+  const uint16_t *scale_from[2], *bias_from[2];
+  auto at_item = [&] {
+    while (first_job[expert + 1] <= ahead.job) ++expert;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      // (past the end: the last row, whose sums are not stored)
+      const int64_t row = int64_t(expert) * N + min(ahead.block * kRows + 8 * half + g, N - 1);
+      from[half] = reinterpret_cast<const uint8_t*>(a.wq) + row * row_bytes + g0 * (8 * BITS) + c * 16;
+      scale_from[half] = static_cast<const uint16_t*>(a.scales) + row * n_groups + g0 + c;
+      bias_from[half] = static_cast<const uint16_t*>(a.biases) + row * n_groups + g0 + c;
+    }
+  };
+  if (ahead.left > 0) at_item();
+  // scale and bias (low and high half) of the stages on their way; 0 for a group past the
+  // warp's last, which then adds nothing
+  uint32_t coming[kAhead + 1][2];
   int slot_in = 0;  // of the ring
   auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) coming[i][half] = coming[i + 1][half];
+    coming[kAhead][0] = coming[kAhead][1] = 0u;
     if (ahead.left > 0) {
-      const int s0 = g0 + ahead.stage * kGroups, n = min(kGroups, g1 - s0);
-      const uint32_t to = ring_u32 + uint32_t(slot_in * R::kStageBytes);
+      const int n = g1 - g0 - ahead.stage * kGroups;  // groups from here on
+      const uint32_t to = ring_to + uint32_t(slot_in * kStageBytes<BITS>);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(a.wq) +
-                              row_of(ahead, half) * row_bytes + s0 * (8 * BITS) + c * 16;
         if constexpr (BITS == 8) {
 #pragma unroll
           for (int i = 0; i < kGroups; ++i)
-            if (i < n) copy16(to + uint32_t(((i * 2 + half) * 32 + lane) * 16), from + i * 64);
+            if (i < n) copy16(to + uint32_t((i * 2 + half) * 512), from[half] + i * 64);
         } else {
-          // two groups of a row are 64 bytes: chunk c of row g at chunk c ^ 2 * (g / 2 % 2)
 #pragma unroll
           for (int i = 0; i < kGroups; i += 2)
-            if (i + c / 2 < n)
-              copy16(to + uint32_t(((i / 2 * 2 + half) * 8 + g) * 64 + (c ^ (g & 2)) * 16),
-                     from + i * 32);
+            if (i + c / 2 < n) copy16(to + uint32_t((i + half) * 512), from[half] + i * 32);
+        }
+        if (c < n) coming[kAhead][half] = uint32_t(*scale_from[half]) | uint32_t(*bias_from[half]) << 16;
+        from[half] += kGroups * 8 * BITS;
+        scale_from[half] += kGroups;
+        bias_from[half] += kGroups;
+      }
+      if (++ahead.stage == per_item) {
+        ahead.stage = 0;
+        if (--ahead.left > 0) {
+          ahead.block += kTeams;
+          settle(ahead);
+          at_item();
         }
       }
-      next(ahead);
     }
     copies_commit();
-    if (++slot_in == R::kStages) slot_in = 0;
+    if (++slot_in == kStages<BITS>) slot_in = 0;
   };
-  // scale and bias (low and high half) of the stage's group c, rows g and g + 8
-  uint32_t sb[2] = {0u, 0u};
-  auto scales_of = [&](const Cursor& q) {
-    const int gr = g0 + q.stage * kGroups + c;
-    if (q.left > 0 && gr < g1) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int64_t i = row_of(q, half) * n_groups + gr;
-        sb[half] = uint32_t(static_cast<const uint16_t*>(a.scales)[i]) |
-                   uint32_t(static_cast<const uint16_t*>(a.biases)[i]) << 16;
-      }
-    }
-  };
+  for (int i = 0; i < kAhead; ++i) fetch();
 
-#pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) fetch();
-  scales_of(now);
-
-  float acc[NT][4];
-  int slot = 0, sum_buf = 0, tile_buf = 0, tile = -1;
-  while (now.left > 0) {
-    __syncwarp();  // every lane is done with the stage whose place is filled next
-    fetch();
-    if (now.job != tile) {
-      // the tokens of another tile (every warp is past the last item's products: its
-      // barrier lies behind them)
-      tile = now.job;
-      tile_buf ^= 1;
-      const ExpertRows r = expert_rows(a, now.expert);
-      const int t0 = (now.job - first_job[now.expert]) * kTokens;
-      if (threadIdx.x < kTokens) {
-        int p = -1;
-        if (t0 + int(threadIdx.x) < r.n) {
-          p = a.order[r.first + t0 + threadIdx.x];
-          if (p < 0 || p >= a.n_pairs) {
-            report(kStatusPlan);
-            p = -1;
-          }
-        }
-        pair_of[tile_buf][threadIdx.x] = p;
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < n_groups * kTokens * 4; i += kThreads) {
-        const int q = i & 3, tok = (i >> 2) % kTokens, gr = (i >> 2) / kTokens;
-        const int p = pair_of[tile_buf][tok];
-        uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-        if (p >= 0) {
-          const uint4* from = reinterpret_cast<const uint4*>(
-              static_cast<const AT*>(a.x) + int64_t(p / a.pairs_per_row) * a.x_stride +
-              gr * kGroup + q * 16);
-          v0 = from[0];
-          v1 = from[1];
-        }
-        float s = sum8<AT>(v0) + sum8<AT>(v1);
-        s += __shfl_xor_sync(kAll, s, 1);  // (i runs in whole warps)
-        s += __shfl_xor_sync(kAll, s, 2);
-        if (q == 0) xsum[gr * kTokens + tok] = s;
-        uint4* to = xs + ((gr * NT + tok / 8) * 2) * 32 + (tok % 8) * 4 + q;
-        to[0] = in_order<C::kOrder>(v0);
-        to[32] = in_order<C::kOrder>(v1);
-      }
-      __syncthreads();
-    }
-    if (now.stage == 0) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-    }
-    const uint32_t sb_now[2] = {sb[0], sb[1]};
-    const Cursor it = now;
-    next(now);
-    scales_of(now);
-    copies_wait<R::kStages - 1>();
-    if constexpr (BITS == 4) __syncwarp();
-    const int s0 = g0 + it.stage * kGroups, n = min(kGroups, g1 - s0);
-    const uint8_t* st = ring + slot * R::kStageBytes;
-    if (++slot == R::kStages) slot = 0;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      if (i >= n) break;
-      uint32_t w[2][kLaneBytes / 4];  // rows g and g + 8: 16 codes each
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if constexpr (BITS == 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + ((i * 2 + half) * 32 + lane) * 16);
-          w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
-        } else {
-          const int chunk = (i % 2 * 2 + c / 2) ^ (g & 2);
-          const uint2 v = *reinterpret_cast<const uint2*>(
-              st + ((i / 2 * 2 + half) * 8 + g) * 64 + chunk * 16 + c % 2 * 8);
-          w[half][0] = v.x, w[half][1] = v.y;
-        }
-      }
-      float p[NT][4] = {};
-      const uint4* xg = xs + ((s0 + i) * NT * 2) * 32 + lane;
-      uint4 b[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        b[t][0] = xg[t * 64];
-        b[t][1] = xg[t * 64 + 32];
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int part = 0; part < C::kParts; ++part) {
-          uint32_t a0, a1, a2, a3;
-          C::pairs(w[0], s, part, a0, a2);
-          C::pairs(w[1], s, part, a1, a3);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint4& v = b[t][s / 2];
-            mma<AT>(p[t], a0, a1, a2, a3, s % 2 ? v.z : v.x, s % 2 ? v.w : v.y);
-          }
-        }
-      float scale[2], rest[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t v = __shfl_sync(kAll, sb_now[half], (lane & ~3) | i);
-        const uint16_t sv = uint16_t(v), bv = uint16_t(v >> 16);
-        scale[half] = Act<AT>::to_f32(*reinterpret_cast<const AT*>(&sv));
-        rest[half] = fmaf(-C::kUnit, scale[half], Act<AT>::to_f32(*reinterpret_cast<const AT*>(&bv)));
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float2 x =
-            *reinterpret_cast<const float2*>(xsum + (s0 + i) * kTokens + 8 * t + 2 * c);
-        acc[t][0] = fmaf(scale[0], p[t][0], fmaf(rest[0], x.x, acc[t][0]));
-        acc[t][1] = fmaf(scale[0], p[t][1], fmaf(rest[0], x.y, acc[t][1]));
-        acc[t][2] = fmaf(scale[1], p[t][2], fmaf(rest[1], x.x, acc[t][2]));
-        acc[t][3] = fmaf(scale[1], p[t][3], fmaf(rest[1], x.y, acc[t][3]));
-      }
-    }
-    if (it.stage + 1 < per_item) continue;
-    // the item's sums: rows g, g + 8 and tokens 2c, 2c + 1 of each tile from every warp
-    float* part = sums + sum_buf * (WK * kTokens * kSumStride);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        part[(wk * kTokens + 8 * t + 2 * c + i % 2) * kSumStride + wn * kRows + 8 * (i / 2) + g] =
-            acc[t][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTokens * kItemRows; i += kThreads) {
-      const int tok = i / kItemRows, r = i % kItemRows;
-      const int p = pair_of[tile_buf][tok];
-      const int64_t row = int64_t(it.block) * kItemRows + r;
-      if (p < 0 || row >= a.N) continue;
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) v += part[(k * kTokens + tok) * kSumStride + r];
-      if (a.y_f32)
-        static_cast<float*>(a.y)[int64_t(p) * a.N + row] = v;
+  float2 acc[NT][2];
+  int slot = 0;
+  const int last_job = int((item0 + n_items - 1) / blocks);
+  for (int job = int(item0 / blocks); job <= last_job; ++job) {
+    // the job's tokens
+    int low = 0, high = a.E;  // first_job[low] <= job < first_job[high]
+    while (high - low > 1) {
+      const int mid = (low + high) / 2;
+      if (first_job[mid] <= job)
+        low = mid;
       else
-        static_cast<AT*>(a.y)[int64_t(p) * a.N + row] = Act<AT>::from_f32_rn(v);
+        high = mid;
     }
-    sum_buf ^= 1;  // (a warp that is an item ahead writes the other one)
+    const ExpertRows r = expert_rows(a, low);
+    const int t0 = (job - first_job[low]) * kTokens;
+    const int tiles = min((r.n - t0 + 7) / 8, NT);
+    int p = -1;
+    if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < r.n) {
+      p = a.order[r.first + t0 + threadIdx.x];
+      if (p < 0 || p >= a.n_pairs) {
+        report(kStatusPlan);
+        p = -1;
+      }
+    }
+    __syncthreads();  // (every team is done with the last job's)
+    if (threadIdx.x < kTokens) pair_of[threadIdx.x] = p;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_groups * tiles * 32; i += kThreads) {
+      const int q = i & 3, tok8 = (i >> 2) & 7, t = (i >> 5) % tiles, gr = (i >> 5) / tiles;
+      const int tok = t * 8 + tok8, pair = pair_of[tok];
+      uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+      if (pair >= 0) {
+        const uint4* x = reinterpret_cast<const uint4*>(
+            static_cast<const AT*>(a.x) + int64_t(pair / a.pairs_per_row) * a.x_stride +
+            gr * kGroup + q * 16);
+        v0 = x[0];
+        v1 = x[1];
+      }
+      const TokenGroup tg = token_quarter<AT>(v0, v1);  // (i runs in whole warps)
+      if (q == 0) xsum[gr * kTokens + tok] = tg;
+      uint4* to = xs + ((gr * NT + t) * 2) * 32 + tok8 * 4 + q;
+      to[0] = in_order<BITS>(v0);
+      to[32] = in_order<BITS>(v1);
+    }
+    __syncthreads();
+    while (now.left > 0 && now.job == job) {
+      __syncwarp();  // every lane is done with the stage whose place is filled next
+      fetch();
+      if (now.stage == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = make_float2(0.f, 0.f);
+      }
+      // (scale, bias - 1024 * scale) of group c, for the warp
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float2 v = widen2<AT>(coming[0][half]);
+        scales[c * kScaleStride + 8 * half + g] = make_float2(v.x, fmaf(-1024.f, v.x, v.y));
+      }
+      copies_wait<kAhead>();
+      __syncwarp();
+      const uint8_t* st = ring + slot * kStageBytes<BITS>;
+      if (++slot == kStages<BITS>) slot = 0;
+      const int s0 = g0 + now.stage * kGroups;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        uint32_t code[4][4];
+        float2 sz[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if constexpr (BITS == 8)
+            codes8(*reinterpret_cast<const uint4*>(st + (i * 2 + half) * 512 + lane * 16), half,
+                   code);
+          else
+            codes4(*reinterpret_cast<const uint2*>(
+                       st + (i / 2 * 2 + half) * 512 + g * 64 +
+                       ((i % 2 * 2 + c / 2) ^ (g & 2)) * 16 + c % 2 * 8),
+                   half, code);
+          sz[half] = scales[i * kScaleStride + 8 * half + g];
+        }
+        // (past the warp's last group its tokens again: what is finite times 0)
+        const int gr = max(min(s0 + i, g1 - 1), 0);
+        const uint4* xg = xs + gr * NT * 64 + lane;
+        const float4* xt = reinterpret_cast<const float4*>(xsum + gr * kTokens + 2 * c);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (t >= tiles) break;
+          const uint4 b0 = xg[t * 64], b1 = xg[t * 64 + 32];
+          const float4 tg = xt[4 * t];  // of tokens 2c and 2c + 1
+          float p0[4] = {0.f, 0.f, 0.f, 0.f}, p1[4] = {0.f, 0.f, 0.f, 0.f};
+          mma(p0, code[0], b0.x, b0.y);
+          mma(p1, code[2], b1.x, b1.y);
+          mma(p0, code[1], b0.z, b0.w);
+          mma(p1, code[3], b1.z, b1.w);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float2 v = __fadd2_rn(make_float2(p0[2 * half], p0[2 * half + 1]),
+                                  make_float2(p1[2 * half], p1[2 * half + 1]));
+            if constexpr (!std::is_same<AT, __half>::value)
+              v = __fmul2_rn(v, make_float2(tg.y, tg.w));
+            acc[t][half] = __ffma2_rn(make_float2(sz[half].y, sz[half].y),
+                                      make_float2(tg.x, tg.z), acc[t][half]);
+            acc[t][half] = __ffma2_rn(make_float2(sz[half].x, sz[half].x), v, acc[t][half]);
+          }
+        }
+      }
+      const int block = now.block;
+      if (++now.stage < per_item) continue;
+      now.stage = 0;
+      if (--now.left > 0) {
+        now.block += kTeams;
+        settle(now);
+      }
+      // the item's sums: rows g, g + 8 and tokens 2c, 2c + 1 of each tile from every warp
+      // of the team
+      float* mine = sums + team * WK * kTokens * kSumStride;
+      if constexpr (WK > 1)  // the team has read the last item's
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(WK * 32) : "memory");
+      else
+        __syncwarp();
+      float* part = mine + wk * kTokens * kSumStride;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (t >= tiles) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          part[(8 * t + 2 * c) * kSumStride + 8 * half + g] = acc[t][half].x;
+          part[(8 * t + 2 * c + 1) * kSumStride + 8 * half + g] = acc[t][half].y;
+        }
+      }
+      if constexpr (WK > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(WK * 32) : "memory");
+      else
+        __syncwarp();
+      for (int i = wk * 32 + lane; i < tiles * 8 * kRows; i += WK * 32) {
+        const int tok = i / kRows, row = block * kRows + i % kRows;
+        const int pair = pair_of[tok];
+        if (pair < 0 || row >= N) continue;
+        const float* sum = mine + tok * kSumStride + i % kRows;
+        float v = sum[0];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) v += sum[k * kTokens * kSumStride];
+        if (a.y_f32)
+          static_cast<float*>(a.y)[int64_t(pair) * N + row] = v;
+        else
+          static_cast<AT*>(a.y)[int64_t(pair) * N + row] = Act<AT>::from_f32_rn(v);
+      }
+    }
   }
   copies_wait<0>();
 }
 
-size_t shared_bytes(int nt, int wk, int64_t K) {
-  const int tokens = 8 * nt;
-  return size_t(kWarps) * kRingBytes +
-         size_t(2) * wk * tokens * (kRows * (kWarps / wk) + 4) * 4 +
-         size_t(K / kGroup) * (tokens * 4 + nt * 1024);
+size_t shared_bytes(int nt, int64_t K) {
+  const size_t tokens = 8 * size_t(nt);
+  return size_t(kWarps) * (kRingBytes + kGroups * kScaleStride * 8 + tokens * kSumStride * 4) +
+         size_t(K / kGroup) * tokens * (sizeof(TokenGroup) + kGroup * 2);
 }
 
 constexpr size_t kMostShared = 227 * 1024 - 2560;  // beside first_job and pair_of
@@ -426,17 +461,14 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), int(kMostShared), &done))
     return check_launch("qlin_expert_linear: shared memory");
-  const size_t smem = shared_bytes(NT, WK, a.K);
   // tiles of tokens: at most one more than full ones for each expert that has any
   const int64_t used = std::min<int64_t>(a.E, a.n_pairs);
   const int64_t jobs = a.n_pairs / (8 * NT) + used;
-  const int64_t rows = kRows * (kWarps / WK);
-  const int64_t items = jobs * ((a.N + rows - 1) / rows);
-  const int64_t resident = int64_t(sm_count()) * (NT < 4 && smem <= 110 * 1024 ? 2 : 1);
+  const int64_t items = jobs * ((a.N + kRows - 1) / kRows);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min(items, resident)));
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(items, sm_count())));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = shared_bytes(NT, a.K);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -449,10 +481,11 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
 
 template <int BITS, typename AT, int NT>
 qlin_status with_warps(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
-  // as many warps to a row as leave each a whole stage
-  const int64_t stages = a.K / (kGroup * kGroups);
-  if (stages >= 8) return launch_t<BITS, AT, NT, 8>(a, flags, st);
-  if (stages >= 4) return launch_t<BITS, AT, NT, 4>(a, flags, st);
+  const int64_t groups = a.K / kGroup;
+  int wk = 2;
+  if (const char* env = std::getenv("QLIN_EXPERT_WK")) wk = std::atoi(env);
+  if (wk >= 8) return launch_t<BITS, AT, NT, 8>(a, flags, st);
+  if (wk >= 4) return launch_t<BITS, AT, NT, 4>(a, flags, st);
   return launch_t<BITS, AT, NT, 2>(a, flags, st);
 }
 
@@ -467,7 +500,8 @@ qlin_status with_tiles(const ExpertArgs& a, int tiles, unsigned flags, cudaStrea
 
 int expert_stream_tiles(int64_t K, double rows) {
   int tiles = rows <= 2.0 ? 1 : rows <= 8.0 ? 2 : 4;
-  while (tiles && shared_bytes(tiles, 8, K) > kMostShared) tiles /= 2;
+  if (const char* env = std::getenv("QLIN_EXPERT_NT")) tiles = std::atoi(env);
+  while (tiles && shared_bytes(tiles, K) > kMostShared) tiles /= 2;
   return tiles;
 }
 
