@@ -26,7 +26,7 @@ SOURCES = ("api.cu", "quant.cu", "qmv.cu", "qmv_chain.cu", "chain_static.cu", "q
            "api_decoder.cu", "add_rms_norm.cu", "rope_append.cu", "cache_attention.cu",
            "attention_split.cu", "attention_tile.cu", "sample.cu", "logprobs.cu",
            "api_experts.cu", "route_experts.cu", "expert_linear.cu",
-           "expert_stream.cu", "combine_experts.cu")
+           "expert_stream.cu", "expert_tile.cu", "combine_experts.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -35,5 +35,8 @@ int expert_stream_tiles(int64_t K, double rows);
 qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, int tiles,
                                  unsigned flags, cudaStream_t st);
 cudaError_t expert_stream_take_status(unsigned* flags);
+qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, double rows,
+                               unsigned flags, cudaStream_t st);
+cudaError_t expert_tile_take_status(unsigned* flags);
 
 }  // namespace qlin

@@ -1,0 +1,508 @@
+// The experts' products where an expert has many rows: tcgen05, as in qmm.cu (128 weight
+// rows as the MMA's M, reconstructed into tensor memory as its A operand, a group of 64
+// of K to a stage), over the tiles of all experts.
+//
+// A tile is 128 rows of an expert's weights and up to BN of its tokens.  CTAs, one on an
+// SM, walk the list of tiles, a job's (an expert and a stretch of its tokens) row tiles
+// one after another, so that those who work on one job share its tokens in L2.  The
+// tokens' rows come by cp.async, 16 bytes a lane, from wherever the plan has them, into
+// the swizzled layout that the MMA reads, and the products of a token are written to its
+// pair's row.  (TMA gathers of four rows took 31 ns each on an SM, 2 us a stage of 256
+// rows: 1185 us for what takes 250 now.)  A tile with fewer tokens than BN fetches and
+// multiplies only what it has, in steps of 8 and 16.
+//
+//   warps 0, 1   fetch the tokens' rows; lane 0 of warp 0 loads the packed tile (TMA)
+//   warp 2       issues the MMAs, converged, with the operands' descriptors uniform
+//   warps 3..10  two warpgroups that reconstruct stages in turn; they also order the
+//                fetched rows before the MMAs that read them (fence.proxy.async)
+//   warps 11..14 epilogue: takes up to 128 of the tokens' columns at a time to registers
+//                at 16 bits, hands the accumulator back with the last, and stores
+//
+// Every wait is bounded (about 2 s); one that gives up sets a status bit, and the CTA
+// waits for its copies and MMAs in flight, frees its tensor memory and leaves.
+
+#include <algorithm>
+
+#include "expert_plan.cuh"
+#include "qmm_core.cuh"
+
+namespace qlin {
+
+__device__ unsigned int g_expert_tile_status = 0;
+
+namespace {
+
+__device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_tile_status, bit); }
+
+constexpr int kDequantGroups = 2;
+constexpr int kDequantWarps = 4 * kDequantGroups;
+constexpr int kFetchWarps = 2;
+constexpr int kEpilogueWarps = 4;
+constexpr int kFirstDequant = kFetchWarps + 1;
+constexpr int kFirstEpilogue = kFirstDequant + kDequantWarps;
+constexpr int kThreads = (kFirstEpilogue + kEpilogueWarps) * 32;
+constexpr int kMaxExperts = 512;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kMaxShared = 227 * 1024;
+
+template <int BITS, int BN, int SPLIT>
+struct Layout {
+  static constexpr int kXBytes = BN * kBK * 2;
+  static constexpr int kWBytes = Geo<BITS>::kPackedBytes;
+  static constexpr int kStageBytes = kXBytes + kWBytes;
+  // two accumulators unless they would leave tensor memory too few A slots
+  static constexpr int kDBufs = BN >= 256 ? 1 : 2;
+  static constexpr int kACol0 = kDBufs * BN;
+  static constexpr int kAColsPerStage = SPLIT * kBK / 2;
+  // first_job, the tiles' pairs, barriers and the tensor memory's address
+  static constexpr int kRestBytes = (kMaxExperts + 4) * 4 + 2 * BN * 4 + 512;
+  static constexpr int kFit = (kMaxShared - 1024 - kRestBytes) / kStageBytes;
+  static constexpr int kSlots = (512 - kACol0) / kAColsPerStage;
+  static constexpr int kStages = kFit < kSlots ? (kFit < 8 ? kFit : 8) : (kSlots < 8 ? kSlots : 8);
+  static constexpr int kTmemCols = kACol0 + kStages * kAColsPerStage <= 256 ? 256 : 512;
+  static_assert(kStageBytes % 1024 == 0 && kStages >= 2, "");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// As mma_f16_ts and mma_commit, by the lane that leads, in a converged warp.
+__device__ __forceinline__ void mma_by(uint32_t leads, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leads)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t leads, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(leads)
+      : "memory");
+}
+
+// Where a CTA is in its list of tiles.
+struct Tile {
+  int expert, n0, t0, count;  // first weight row, first token of the expert, tokens
+  ExpertRows rows;
+};
+
+template <int BITS, typename AT, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tm_w, const ExpertArgs a) {
+  constexpr int kSplit = OperandSplit<AT>::value;
+  using L = Layout<BITS, BN, kSplit>;
+  using G = Geo<BITS>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw_base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kb_count = int(a.K) / kBK, N = int(a.N);
+  const int n_tiles = (N + kBM - 1) / kBM;
+
+  auto x_addr = [&](int s) { return base + uint32_t(s * L::kStageBytes); };
+  auto w_addr = [&](int s) { return x_addr(s) + uint32_t(L::kXBytes); };
+  const uint32_t bar_base = base + uint32_t(kStages * L::kStageBytes);
+  // (one "loaded" barrier per stage and warpgroup: use u of the ring signals that of
+  // group u % 2, so that no group waits two phases ahead)
+  auto full_bar = [&](int g, int s) { return bar_base + 8u * (g * kStages + s); };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kDequantGroups * kStages + s); };
+  auto afull_bar = [&](int s) { return bar_base + 8u * ((kDequantGroups + 1) * kStages + s); };
+  const uint32_t accf_bar = bar_base + 8u * ((kDequantGroups + 2) * kStages);  // [2]
+  const uint32_t acce_bar = accf_bar + 16u;                                     // [2]
+  const uint32_t done_bar = acce_bar + 16u;
+  static_assert(8 * ((kDequantGroups + 2) * 8 + 5) + 4 <= 512, "barrier block");
+  uint8_t* const rest = gbase + kStages * L::kStageBytes;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
+  int* first_job = reinterpret_cast<int*>(rest + 512);  // the jobs of the experts before each
+  int* pairs = first_job + kMaxExperts + 4;             // [2][BN], of the tile's tokens
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      for (int g = 0; g < kDequantGroups; ++g) ptx::mbar_init(full_bar(g, s), 1 + kFetchWarps * 32);
+      ptx::mbar_init(empty_bar(s), 1 + 4);  // the MMAs' commit and the warps of a group
+      ptx::mbar_init(afull_bar(s), 4);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(accf_bar + 8u * b, 1);
+      ptx::mbar_init(acce_bar + 8u * b, kEpilogueWarps);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tm_w);
+  }
+  if (warp == kFetchWarps) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), uint32_t(L::kTmemCols));
+    ptx::tmem_relinquish();
+  }
+  grid_dependency_wait();  // the plan, x and y are the preceding kernels'
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    const ExpertRows r = expert_rows(a, e);
+    if (r.bad && blockIdx.x == 0) report(kStatusPlan);
+    first_job[e + 1] = (r.n + BN - 1) / BN;
+  }
+  if (threadIdx.x == 0) first_job[0] = 0;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 0) {
+    int before = 0;
+    for (int e0 = 1; e0 <= a.E; e0 += 32) {
+      int v = e0 + lane <= a.E ? first_job[e0 + lane] : 0;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, v, d);
+        if (lane >= d) v += o;
+      }
+      if (e0 + lane <= a.E) first_job[e0 + lane] = before + v;
+      before += __shfl_sync(kAll, v, 31);
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem_base = *tmem_slot;
+  // (a kernel that starts from here on finds this one's tensor memory taken already)
+  grid_launch_dependents();
+  const int total = first_job[a.E] * n_tiles;
+  auto tile_at = [&](int t, int& expert) {
+    const int job = t / n_tiles;
+    while (first_job[expert + 1] <= job) ++expert;
+    Tile q;
+    q.expert = expert;
+    q.n0 = (t - job * n_tiles) * kBM;
+    q.rows = expert_rows(a, expert);
+    q.t0 = (job - first_job[expert]) * BN;
+    q.count = min(q.rows.n - q.t0, BN);
+    return q;
+  };
+
+  if (warp < kFetchWarps) {
+    // ------------------------------------------------------------ producers
+    // A row's group is 128 bytes, 8 lanes; this lane has chunk `lane % 8` of rows first,
+    // first + 8, ...  (first, the row within 8, sets the swizzle of all of them)
+    constexpr int kTurns = BN / 8;
+    const int first = warp * 4 + lane / 8;
+    const uint32_t to = uint32_t(first * 128 + ((lane % 8) ^ first) * 16);
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + (lane % 8) * 16;
+    int s = 0, g = 0, issued = 0, expert = 0;
+    uint32_t round = 0;
+    uint32_t full_ph = 0;  // bit g*8+s: parity of the next phase of full_bar(g, s)
+    bool ok = true;
+    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
+      const Tile q = tile_at(t, expert);
+      uint32_t row[kTurns];  // in 16 bytes (a pair that is none: row 0, whose product is not stored)
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        row[i] = 0u;
+        if (first + 8 * i < q.count) {
+          const int p = a.order[q.rows.first + q.t0 + first + 8 * i];
+          if (p >= 0 && p < a.n_pairs)
+            row[i] = uint32_t(p / a.pairs_per_row) * uint32_t(a.x_stride / 8);
+        }
+      }
+      const int turns = (q.count + 7) / 8;
+      for (int kb = 0; kb < kb_count; ++kb) {
+        if (round > 0 && !__all_sync(kAll, ptx::mbar_wait(empty_bar(s), (round - 1) & 1u))) {
+          report(kStatusWait);
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full_bar(g, s);
+        if (threadIdx.x == 0) {
+          ptx::mbar_arrive_expect_tx(fb, L::kWBytes);
+          ptx::tma_load_2d(w_addr(s), &tm_w, fb, kb * G::kWordsPerGroup, q.expert * N + q.n0);
+        }
+        __syncwarp();
+        const uint8_t* from = x + int64_t(kb) * (kBK * 2);
+        const uint32_t dst = x_addr(s) + to;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i)
+          if (i < turns) copy16(dst + uint32_t(i * 1024), from + uint64_t(row[i]) * 16);
+        copies_arrive(fb);
+        full_ph ^= 1u << (g * 8 + s);
+        ++issued;
+        if (++g == kDequantGroups) g = 0;
+        if (++s == kStages) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && threadIdx.x == 0) {
+      // the last loads, one per stage, may be in flight
+      const int v0 = issued > kStages ? issued - kStages : 0;
+      for (int v = v0; v < issued; ++v) {
+        const int vg = v % kDequantGroups, vs = v % kStages;
+        const uint32_t parity = ((full_ph >> (vg * 8 + vs)) & 1u) ^ 1u;
+        if (!ptx::mbar_wait(full_bar(vg, vs), parity)) report(kStatusWait);
+      }
+    }
+  } else if (warp == kFetchWarps) {
+    // ----------------------------------------------------------- MMA issuer
+    constexpr uint32_t fmt = std::is_same<AT, __half>::value ? 0u : 1u;
+    const uint32_t leads = lane == 0;
+    const uint64_t b_desc0 = ptx::sw128_kmajor_desc(base);
+    int s = 0, i = 0, expert = 0;
+    uint32_t phase = 0;
+    bool ok = true, any = false;
+    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x), ++i) {
+      const Tile q = tile_at(t, expert);
+      const uint32_t idesc = ptx::idesc_f16(fmt, kBM, uint32_t((q.count + 15) & ~15));
+      const int buf = i % L::kDBufs;
+      if (i >= L::kDBufs &&
+          !__all_sync(kAll, ptx::mbar_wait(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u))) {
+        report(kStatusWait);
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t d_tmem = tmem_base + uint32_t(buf * BN);
+      uint32_t more = 0;
+      for (int kb = 0; kb < kb_count; ++kb) {
+        // (A ready implies that the stage's bytes have landed)
+        if (!__all_sync(kAll, ptx::mbar_wait(afull_bar(s), phase))) {
+          report(kStatusWait);
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t a_tmem = tmem_base + uint32_t(L::kACol0 + s * L::kAColsPerStage);
+        const uint64_t bd = b_desc0 + uint64_t(uint32_t(s * L::kStageBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+          mma_by(leads, d_tmem, a_tmem + uint32_t(8 * kk), bd + uint64_t(2 * kk), idesc,
+                 kk > 0 ? 1u : more);
+          if constexpr (kSplit == 2)  // the bfloat16 residual
+            mma_by(leads, d_tmem, a_tmem + uint32_t(32 + 8 * kk), bd + uint64_t(2 * kk), idesc, 1u);
+        }
+        more = 1;
+        any = true;
+        commit_by(leads, empty_bar(s));
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) commit_by(leads, accf_bar + 8u * buf);
+    }
+    // before tensor memory is freed every MMA issued here must have completed
+    commit_by(leads, done_bar);
+    if (any && !ptx::mbar_wait(done_bar, 0)) report(kStatusWait);
+    __syncwarp();
+  } else if (warp < kFirstEpilogue) {
+    // -------------------------------- reconstruct (the warpgroups in turn)
+    const int grp = (warp - kFirstDequant) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // weight row within the tile
+    const uint32_t a_lane = tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(L::kACol0);
+    int s = 0, u = 0, expert = 0;
+    uint32_t full_ph = 0;  // bit s: parity of the next phase of full_bar(grp, s)
+    bool ok = true;
+    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
+      const Tile q = tile_at(t, expert);
+      const int n = q.n0 + r;
+      const bool row_ok = n < N;
+      const int64_t at = (int64_t(q.expert) * N + min(n, N - 1)) * kb_count;
+      const AT* srow = static_cast<const AT*>(a.scales) + at;
+      const AT* brow = static_cast<const AT*>(a.biases) + at;
+      for (int kb = 0; kb < kb_count; ++kb, ++u) {
+        const int cs = s;
+        if (++s == kStages) s = 0;
+        if (u % kDequantGroups != grp) continue;
+        const AT sc = srow[kb], bc = brow[kb];
+        if (!__all_sync(kAll, ptx::mbar_wait(full_bar(grp, cs), (full_ph >> cs) & 1u))) {
+          report(kStatusWait);
+          ok = false;
+          break;
+        }
+        full_ph ^= 1u << cs;
+        const uint8_t* wrow = gbase + (w_addr(cs) - base) + r * G::kPackedRowBytes;
+        uint32_t w[32];
+        uint32_t lo[kSplit == 2 ? 32 : 1];
+        dequant_row<BITS, AT, kSplit>(wrow, r, sc, bc, row_ok, w, lo);
+        tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage), w);
+        if constexpr (kSplit == 2)
+          tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage + 32), lo);
+        tmem_wait_st();
+        // (the tokens' rows, whose barrier lies behind, for the MMAs' proxy)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(afull_bar(cs));
+          ptx::mbar_arrive(empty_bar(cs));
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, et = threadIdx.x - kFirstEpilogue * 32;
+    constexpr int kCols = BN < 128 ? BN : 128;  // at a time
+    int i = 0, expert = 0;
+    for (int t = int(blockIdx.x); t < total; t += int(gridDim.x), ++i) {
+      const Tile q = tile_at(t, expert);
+      int* mine = pairs + (i & 1) * BN;
+      for (int j = et; j < BN; j += kEpilogueWarps * 32) {
+        int p = -1;
+        if (j < q.count) {
+          p = a.order[q.rows.first + q.t0 + j];
+          if (p < 0 || p >= a.n_pairs) {
+            report(kStatusPlan);
+            p = -1;
+          }
+        }
+        mine[j] = p;
+      }
+      // (two lists: nobody is still at the one before the last)
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+      const int buf = i % L::kDBufs;
+      if (!__all_sync(kAll, ptx::mbar_wait(accf_bar + 8u * buf, uint32_t(i / L::kDBufs) & 1u))) {
+        report(kStatusWait);
+        break;
+      }
+      ptx::tc_fence_after();
+      const int n = q.n0 + quarter * 32 + lane;
+      const uint32_t t_lane = tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * BN);
+      auto hand_back = [&] {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(acce_bar + 8u * buf);
+      };
+      if (a.y_f32) {
+#pragma unroll 1
+        for (int c = 0; c < q.count; c += 16) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c), v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int p = mine[c + j];  // (-1 past the last token)
+            if (n < N && p >= 0)
+              static_cast<float*>(a.y)[int64_t(p) * N + n] = __uint_as_float(v[j]);
+          }
+        }
+        hand_back();
+        continue;
+      }
+      uint16_t* y = static_cast<uint16_t*>(a.y) + n;
+#pragma unroll 1
+      for (int c0 = 0; c0 < q.count; c0 += kCols) {
+        uint32_t out[kCols / 2];  // two tokens each
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          if (c0 + c < q.count) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c0 + c), v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              typename Act<AT>::T2 h;
+              h.x = Act<AT>::from_f32_rn(__uint_as_float(v[2 * j]));
+              h.y = Act<AT>::from_f32_rn(__uint_as_float(v[2 * j + 1]));
+              out[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+        }
+        if (c0 + kCols >= q.count) hand_back();
+        if (n < N) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            if (c0 + c < q.count) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int p = mine[c0 + c + j];
+                const uint32_t v = out[(c + j) / 2];
+                if (p >= 0) y[int64_t(p) * N] = uint16_t(j % 2 ? v >> 16 : v);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kFetchWarps) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, uint32_t(L::kTmemCols));
+  }
+}
+
+template <int BITS, typename AT, int BN>
+qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
+  using L = Layout<BITS, BN, OperandSplit<AT>::value>;
+  constexpr int kBytes = 1024 + L::kStages * L::kStageBytes + L::kRestBytes;
+  static_assert(kBytes <= kMaxShared, "");
+  auto kern = tile_kernel<BITS, AT, BN>;
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_shared(reinterpret_cast<const void*>(kern), kBytes, &done))
+    return check_launch("qlin_expert_linear: shared memory");
+  const int64_t x_rows = a.n_pairs / a.pairs_per_row;
+  const int64_t words = a.K * BITS / 32;
+  if (x_rows * (a.x_stride / 8) > int64_t(0xffffffffu))
+    return fail(QLIN_ERR_UNSUPPORTED, "qlin_expert_linear: x spans more than 64 GiB");
+  CUtensorMap tm_w;
+  const qlin_status s =
+      make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wq, uint64_t(words),
+               uint64_t(a.E) * uint64_t(a.N), uint64_t(words) * 4, Geo<BITS>::kWordsPerGroup, kBM,
+               BITS == 4 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
+  if (s != QLIN_OK) return s;
+  const int64_t jobs = a.n_pairs / BN + std::min<int64_t>(a.E, a.n_pairs);
+  const int64_t tiles = jobs * ((a.N + kBM - 1) / kBM);
+  if (tiles > (int64_t(1) << 30))
+    return fail(QLIN_ERR_UNSUPPORTED, "qlin_expert_linear: too many tiles");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, sm_count())));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kern, tm_w, a);
+  return check_launch("qlin_expert_linear");
+}
+
+template <int BITS, typename AT>
+qlin_status dispatch(const ExpertArgs& a, double rows, unsigned flags, cudaStream_t st) {
+  if (rows <= 64.0) return launch_t<BITS, AT, 64>(a, flags, st);
+  if (rows <= 128.0) return launch_t<BITS, AT, 128>(a, flags, st);
+  return launch_t<BITS, AT, 256>(a, flags, st);
+}
+
+}  // namespace
+
+qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, double rows,
+                               unsigned flags, cudaStream_t st) {
+  if (dtype == QLIN_F16)
+    return bits == 4 ? dispatch<4, __half>(a, rows, flags, st)
+                     : dispatch<8, __half>(a, rows, flags, st);
+  return bits == 4 ? dispatch<4, __nv_bfloat16>(a, rows, flags, st)
+                   : dispatch<8, __nv_bfloat16>(a, rows, flags, st);
+}
+
+cudaError_t expert_tile_take_status(unsigned* flags) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_expert_tile_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  e = cudaMemcpyToSymbol(g_expert_tile_status, &zero, sizeof(zero));
+  *flags = v;
+  return e;
+}
+
+}  // namespace qlin
