@@ -552,6 +552,10 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
                                qlin_dtype ldtype, void* workspace, size_t workspace_bytes,
                                unsigned flags, void* stream);
 
+/* Bytes of device scratch that qlin_expert_linear needs (0 where experts have few
+ * rows; else the rows of x in the plan's order). */
+size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K);
+
 /*
  * y[p] = x[p / pairs_per_row] . W_hat[e]^T for every pair p of each expert e of
  * a plan (order, offsets), from packed weights as above with E in front:
@@ -562,7 +566,9 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
  *   y        y_dtype [n_pairs][N] (dtype, one rounding, or QLIN_F32); rows of
  *            pairs without an expert are not written
  * float32 sums; accuracy as qlin_linear.  x and wq 16-byte aligned, x_stride a
- * multiple of 8; y apart from all else.  Experts whose offsets are not a plan's
+ * multiple of 8; y apart from all else.  workspace:
+ * qlin_expert_linear_workspace_size bytes, 16-byte aligned, with anything in them
+ * (NULL where that is 0); calls that can overlap need one each.  Experts whose offsets are not a plan's
  * and pairs outside n_pairs are left out and set a device status bit.
  * QLIN_OVERLAP_PREVIOUS: as for qlin_qmv_ex (weights may be read before the
  * preceding kernel has completed; x, order and offsets are not).
@@ -571,8 +577,8 @@ qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_ro
                                const int32_t* order, const int32_t* offsets, int64_t n_pairs,
                                const uint32_t* wq, const void* scales, const void* biases, void* y,
                                int E, int64_t N, int64_t K, int bits, int group_size,
-                               qlin_dtype dtype, qlin_dtype y_dtype, unsigned flags,
-                               void* stream);
+                               qlin_dtype dtype, qlin_dtype y_dtype, void* workspace,
+                               size_t workspace_bytes, unsigned flags, void* stream);
 
 /*
  * out[t] = add[t] + sum_j weights[t][j] * y[t*top_k + j]  over the j with

@@ -87,7 +87,9 @@ _SIGNATURES = {
                            + [_c_vp] * 4 + [_c_i64, _c_int, _c_int, _c_vp, ctypes.c_size_t,
                                             ctypes.c_uint, _c_vp]),
     "qlin_expert_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_i64] + [_c_vp] * 4
-                           + [_c_int, _c_i64, _c_i64] + [_c_int] * 4 + [ctypes.c_uint, _c_vp]),
+                           + [_c_int, _c_i64, _c_i64] + [_c_int] * 4
+                           + [_c_vp, ctypes.c_size_t, ctypes.c_uint, _c_vp]),
+    "qlin_expert_linear_workspace_size": (ctypes.c_size_t, [_c_i64, _c_int, _c_i64]),
     "qlin_combine_experts": (_c_int, [_c_vp] * 4 + [_c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int,
                                                     _c_int, ctypes.c_uint, _c_vp]),
     # include/qlin_testing.h: failure paths and host-side choices, for the
@@ -829,11 +831,15 @@ def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
                  "scales and biases must be contiguous [n_experts, N, K/64] in x's dtype, on its "
                  "device"),
                 (False, "out must be contiguous [T*top_k, N], on x's device, in out_dtype"))
-    status = lib().qlin_expert_linear(
+    L = lib()
+    size = L.qlin_expert_linear_workspace_size(pairs, routing.n_experts, shape[1])
+    workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+    status = L.qlin_expert_linear(
         x.data_ptr(), _row_stride(x, shape[1]), 1 if shape[0] == pairs else routing.top_k,
         routing.order.data_ptr(), routing.offsets.data_ptr(), pairs, wq.data_ptr(),
         scales.data_ptr(), biases.data_ptr(), out.data_ptr(), routing.n_experts, n, shape[1], bits,
-        group_size, _DTYPE_CODE[dt], _DTYPE_CODE[out_dtype], 1 if overlap_previous else 0,
+        group_size, _DTYPE_CODE[dt], _DTYPE_CODE[out_dtype],
+        workspace.data_ptr() if size else None, size, 1 if overlap_previous else 0,
         _current_raw_stream(index))
     if status:
         _check(status)

@@ -79,12 +79,16 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
   return launch_route_experts(a, workspace, flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K) {
+  return n_pairs < 1 || E < 1 || K < 1 ? 0 : expert_linear_workspace_size(n_pairs, E, K);
+}
+
 qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_row,
                                const int32_t* order, const int32_t* offsets, int64_t n_pairs,
                                const uint32_t* wq, const void* scales, const void* biases, void* y,
                                int E, int64_t N, int64_t K, int bits, int group_size,
-                               qlin_dtype dtype, qlin_dtype y_dtype, unsigned flags,
-                               void* stream) {
+                               qlin_dtype dtype, qlin_dtype y_dtype, void* workspace,
+                               size_t workspace_bytes, unsigned flags, void* stream) {
   const char* name = "qlin_expert_linear";
   clear_error();
   qlin_status s = check_flags(name, flags);
@@ -111,15 +115,18 @@ qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_ro
   if (!x || !order || !offsets || !wq || !scales || !biases || !y)
     return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
   if (x_stride < K) return fail(QLIN_ERR_INVALID_ARG, "%s: x_stride is shorter than K", name);
-  if (!aligned(x, 16) || x_stride % 8 || !aligned(wq, 16) || !aligned(scales, 2) ||
+  const size_t need = expert_linear_workspace_size(n_pairs, E, K);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(QLIN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, need);
+  if (!aligned(x, 16) || x_stride % 8 || !aligned(wq, 16) || !aligned(workspace, 16) || !aligned(scales, 2) ||
       !aligned(biases, 2) || !aligned(y, y_dtype == QLIN_F32 ? 4 : 2) || !aligned(order, 4) ||
       !aligned(offsets, 4))
     return fail(QLIN_ERR_MISALIGNED,
-                "%s: x and wq must be 16-byte aligned, x_stride a multiple of 8, the rest aligned "
+                "%s: x, wq and workspace must be 16-byte aligned, x_stride a multiple of 8, the rest aligned "
                 "to its elements", name);
   const ExpertArgs a = {x,      x_stride, pairs_per_row, order, offsets,
                         n_pairs, wq,      scales,        biases, y,
-                        y_dtype == QLIN_F32 ? 1 : 0, E, N, K};
+                        y_dtype == QLIN_F32 ? 1 : 0, E, N, K, workspace};
   return launch_expert_linear(a, bits, dtype, flags, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -8,15 +8,32 @@
 
 namespace qlin {
 
+namespace {
+
+// Rows of an expert, were they spread evenly (the routing itself is on the device).
+double rows_of(int64_t n_pairs, int E) {
+  return double(n_pairs) / double(E < n_pairs ? E : n_pairs);
+}
+
+// Tiles of 8 tokens for the streaming kernel; 0: the tensor-core kernel.
+int stream_tiles(int64_t n_pairs, int E, int64_t K) {
+  const double rows = rows_of(n_pairs, E);
+  double most = 32.0;
+  if (const char* env = std::getenv("QLIN_EXPERT_MOST")) most = std::atof(env);
+  return rows <= most ? expert_stream_tiles(K, rows) : 0;
+}
+
+}  // namespace
+
+size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K) {
+  return n_pairs > 0 && !stream_tiles(n_pairs, E, K) ? size_t(n_pairs) * K * 2 : 0;
+}
+
 qlin_status launch_expert_linear(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
                                  cudaStream_t st) {
-  // rows of an expert, were they spread evenly (the routing itself is on the device)
-  const double rows = double(a.n_pairs) / double(a.E < a.n_pairs ? a.E : a.n_pairs);
-  const int tiles = expert_stream_tiles(a.K, rows);
-  double most = 16.0;
-  if (const char* env = std::getenv("QLIN_EXPERT_MOST")) most = std::atof(env);
-  if (tiles && rows <= most) return launch_expert_stream(a, bits, dtype, tiles, flags, st);
-  return launch_expert_tile(a, bits, dtype, rows, flags, st);
+  const int tiles = stream_tiles(a.n_pairs, a.E, a.K);
+  if (tiles) return launch_expert_stream(a, bits, dtype, tiles, flags, st);
+  return launch_expert_tile(a, bits, dtype, rows_of(a.n_pairs, a.E), flags, st);
 }
 
 cudaError_t expert_take_device_status(unsigned* flags) {

@@ -4,19 +4,22 @@
 //
 // A tile is 128 rows of an expert's weights and up to BN of its tokens.  CTAs, one on an
 // SM, walk the list of tiles, a job's (an expert and a stretch of its tokens) row tiles
-// one after another, so that those who work on one job share its tokens in L2.  The
-// tokens' rows come by cp.async, 16 bytes a lane, from wherever the plan has them, into
-// the swizzled layout that the MMA reads, and the products of a token are written to its
-// pair's row.  (TMA gathers of four rows took 31 ns each on an SM, 2 us a stage of 256
-// rows: 1185 us for what takes 250 now.)  A tile with fewer tokens than BN fetches and
-// multiplies only what it has, in steps of 8 and 16.
+// one after another, so that those who work on one job share its tokens in L2.
 //
-//   warps 0, 1   fetch the tokens' rows; lane 0 of warp 0 loads the packed tile (TMA)
-//   warp 2       issues the MMAs, converged, with the operands' descriptors uniform
-//   warps 3..10  two warpgroups that reconstruct stages in turn; they also order the
-//                fetched rows before the MMAs that read them (fence.proxy.async)
-//   warps 11..14 epilogue: takes up to 128 of the tokens' columns at a time to registers
-//                at 16 bits, hands the accumulator back with the last, and stores
+// A first kernel copies the tokens' rows in the plan's order to the workspace, so that a
+// tile's are neighbours and come as one TMA box a stage; a token's products are written
+// to its pair's row.  The copy of 32768 rows of 2048 (134 MB) takes about 25 us of FIXME.
+// (Fetching rows from where they are was slower: by TMA gathers of four rows, 31 ns each
+// on an SM, 1185 us; by cp.async of two or four warps 517 and 425.)
+//
+//   warp 0       loads the tokens' rows and the packed tile (TMA, one thread)
+//   warp 1       issues the MMAs, converged, with the operands' descriptors uniform; a
+//                tile with fewer tokens than BN multiplies what it has, in steps of 16
+//   warps 2..9   two warpgroups that reconstruct stages in turn
+//   warps 10..13 epilogue: takes up to 128 of the tokens' columns at a time to registers
+//                at 16 bits, hands the accumulator back with the last, and stores 16 bytes
+//                a lane by way of shared memory (2 bytes a lane, 64 a warp: 304 us for
+//                what takes FIXME)
 //
 // Every wait is bounded (about 2 s); one that gives up sets a status bit, and the CTA
 // waits for its copies and MMAs in flight, frees its tensor memory and leaves.
@@ -36,14 +39,16 @@ __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_tile_s
 
 constexpr int kDequantGroups = 2;
 constexpr int kDequantWarps = 4 * kDequantGroups;
-constexpr int kFetchWarps = 2;
 constexpr int kEpilogueWarps = 4;
-constexpr int kFirstDequant = kFetchWarps + 1;
+constexpr int kFirstDequant = 2;
 constexpr int kFirstEpilogue = kFirstDequant + kDequantWarps;
 constexpr int kThreads = (kFirstEpilogue + kEpilogueWarps) * 32;
 constexpr int kMaxExperts = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxShared = 227 * 1024;
+// Tokens whose outputs are turned around in shared memory at a time, and two of those.
+constexpr int kOutTokens = 32;
+constexpr int kOutBytes = 2 * kOutTokens * kBM * 2;
 
 template <int BITS, int BN, int SPLIT>
 struct Layout {
@@ -54,22 +59,15 @@ struct Layout {
   static constexpr int kDBufs = BN >= 256 ? 1 : 2;
   static constexpr int kACol0 = kDBufs * BN;
   static constexpr int kAColsPerStage = SPLIT * kBK / 2;
-  // first_job, the tiles' pairs, barriers and the tensor memory's address
-  static constexpr int kRestBytes = (kMaxExperts + 4) * 4 + 2 * BN * 4 + 512;
+  // barriers and the tensor memory's address, the epilogue's tiles, first_job, the tiles'
+  // pairs
+  static constexpr int kRestBytes = 512 + kOutBytes + (kMaxExperts + 4) * 4 + 2 * BN * 4;
   static constexpr int kFit = (kMaxShared - 1024 - kRestBytes) / kStageBytes;
   static constexpr int kSlots = (512 - kACol0) / kAColsPerStage;
   static constexpr int kStages = kFit < kSlots ? (kFit < 8 ? kFit : 8) : (kSlots < 8 ? kSlots : 8);
   static constexpr int kTmemCols = kACol0 + kStages * kAColsPerStage <= 256 ? 256 : 512;
   static_assert(kStageBytes % 1024 == 0 && kStages >= 2, "");
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// Arrives on `bar` when this thread's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // As mma_f16_ts and mma_commit, by the lane that leads, in a converged warp.
 __device__ __forceinline__ void mma_by(uint32_t leads, uint32_t d_tmem, uint32_t a_tmem,
@@ -100,7 +98,8 @@ struct Tile {
 
 template <int BITS, typename AT, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_kernel(const __grid_constant__ CUtensorMap tm_w, const ExpertArgs a) {
+    tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                const ExpertArgs a) {
   constexpr int kSplit = OperandSplit<AT>::value;
   using L = Layout<BITS, BN, kSplit>;
   using G = Geo<BITS>;
@@ -127,12 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(8 * ((kDequantGroups + 2) * 8 + 5) + 4 <= 512, "barrier block");
   uint8_t* const rest = gbase + kStages * L::kStageBytes;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
-  int* first_job = reinterpret_cast<int*>(rest + 512);  // the jobs of the experts before each
+  uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][kOutTokens][kBM]
+  int* first_job = reinterpret_cast<int*>(rest + 512 + kOutBytes);  // the jobs of the experts before each
   int* pairs = first_job + kMaxExperts + 4;             // [2][BN], of the tile's tokens
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      for (int g = 0; g < kDequantGroups; ++g) ptx::mbar_init(full_bar(g, s), 1 + kFetchWarps * 32);
+      for (int g = 0; g < kDequantGroups; ++g) ptx::mbar_init(full_bar(g, s), 1);
       ptx::mbar_init(empty_bar(s), 1 + 4);  // the MMAs' commit and the warps of a group
       ptx::mbar_init(afull_bar(s), 4);
     }
@@ -142,9 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(done_bar, 1);
     ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tm_x);
     ptx::tma_prefetch_desc(&tm_w);
   }
-  if (warp == kFetchWarps) {
+  if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), uint32_t(L::kTmemCols));
     ptx::tmem_relinquish();
   }
@@ -187,69 +188,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     return q;
   };
 
-  if (warp < kFetchWarps) {
-    // ------------------------------------------------------------ producers
-    // A row's group is 128 bytes, 8 lanes; this lane has chunk `lane % 8` of rows first,
-    // first + 8, ...  (first, the row within 8, sets the swizzle of all of them)
-    constexpr int kTurns = BN / 8;
-    const int first = warp * 4 + lane / 8;
-    const uint32_t to = uint32_t(first * 128 + ((lane % 8) ^ first) * 16);
-    const uint8_t* x = static_cast<const uint8_t*>(a.x) + (lane % 8) * 16;
-    int s = 0, g = 0, issued = 0, expert = 0;
-    uint32_t round = 0;
-    uint32_t full_ph = 0;  // bit g*8+s: parity of the next phase of full_bar(g, s)
-    bool ok = true;
-    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
-      const Tile q = tile_at(t, expert);
-      uint32_t row[kTurns];  // in 16 bytes (a pair that is none: row 0, whose product is not stored)
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        row[i] = 0u;
-        if (first + 8 * i < q.count) {
-          const int p = a.order[q.rows.first + q.t0 + first + 8 * i];
-          if (p >= 0 && p < a.n_pairs)
-            row[i] = uint32_t(p / a.pairs_per_row) * uint32_t(a.x_stride / 8);
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0, g = 0, issued = 0, expert = 0;
+      uint32_t round = 0;
+      uint32_t full_ph = 0;  // bit g*8+s: parity of the next phase of full_bar(g, s)
+      bool ok = true;
+      for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
+        const Tile q = tile_at(t, expert);
+        // (rows past the tile's tokens are the next expert's, or zeros past the last)
+        const int x_row = q.rows.first + q.t0, w_row = q.expert * N + q.n0;
+        for (int kb = 0; kb < kb_count; ++kb) {
+          if (round > 0 && !ptx::mbar_wait(empty_bar(s), (round - 1) & 1u)) {
+            report(kStatusWait);
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full_bar(g, s);
+          ptx::mbar_arrive_expect_tx(fb, L::kStageBytes);
+          ptx::tma_load_2d(x_addr(s), &tm_x, fb, kb * kBK, x_row);
+          ptx::tma_load_2d(w_addr(s), &tm_w, fb, kb * G::kWordsPerGroup, w_row);
+          full_ph ^= 1u << (g * 8 + s);
+          ++issued;
+          if (++g == kDequantGroups) g = 0;
+          if (++s == kStages) {
+            s = 0;
+            ++round;
+          }
         }
       }
-      const int turns = (q.count + 7) / 8;
-      for (int kb = 0; kb < kb_count; ++kb) {
-        if (round > 0 && !__all_sync(kAll, ptx::mbar_wait(empty_bar(s), (round - 1) & 1u))) {
-          report(kStatusWait);
-          ok = false;
-          break;
-        }
-        const uint32_t fb = full_bar(g, s);
-        if (threadIdx.x == 0) {
-          ptx::mbar_arrive_expect_tx(fb, L::kWBytes);
-          ptx::tma_load_2d(w_addr(s), &tm_w, fb, kb * G::kWordsPerGroup, q.expert * N + q.n0);
-        }
-        __syncwarp();
-        const uint8_t* from = x + int64_t(kb) * (kBK * 2);
-        const uint32_t dst = x_addr(s) + to;
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i)
-          if (i < turns) copy16(dst + uint32_t(i * 1024), from + uint64_t(row[i]) * 16);
-        copies_arrive(fb);
-        full_ph ^= 1u << (g * 8 + s);
-        ++issued;
-        if (++g == kDequantGroups) g = 0;
-        if (++s == kStages) {
-          s = 0;
-          ++round;
+      if (!ok) {
+        // the last loads, one per stage, may be in flight
+        const int v0 = issued > kStages ? issued - kStages : 0;
+        for (int v = v0; v < issued; ++v) {
+          const int vg = v % kDequantGroups, vs = v % kStages;
+          const uint32_t parity = ((full_ph >> (vg * 8 + vs)) & 1u) ^ 1u;
+          if (!ptx::mbar_wait(full_bar(vg, vs), parity)) report(kStatusWait);
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && threadIdx.x == 0) {
-      // the last loads, one per stage, may be in flight
-      const int v0 = issued > kStages ? issued - kStages : 0;
-      for (int v = v0; v < issued; ++v) {
-        const int vg = v % kDequantGroups, vs = v % kStages;
-        const uint32_t parity = ((full_ph >> (vg * 8 + vs)) & 1u) ^ 1u;
-        if (!ptx::mbar_wait(full_bar(vg, vs), parity)) report(kStatusWait);
-      }
-    }
-  } else if (warp == kFetchWarps) {
+  } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     constexpr uint32_t fmt = std::is_same<AT, __half>::value ? 0u : 1u;
     const uint32_t leads = lane == 0;
@@ -335,8 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kSplit == 2)
           tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage + 32), lo);
         tmem_wait_st();
-        // (the tokens' rows, whose barrier lies behind, for the MMAs' proxy)
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -349,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, et = threadIdx.x - kFirstEpilogue * 32;
     constexpr int kCols = BN < 128 ? BN : 128;  // at a time
+    static_assert(kCols % (2 * kOutTokens) == 0, "the tiles take turns");
+    const bool wide = N % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
     int i = 0, expert = 0;
     for (int t = int(blockIdx.x); t < total; t += int(gridDim.x), ++i) {
       const Tile q = tile_at(t, expert);
@@ -415,7 +394,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (c0 + kCols >= q.count) hand_back();
-        if (n < N) {
+        if (wide) {
+          // by way of shared memory, so that 16 lanes store a token's 128 outputs
+#pragma unroll
+          for (int c = 0; c < kCols; c += kOutTokens) {
+            if (c0 + c < q.count) {
+              uint16_t* tile = turned + (c / kOutTokens & 1) * (kOutTokens * kBM);
+#pragma unroll
+              for (int j = 0; j < kOutTokens; j += 2) {
+                const uint32_t v = out[(c + j) / 2];
+                tile[j * kBM + quarter * 32 + lane] = uint16_t(v);
+                tile[(j + 1) * kBM + quarter * 32 + lane] = uint16_t(v >> 16);
+              }
+              // (who fills a tile again has passed the other's barrier since)
+              asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+              const int n8 = et % 16 * 8;
+#pragma unroll
+              for (int j = 0; j < kOutTokens; j += kEpilogueWarps * 2) {
+                const int p = mine[c0 + c + j + et / 16];
+                if (p >= 0 && q.n0 + n8 < N)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + int64_t(p) * N + q.n0 +
+                                            n8) =
+                      *reinterpret_cast<const uint4*>(tile + (j + et / 16) * kBM + n8);
+              }
+            }
+          }
+        } else if (n < N) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 16) {
             if (c0 + c < q.count) {
@@ -434,9 +438,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kFetchWarps) {
+  if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, uint32_t(L::kTmemCols));
+  }
+}
+
+// The rows of x in the plan's order: a warp a row, pairs that are none left out.
+constexpr int kSortWarps = 8;
+
+__global__ void __launch_bounds__(kSortWarps * 32)
+    sort_rows_kernel(const ExpertArgs a, uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = int64_t(blockIdx.x) * kSortWarps + (threadIdx.x >> 5);
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (i >= a.n_pairs) return;
+  const int p = a.order[i];
+  if (p < 0 || p >= a.n_pairs) return;
+  const int packs = int(a.K) / 8;
+  const uint4* from =
+      reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
+                                     int64_t(p / a.pairs_per_row) * a.x_stride);
+  uint4* to = out + i * packs;
+  // four loads before the first store
+  for (int k0 = lane; k0 < packs; k0 += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k0 + 32 * j < packs) v[j] = from[k0 + 32 * j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k0 + 32 * j < packs) to[k0 + 32 * j] = v[j];
   }
 }
 
@@ -449,13 +482,15 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), kBytes, &done))
     return check_launch("qlin_expert_linear: shared memory");
-  const int64_t x_rows = a.n_pairs / a.pairs_per_row;
   const int64_t words = a.K * BITS / 32;
-  if (x_rows * (a.x_stride / 8) > int64_t(0xffffffffu))
-    return fail(QLIN_ERR_UNSUPPORTED, "qlin_expert_linear: x spans more than 64 GiB");
-  CUtensorMap tm_w;
-  const qlin_status s =
-      make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wq, uint64_t(words),
+  CUtensorMap tm_x, tm_w;
+  qlin_status s = make_map(&tm_x,
+                           std::is_same<AT, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           a.workspace, uint64_t(a.K), uint64_t(a.n_pairs), uint64_t(a.K) * 2, kBK,
+                           BN, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s != QLIN_OK) return s;
+  s = make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wq, uint64_t(words),
                uint64_t(a.E) * uint64_t(a.N), uint64_t(words) * 4, Geo<BITS>::kWordsPerGroup, kBM,
                BITS == 4 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != QLIN_OK) return s;
@@ -464,16 +499,22 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   if (tiles > (int64_t(1) << 30))
     return fail(QLIN_ERR_UNSUPPORTED, "qlin_expert_linear: too many tiles");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, sm_count())));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kBytes;
+  cfg.gridDim = dim3(unsigned((a.n_pairs + kSortWarps - 1) / kSortWarps));
+  cfg.blockDim = dim3(kSortWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, kern, tm_w, a);
+  if (cudaLaunchKernelEx(&cfg, sort_rows_kernel, a, static_cast<uint4*>(a.workspace)) !=
+      cudaSuccess)
+    return check_launch("qlin_expert_linear");
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, sm_count())));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a);
   return check_launch("qlin_expert_linear");
 }
 

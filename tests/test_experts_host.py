@@ -66,9 +66,10 @@ def test_route_refusals(L):
 
 
 def linear(L, x=FAKE, xs=128, ppr=2, order=FAKE, offsets=FAKE, P=6, wq=FAKE, sc=FAKE, bi=FAKE,
-           y=FAKE, E=4, N=32, K=128, bits=4, group=64, dt=q.QLIN_F16, ydt=q.QLIN_F16, flags=0):
+           y=FAKE, E=4, N=32, K=128, bits=4, group=64, dt=q.QLIN_F16, ydt=q.QLIN_F16, flags=0,
+           ws=None, size=0):
     return L.qlin_expert_linear(x, xs, ppr, order, offsets, P, wq, sc, bi, y, E, N, K, bits, group,
-                                dt, ydt, flags, None)
+                                dt, ydt, ws, size, flags, None)
 
 
 def test_expert_linear_refusals(L):
@@ -96,6 +97,11 @@ def test_expert_linear_refusals(L):
     assert linear(L, sc=FAKE + 1) == MISALIGNED
     assert linear(L, y=FAKE + 2, ydt=q.QLIN_F32) == MISALIGNED
     assert linear(L, P=0, x=None, y=None) == OK
+    need = L.qlin_expert_linear_workspace_size(4000, 4, 128)
+    assert need >= 4000 * 128 * 2 and L.qlin_expert_linear_workspace_size(6, 4, 128) == 0
+    assert linear(L, P=4000) == INVALID
+    assert linear(L, P=4000, ws=FAKE, size=need - 1) == INVALID
+    assert linear(L, P=4000, ws=FAKE + 8, size=need) == MISALIGNED
 
 
 def test_combine_refusals(L):
