@@ -69,25 +69,26 @@ struct Layout {
   static_assert(kStageBytes % 1024 == 0 && kStages >= 2, "");
 };
 
-// As mma_f16_ts and mma_commit, by the lane that leads, in a converged warp.
-__device__ __forceinline__ void mma_by(uint32_t leads, uint32_t d_tmem, uint32_t a_tmem,
-                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// True in one lane of a converged warp, which the compiler knows to be one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leads)
-      : "memory");
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
-__device__ __forceinline__ void commit_by(uint32_t leads, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          bar),
-      "r"(leads)
-      : "memory");
+
+// mbar_wait of a whole warp, converged.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  if (__all_sync(kAll, ptx::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(kAll, ptx::mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 0 && __any_sync(kAll, ptx::globaltimer_ns() - t0 > 2000000000ull))
+      return false;
+  }
 }
 
 // Where a CTA is in its list of tiles.
@@ -108,7 +109,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw_base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (what comes from a shuffle the compiler knows to be the same in a warp, and keeps the
+  // issuer's loop in uniform registers, as the MMA takes its operands)
+  const int warp = __shfl_sync(kAll, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int kb_count = int(a.K) / kBK, N = int(a.N);
   const int n_tiles = (N + kBM - 1) / kBM;
 
@@ -172,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(kAll, *tmem_slot, 0);
   // (a kernel that starts from here on finds this one's tensor memory taken already)
   grid_launch_dependents();
-  const int total = first_job[a.E] * n_tiles;
+  const int total = __shfl_sync(kAll, first_job[a.E] * n_tiles, 0);
   auto tile_at = [&](int t, int& expert) {
     const int job = t / n_tiles;
     while (first_job[expert + 1] <= job) ++expert;
@@ -231,17 +234,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     constexpr uint32_t fmt = std::is_same<AT, __half>::value ? 0u : 1u;
-    const uint32_t leads = lane == 0;
+    const bool leads = elect_one();
     const uint64_t b_desc0 = ptx::sw128_kmajor_desc(base);
     int s = 0, i = 0, expert = 0;
     uint32_t phase = 0;
     bool ok = true, any = false;
     for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x), ++i) {
       const Tile q = tile_at(t, expert);
-      const uint32_t idesc = ptx::idesc_f16(fmt, kBM, uint32_t((q.count + 15) & ~15));
+      const uint32_t columns = uint32_t(__shfl_sync(kAll, (q.count + 15) & ~15, 0));
+      const uint32_t idesc = ptx::idesc_f16(fmt, kBM, columns);
       const int buf = i % L::kDBufs;
       if (i >= L::kDBufs &&
-          !__all_sync(kAll, ptx::mbar_wait(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u))) {
+          !wait_warp(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u)) {
         report(kStatusWait);
         ok = false;
         break;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t more = 0;
       for (int kb = 0; kb < kb_count; ++kb) {
         // (A ready implies that the stage's bytes have landed)
-        if (!__all_sync(kAll, ptx::mbar_wait(afull_bar(s), phase))) {
+        if (!wait_warp(afull_bar(s), phase)) {
           report(kStatusWait);
           ok = false;
           break;
@@ -259,25 +263,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const uint32_t a_tmem = tmem_base + uint32_t(L::kACol0 + s * L::kAColsPerStage);
         const uint64_t bd = b_desc0 + uint64_t(uint32_t(s * L::kStageBytes) >> 4);
+        if (leads) {
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {
-          mma_by(leads, d_tmem, a_tmem + uint32_t(8 * kk), bd + uint64_t(2 * kk), idesc,
-                 kk > 0 ? 1u : more);
-          if constexpr (kSplit == 2)  // the bfloat16 residual
-            mma_by(leads, d_tmem, a_tmem + uint32_t(32 + 8 * kk), bd + uint64_t(2 * kk), idesc, 1u);
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            mma_f16_ts(d_tmem, a_tmem + uint32_t(8 * kk), bd + uint64_t(2 * kk), idesc,
+                       kk > 0 ? 1u : more);
+            if constexpr (kSplit == 2)  // the bfloat16 residual
+              mma_f16_ts(d_tmem, a_tmem + uint32_t(32 + 8 * kk), bd + uint64_t(2 * kk), idesc, 1u);
+          }
+          ptx::mma_commit(empty_bar(s));
         }
+        __syncwarp();
         more = 1;
         any = true;
-        commit_by(leads, empty_bar(s));
         if (++s == kStages) {
           s = 0;
           phase ^= 1u;
         }
       }
-      if (ok) commit_by(leads, accf_bar + 8u * buf);
+      if (ok && leads) ptx::mma_commit(accf_bar + 8u * buf);
+      __syncwarp();
     }
     // before tensor memory is freed every MMA issued here must have completed
-    commit_by(leads, done_bar);
+    if (leads) ptx::mma_commit(done_bar);
+    __syncwarp();
     if (any && !ptx::mbar_wait(done_bar, 0)) report(kStatusWait);
     __syncwarp();
   } else if (warp < kFirstEpilogue) {
