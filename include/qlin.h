@@ -554,7 +554,7 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
 
 /* Bytes of device scratch that qlin_expert_linear needs (0 where experts have few
  * rows; else the rows of x in the plan's order). */
-size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K);
+size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K);
 
 /*
  * y[p] = x[p / pairs_per_row] . W_hat[e]^T for every pair p of each expert e of

@@ -89,7 +89,7 @@ _SIGNATURES = {
     "qlin_expert_linear": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_vp, _c_i64] + [_c_vp] * 4
                            + [_c_int, _c_i64, _c_i64] + [_c_int] * 4
                            + [_c_vp, ctypes.c_size_t, ctypes.c_uint, _c_vp]),
-    "qlin_expert_linear_workspace_size": (ctypes.c_size_t, [_c_i64, _c_int, _c_i64]),
+    "qlin_expert_linear_workspace_size": (ctypes.c_size_t, [_c_i64, _c_int, _c_i64, _c_i64]),
     "qlin_combine_experts": (_c_int, [_c_vp] * 4 + [_c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_int,
                                                     _c_int, ctypes.c_uint, _c_vp]),
     # include/qlin_testing.h: failure paths and host-side choices, for the
@@ -832,7 +832,7 @@ def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
                  "device"),
                 (False, "out must be contiguous [T*top_k, N], on x's device, in out_dtype"))
     L = lib()
-    size = L.qlin_expert_linear_workspace_size(pairs, routing.n_experts, shape[1])
+    size = L.qlin_expert_linear_workspace_size(pairs, routing.n_experts, n, shape[1])
     workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     status = L.qlin_expert_linear(
         x.data_ptr(), _row_stride(x, shape[1]), 1 if shape[0] == pairs else routing.top_k,

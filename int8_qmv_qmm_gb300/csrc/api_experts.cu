@@ -79,8 +79,8 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
   return launch_route_experts(a, workspace, flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K) {
-  return n_pairs < 1 || E < 1 || K < 1 ? 0 : expert_linear_workspace_size(n_pairs, E, K);
+size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K) {
+  return n_pairs < 1 || E < 1 || N < 1 || K < 1 ? 0 : expert_linear_workspace_size(n_pairs, E, N, K);
 }
 
 qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_row,
@@ -115,7 +115,7 @@ qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_ro
   if (!x || !order || !offsets || !wq || !scales || !biases || !y)
     return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
   if (x_stride < K) return fail(QLIN_ERR_INVALID_ARG, "%s: x_stride is shorter than K", name);
-  const size_t need = expert_linear_workspace_size(n_pairs, E, K);
+  const size_t need = expert_linear_workspace_size(n_pairs, E, N, K);
   if (need && (!workspace || workspace_bytes < need))
     return fail(QLIN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, need);
   if (!aligned(x, 16) || x_stride % 8 || !aligned(wq, 16) || !aligned(workspace, 16) || !aligned(scales, 2) ||

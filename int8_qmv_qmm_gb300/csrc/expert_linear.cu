@@ -25,8 +25,9 @@ int stream_tiles(int64_t n_pairs, int E, int64_t K) {
 
 }  // namespace
 
-size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K) {
-  return n_pairs > 0 && !stream_tiles(n_pairs, E, K) ? size_t(n_pairs) * K * 2 : 0;
+size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K) {
+  return n_pairs > 0 && !stream_tiles(n_pairs, E, K) ? expert_tile_workspace_size(n_pairs, E, N, K)
+                                                   : 0;
 }
 
 qlin_status launch_expert_linear(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,

@@ -37,6 +37,7 @@ qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype
 cudaError_t expert_stream_take_status(unsigned* flags);
 qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, double rows,
                                unsigned flags, cudaStream_t st);
+size_t expert_tile_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K);
 cudaError_t expert_tile_take_status(unsigned* flags);
 
 }  // namespace qlin

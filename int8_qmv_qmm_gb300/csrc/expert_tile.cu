@@ -8,18 +8,27 @@
 //
 // A first kernel copies the tokens' rows in the plan's order to the workspace, so that a
 // tile's are neighbours and come as one TMA box a stage; a token's products are written
-// to its pair's row.  The copy of 32768 rows of 2048 (134 MB) takes about 25 us of FIXME.
-// (Fetching rows from where they are was slower: by TMA gathers of four rows, 31 ns each
-// on an SM, 1185 us; by cp.async of two or four warps 517 and 425.)
+// to its pair's row.  (Fetching rows from where they are was slower: by TMA gathers of
+// four rows, 31 ns each on an SM, 1185 us for 4096 tokens; by cp.async of two or four
+// warps 517 and 425; sorted first 304 at the time.)
+//
+// Both types multiply in f16.  bfloat16 is brought there by powers of two, which the
+// outputs are multiplied back by: one for each token (its largest element to 2^14, exact
+// down to 2^-28 of it) and one for each weight row (found from its scales and biases; a
+// weight is then rounded to f16's 11 bits, or to 2^-38 of the row's largest).  The first
+// kernel finds them.  (Two bfloat16 products for the high and low part of a weight, as
+// qmm.cu has them, took 361 us where f16 took 241.)
 //
 //   warp 0       loads the tokens' rows and the packed tile (TMA, one thread)
-//   warp 1       issues the MMAs, converged, with the operands' descriptors uniform; a
-//                tile with fewer tokens than BN multiplies what it has, in steps of 16
-//   warps 2..9   two warpgroups that reconstruct stages in turn
-//   warps 10..13 epilogue: takes up to 128 of the tokens' columns at a time to registers
-//                at 16 bits, hands the accumulator back with the last, and stores 16 bytes
-//                a lane by way of shared memory (2 bytes a lane, 64 a warp: 304 us for
-//                what takes FIXME)
+//   warp 1       issues the MMAs, converged, with the operands' descriptors in uniform
+//                registers (a loop of one thread alone took 84 cycles an MMA, and set the
+//                pace); a tile with fewer tokens than BN multiplies what it has, in steps
+//                of 16
+//   then         warpgroups that reconstruct stages in turn
+//   last         epilogue, two warps for each quarter of the rows: each takes half of the
+//                tokens' columns to registers at 16 bits, hands the accumulator back, and
+//                stores 16 bytes a lane by way of shared memory while the next tile runs
+//                (2 bytes a lane, 64 a warp, took 304 us where this took 271)
 //
 // Every wait is bounded (about 2 s); one that gives up sets a status bit, and the CTA
 // waits for its copies and MMAs in flight, frees its tensor memory and leaves.
@@ -39,18 +48,18 @@ __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_tile_s
 
 constexpr int kDequantGroups = 2;
 constexpr int kDequantWarps = 4 * kDequantGroups;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;
 constexpr int kFirstDequant = 2;
 constexpr int kFirstEpilogue = kFirstDequant + kDequantWarps;
 constexpr int kThreads = (kFirstEpilogue + kEpilogueWarps) * 32;
 constexpr int kMaxExperts = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxShared = 227 * 1024;
-// Tokens whose outputs are turned around in shared memory at a time, and two of those.
-constexpr int kOutTokens = 32;
-constexpr int kOutBytes = 2 * kOutTokens * kBM * 2;
+// Tokens whose outputs are turned around in shared memory at a time.
+constexpr int kOutTokens = 16;
+constexpr int kOutBytes = 2 * 2 * kOutTokens * kBM * 2;  // two for each half
 
-template <int BITS, int BN, int SPLIT>
+template <int BITS, int BN>
 struct Layout {
   static constexpr int kXBytes = BN * kBK * 2;
   static constexpr int kWBytes = Geo<BITS>::kPackedBytes;
@@ -58,16 +67,31 @@ struct Layout {
   // two accumulators unless they would leave tensor memory too few A slots
   static constexpr int kDBufs = BN >= 256 ? 1 : 2;
   static constexpr int kACol0 = kDBufs * BN;
-  static constexpr int kAColsPerStage = SPLIT * kBK / 2;
+  static constexpr int kAColsPerStage = kBK / 2;
   // barriers and the tensor memory's address, the epilogue's tiles, first_job, the tiles'
-  // pairs
-  static constexpr int kRestBytes = 512 + kOutBytes + (kMaxExperts + 4) * 4 + 2 * BN * 4;
+  // pairs and factors
+  static constexpr int kRestBytes = 512 + kOutBytes + (kMaxExperts + 4) * 4 + 2 * BN * 8;
   static constexpr int kFit = (kMaxShared - 1024 - kRestBytes) / kStageBytes;
   static constexpr int kSlots = (512 - kACol0) / kAColsPerStage;
   static constexpr int kStages = kFit < kSlots ? (kFit < 8 ? kFit : 8) : (kSlots < 8 ? kSlots : 8);
   static constexpr int kTmemCols = kACol0 + kStages * kAColsPerStage <= 256 ? 256 : 512;
   static_assert(kStageBytes % 1024 == 0 && kStages >= 2, "");
 };
+
+// What the first kernel leaves in the workspace.
+struct Sorted {
+  uint4* x;           // f16 [n_pairs][K]
+  float* token_back;  // [n_pairs] (bfloat16)
+  float* row_factor;  // [E][N] (bfloat16)
+};
+Sorted sorted_in(void* workspace, int64_t n_pairs, int64_t K) {
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  Sorted r;
+  r.x = reinterpret_cast<uint4*>(p);
+  r.token_back = reinterpret_cast<float*>(p + n_pairs * K * 2);
+  r.row_factor = r.token_back + n_pairs;
+  return r;
+}
 
 // True in one lane of a converged warp, which the compiler knows to be one.
 __device__ __forceinline__ bool elect_one() {
@@ -100,9 +124,9 @@ struct Tile {
 template <int BITS, typename AT, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                const ExpertArgs a) {
-  constexpr int kSplit = OperandSplit<AT>::value;
-  using L = Layout<BITS, BN, kSplit>;
+                const ExpertArgs a, const Sorted sorted) {
+  constexpr bool kHalf = std::is_same<AT, __half>::value;
+  using L = Layout<BITS, BN>;
   using G = Geo<BITS>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -129,9 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(8 * ((kDequantGroups + 2) * 8 + 5) + 4 <= 512, "barrier block");
   uint8_t* const rest = gbase + kStages * L::kStageBytes;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
-  uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][kOutTokens][kBM]
+  uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][2][kOutTokens][kBM]
   int* first_job = reinterpret_cast<int*>(rest + 512 + kOutBytes);  // the jobs of the experts before each
   int* pairs = first_job + kMaxExperts + 4;             // [2][BN], of the tile's tokens
+  float* factors = reinterpret_cast<float*>(pairs + 2 * BN);  // [2][BN] (bfloat16)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -233,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    constexpr uint32_t fmt = std::is_same<AT, __half>::value ? 0u : 1u;
     const bool leads = elect_one();
     const uint64_t b_desc0 = ptx::sw128_kmajor_desc(base);
     int s = 0, i = 0, expert = 0;
@@ -242,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x), ++i) {
       const Tile q = tile_at(t, expert);
       const uint32_t columns = uint32_t(__shfl_sync(kAll, (q.count + 15) & ~15, 0));
-      const uint32_t idesc = ptx::idesc_f16(fmt, kBM, columns);
+      const uint32_t idesc = ptx::idesc_f16(0u, kBM, columns);
       const int buf = i % L::kDBufs;
       if (i >= L::kDBufs &&
           !wait_warp(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u)) {
@@ -268,8 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kBK / 16; ++kk) {
             mma_f16_ts(d_tmem, a_tmem + uint32_t(8 * kk), bd + uint64_t(2 * kk), idesc,
                        kk > 0 ? 1u : more);
-            if constexpr (kSplit == 2)  // the bfloat16 residual
-              mma_f16_ts(d_tmem, a_tmem + uint32_t(32 + 8 * kk), bd + uint64_t(2 * kk), idesc, 1u);
           }
           ptx::mma_commit(empty_bar(s));
         }
@@ -304,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = (int64_t(q.expert) * N + min(n, N - 1)) * kb_count;
       const AT* srow = static_cast<const AT*>(a.scales) + at;
       const AT* brow = static_cast<const AT*>(a.biases) + at;
+      float factor = 1.f;
+      if constexpr (!kHalf) factor = sorted.row_factor[int64_t(q.expert) * N + min(n, N - 1)];
       for (int kb = 0; kb < kb_count; ++kb, ++u) {
         const int cs = s;
         if (++s == kStages) s = 0;
@@ -316,12 +340,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         full_ph ^= 1u << cs;
         const uint8_t* wrow = gbase + (w_addr(cs) - base) + r * G::kPackedRowBytes;
-        uint32_t w[32];
-        uint32_t lo[kSplit == 2 ? 32 : 1];
-        dequant_row<BITS, AT, kSplit>(wrow, r, sc, bc, row_ok, w, lo);
+        __half scale, bias;
+        if constexpr (kHalf) {
+          scale = sc;
+          bias = bc;
+        } else {
+          scale = __float2half_rn(Act<AT>::to_f32(sc) * factor);
+          bias = __float2half_rn(Act<AT>::to_f32(bc) * factor);
+        }
+        uint32_t w[32], none[1];
+        dequant_row<BITS, __half, 1>(wrow, r, scale, bias, row_ok, w, none);
         tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage), w);
-        if constexpr (kSplit == 2)
-          tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage + 32), lo);
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -333,111 +362,126 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, et = threadIdx.x - kFirstEpilogue * 32;
-    constexpr int kCols = BN < 128 ? BN : 128;  // at a time
+    const int quarter = warp & 3, half = (warp - kFirstEpilogue) >> 2;
+    const int et = (threadIdx.x - kFirstEpilogue * 32) & 127;  // within the half
+    constexpr int kCols = BN / 2;                              // of a half
     static_assert(kCols % (2 * kOutTokens) == 0, "the tiles take turns");
     const bool wide = N % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+    auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
     int i = 0, expert = 0;
     for (int t = int(blockIdx.x); t < total; t += int(gridDim.x), ++i) {
       const Tile q = tile_at(t, expert);
-      int* mine = pairs + (i & 1) * BN;
-      for (int j = et; j < BN; j += kEpilogueWarps * 32) {
+      int* mine = pairs + (i & 1) * BN + half * kCols;
+      float* back = factors + (i & 1) * BN + half * kCols;
+      const int count = min(q.count - half * kCols, kCols);  // tokens of the half
+      for (int j = et; j < kCols; j += 128) {
         int p = -1;
-        if (j < q.count) {
-          p = a.order[q.rows.first + q.t0 + j];
+        if (j < count) {
+          const int at = q.rows.first + q.t0 + half * kCols + j;
+          p = a.order[at];
           if (p < 0 || p >= a.n_pairs) {
             report(kStatusPlan);
             p = -1;
           }
+          if constexpr (!kHalf) back[j] = sorted.token_back[at];
         }
         mine[j] = p;
       }
+      const int n = q.n0 + quarter * 32 + lane;
+      float row_back = 1.f;
+      if constexpr (!kHalf)
+        row_back = 1.f / sorted.row_factor[int64_t(q.expert) * N + min(n, N - 1)];
       // (two lists: nobody is still at the one before the last)
-      asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+      half_sync();
       const int buf = i % L::kDBufs;
       if (!__all_sync(kAll, ptx::mbar_wait(accf_bar + 8u * buf, uint32_t(i / L::kDBufs) & 1u))) {
         report(kStatusWait);
         break;
       }
       ptx::tc_fence_after();
-      const int n = q.n0 + quarter * 32 + lane;
-      const uint32_t t_lane = tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * BN);
+      const uint32_t t_lane = tmem_base + (uint32_t(quarter * 32) << 16) +
+                              uint32_t(buf * BN + half * kCols);
       auto hand_back = [&] {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(acce_bar + 8u * buf);
       };
+      // sixteen tokens' sums, as they are or (bfloat16) multiplied back
+      auto load = [&](int c, float (&f)[16]) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c), v);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          f[j] = __uint_as_float(v[j]);
+          if constexpr (!kHalf) f[j] = f[j] * row_back * back[c + j];
+        }
+      };
       if (a.y_f32) {
 #pragma unroll 1
-        for (int c = 0; c < q.count; c += 16) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c), v);
-          ptx::tmem_wait_ld();
+        for (int c = 0; c < count; c += 16) {
+          float f[16];
+          load(c, f);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int p = mine[c + j];  // (-1 past the last token)
-            if (n < N && p >= 0)
-              static_cast<float*>(a.y)[int64_t(p) * N + n] = __uint_as_float(v[j]);
+            if (n < N && p >= 0) static_cast<float*>(a.y)[int64_t(p) * N + n] = f[j];
           }
         }
         hand_back();
         continue;
       }
-      uint16_t* y = static_cast<uint16_t*>(a.y) + n;
-#pragma unroll 1
-      for (int c0 = 0; c0 < q.count; c0 += kCols) {
-        uint32_t out[kCols / 2];  // two tokens each
+      uint32_t out[kCols / 2];  // two tokens each
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          if (c0 + c < q.count) {
-            uint32_t v[16];
-            ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c0 + c), v);
-            ptx::tmem_wait_ld();
+      for (int c = 0; c < kCols; c += 16) {
+        if (c < count) {
+          float f[16];
+          load(c, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              typename Act<AT>::T2 h;
-              h.x = Act<AT>::from_f32_rn(__uint_as_float(v[2 * j]));
-              h.y = Act<AT>::from_f32_rn(__uint_as_float(v[2 * j + 1]));
-              out[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int j = 0; j < 8; ++j) {
+            typename Act<AT>::T2 h;
+            h.x = Act<AT>::from_f32_rn(f[2 * j]);
+            h.y = Act<AT>::from_f32_rn(f[2 * j + 1]);
+            out[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+      hand_back();
+      if (wide) {
+        // by way of shared memory, so that 16 lanes store a token's 128 outputs
+#pragma unroll
+        for (int c = 0; c < kCols; c += kOutTokens) {
+          if (c < count) {
+            uint16_t* tile = turned + (half * 2 + (c / kOutTokens & 1)) * (kOutTokens * kBM);
+#pragma unroll
+            for (int j = 0; j < kOutTokens; j += 2) {
+              const uint32_t v = out[(c + j) / 2];
+              tile[j * kBM + quarter * 32 + lane] = uint16_t(v);
+              tile[(j + 1) * kBM + quarter * 32 + lane] = uint16_t(v >> 16);
+            }
+            // (who fills a tile again has passed the other's barrier since)
+            half_sync();
+            const int n8 = et % 16 * 8;
+#pragma unroll
+            for (int j = 0; j < kOutTokens; j += 8) {
+              const int p = mine[c + j + et / 16];
+              if (p >= 0 && q.n0 + n8 < N)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + int64_t(p) * N + q.n0 +
+                                          n8) =
+                    *reinterpret_cast<const uint4*>(tile + (j + et / 16) * kBM + n8);
             }
           }
         }
-        if (c0 + kCols >= q.count) hand_back();
-        if (wide) {
-          // by way of shared memory, so that 16 lanes store a token's 128 outputs
+      } else if (n < N) {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + n;
 #pragma unroll
-          for (int c = 0; c < kCols; c += kOutTokens) {
-            if (c0 + c < q.count) {
-              uint16_t* tile = turned + (c / kOutTokens & 1) * (kOutTokens * kBM);
+        for (int c = 0; c < kCols; c += 16) {
+          if (c < count) {
 #pragma unroll
-              for (int j = 0; j < kOutTokens; j += 2) {
-                const uint32_t v = out[(c + j) / 2];
-                tile[j * kBM + quarter * 32 + lane] = uint16_t(v);
-                tile[(j + 1) * kBM + quarter * 32 + lane] = uint16_t(v >> 16);
-              }
-              // (who fills a tile again has passed the other's barrier since)
-              asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
-              const int n8 = et % 16 * 8;
-#pragma unroll
-              for (int j = 0; j < kOutTokens; j += kEpilogueWarps * 2) {
-                const int p = mine[c0 + c + j + et / 16];
-                if (p >= 0 && q.n0 + n8 < N)
-                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + int64_t(p) * N + q.n0 +
-                                            n8) =
-                      *reinterpret_cast<const uint4*>(tile + (j + et / 16) * kBM + n8);
-              }
-            }
-          }
-        } else if (n < N) {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 16) {
-            if (c0 + c < q.count) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int p = mine[c0 + c + j];
-                const uint32_t v = out[(c + j) / 2];
-                if (p >= 0) y[int64_t(p) * N] = uint16_t(j % 2 ? v >> 16 : v);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int p = mine[c + j];
+              const uint32_t v = out[(c + j) / 2];
+              if (p >= 0) y[int64_t(p) * N] = uint16_t(j % 2 ? v >> 16 : v);
             }
           }
         }
@@ -453,15 +497,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The rows of x in the plan's order: a warp a row, pairs that are none left out.
+// ------------------------------------------------------------------- rows in order
 constexpr int kSortWarps = 8;
+constexpr int kRowsAWarp = 8;  // weight rows whose factor a warp finds at a time
 
+// The power of two that brings a magnitude of these float bits to 2^14 .. 2^15; for none
+// (0, or not finite) 1.  Below 2^-100 it stays at 2^114.
+__device__ __forceinline__ float factor_for(uint32_t bits) {
+  const int e = int(bits >> 23);
+  const int up = e == 255 || bits == 0u ? 127 : e < 27 ? 127 + 114 : 127 + 14 + 127 - e;
+  return __uint_as_float(uint32_t(up) << 23);
+}
+
+// The rows of x in the plan's order, a warp a row (pairs that are none left out), and for
+// bfloat16, in f16 by their factors, whose inverses go to token_back; further CTAs find
+// the factors of the weight rows.
+template <typename AT>
 __global__ void __launch_bounds__(kSortWarps * 32)
-    sort_rows_kernel(const ExpertArgs a, uint4* __restrict__ out) {
+    sort_rows_kernel(const ExpertArgs a, const Sorted out, int64_t row_ctas, int qmax) {
+  constexpr bool kHalf = std::is_same<AT, __half>::value;
   const int lane = threadIdx.x & 31;
-  const int64_t i = int64_t(blockIdx.x) * kSortWarps + (threadIdx.x >> 5);
   grid_launch_dependents();
   grid_dependency_wait();
+  if (!kHalf && blockIdx.x >= row_ctas) {
+    // a weight is between its group's bias and bias + qmax * scale
+    const int64_t row = ((int64_t(blockIdx.x) - row_ctas) * kSortWarps + (threadIdx.x >> 5)) *
+                            kRowsAWarp + lane / 4;
+    if (row >= int64_t(a.E) * a.N) return;
+    const int groups = int(a.K) / kGroup;
+    const AT* s = static_cast<const AT*>(a.scales) + row * groups;
+    const AT* b = static_cast<const AT*>(a.biases) + row * groups;
+    uint32_t most = 0u;
+#pragma unroll 4
+    for (int g = lane % 4; g < groups; g += 4) {
+      const float low = Act<AT>::to_f32(b[g]);
+      const float high = fmaf(float(qmax), Act<AT>::to_f32(s[g]), low);
+      most = max(most, max(__float_as_uint(fabsf(low)), __float_as_uint(fabsf(high))));
+    }
+    // (the four lanes of a row leave together)
+    const unsigned mask = 15u << (lane & ~3);
+    for (int d = 1; d < 4; d <<= 1) most = max(most, __shfl_xor_sync(mask, most, d));
+    if (lane % 4 == 0) out.row_factor[row] = factor_for(most);
+    return;
+  }
+  const int64_t i = int64_t(blockIdx.x) * kSortWarps + (threadIdx.x >> 5);
   if (i >= a.n_pairs) return;
   const int p = a.order[i];
   if (p < 0 || p >= a.n_pairs) return;
@@ -469,7 +548,21 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   const uint4* from =
       reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
                                      int64_t(p / a.pairs_per_row) * a.x_stride);
-  uint4* to = out + i * packs;
+  uint4* to = out.x + i * packs;
+  float factor = 1.f;
+  if constexpr (!kHalf) {
+    uint32_t most = 0u;  // magnitudes' bits, two at a time
+#pragma unroll 4
+    for (int k = lane; k < packs; k += 32) {
+      const uint4 v = from[k];
+      most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    most = max(most & 0xffffu, most >> 16) << 16;
+    most = __reduce_max_sync(kAll, most);
+    factor = factor_for(most);
+    if (lane == 0) out.token_back[i] = 1.f / factor;
+  }
   // four loads before the first store
   for (int k0 = lane; k0 < packs; k0 += 128) {
     uint4 v[4];
@@ -477,14 +570,24 @@ __global__ void __launch_bounds__(kSortWarps * 32)
     for (int j = 0; j < 4; ++j)
       if (k0 + 32 * j < packs) v[j] = from[k0 + 32 * j];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (!kHalf) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * factor,
+                                              __uint_as_float(w[e] & 0xffff0000u) * factor);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
       if (k0 + 32 * j < packs) to[k0 + 32 * j] = v[j];
+    }
   }
 }
 
 template <int BITS, typename AT, int BN>
 qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
-  using L = Layout<BITS, BN, OperandSplit<AT>::value>;
+  using L = Layout<BITS, BN>;
   constexpr int kBytes = 1024 + L::kStages * L::kStageBytes + L::kRestBytes;
   static_assert(kBytes <= kMaxShared, "");
   auto kern = tile_kernel<BITS, AT, BN>;
@@ -493,11 +596,9 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
     return check_launch("qlin_expert_linear: shared memory");
   const int64_t words = a.K * BITS / 32;
   CUtensorMap tm_x, tm_w;
-  qlin_status s = make_map(&tm_x,
-                           std::is_same<AT, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                           a.workspace, uint64_t(a.K), uint64_t(a.n_pairs), uint64_t(a.K) * 2, kBK,
-                           BN, CU_TENSOR_MAP_SWIZZLE_128B);
+  const Sorted sorted = sorted_in(a.workspace, a.n_pairs, a.K);
+  qlin_status s = make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, sorted.x, uint64_t(a.K), uint64_t(a.n_pairs),
+                           uint64_t(a.K) * 2, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s != QLIN_OK) return s;
   s = make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wq, uint64_t(words),
                uint64_t(a.E) * uint64_t(a.N), uint64_t(words) * 4, Geo<BITS>::kWordsPerGroup, kBM,
@@ -508,7 +609,11 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   if (tiles > (int64_t(1) << 30))
     return fail(QLIN_ERR_UNSUPPORTED, "qlin_expert_linear: too many tiles");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((a.n_pairs + kSortWarps - 1) / kSortWarps));
+  const int64_t row_ctas = (a.n_pairs + kSortWarps - 1) / kSortWarps;
+  const int64_t at_once = kSortWarps * kRowsAWarp;
+  const int64_t factor_ctas =
+      std::is_same<AT, __half>::value ? 0 : (int64_t(a.E) * a.N + at_once - 1) / at_once;
+  cfg.gridDim = dim3(unsigned(row_ctas + factor_ctas));
   cfg.blockDim = dim3(kSortWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -516,14 +621,14 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, sort_rows_kernel, a, static_cast<uint4*>(a.workspace)) !=
+  if (cudaLaunchKernelEx(&cfg, sort_rows_kernel<AT>, a, sorted, row_ctas, (1 << BITS) - 1) !=
       cudaSuccess)
     return check_launch("qlin_expert_linear");
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, sm_count())));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a);
+  cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a, sorted);
   return check_launch("qlin_expert_linear");
 }
 
@@ -543,6 +648,10 @@ qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, 
                      : dispatch<8, __half>(a, rows, flags, st);
   return bits == 4 ? dispatch<4, __nv_bfloat16>(a, rows, flags, st)
                    : dispatch<8, __nv_bfloat16>(a, rows, flags, st);
+}
+
+size_t expert_tile_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K) {
+  return size_t(n_pairs) * K * 2 + size_t(n_pairs + int64_t(E) * N) * 4;
 }
 
 cudaError_t expert_tile_take_status(unsigned* flags) {

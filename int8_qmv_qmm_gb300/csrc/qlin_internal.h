@@ -149,7 +149,7 @@ struct ExpertArgs {
   int64_t N, K;
   void* workspace;
 };
-size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t K);
+size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K);
 qlin_status launch_expert_linear(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
                                  cudaStream_t st);
 qlin_status launch_combine_experts(const void* y, const int32_t* experts, const float* weights,

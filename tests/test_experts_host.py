@@ -97,8 +97,8 @@ def test_expert_linear_refusals(L):
     assert linear(L, sc=FAKE + 1) == MISALIGNED
     assert linear(L, y=FAKE + 2, ydt=q.QLIN_F32) == MISALIGNED
     assert linear(L, P=0, x=None, y=None) == OK
-    need = L.qlin_expert_linear_workspace_size(4000, 4, 128)
-    assert need >= 4000 * 128 * 2 and L.qlin_expert_linear_workspace_size(6, 4, 128) == 0
+    need = L.qlin_expert_linear_workspace_size(4000, 4, 32, 128)
+    assert need >= 4000 * 128 * 2 and L.qlin_expert_linear_workspace_size(6, 4, 32, 128) == 0
     assert linear(L, P=4000) == INVALID
     assert linear(L, P=4000, ws=FAKE, size=need - 1) == INVALID
     assert linear(L, P=4000, ws=FAKE + 8, size=need) == MISALIGNED
