@@ -68,9 +68,9 @@ struct Layout {
   static constexpr int kDBufs = BN >= 256 ? 1 : 2;
   static constexpr int kACol0 = kDBufs * BN;
   static constexpr int kAColsPerStage = kBK / 2;
-  // barriers and the tensor memory's address, the epilogue's tiles, first_job, the tiles'
+  // barriers and the tensor memory's address, the epilogue's tiles, the plan, the tiles'
   // pairs and factors
-  static constexpr int kRestBytes = 512 + kOutBytes + (kMaxExperts + 4) * 4 + 2 * BN * 8;
+  static constexpr int kRestBytes = 512 + kOutBytes + (3 * kMaxExperts + 4) * 4 + 2 * BN * 8;
   static constexpr int kFit = (kMaxShared - 1024 - kRestBytes) / kStageBytes;
   static constexpr int kSlots = (512 - kACol0) / kAColsPerStage;
   static constexpr int kStages = kFit < kSlots ? (kFit < 8 ? kFit : 8) : (kSlots < 8 ? kSlots : 8);
@@ -115,10 +115,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   }
 }
 
-// Where a CTA is in its list of tiles.
+// Where a CTA is in its list of tiles: a job (an expert and a stretch of its tokens) and
+// a block of its weight rows.
 struct Tile {
-  int expert, n0, t0, count;  // first weight row, first token of the expert, tokens
-  ExpertRows rows;
+  int job, n_tile, expert;
+  int n0, at, count;  // the first weight row, the first token's place in order, tokens
 };
 
 template <int BITS, typename AT, int BN>
@@ -155,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
   uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][2][kOutTokens][kBM]
   int* first_job = reinterpret_cast<int*>(rest + 512 + kOutBytes);  // the jobs of the experts before each
-  int* pairs = first_job + kMaxExperts + 4;             // [2][BN], of the tile's tokens
+  int* first_row = first_job + kMaxExperts + 4;         // of each expert in order
+  int* row_count = first_row + kMaxExperts;
+  int* pairs = row_count + kMaxExperts;                 // [2][BN], of the tile's tokens
   float* factors = reinterpret_cast<float*>(pairs + 2 * BN);  // [2][BN] (bfloat16)
 
   if (threadIdx.x == 0) {
@@ -182,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const ExpertRows r = expert_rows(a, e);
     if (r.bad && blockIdx.x == 0) report(kStatusPlan);
     first_job[e + 1] = (r.n + BN - 1) / BN;
+    first_row[e] = r.first;
+    row_count[e] = r.n;
   }
   if (threadIdx.x == 0) first_job[0] = 0;
   ptx::tc_fence_before();
@@ -203,30 +208,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = __shfl_sync(kAll, *tmem_slot, 0);
   // (a kernel that starts from here on finds this one's tensor memory taken already)
   grid_launch_dependents();
-  const int total = __shfl_sync(kAll, first_job[a.E] * n_tiles, 0);
-  auto tile_at = [&](int t, int& expert) {
-    const int job = t / n_tiles;
-    while (first_job[expert + 1] <= job) ++expert;
+  // (from shared memory and without a division: an access to the plan at every tile took
+  // each role a thousand cycles)
+  const int jobs = __shfl_sync(kAll, first_job[a.E], 0);
+  const int step_jobs = int(gridDim.x) / n_tiles, step_tiles = int(gridDim.x) % n_tiles;
+  auto fill = [&](Tile& q) {
+    while (first_job[q.expert + 1] <= q.job) ++q.expert;
+    const int t0 = (q.job - first_job[q.expert]) * BN;
+    q.n0 = q.n_tile * kBM;
+    q.at = first_row[q.expert] + t0;
+    q.count = min(row_count[q.expert] - t0, BN);
+  };
+  auto first_tile = [&] {
     Tile q;
-    q.expert = expert;
-    q.n0 = (t - job * n_tiles) * kBM;
-    q.rows = expert_rows(a, expert);
-    q.t0 = (job - first_job[expert]) * BN;
-    q.count = min(q.rows.n - q.t0, BN);
+    q.job = int(blockIdx.x) / n_tiles;
+    q.n_tile = int(blockIdx.x) - q.job * n_tiles;
+    q.expert = 0;
+    if (q.job < jobs) fill(q);
     return q;
+  };
+  auto next_tile = [&](Tile& q) {
+    q.job += step_jobs;
+    q.n_tile += step_tiles;
+    if (q.n_tile >= n_tiles) {
+      q.n_tile -= n_tiles;
+      ++q.job;
+    }
+    if (q.job < jobs) fill(q);
   };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int s = 0, g = 0, issued = 0, expert = 0;
+      int s = 0, g = 0, issued = 0;
       uint32_t round = 0;
       uint32_t full_ph = 0;  // bit g*8+s: parity of the next phase of full_bar(g, s)
       bool ok = true;
-      for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
-        const Tile q = tile_at(t, expert);
+      for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
         // (rows past the tile's tokens are the next expert's, or zeros past the last)
-        const int x_row = q.rows.first + q.t0, w_row = q.expert * N + q.n0;
+        const int x_row = q.at, w_row = q.expert * N + q.n0;
         for (int kb = 0; kb < kb_count; ++kb) {
           if (round > 0 && !ptx::mbar_wait(empty_bar(s), (round - 1) & 1u)) {
             report(kStatusWait);
@@ -260,11 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     const bool leads = elect_one();
     const uint64_t b_desc0 = ptx::sw128_kmajor_desc(base);
-    int s = 0, i = 0, expert = 0;
+    int s = 0, i = 0;
     uint32_t phase = 0;
     bool ok = true, any = false;
-    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x), ++i) {
-      const Tile q = tile_at(t, expert);
+    for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q), ++i) {
       const uint32_t columns = uint32_t(__shfl_sync(kAll, (q.count + 15) & ~15, 0));
       const uint32_t idesc = ptx::idesc_f16(0u, kBM, columns);
       const int buf = i % L::kDBufs;
@@ -316,11 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = (warp - kFirstDequant) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // weight row within the tile
     const uint32_t a_lane = tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(L::kACol0);
-    int s = 0, u = 0, expert = 0;
+    int s = 0, u = 0;
     uint32_t full_ph = 0;  // bit s: parity of the next phase of full_bar(grp, s)
     bool ok = true;
-    for (int t = int(blockIdx.x); t < total && ok; t += int(gridDim.x)) {
-      const Tile q = tile_at(t, expert);
+    for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
       const int n = q.n0 + r;
       const bool row_ok = n < N;
       const int64_t at = (int64_t(q.expert) * N + min(n, N - 1)) * kb_count;
@@ -368,16 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(kCols % (2 * kOutTokens) == 0, "the tiles take turns");
     const bool wide = N % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
     auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
-    int i = 0, expert = 0;
-    for (int t = int(blockIdx.x); t < total; t += int(gridDim.x), ++i) {
-      const Tile q = tile_at(t, expert);
+    int i = 0;
+    for (Tile q = first_tile(); q.job < jobs; next_tile(q), ++i) {
       int* mine = pairs + (i & 1) * BN + half * kCols;
       float* back = factors + (i & 1) * BN + half * kCols;
       const int count = min(q.count - half * kCols, kCols);  // tokens of the half
       for (int j = et; j < kCols; j += 128) {
         int p = -1;
         if (j < count) {
-          const int at = q.rows.first + q.t0 + half * kCols + j;
+          const int at = q.at + half * kCols + j;
           p = a.order[at];
           if (p < 0 || p >= a.n_pairs) {
             report(kStatusPlan);
@@ -433,15 +450,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t out[kCols / 2];  // two tokens each
 #pragma unroll
-      for (int c = 0; c < kCols; c += 16) {
+      for (int c = 0; c < kCols; c += 32) {
         if (c < count) {
-          float f[16];
-          load(c, f);
+          uint32_t v[32];  // (two loads, one wait)
+          ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c), *reinterpret_cast<uint32_t(*)[16]>(v));
+          ptx::tmem_ld_32x32b_x16(t_lane + uint32_t(c + 16), *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+          ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
+            float x = __uint_as_float(v[2 * j]), y = __uint_as_float(v[2 * j + 1]);
+            if constexpr (!kHalf) {
+              x = x * row_back * back[c + 2 * j];
+              y = y * row_back * back[c + 2 * j + 1];
+            }
             typename Act<AT>::T2 h;
-            h.x = Act<AT>::from_f32_rn(f[2 * j]);
-            h.y = Act<AT>::from_f32_rn(f[2 * j + 1]);
+            h.x = Act<AT>::from_f32_rn(x);
+            h.y = Act<AT>::from_f32_rn(y);
             out[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
