@@ -1,17 +1,43 @@
 // Log probabilities of given tokens, the entropy and the likeliest tokens of rows of
-// logits (qlin.h has the definition).
+// logits (qlin.h has the definition), in one pass over a row.
+//
+// A thread takes every T-th 16 bytes of the row (of a part of it, where a cluster of CTAs
+// shares a row) and keeps, in float32, its largest logit m and where it stands, a
+// reference c <= m, and sums over its logits of e = exp(x - c) and of e * (x - c): with
+// the row's largest logit M they become Z and the entropy's mean.  The reference moves
+// only where a logit passes it by 60, so that no sum is rescaled on the way, and x - c is
+// a difference of the logits themselves: an exponential's error does not grow with them.
+//
+// The likeliest n tokens lie with the n threads whose largest logits are the largest, in
+// the order of logits and indices: were one with another thread, the n threads' best
+// would all come before it.  So those n threads' logits are looked over again (a few
+// thousand bytes, in L2), the ones that come before the n-th thread's best are listed,
+// and a listed one's place is the number of better ones.
+//
+// Logits of -infinity, NaN and the types' lowest values count as `lowest` on the way, of
+// exponential 0.  Where that does not do (a part whose largest logit is near it, above
+// 1e37 or infinite, fewer than n threads with a logit above it) a second, slower way takes
+// the part: the definition, logit by logit.
+//
+// 2048 rows of 128256 in 16 bits are 525 MB; the instructions for an exponential and two
+// sums of each logit take about as long as reading it.
 
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "qlin_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace qlin {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTop = 32;
+constexpr int kMaxCluster = 8;
+constexpr int kList = 1024;  // logits that are ranked by counting
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+using u64 = unsigned long long;
 
 struct Args {
   const void* logits;
@@ -30,104 +56,444 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
 __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Bits that order as the numbers do; 0 for what has no share (-infinity, NaN).
 __device__ __forceinline__ uint32_t key_of(float v) {
   if (!(v > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(v + 0.f);
+  const uint32_t b = __float_as_uint(v + 0.f);  // (-0 becomes 0)
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   if (!key) return -INFINITY;
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+__device__ __forceinline__ u64 place_of(float v, int index) {
+  const uint32_t k = key_of(v);
+  return k ? u64(k) << 32 | uint32_t(~index) : 0ull;
+}
 
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ u64 warp_max(u64 v) {
+  const uint32_t hi = __reduce_max_sync(kAll, uint32_t(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
+  return u64(hi) << 32 | lo;
+}
+
+// What a logit that has no share counts as, and the largest logit below which that is
+// not far enough away.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
-  __shared__ unsigned long long best_of[kWarps];
-  __shared__ float sums[2][kWarps];
-  __shared__ unsigned long long s_best;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int64_t m = blockIdx.x;
+struct Bounds {
+  static constexpr float kLowest = -1e30f, kLow = -1e29f;
+};
+template <>
+struct Bounds<__half> {
+  static constexpr float kLowest = -65504.f, kLow = -60000.f;
+};
+constexpr float kHigh = 1e37f;
+
+// 16 bytes of logits, none below kLowest, as pairs; and the largest.
+template <typename T>
+struct Pack {
+  static constexpr int kElems = 16 / sizeof(T);
+  float2 v[kElems / 2];
+  float most;
+};
+template <typename T>
+__device__ __forceinline__ Pack<T> clean(uint4 raw) {
+  Pack<T> r;
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (std::is_same<T, float>::value) {
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fmaxf(__uint_as_float(w[i]), Bounds<T>::kLowest);
+    r.v[0] = make_float2(f[0], f[1]);
+    r.v[1] = make_float2(f[2], f[3]);
+    r.most = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+  } else {
+    using T2 = typename Act<T>::T2;
+    T2 low;
+    low.x = low.y = Act<T>::from_f32_rn(Bounds<T>::kLowest);
+    T2 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __hmax2(*reinterpret_cast<const T2*>(&w[i]), low);
+    const T2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    r.most = fmaxf(Act<T>::to_f32(m.x), Act<T>::to_f32(m.y));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        r.v[i] = __half22float2(h[i]);
+      } else {
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(&h[i]);
+        r.v[i] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+      }
+    }
+  }
+  return r;
+}
+
+// A CTA's part of a row, in 16-byte vectors on the memory's own boundaries: vector k is
+// elements k * kElems - shift .., of which those in [0, n) are the row's.
+template <typename T>
+struct Part {
+  static constexpr int kElems = 16 / sizeof(T);
+  const T* row;
+  int n, shift;
+  int first, end;  // vectors
+
+  __device__ __forceinline__ bool whole(int k) const {
+    return k * kElems >= shift && (k + 1) * kElems - shift <= n;
+  }
+  __device__ __forceinline__ uint4 load(int k) const {
+    if (whole(k)) return __ldg(reinterpret_cast<const uint4*>(row + (k * kElems - shift)));
+    // an edge: what is not the row's counts as -infinity
+    constexpr uint32_t kNone = std::is_same<T, float>::value    ? 0xff800000u
+                               : std::is_same<T, __half>::value ? 0xfc00fc00u
+                                                                : 0xff80ff80u;
+    uint32_t w[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) {
+      const int i = k * kElems - shift + e;
+      if (i >= 0 && i < n) {
+        if constexpr (std::is_same<T, float>::value) {
+          w[e] = __float_as_uint(row[i]);
+        } else {
+          const uint32_t b = *reinterpret_cast<const uint16_t*>(row + i);
+          w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | b << 16 : (w[e / 2] & 0xffff0000u) | b;
+        }
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // f(value, index) for every logit of vector k
+  template <class F>
+  __device__ __forceinline__ void each(int k, F f) const {
+    const uint4 raw = load(k);
+    const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) f(widen(t[e]), k * kElems - shift + e);
+  }
+};
+
+template <int THREADS>
+struct Shared {
+  static constexpr int kWarps = THREADS / 32;
+  float red[3][kWarps];
+  u64 sorted[kWarps][32];    // the threads' largest logits and their vectors
+  int chosen[kMaxTop];       // threads
+  int n_list;
+  u64 last;                  // the last chosen one's
+  u64 warp_best[kWarps];
+  u64 list[kList];
+  u64 best[kMaxTop];         // the part's likeliest, in order
+  // of the cluster's CTAs (rank 0's are used)
+  float sums[kMaxCluster][3];
+  u64 all[kMaxCluster][kMaxTop];
+};
+
+template <int THREADS, class Op>
+__device__ __forceinline__ float block_reduce(float v, float* buf, Op op) {
+  for (int d = 16; d; d >>= 1) v = op(v, __shfl_xor_sync(kAll, v, d));
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = buf[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v = op(v, buf[w]);
+  return v;
+}
+
+// The part's likeliest `top` logits, one after another (the slower way).
+template <typename T, int THREADS>
+__device__ void pick_slowly(const Part<T>& part, int top, Shared<THREADS>& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* row = static_cast<const T*>(a.logits) + m * a.stride;
-  // the elements in order: larger ones first, equal ones by index
-  auto next = [&](unsigned long long below) {
-    unsigned long long best = 0;
-    for (int i = threadIdx.x; i < a.V; i += kThreads) {
-      const uint32_t k = key_of(widen(row[i]));
-      const unsigned long long v = k ? (unsigned long long)(k) << 32 | uint32_t(~i) : 0ull;
-      if (v < below && v > best) best = v;
-    }
-    for (int d = 16; d; d >>= 1) {
-      const unsigned long long o = __shfl_xor_sync(kAll, best, d);
-      best = o > best ? o : best;
-    }
+  u64 mine = 0;
+  for (int k = part.first + int(threadIdx.x); k < part.end; k += THREADS)
+    part.each(k, [&](float v, int i) {
+      const u64 p = place_of(v, i);
+      mine = p > mine ? p : mine;
+    });
+  for (int j = 0; j < top; ++j) {
+    const u64 w = warp_max(mine);
     __syncthreads();
-    if (lane == 0) best_of[warp] = best;
+    if (lane == 0) s.warp_best[warp] = w;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) best = best_of[w] > best ? best_of[w] : best;
-      s_best = best;
+    u64 best = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) best = s.warp_best[i] > best ? s.warp_best[i] : best;
+    if (threadIdx.x == 0) s.best[j] = best;
+    if (!best) continue;
+    const int k = (int(~uint32_t(best)) + part.shift) / Part<T>::kElems;
+    const int owner = (k - part.first) % THREADS;
+    if (warp == owner / 32) {  // its warp looks for its next one
+      u64 next = 0;
+      for (int v = part.first + owner + THREADS * lane; v < part.end; v += THREADS * 32)
+        part.each(v, [&](float x, int i) {
+          const u64 p = place_of(x, i);
+          if (p < best && p > next) next = p;
+        });
+      next = warp_max(next);
+      if (lane == owner % 32) mine = next;
     }
-    __syncthreads();
-    return s_best;
-  };
-  const unsigned long long first = next(~0ull);
-  const float top = value_of(uint32_t(first >> 32));
-  float z = 0.f, u = 0.f;
-  for (int i = threadIdx.x; i < a.V; i += kThreads) {
-    const float v = widen(row[i]);
-    if (!(v > -INFINITY)) continue;
-    const float d = v == top ? 0.f : v - top, e = expf(d);
-    z += e;
-    if (e > 0.f) u += e * d;
-  }
-  for (int d = 16; d; d >>= 1) {
-    z += __shfl_xor_sync(kAll, z, d);
-    u += __shfl_xor_sync(kAll, u, d);
-  }
-  if (lane == 0) {
-    sums[0][warp] = z;
-    sums[1][warp] = u;
   }
   __syncthreads();
-  z = u = 0.f;
-  for (int w = 0; w < kWarps; ++w) {
-    z += sums[0][w];
-    u += sums[1][w];
+}
+
+// Sorts a warp's values, the largest to lane 0.
+__device__ __forceinline__ u64 warp_sort(u64 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size / 2; d; d >>= 1) {
+      const u64 o = __shfl_xor_sync(kAll, v, d);
+      // (the larger one to the lower lane in the stretches that descend)
+      const bool larger = ((lane & d) == 0) == ((lane & size) == 0 || size == 32);
+      v = (o > v) == larger ? o : v;
+    }
+  return v;
+}
+
+// The part's likeliest `top` logits from the threads that have them; false where fewer
+// threads have a logit to speak of, or the logits to rank are too many.
+//
+// The threads' best ones are sorted in each warp, and ranked by a search in each other
+// warp's list.  (One warp picking the best of all, `top` times: 2048 rows with their
+// first 5 took 119 us, with 20 172, where this takes 111 and 127; without any, 97.)
+template <typename T, int THREADS>
+__device__ bool pick(const Part<T>& part, int top, float most, int at, Shared<THREADS>& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 mine = warp_sort(
+      most > Bounds<T>::kLowest ? u64(key_of(most)) << 32 | uint32_t(~at) : 0ull);
+  s.sorted[warp][lane] = mine;
+  if (threadIdx.x == 0) {
+    s.n_list = 0;
+    s.last = 0;
+  }
+  __syncthreads();
+  if (lane < top && mine) {
+    int rank = lane;
+#pragma unroll
+    for (int i = 1; i < THREADS / 32; ++i) {
+      const u64* list = s.sorted[(warp + i) % (THREADS / 32)];
+      int n = 0;  // of the list's that are larger
+#pragma unroll
+      for (int d = 16; d; d >>= 1)
+        if (list[n + d - 1] > mine) n += d;
+      rank += n + (n == 31 && list[31] > mine ? 1 : 0);
+    }
+    if (rank < top) s.chosen[rank] = (int(~uint32_t(mine)) - part.first) % THREADS;
+    if (rank == top - 1) s.last = mine;
+  }
+  __syncthreads();
+  const u64 last = s.last;
+  if (!last) return false;
+  const float last_value = value_of(uint32_t(last >> 32));
+  const int last_at = int(~uint32_t(last));
+  for (int j = warp; j < top; j += THREADS / 32) {
+    for (int k = part.first + s.chosen[j] + THREADS * lane; k < part.end; k += THREADS * 32) {
+      if (clean<T>(part.load(k)).most < last_value) continue;
+      part.each(k, [&](float v, int i) {
+        if (v > last_value || (v == last_value && k <= last_at)) {
+          const int n = atomicAdd(&s.n_list, 1);
+          if (n < kList) s.list[n] = place_of(v, i);
+        }
+      });
+    }
+  }
+  __syncthreads();
+  const int n = s.n_list;
+  if (n > kList) return false;
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const u64 p = s.list[i];
+    int better = 0;
+    for (int j = 0; j < n; ++j) better += s.list[j] > p;
+    if (better < top) s.best[better] = p;
+  }
+  __syncthreads();
+  return true;
+}
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    logprobs_kernel(const Args a, int ranks) {
+  __shared__ Shared<THREADS> s;
+  constexpr int kElems = Part<T>::kElems, kUnroll = 4;
+  const int rank = ranks > 1 ? int(ptx::cluster_ctarank()) : 0;
+  const int64_t m = int64_t(blockIdx.x) / ranks;
+  Part<T> part;
+  part.row = static_cast<const T*>(a.logits) + m * a.stride;
+  part.n = a.V;
+  part.shift = int(reinterpret_cast<uintptr_t>(part.row) % 16 / sizeof(T));
+  const int vectors = (a.V + part.shift + kElems - 1) / kElems;
+  part.first = int(int64_t(vectors) * rank / ranks);
+  part.end = int(int64_t(vectors) * (rank + 1) / ranks);
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (ranks > 1) ptx::cluster_arrive_relaxed();  // (waited for before the first store to a peer)
+
+  // the thread's logits
+  float most = Bounds<T>::kLowest, c = Bounds<T>::kLowest;
+  int at = 0;
+  float2 sum = make_float2(0.f, 0.f), mean = make_float2(0.f, 0.f);
+  auto take = [&](uint4 raw, int k) {
+    const Pack<T> p = clean<T>(raw);
+    if (p.most > c + 60.f) {
+      const float d = (c - p.most) * kLog2e, f = exp2_fast(d);
+      mean.x = (mean.x + sum.x * d) * f;
+      mean.y = (mean.y + sum.y * d) * f;
+      sum.x *= f;
+      sum.y *= f;
+      c = p.most;
+    }
+    if (p.most > most) {
+      most = p.most;
+      at = k;
+    }
+    const float2 minus_c = make_float2(-c, -c), scale = make_float2(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i < kElems / 2; ++i) {
+      const float2 d = __fmul2_rn(__fadd2_rn(p.v[i], minus_c), scale);
+      const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+      sum = __fadd2_rn(sum, e);
+      mean = __ffma2_rn(e, d, mean);
+    }
+  };
+  int k = part.first + int(threadIdx.x);
+  for (; k + (kUnroll - 1) * THREADS < part.end; k += kUnroll * THREADS) {
+    uint4 raw[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) raw[i] = part.load(k + i * THREADS);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) take(raw[i], k + i * THREADS);
+  }
+  for (; k < part.end; k += THREADS) take(part.load(k), k);
+
+  // the part's: largest logit, sum of exponentials under it, and of those times the
+  // exponents (in powers of two)
+  float high = block_reduce<THREADS>(most, s.red[0], [](float x, float y) { return fmaxf(x, y); });
+  float z = 0.f, u = 0.f;
+  const bool plain = high >= Bounds<T>::kLow && high <= kHigh;  // of the CTA
+  if (plain) {
+    if (most > Bounds<T>::kLowest) {
+      const float d = (c - high) * kLog2e, f = exp2_fast(d);
+      const float own = sum.x + sum.y;
+      z = own * f;
+      u = (mean.x + mean.y + own * d) * f;
+    }
+  } else {
+    float top = -INFINITY;
+    for (int j = part.first + int(threadIdx.x); j < part.end; j += THREADS)
+      part.each(j, [&](float v, int) { top = fmaxf(top, v); });
+    __syncthreads();
+    high = block_reduce<THREADS>(top, s.red[0], [](float x, float y) { return fmaxf(x, y); });
+    for (int j = part.first + int(threadIdx.x); j < part.end; j += THREADS)
+      part.each(j, [&](float v, int) {
+        if (!(v > -INFINITY)) return;
+        const float d = v == high ? 0.f : (v - high) * kLog2e, e = exp2f(d);
+        z += e;
+        if (e > 0.f) u += e * d;
+      });
+  }
+  z = block_reduce<THREADS>(z, s.red[1], [](float x, float y) { return x + y; });
+  u = block_reduce<THREADS>(u, s.red[2], [](float x, float y) { return x + y; });
+  if (a.top && !(plain && pick<T, THREADS>(part, a.top, most, at, s)))
+    pick_slowly<T, THREADS>(part, a.top, s);
+
+  if (ranks > 1) {
+    // to the first CTA of the cluster
+    ptx::cluster_wait();  // it has started
+    if (int(threadIdx.x) < a.top)
+      st_cluster_u64(ptx::map_shared_rank(ptx::smem_u32(&s.all[rank][threadIdx.x]), 0u),
+                     s.best[threadIdx.x]);
+    if (threadIdx.x < 3)
+      ptx::st_cluster_f32(ptx::map_shared_rank(ptx::smem_u32(&s.sums[rank][threadIdx.x]), 0u),
+                          threadIdx.x == 0 ? high : threadIdx.x == 1 ? z : u);
+    ptx::cluster_sync();
+    if (rank) return;
+    high = s.sums[0][0];
+    for (int r = 1; r < ranks; ++r) high = fmaxf(high, s.sums[r][0]);
+    z = u = 0.f;
+    for (int r = 0; r < ranks; ++r) {
+      const float h = s.sums[r][0];
+      const float d = h == high ? 0.f : (h - high) * kLog2e, f = exp2f(d);
+      if (f > 0.f) {
+        z += s.sums[r][1] * f;
+        u += (s.sums[r][2] + s.sums[r][1] * d) * f;
+      }
+    }
+    // a logit's place among all lists: the number of better ones
+    for (int i = threadIdx.x; i < ranks * a.top; i += THREADS) {
+      const u64 p = s.all[i / a.top][i % a.top];
+      int better = 0;
+      for (int r = 0; r < ranks; ++r)
+        for (int j = 0; j < a.top; ++j) {
+          // (those without a logit behind all others, in their own order)
+          const u64 o = s.all[r][j];
+          better += o > p || (!p && !o && r * a.top + j < i);
+        }
+      if (better < a.top) s.best[better] = p;
+    }
+    __syncthreads();
   }
   const float log_z = logf(z);
   auto logprob = [&](float v) {
     if (!(v > -INFINITY)) return -INFINITY;
-    return (v == top ? 0.f : v - top) - log_z;
+    return (v == high ? 0.f : v - high) - log_z;
   };
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == THREADS - 1) {
     const int t = a.tokens[m];
-    a.logprobs[m] = t >= 0 && t < a.V ? logprob(widen(row[t])) : -INFINITY;
-    a.entropy[m] = first ? log_z - u / z : 0.f;
+    a.logprobs[m] = t >= 0 && t < a.V ? logprob(widen(part.row[t])) : -INFINITY;
+    a.entropy[m] = high > -INFINITY ? log_z - u / z * kLn2 : 0.f;
   }
-  unsigned long long at = first;
-  for (int j = 0; j < a.top; ++j) {
-    if (j) at = at ? next(at) : 0ull;
-    if (threadIdx.x == 0) {
-      a.top_tokens[m * a.top + j] = at ? int32_t(~uint32_t(at)) : -1;
-      a.top_logprobs[m * a.top + j] = at ? logprob(value_of(uint32_t(at >> 32))) : -INFINITY;
-    }
+  if (int(threadIdx.x) < a.top) {
+    const u64 p = s.best[threadIdx.x];
+    a.top_tokens[m * a.top + threadIdx.x] = p ? int32_t(~uint32_t(p)) : -1;
+    a.top_logprobs[m * a.top + threadIdx.x] = logprob(value_of(uint32_t(p >> 32)));
   }
 }
 
-template <typename T>
-void launch_t(const Args& a, unsigned flags, cudaStream_t st) {
+template <typename T, int THREADS>
+void launch_t(const Args& a, int ranks, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.M));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(unsigned(a.M * ranks));
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (ranks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = unsigned(ranks);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (flags & QLIN_OVERLAP_PREVIOUS) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = (flags & QLIN_OVERLAP_PREVIOUS) ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a);
+  cfg.numAttrs = n;
+  cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a, ranks);
+}
+
+template <typename T>
+void dispatch(const Args& a, unsigned flags, cudaStream_t st) {
+  // CTAs of 256 threads, four to an SM, a row each, where rows fill the SMs so; else CTAs
+  // of 512, and as many to a row as two to an SM allow and leave each thread 16 logits
+  const int64_t sms = sm_count();
+  if (a.M >= 2 * sms) return launch_t<T, 256>(a, 1, flags, st);
+  int ranks = 1;
+  while (ranks < kMaxCluster && a.M * ranks * 2 <= 2 * sms && a.V / (ranks * 2) >= 16 * 512)
+    ranks *= 2;
+  launch_t<T, 512>(a, ranks, flags, st);
 }
 
 }  // namespace
@@ -139,11 +505,11 @@ qlin_status launch_token_logprobs(const void* logits, int64_t stride, const int3
   const Args a = {logits, stride, tokens, logprobs, entropy, top, top_tokens, top_logprobs, M,
                   int(V)};
   if (ldtype == QLIN_F32)
-    launch_t<float>(a, flags, st);
+    dispatch<float>(a, flags, st);
   else if (ldtype == QLIN_F16)
-    launch_t<__half>(a, flags, st);
+    dispatch<__half>(a, flags, st);
   else
-    launch_t<__nv_bfloat16>(a, flags, st);
+    dispatch<__nv_bfloat16>(a, flags, st);
   return check_launch("qlin_token_logprobs");
 }
 
