@@ -542,8 +542,8 @@ size_t qlin_route_experts_workspace_size(int64_t T, int E);
  * NaN, which counts as that) is never chosen: where fewer than top_k remain the
  * rest of the row is expert -1, weight 0.  With T = 0 offsets is still written.
  * groups: 1 .. 32, a divisor of E.  workspace: qlin_route_experts_workspace_size
- * bytes with anything in them (NULL where that is 0); calls that can overlap
- * need one each.
+ * bytes, 16-byte aligned, with anything in them (NULL where that is 0); calls that
+ * can overlap need one each.
  */
 qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const float* bias,
                                int scoring, int groups, int top_groups, int group_score, int top_k,

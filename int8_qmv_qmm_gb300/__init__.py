@@ -766,20 +766,21 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
     L = lib()
     pairs = t * top_k
     size = int(L.qlin_route_experts_workspace_size(t, e)) // 4
-    # one allocation: experts, order, offsets and the scratch
-    ints = torch.empty(2 * pairs + e + 1 + size, dtype=torch.int32, device=logits.device)
+    # one allocation: the scratch, experts, order and offsets
+    scratch, experts, order, offsets = torch.empty(
+        size + 2 * pairs + e + 1, dtype=torch.int32,
+        device=logits.device).split((size, pairs, pairs, e + 1))
     weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
-    at = ints.data_ptr()
     status = L.qlin_route_experts(
         logits.data_ptr(), _row_stride(logits, e), None if bias is None else bias.data_ptr(),
         _SCORING[scoring], groups, top_groups, _GROUP_SCORE[group_score], top_k,
-        1 if renormalise else 0, scale, at, weights.data_ptr(), at + 4 * pairs, at + 8 * pairs, t,
-        e, _DTYPE_CODE[logits.dtype], at + 8 * pairs + 4 * (e + 1) if size else None, 4 * size,
+        1 if renormalise else 0, scale, experts.data_ptr(), weights.data_ptr(), order.data_ptr(),
+        offsets.data_ptr(), t,
+        e, _DTYPE_CODE[logits.dtype], scratch.data_ptr() if size else None, 4 * size,
         1 if overlap_previous else 0, _current_raw_stream(index))
     if status:
         _check(status)
-    return Routing.__new__(Routing)._set(ints[:pairs].view(t, top_k), weights,
-                                         ints[pairs:2 * pairs], ints[2 * pairs:2 * pairs + e + 1])
+    return Routing.__new__(Routing)._set(experts.view(t, top_k), weights, order, offsets)
 
 
 def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,

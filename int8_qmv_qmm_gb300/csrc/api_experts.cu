@@ -71,8 +71,9 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
   if (need && (!workspace || workspace_bytes < need))
     return fail(QLIN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, need);
   if (!aligned(logits, ldtype == QLIN_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(experts, 4) ||
-      !aligned(weights, 4) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(workspace, 4))
-    return fail(QLIN_ERR_MISALIGNED, "%s: a pointer is not aligned to its elements", name);
+      !aligned(weights, 4) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(workspace, 16))
+    return fail(QLIN_ERR_MISALIGNED,
+                "%s: a pointer is not aligned to its elements, or workspace to 16 bytes", name);
   const RouteArgs a = {logits,  logits_stride, bias,        scoring, groups, top_groups,
                        group_score, top_k,     renormalise, scale,   experts, weights,
                        order,   offsets,       T,           E,       ldtype};

@@ -19,10 +19,13 @@
 namespace qlin {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxExperts = 512;
-static_assert(kMaxExperts <= kThreads, "a thread for each expert in the scans");
+// Warps of a CTA: as many as fit with their scratch.
+template <int NE>
+constexpr int kWarpsFor = NE == 16 ? 16 : 32;
+
+// A warp's scratch holds an expert's value at spot(e): groups of 32 neighbours, read
+// side by side, start in different banks.
+__host__ __device__ constexpr int spot(int e) { return e + (e >> 5) * 4; }
 
 struct Args {
   const void* logits;
@@ -34,7 +37,7 @@ struct Args {
   float* weights;
   int32_t* order;
   int32_t* offsets;
-  int32_t* counts;  // [CTAs][E + 1] (more than one CTA)
+  int32_t* counts;  // [CTAs][stride_of(E)] (more than one CTA)
   int64_t T;
   int E;
   int64_t per;  // tokens of a CTA
@@ -53,27 +56,36 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Whether each of a lane's experts is in a group that is kept.  v: what a group's
-// value is made of (-infinity: not eligible), through the warp's scratch.
+// What a lane keeps over its tokens.
 template <int NE>
-__device__ __forceinline__ void keep_groups(const Args& a, const float (&v)[NE], float* scratch,
+struct Lane {
+  float bias[NE];
+  int group[NE];  // bit of each of its experts' groups among the groups that are kept
+  int lanes;      // that share a group
+};
+
+// Leaves out the experts in groups that are not kept.  v: what a group's value is made
+// of (-infinity: not eligible), through the warp's scratch.
+template <int NE>
+__device__ __forceinline__ void keep_groups(const Args& a, const Lane<NE>& own,
+                                            const float (&v)[NE], float* scratch,
                                             uint32_t (&key)[NE]) {
   const int lane = threadIdx.x & 31, size = a.E / a.groups;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (lane + 32 * i < a.E) scratch[lane + 32 * i] = v[i];
+    if (lane + 32 * i < a.E) scratch[spot(lane + 32 * i)] = v[i];
   __syncwarp();
-  int lanes = 32;  // that share a group
-  while (lanes * a.groups > 32) lanes >>= 1;
-  const int g = lane / lanes;
+  const int lanes = own.lanes, g = lane / lanes;
   float v1 = -INFINITY, v2 = -INFINITY;
-  if (g < a.groups)
+  if (g < a.groups) {
+#pragma unroll 4
     for (int j = lane % lanes; j < size; j += lanes) {
-      const float t = scratch[g * size + j];
+      const float t = scratch[spot(g * size + j)];
       v2 = fmaxf(v2, fminf(v1, t));
       v1 = fmaxf(v1, t);
     }
+  }
   for (int d = lanes / 2; d; d >>= 1) {
     const float o1 = __shfl_xor_sync(kAll, v1, d), o2 = __shfl_xor_sync(kAll, v2, d);
     v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
@@ -88,94 +100,97 @@ __device__ __forceinline__ void keep_groups(const Args& a, const float (&v)[NE],
   }
   const unsigned kept = __ballot_sync(kAll, g < a.groups && better < a.top_groups);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = lane + 32 * i;
-    if (e < a.E && !(kept >> (e / size * lanes) & 1u)) key[i] = 0u;
-  }
+  for (int i = 0; i < NE; ++i)
+    if (!(kept >> own.group[i] & 1u)) key[i] = 0u;
 }
 
-// Chooses token t's experts; lane j returns its j-th one (-1: none).
 template <typename T, int NE>
-__device__ int route_token(const Args& a, int64_t t, float* scratch) {
+__device__ __forceinline__ void load_row(const Args& a, int64_t t, T (&x)[NE]) {
   const int lane = threadIdx.x & 31;
   const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (lane + 32 * i < a.E) x[i] = row[lane + 32 * i];
+}
+
+// Chooses token t's experts from its logits; lane j returns its j-th one (-1: none).
+template <typename T, int NE>
+__device__ int route_token(const Args& a, const Lane<NE>& own, int64_t t, const T (&raw)[NE],
+                           float* scratch) {
+  const int lane = threadIdx.x & 31;
   float x[NE], score[NE];
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = e < a.E ? widen(row[e]) : -INFINITY;
-    x[i] = fmaxf(x[i], -INFINITY);  // (-infinity for NaN)
+    x[i] = lane + 32 * i < a.E ? fmaxf(widen(raw[i]), -INFINITY) : -INFINITY;  // (NaN goes)
     top = fmaxf(top, x[i]);
   }
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
   const bool softmax = !a.sigmoid;
-  if (softmax) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      score[i] = x[i] == top ? 1.f : expf(x[i] - top);
-    // (no row of -infinity alone comes here with x == top and a use for its score)
-  } else {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) score[i] = __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x[i])));
-  }
-  uint32_t key[NE];
-  float group_part[NE];
   // the scores' own sum, where a choice (which has to come out the same in any order
   // of summing: in 64 bits) or the weights need it
   float sum = 1.f;
-  if (softmax && a.bias) {
-    double z = 0.0;
+  if (softmax) {
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
 #pragma unroll
-    for (int i = 0; i < NE; ++i) z += x[i] > -INFINITY ? double(score[i]) : 0.0;
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
-    sum = float(z);
-  } else if (softmax && !a.renormalise) {
-    sum = 0.f;
+    for (int i = 0; i < NE; ++i) score[i] = x[i] == top ? 1.f : expf(x[i] - top);
+    if (a.bias) {
+      double z = 0.0;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) sum += x[i] > -INFINITY ? score[i] : 0.f;
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+      for (int i = 0; i < NE; ++i) z += x[i] > -INFINITY ? double(score[i]) : 0.0;
+      for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kAll, z, d);
+      sum = float(z);
+    } else if (!a.renormalise) {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) sum += x[i] > -INFINITY ? score[i] : 0.f;
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) score[i] = __frcp_rn(__fadd_rn(1.f, expf(-x[i])));
   }
+  uint32_t key[NE];
+  float group_part[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int e = lane + 32 * i;
     float choice = x[i];
     if (a.bias) {
       if (softmax) score[i] = __fdiv_rn(score[i], sum);
-      choice = e < a.E ? __fadd_rn(score[i], a.bias[e]) : -INFINITY;
+      choice = __fadd_rn(score[i], own.bias[i]);
     }
     key[i] = x[i] > -INFINITY ? key_of(choice) : 0u;
     group_part[i] = !key[i] ? -INFINITY : !a.bias && a.top2 ? score[i] : choice;
   }
   if (a.bias && softmax) sum = 1.f;  // (they are shares already)
-  if (a.groups > 1) keep_groups<NE>(a, group_part, scratch, key);
+  if (a.groups > 1) keep_groups<NE>(a, own, group_part, scratch, key);
 
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (lane + 32 * i < a.E) scratch[spot(lane + 32 * i)] = score[i];
   int chosen = -1;
-  float got = 0.f;
   for (int j = 0; j < a.top_k; ++j) {
     uint32_t best = 0u;
     int at = 0;
-    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i;
-        s = score[i];
       }
     const uint32_t most = __reduce_max_sync(kAll, best);
     if (!most) break;
-    const unsigned e = __reduce_min_sync(kAll, best == most ? unsigned(lane + 32 * at) : ~0u);
-    const int owner = int(e & 31u);
+    const unsigned mine = best == most ? unsigned(lane + 32 * at) : ~0u;
+    const unsigned e = __reduce_min_sync(kAll, mine);
+    if (mine == e) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (lane == owner && i == int(e >> 5)) key[i] = 0u;
-    s = __shfl_sync(kAll, s, owner);
-    if (lane == j) {
-      chosen = int(e);
-      got = s;
+      for (int i = 0; i < NE; ++i)
+        if (i == at) key[i] = 0u;
     }
+    if (lane == j) chosen = int(e);
   }
+  __syncwarp();
+  const float got = chosen >= 0 ? scratch[spot(chosen)] : 0.f;
   if (a.renormalise) {
     sum = got;
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
@@ -188,7 +203,7 @@ __device__ int route_token(const Args& a, int64_t t, float* scratch) {
   return chosen;
 }
 
-// The sum of v over the threads before this one (all threads; buf: kWarps ints).
+// The sum of v over the threads before this one (all threads; buf: an int a warp).
 __device__ __forceinline__ int scan_before(int v, int* buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int upto = v;
@@ -207,8 +222,10 @@ __device__ __forceinline__ int scan_before(int v, int* buf) {
 // Writes the order of the pairs [p0, p1): a pair's place is base[its expert] + the
 // number of pairs of that expert before it.  Each warp takes a stretch of its own,
 // counts its experts, and goes on from what the warps before it have.  counts:
-// [kWarps][E + 1] of shared memory.  (Pairs without an expert count as expert E.)
+// [WARPS][E + 1] of shared memory.  (Pairs without an expert count as expert E.)
+template <int kWarps>
 __device__ void place_pairs(const Args& a, int64_t p0, int64_t p1, const int* base, int* counts) {
+  constexpr int kThreads = kWarps * 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int width = a.E + 1;
   for (int i = threadIdx.x; i < kWarps * width; i += kThreads) counts[i] = 0;
@@ -230,10 +247,15 @@ __device__ void place_pairs(const Args& a, int64_t p0, int64_t p1, const int* ba
   __syncthreads();
   for (int e = threadIdx.x; e < width; e += kThreads) {
     int at = base[e];
-    for (int w = 0; w < kWarps; ++w) {
-      const int n = counts[w * width + e];
-      counts[w * width + e] = at;
-      at += n;
+    for (int w0 = 0; w0 < kWarps; w0 += 8) {
+      int n[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) n[w] = counts[(w0 + w) * width + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        counts[(w0 + w) * width + e] = at;
+        at += n[w];
+      }
     }
   }
   __syncthreads();
@@ -267,83 +289,124 @@ __device__ void offsets_of(const Args& a, int* base, int* buf, bool write) {
   __syncthreads();
 }
 
+// Counts of a CTA in the workspace: whole vectors of four.
+__host__ __device__ constexpr int stride_of(int E) { return (E + 4) / 4 * 4; }
+
+template <int NE>
+__host__ __device__ constexpr int scratch_words(int E) {
+  const int words = spot(E - 1) + 1;
+  return words > E + 1 ? words : E + 1;
+}
+
 template <typename T, int NE>
-__global__ void __launch_bounds__(kThreads) route_kernel(const Args a) {
-  // [kWarps][E + 1] words: the warps' groups, later their counts; base [E + 1]
+__global__ void __launch_bounds__(kWarpsFor<NE> * 32) route_kernel(const Args a) {
+  constexpr int kWarps = kWarpsFor<NE>, kThreads = kWarps * 32;
+  // [kWarps][scratch]: the warps' groups and scores, later their counts; base [E + 1]
   extern __shared__ int shared[];
   __shared__ int buf[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int width = a.E + 1;
-  int* base = shared + kWarps * width;
+  const int width = a.E + 1, words = scratch_words<NE>(a.E);
+  int* base = shared + kWarps * words;
   for (int i = threadIdx.x; i < width; i += kThreads) base[i] = 0;
+  Lane<NE> own;
+  own.lanes = 32;
+  while (own.lanes * a.groups > 32) own.lanes >>= 1;
+  const int size = a.E / a.groups;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) own.group[i] = min((lane + 32 * i) / size * own.lanes, 31);
   __syncthreads();
   grid_launch_dependents();
   grid_dependency_wait();
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    own.bias[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
   const int64_t t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
+  T x[NE], next[NE];
+  if (t0 + warp < t1) load_row<T, NE>(a, t0 + warp, next);
   for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-    const int e = route_token<T, NE>(a, t, reinterpret_cast<float*>(shared) + warp * width);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] = next[i];
+    if (t + kWarps < t1) load_row<T, NE>(a, t + kWarps, next);
+    const int e =
+        route_token<T, NE>(a, own, t, x, reinterpret_cast<float*>(shared) + warp * words);
     if (lane < a.top_k) atomicAdd(base + (e < 0 ? a.E : e), 1);
   }
   __syncthreads();
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < width; e += kThreads)
-      a.counts[int64_t(blockIdx.x) * width + e] = base[e];
+    for (int e = threadIdx.x; e < stride_of(a.E); e += kThreads)
+      a.counts[int64_t(blockIdx.x) * stride_of(a.E) + e] = e < width ? base[e] : 0;
     return;
   }
   offsets_of(a, base, buf, true);
-  place_pairs(a, 0, a.T * a.top_k, base, shared);
+  place_pairs<kWarps>(a, 0, a.T * a.top_k, base, shared);
 }
 
 // The second launch, one CTA for each of the first's.
-__global__ void __launch_bounds__(kThreads) place_kernel(const Args a) {
+template <int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) place_kernel(const Args a) {
+  constexpr int kThreads = kWarps * 32;
   extern __shared__ int shared[];
   __shared__ int buf[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int width = a.E + 1;
   int* base = shared + kWarps * width;
-  int* before = base + width;  // of the pairs in the CTAs before this one
-  for (int i = threadIdx.x; i < 2 * width; i += kThreads) base[i] = 0;
+  int* before = base + stride_of(a.E);  // of the pairs in the CTAs before this one
+  for (int i = threadIdx.x; i < 2 * stride_of(a.E); i += kThreads) base[i] = 0;
   __syncthreads();
   grid_launch_dependents();
   grid_dependency_wait();
-  for (int e = lane; e < width; e += 32) {
-    int all = 0, first = 0;
-#pragma unroll 4
-    for (int c = warp; c < int(gridDim.x); c += kWarps) {
-      const int n = a.counts[int64_t(c) * width + e];
-      all += n;
-      first += c < int(blockIdx.x) ? n : 0;
+  // four experts a load, the CTAs' counts over as many threads as there are
+  const int vectors = stride_of(a.E) / 4, teams = kThreads / vectors;
+  const int team = int(threadIdx.x) / vectors, v = int(threadIdx.x) % vectors;
+  if (team < teams) {
+    int4 all = make_int4(0, 0, 0, 0), first = all;
+#pragma unroll 12
+    for (int c = team; c < int(gridDim.x); c += teams) {
+      const int4 n = reinterpret_cast<const int4*>(a.counts)[int64_t(c) * vectors + v];
+      all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+      if (c < int(blockIdx.x)) first.x += n.x, first.y += n.y, first.z += n.z, first.w += n.w;
     }
-    atomicAdd(base + e, all);
-    atomicAdd(before + e, first);
+    atomicAdd(base + 4 * v, all.x);
+    atomicAdd(base + 4 * v + 1, all.y);
+    atomicAdd(base + 4 * v + 2, all.z);
+    atomicAdd(base + 4 * v + 3, all.w);
+    atomicAdd(before + 4 * v, first.x);
+    atomicAdd(before + 4 * v + 1, first.y);
+    atomicAdd(before + 4 * v + 2, first.z);
+    atomicAdd(before + 4 * v + 3, first.w);
   }
   __syncthreads();
   offsets_of(a, base, buf, blockIdx.x == 0);
   for (int e = threadIdx.x; e < width; e += kThreads) base[e] += before[e];
   __syncthreads();
   const int64_t t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
-  place_pairs(a, t0 * a.top_k, t1 * a.top_k, base, shared);
+  place_pairs<kWarps>(a, t0 * a.top_k, t1 * a.top_k, base, shared);
 }
 
 // Tokens that one CTA takes with its warps: up to this many in one launch.
-constexpr int64_t kOneCta = 4 * kWarps;
-
-int64_t ctas_for(int64_t T, int sms) {
-  if (T <= kOneCta) return 1;
-  const int64_t n = (T + kWarps - 1) / kWarps;
-  return n < sms ? n : sms;
-}
+constexpr int64_t kOneCta = 32;
+constexpr int64_t kTokensACta = 16;  // at least, in two launches
+constexpr int kMostCtas = 1024;
 
 template <typename T, int NE>
 qlin_status launch_t(Args a, unsigned flags, cudaStream_t st) {
-  int64_t ctas = ctas_for(a.T, sm_count());
+  constexpr int kWarps = kWarpsFor<NE>;
+  int64_t ctas = 1;
+  if (a.T > kOneCta) {
+    const int64_t most = sm_count() < kMostCtas ? sm_count() : kMostCtas;
+    ctas = (a.T + kTokensACta - 1) / kTokensACta;
+    ctas = ctas < most ? ctas : most;
+  }
   a.per = (a.T + ctas - 1) / ctas;
   if (ctas > 1) ctas = (a.T + a.per - 1) / a.per;
-  static_assert((kWarps + 2) * (kMaxExperts + 1) * 4 <= 40 * 1024, "without asking for more");
+  static_assert((kWarpsFor<16> * scratch_words<16>(512) + 513) * 4 <= 48 * 1024 - 256 &&
+                    (kWarpsFor<8> * scratch_words<8>(256) + 257) * 4 <= 48 * 1024 - 256 &&
+                    (kWarpsFor<16> * 513 + 2 * 516) * 4 <= 48 * 1024 - 256 &&
+                    (kWarpsFor<8> * 257 + 2 * 260) * 4 <= 48 * 1024 - 256,
+                "without asking for more");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(kWarps + 2) * (a.E + 1) * 4;
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = size_t(kWarps * scratch_words<NE>(a.E) + a.E + 1) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -353,8 +416,9 @@ qlin_status launch_t(Args a, unsigned flags, cudaStream_t st) {
   if (cudaLaunchKernelEx(&cfg, route_kernel<T, NE>, a) != cudaSuccess)
     return check_launch("qlin_route_experts");
   if (ctas > 1) {
+    cfg.dynamicSmemBytes = size_t(kWarps * (a.E + 1) + 2 * stride_of(a.E)) * 4;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, place_kernel, a);
+    cudaLaunchKernelEx(&cfg, place_kernel<kWarps>, a);
   }
   return check_launch("qlin_route_experts");
 }
@@ -372,9 +436,9 @@ qlin_status dispatch(const Args& a, unsigned flags, cudaStream_t st) {
 
 size_t route_experts_workspace_size(int64_t T, int E) {
   if (T <= kOneCta) return 0;
-  const int64_t n = (T + kWarps - 1) / kWarps;
-  // (at most one CTA for each of 1024 SMs: the size does not depend on the device)
-  return size_t(n < 1024 ? n : 1024) * (E + 1) * 4;
+  // (for as many CTAs as any device takes: the size does not depend on it)
+  const int64_t n = (T + kTokensACta - 1) / kTokensACta;
+  return size_t(n < kMostCtas ? n : kMostCtas) * stride_of(E) * 4;
 }
 
 qlin_status launch_route_experts(const RouteArgs& r, void* workspace, unsigned flags,
