@@ -693,17 +693,18 @@ def token_logprobs(logits, tokens, top: int = 0, overlap_previous=False):
                 (logits.dtype in _DTYPE_CODE, "logits must be float32, float16 or bfloat16"),
                 (0 <= top <= 32, "top must be 0 .. 32"),
                 (False, "tokens must be int32 [M] on the logits' device"))
-    # one allocation: two values a row, then the top ones and their tokens
-    values = torch.empty(m * (2 + 2 * top), dtype=torch.float32, device=logits.device)
-    logprobs, entropy, top_logprobs, top_tokens = values.split((m, m, m * top, m * top))
-    top_tokens = top_tokens.view(torch.int32)
+    dev = logits.device
+    logprobs = torch.empty(m, dtype=torch.float32, device=dev)
+    entropy = torch.empty(m, dtype=torch.float32, device=dev)
+    top_tokens = torch.empty((m, top), dtype=torch.int32, device=dev)
+    top_logprobs = torch.empty((m, top), dtype=torch.float32, device=dev)
     status = lib().qlin_token_logprobs(
         logits.data_ptr(), _row_stride(logits, shape[1]), tokens.data_ptr(), logprobs.data_ptr(),
         entropy.data_ptr(), top, top_tokens.data_ptr(), top_logprobs.data_ptr(), m, shape[1],
         _DTYPE_CODE[logits.dtype], 1 if overlap_previous else 0, _current_raw_stream(index))
     if status:
         _check(status)
-    return logprobs, entropy, top_tokens.view(m, top), top_logprobs.view(m, top)
+    return logprobs, entropy, top_tokens, top_logprobs
 
 
 class Routing:
@@ -731,6 +732,7 @@ class Routing:
         self.tokens, self.top_k = experts.shape
         self.pairs, self.n_experts = self.tokens * self.top_k, offsets.shape[0] - 1
         self._index = experts.get_device()
+        self._at = (experts.data_ptr(), weights.data_ptr(), order.data_ptr(), offsets.data_ptr())
         return self
 
 
@@ -764,23 +766,24 @@ def route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, group
                 (False, "bias must be float32 [n_experts] on the logits' device"))
     t, e = shape
     L = lib()
-    pairs = t * top_k
-    size = int(L.qlin_route_experts_workspace_size(t, e)) // 4
-    # one allocation: the scratch, experts, order and offsets
-    scratch, experts, order, offsets = torch.empty(
-        size + 2 * pairs + e + 1, dtype=torch.int32,
-        device=logits.device).split((size, pairs, pairs, e + 1))
-    weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    size = L.qlin_route_experts_workspace_size(t, e)
+    dev = logits.device
+    # (tensors of their own: as slices of one allocation they took twice as long)
+    routing = Routing.__new__(Routing)._set(
+        torch.empty((t, top_k), dtype=torch.int32, device=dev),
+        torch.empty((t, top_k), dtype=torch.float32, device=dev),
+        torch.empty(t * top_k, dtype=torch.int32, device=dev),
+        torch.empty(e + 1, dtype=torch.int32, device=dev))
+    scratch = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     status = L.qlin_route_experts(
         logits.data_ptr(), _row_stride(logits, e), None if bias is None else bias.data_ptr(),
         _SCORING[scoring], groups, top_groups, _GROUP_SCORE[group_score], top_k,
-        1 if renormalise else 0, scale, experts.data_ptr(), weights.data_ptr(), order.data_ptr(),
-        offsets.data_ptr(), t,
-        e, _DTYPE_CODE[logits.dtype], scratch.data_ptr() if size else None, 4 * size,
-        1 if overlap_previous else 0, _current_raw_stream(index))
+        1 if renormalise else 0, scale, *routing._at, t, e, _DTYPE_CODE[logits.dtype],
+        scratch.data_ptr() if size else None, size, 1 if overlap_previous else 0,
+        _current_raw_stream(index))
     if status:
         _check(status)
-    return Routing.__new__(Routing)._set(experts.view(t, top_k), weights, order, offsets)
+    return routing
 
 
 def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
@@ -837,7 +840,7 @@ def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
     workspace = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     status = L.qlin_expert_linear(
         x.data_ptr(), _row_stride(x, shape[1]), 1 if shape[0] == pairs else routing.top_k,
-        routing.order.data_ptr(), routing.offsets.data_ptr(), pairs, wq.data_ptr(),
+        routing._at[2], routing._at[3], pairs, wq.data_ptr(),
         scales.data_ptr(), biases.data_ptr(), out.data_ptr(), routing.n_experts, n, shape[1], bits,
         group_size, _DTYPE_CODE[dt], _DTYPE_CODE[out_dtype],
         workspace.data_ptr() if size else None, size, 1 if overlap_previous else 0,
@@ -882,7 +885,7 @@ def combine_experts(y, routing: Routing, add=None, out=None, out_dtype=None,
                  "add must be [T, N] with contiguous rows in the result's dtype"),
                 (False, "out must be contiguous [T, N] on y's device"))
     status = lib().qlin_combine_experts(
-        y.data_ptr(), routing.experts.data_ptr(), routing.weights.data_ptr(),
+        y.data_ptr(), routing._at[0], routing._at[1],
         None if add is None else add.data_ptr(), 0 if add is None else _row_stride(add, shape[1]),
         out.data_ptr(), t, routing.top_k, shape[1], _DTYPE_CODE[dt], _DTYPE_CODE[ydt],
         1 if overlap_previous else 0, _current_raw_stream(index))
