@@ -582,8 +582,8 @@ qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_ro
 
 /*
  * out[t] = add[t] + sum_j weights[t][j] * y[t*top_k + j]  over the j with
- * experts[t][j] >= 0 (the rows of the others are not read), float32 sums in the
- * order of j, one rounding.  y: y_dtype [T*top_k][N] (dtype or QLIN_F32); add:
+ * experts[t][j] >= 0 (what the rows of the others hold does not matter), float32
+ * sums in the order of j, one rounding.  y: y_dtype [T*top_k][N] (dtype or QLIN_F32); add:
  * dtype, rows add_stride elements apart, or NULL; out: dtype [T][N], may be add
  * with add_stride = N.  top_k at most 32.
  */

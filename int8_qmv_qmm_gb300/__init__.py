@@ -853,7 +853,7 @@ def expert_linear(x, routing: Routing, wq, scales, biases, bits: int,
 def combine_experts(y, routing: Routing, add=None, out=None, out_dtype=None,
                     overlap_previous=False):
     """out[t] = add[t] + sum_j weights[t, j] * y[t*top_k + j] over the experts of
-    token t (rows of pairs without one are not read).
+    token t (what rows of pairs without one hold does not matter).
 
     y [T*top_k, N] from expert_linear (float32 or the activation dtype), add
     [T, N] in the activation dtype (rows may be strided).  Returns [T, N] in the

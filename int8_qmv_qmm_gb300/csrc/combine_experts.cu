@@ -10,7 +10,7 @@
 namespace qlin {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (256: 32 us for 30, 512: 43)
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
@@ -44,22 +44,25 @@ __global__ void __launch_bounds__(kThreads)
   const Y* row = y + t * top_k * N + n;
   const int32_t* ex = experts + t * top_k;
   const float* wt = weights + t * top_k;
-  // eight rows' loads before the first sum
+  // eight rows' loads before the first use of anything (also of rows without an expert,
+  // which are then left out: waiting for the experts first took 41 us where this takes
+  // 30, 4096 tokens of 8 rows of 2048)
   for (int j0 = 0; j0 < top_k; j0 += 8) {
     Pack<Y, VEC> v[8];
     float w[8];
-    bool there[8];
+    int e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      there[j] = j0 + j < top_k && ex[j0 + j] >= 0;
-      w[j] = there[j] ? wt[j0 + j] : 0.f;
-      if (there[j]) v[j] = *reinterpret_cast<const Pack<Y, VEC>*>(row + (j0 + j) * N);
+      const int at = min(j0 + j, top_k - 1);
+      v[j] = *reinterpret_cast<const Pack<Y, VEC>*>(row + at * N);
+      w[j] = wt[at];
+      e[j] = j0 + j < top_k ? ex[at] : -1;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (there[j])
+      if (e[j] >= 0)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e] = fmaf(w[j], widen(v[j].v[e]), sum[e]);
+        for (int i = 0; i < VEC; ++i) sum[i] = fmaf(w[j], widen(v[j].v[i]), sum[i]);
   }
   Pack<T, VEC> r;
 #pragma unroll
