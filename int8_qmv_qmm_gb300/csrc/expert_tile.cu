@@ -19,7 +19,7 @@
 // kernel finds them.  (Two bfloat16 products for the high and low part of a weight, as
 // qmm.cu has them, took 361 us where f16 took 241.)
 //
-//   warp 0       loads the tokens' rows and the packed tile (TMA, one thread)
+//   warps 0, 2   load the tokens' rows and the packed tiles (TMA, one thread each)
 //   warp 1       issues the MMAs, converged, with the operands' descriptors in uniform
 //                registers (a loop of one thread alone took 84 cycles an MMA, and set the
 //                pace); a tile with fewer tokens than BN multiplies what it has, in steps
@@ -49,7 +49,7 @@ __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_tile_s
 constexpr int kDequantGroups = 2;
 constexpr int kDequantWarps = 4 * kDequantGroups;
 constexpr int kEpilogueWarps = 8;
-constexpr int kFirstDequant = 2;
+constexpr int kFirstDequant = 3;
 constexpr int kFirstEpilogue = kFirstDequant + kDequantWarps;
 constexpr int kThreads = (kFirstEpilogue + kEpilogueWarps) * 32;
 constexpr int kMaxExperts = 512;
@@ -59,23 +59,31 @@ constexpr int kMaxShared = 227 * 1024;
 constexpr int kOutTokens = 16;
 constexpr int kOutBytes = 2 * 2 * kOutTokens * kBM * 2;  // two for each half
 
+// Three rings with the same index, so that each stage of the way has as many in flight
+// as it needs: the tokens' rows and the packed tiles in shared memory, and the A slots in
+// tensor memory.  (One ring of five stages for all three held each stage's 36 KB for the
+// way of all: 229 us where this takes FIXME.)
 template <int BITS, int BN>
 struct Layout {
   static constexpr int kXBytes = BN * kBK * 2;
   static constexpr int kWBytes = Geo<BITS>::kPackedBytes;
-  static constexpr int kStageBytes = kXBytes + kWBytes;
   // two accumulators unless they would leave tensor memory too few A slots
   static constexpr int kDBufs = BN >= 256 ? 1 : 2;
   static constexpr int kACol0 = kDBufs * BN;
-  static constexpr int kAColsPerStage = kBK / 2;
+  static constexpr int kACols = kBK / 2;  // of a slot
+  static constexpr int kA = 8;
+  static constexpr int kX = BN >= 256 ? 4 : 8;
+  static constexpr int kW = 8;
+  static constexpr int kRings = kX * kXBytes + kW * kWBytes;
   // barriers and the tensor memory's address, the epilogue's tiles, the plan, the tiles'
   // pairs and factors
   static constexpr int kRestBytes = 512 + kOutBytes + (3 * kMaxExperts + 4) * 4 + 2 * BN * 8;
-  static constexpr int kFit = (kMaxShared - 1024 - kRestBytes) / kStageBytes;
-  static constexpr int kSlots = (512 - kACol0) / kAColsPerStage;
-  static constexpr int kStages = kFit < kSlots ? (kFit < 8 ? kFit : 8) : (kSlots < 8 ? kSlots : 8);
-  static constexpr int kTmemCols = kACol0 + kStages * kAColsPerStage <= 256 ? 256 : 512;
-  static_assert(kStageBytes % 1024 == 0 && kStages >= 2, "");
+  static constexpr int kTmemCols = 512;
+  static_assert(kACol0 + kA * kACols <= kTmemCols, "");
+  // (a barrier of the A ring tells the other two how far the MMAs are; the groups take
+  // turns, so that a place of a ring is always the same group's)
+  static_assert(kX <= kA && kW % kDequantGroups == 0 && kA % kDequantGroups == 0, "");
+  static_assert(1024 + kRings + kRestBytes <= kMaxShared, "");
 };
 
 // What the first kernel leaves in the workspace.
@@ -129,7 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kHalf = std::is_same<AT, __half>::value;
   using L = Layout<BITS, BN>;
   using G = Geo<BITS>;
-  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -140,19 +147,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb_count = int(a.K) / kBK, N = int(a.N);
   const int n_tiles = (N + kBM - 1) / kBM;
 
-  auto x_addr = [&](int s) { return base + uint32_t(s * L::kStageBytes); };
-  auto w_addr = [&](int s) { return x_addr(s) + uint32_t(L::kXBytes); };
-  const uint32_t bar_base = base + uint32_t(kStages * L::kStageBytes);
-  // (one "loaded" barrier per stage and warpgroup: use u of the ring signals that of
-  // group u % 2, so that no group waits two phases ahead)
-  auto full_bar = [&](int g, int s) { return bar_base + 8u * (g * kStages + s); };
-  auto empty_bar = [&](int s) { return bar_base + 8u * (kDequantGroups * kStages + s); };
-  auto afull_bar = [&](int s) { return bar_base + 8u * ((kDequantGroups + 1) * kStages + s); };
-  const uint32_t accf_bar = bar_base + 8u * ((kDequantGroups + 2) * kStages);  // [2]
-  const uint32_t acce_bar = accf_bar + 16u;                                     // [2]
+  auto x_addr = [&](int s) { return base + uint32_t(s * L::kXBytes); };
+  auto w_addr = [&](int s) { return base + uint32_t(L::kX * L::kXBytes + s * L::kWBytes); };
+  const uint32_t bar_base = base + uint32_t(L::kRings);
+  auto w_full = [&](int s) { return bar_base + 8u * s; };
+  auto w_empty = [&](int s) { return bar_base + 8u * (L::kW + s); };
+  // a use's A slot and the tokens' rows are there (one barrier: a wait of the issuer costs
+  // what an MMA does)
+  auto ready = [&](int s) { return bar_base + 8u * (2 * L::kW + s); };
+  // the MMAs of a use have completed: its A slot and its rows are free
+  auto done = [&](int s) { return bar_base + 8u * (2 * L::kW + L::kA + s); };
+  const uint32_t accf_bar = bar_base + 8u * (2 * L::kW + 2 * L::kA);  // [2]
+  const uint32_t acce_bar = accf_bar + 16u;                                    // [2]
   const uint32_t done_bar = acce_bar + 16u;
-  static_assert(8 * ((kDequantGroups + 2) * 8 + 5) + 4 <= 512, "barrier block");
-  uint8_t* const rest = gbase + kStages * L::kStageBytes;
+  static_assert(8 * (2 * L::kW + 2 * L::kA + 5) + 4 <= 508, "barrier block");
+  uint8_t* const rest = gbase + L::kRings;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
   uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][2][kOutTokens][kBM]
   int* first_job = reinterpret_cast<int*>(rest + 512 + kOutBytes);  // the jobs of the experts before each
@@ -162,10 +171,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* factors = reinterpret_cast<float*>(pairs + 2 * BN);  // [2][BN] (bfloat16)
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      for (int g = 0; g < kDequantGroups; ++g) ptx::mbar_init(full_bar(g, s), 1);
-      ptx::mbar_init(empty_bar(s), 1 + 4);  // the MMAs' commit and the warps of a group
-      ptx::mbar_init(afull_bar(s), 4);
+    for (int s = 0; s < L::kW; ++s) {
+      ptx::mbar_init(w_full(s), 1);
+      ptx::mbar_init(w_empty(s), 4);  // the warps of a group
+    }
+    for (int s = 0; s < L::kA; ++s) {
+      ptx::mbar_init(ready(s), 4 + 1);  // the warps of a group and the rows' bytes
+      ptx::mbar_init(done(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar + 8u * b, 1);
@@ -238,49 +250,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------------- producer of tokens' rows
     if (lane == 0) {
-      int s = 0, g = 0, issued = 0;
-      uint32_t round = 0;
-      uint32_t full_ph = 0;  // bit g*8+s: parity of the next phase of full_bar(g, s)
+      int s = 0, u = 0;
       bool ok = true;
       for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
         // (rows past the tile's tokens are the next expert's, or zeros past the last)
-        const int x_row = q.at, w_row = q.expert * N + q.n0;
-        for (int kb = 0; kb < kb_count; ++kb) {
-          if (round > 0 && !ptx::mbar_wait(empty_bar(s), (round - 1) & 1u)) {
+        for (int kb = 0; kb < kb_count; ++kb, ++u) {
+          const int before = u - L::kX;  // the use that had the place
+          if (before >= 0 &&
+              !ptx::mbar_wait(done(before % L::kA), uint32_t(before / L::kA) & 1u)) {
             report(kStatusWait);
             ok = false;
             break;
           }
-          const uint32_t fb = full_bar(g, s);
-          ptx::mbar_arrive_expect_tx(fb, L::kStageBytes);
-          ptx::tma_load_2d(x_addr(s), &tm_x, fb, kb * kBK, x_row);
-          ptx::tma_load_2d(w_addr(s), &tm_w, fb, kb * G::kWordsPerGroup, w_row);
-          full_ph ^= 1u << (g * 8 + s);
-          ++issued;
-          if (++g == kDequantGroups) g = 0;
-          if (++s == kStages) {
+          ptx::mbar_arrive_expect_tx(ready(u % L::kA), L::kXBytes);
+          ptx::tma_load_2d(x_addr(s), &tm_x, ready(u % L::kA), kb * kBK, q.at);
+          if (++s == L::kX) s = 0;
+        }
+      }
+      // (after a wait that gave up: the last loads, one for each place, may be in flight)
+      if (!ok)
+        for (int v = u > L::kX ? u - L::kX : 0; v < u; ++v)
+          if (!ptx::mbar_wait(ready(v % L::kA), uint32_t(v / L::kA) & 1u)) report(kStatusWait);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------- producer of packed tiles
+    if (lane == 0) {
+      int s = 0, u = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
+        const int row = q.expert * N + q.n0;
+        for (int kb = 0; kb < kb_count; ++kb, ++u) {
+          if (u >= L::kW && !ptx::mbar_wait(w_empty(s), phase ^ 1u)) {
+            report(kStatusWait);
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(w_full(s), L::kWBytes);
+          ptx::tma_load_2d(w_addr(s), &tm_w, w_full(s), kb * G::kWordsPerGroup, row);
+          if (++s == L::kW) {
             s = 0;
-            ++round;
+            phase ^= 1u;
           }
         }
       }
-      if (!ok) {
-        // the last loads, one per stage, may be in flight
-        const int v0 = issued > kStages ? issued - kStages : 0;
-        for (int v = v0; v < issued; ++v) {
-          const int vg = v % kDequantGroups, vs = v % kStages;
-          const uint32_t parity = ((full_ph >> (vg * 8 + vs)) & 1u) ^ 1u;
-          if (!ptx::mbar_wait(full_bar(vg, vs), parity)) report(kStatusWait);
+      if (!ok)
+        for (int v = 0; v < L::kW && v < u; ++v) {
+          if (--s < 0) {
+            s = L::kW - 1;
+            phase ^= 1u;
+          }
+          if (!ptx::mbar_wait(w_full(s), phase)) report(kStatusWait);
         }
-      }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     const bool leads = elect_one();
     const uint64_t b_desc0 = ptx::sw128_kmajor_desc(base);
-    int s = 0, i = 0;
+    int s = 0, xs = 0, i = 0;
     uint32_t phase = 0;
     bool ok = true, any = false;
     for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q), ++i) {
@@ -297,30 +326,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_tmem = tmem_base + uint32_t(buf * BN);
       uint32_t more = 0;
       for (int kb = 0; kb < kb_count; ++kb) {
-        // (A ready implies that the stage's bytes have landed)
-        if (!wait_warp(afull_bar(s), phase)) {
+        if (!wait_warp(ready(s), phase)) {
           report(kStatusWait);
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t a_tmem = tmem_base + uint32_t(L::kACol0 + s * L::kAColsPerStage);
-        const uint64_t bd = b_desc0 + uint64_t(uint32_t(s * L::kStageBytes) >> 4);
+        const uint32_t a_tmem = tmem_base + uint32_t(L::kACol0 + s * L::kACols);
+        const uint64_t bd = b_desc0 + uint64_t(uint32_t(xs * L::kXBytes) >> 4);
         if (leads) {
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
             mma_f16_ts(d_tmem, a_tmem + uint32_t(8 * kk), bd + uint64_t(2 * kk), idesc,
                        kk > 0 ? 1u : more);
           }
-          ptx::mma_commit(empty_bar(s));
+          ptx::mma_commit(done(s));
         }
         __syncwarp();
         more = 1;
         any = true;
-        if (++s == kStages) {
+        if (++s == L::kA) {
           s = 0;
           phase ^= 1u;
         }
+        if (++xs == L::kX) xs = 0;
       }
       if (ok && leads) ptx::mma_commit(accf_bar + 8u * buf);
       __syncwarp();
@@ -335,8 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = (warp - kFirstDequant) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // weight row within the tile
     const uint32_t a_lane = tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(L::kACol0);
-    int s = 0, u = 0;
-    uint32_t full_ph = 0;  // bit s: parity of the next phase of full_bar(grp, s)
+    int u = grp;  // the group's next use
+    int ws = grp, as = grp;
+    uint32_t w_phase = 0, a_phase = 0;
+    int kb0 = grp;  // its first stage of the tile
     bool ok = true;
     for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
       const int n = q.n0 + r;
@@ -346,18 +377,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const AT* brow = static_cast<const AT*>(a.biases) + at;
       float factor = 1.f;
       if constexpr (!kHalf) factor = sorted.row_factor[int64_t(q.expert) * N + min(n, N - 1)];
-      for (int kb = 0; kb < kb_count; ++kb, ++u) {
-        const int cs = s;
-        if (++s == kStages) s = 0;
-        if (u % kDequantGroups != grp) continue;
-        const AT sc = srow[kb], bc = brow[kb];
-        if (!__all_sync(kAll, ptx::mbar_wait(full_bar(grp, cs), (full_ph >> cs) & 1u))) {
+      int kb = kb0;
+      AT next_sc, next_bc;  // (a stage ahead: their way is longer than a stage)
+      if (kb < kb_count) {
+        next_sc = srow[kb];
+        next_bc = brow[kb];
+      }
+      for (; kb < kb_count; kb += kDequantGroups, u += kDequantGroups) {
+        const AT sc = next_sc, bc = next_bc;
+        if (kb + kDequantGroups < kb_count) {
+          next_sc = srow[kb + kDequantGroups];
+          next_bc = brow[kb + kDequantGroups];
+        }
+        if (!wait_warp(w_full(ws), w_phase)) {
           report(kStatusWait);
           ok = false;
           break;
         }
-        full_ph ^= 1u << cs;
-        const uint8_t* wrow = gbase + (w_addr(cs) - base) + r * G::kPackedRowBytes;
+        const uint8_t* wrow = gbase + (w_addr(ws) - base) + r * G::kPackedRowBytes;
         __half scale, bias;
         if constexpr (kHalf) {
           scale = sc;
@@ -368,15 +405,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t w[32], none[1];
         dequant_row<BITS, __half, 1>(wrow, r, scale, bias, row_ok, w, none);
-        tmem_st_32x32b_x32(a_lane + uint32_t(cs * L::kAColsPerStage), w);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(w_empty(ws));
+        // the A slot's last products
+        if (u >= L::kA && !wait_warp(done(as), a_phase ^ 1u)) {
+          report(kStatusWait);
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        tmem_st_32x32b_x32(a_lane + uint32_t(as * L::kACols), w);
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(afull_bar(cs));
-          ptx::mbar_arrive(empty_bar(cs));
+        if (lane == 0) ptx::mbar_arrive(ready(as));
+        if ((ws += kDequantGroups) >= L::kW) {
+          ws = grp;
+          w_phase ^= 1u;
+        }
+        if ((as += kDequantGroups) >= L::kA) {
+          as = grp;
+          a_phase ^= 1u;
         }
       }
+      kb0 = kb - kb_count;  // (the turns go on from tile to tile)
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -612,8 +664,7 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 template <int BITS, typename AT, int BN>
 qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   using L = Layout<BITS, BN>;
-  constexpr int kBytes = 1024 + L::kStages * L::kStageBytes + L::kRestBytes;
-  static_assert(kBytes <= kMaxShared, "");
+  constexpr int kBytes = 1024 + L::kRings + L::kRestBytes;
   auto kern = tile_kernel<BITS, AT, BN>;
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), kBytes, &done))
