@@ -29,11 +29,10 @@ __device__ __forceinline__ ExpertRows expert_rows(const ExpertArgs& a, int exper
   return r;
 }
 
-// Tiles of 8 tokens (1, 2 or 4; 0: none fits) that the streaming kernel takes at a
-// time for experts of `rows` rows.
-int expert_stream_tiles(int64_t K, double rows);
-qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, int tiles,
-                                 unsigned flags, cudaStream_t st);
+// Whether the streaming kernel's tokens fit in shared memory.
+bool expert_stream_fits(int64_t K);
+qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
+                                 cudaStream_t st);
 cudaError_t expert_stream_take_status(unsigned* flags);
 qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, double rows,
                                unsigned flags, cudaStream_t st);

@@ -21,7 +21,6 @@
 // are joined.
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -39,6 +38,13 @@ __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_expert_stream
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+// Warps of a team, which share an item's K.  (2, 4 and 8: 32 tokens' down in 33, 35 and 60
+// us, one token's up in 13.2, 13.4 and 14.5.)
+constexpr int kTeam = 2;
+constexpr int kTeams = kWarps / kTeam;
+// Tokens of a tile, a product's columns.  (With 16 and 32 of them: 36 and 36 us for 32;
+// an expert that has more than 8 tokens finds its weights in L2.)
+constexpr int kTokens = 8;
 constexpr int kRows = 16;  // of an item
 constexpr int kGroups = 4;               // of a stage
 constexpr int kRingBytes = 8 * 1024;     // of a warp
@@ -151,15 +157,14 @@ __device__ __forceinline__ TokenGroup token_quarter(uint4& v0, uint4& v1) {
   return TokenGroup{sum, back};
 }
 
-// NT: tiles of 8 tokens that an item can have; WK: warps of a team.
-template <int BITS, typename AT, int NT, int WK>
+template <int BITS, typename AT>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a) {
-  constexpr int kTokens = 8 * NT, kTeams = kWarps / WK, kAhead = kStages<BITS> - 1;
+  constexpr int kAhead = kStages<BITS> - 1;
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int first_job[kMaxExperts + 1];  // the tiles of the experts before each
   __shared__ int pair_of[kTokens];            // of the tile's tokens (-1: none)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wk = warp % WK, team = warp / WK;
+  const int wk = warp % kTeam, team = warp / kTeam;
   const int g = lane >> 2, c = lane & 3;
   const int n_groups = int(a.K) / kGroup, N = int(a.N);
   // rings | scales [kWarps][kGroups][kScaleStride] | sums [kWarps][kTokens][kSumStride] |
@@ -214,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   if (n_items == 0) return;
 
   // this warp's groups, and the stages that every warp of a team takes for an item
-  const int g0 = wk * n_groups / WK, g1 = (wk + 1) * n_groups / WK;
-  const int per_item = ((n_groups + WK - 1) / WK + kGroups - 1) / kGroups;
+  const int g0 = wk * n_groups / kTeam, g1 = (wk + 1) * n_groups / kTeam;
+  const int per_item = ((n_groups + kTeam - 1) / kTeam + kGroups - 1) / kGroups;
   const int64_t row_bytes = a.K * BITS / 8;
 
   // The team's items: a tile of an expert's tokens (job) and a block of rows.
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch();
 
-  float2 acc[NT][2];
+  float2 acc[2];
   int slot = 0;
   const int last_job = int((item0 + n_items - 1) / blocks);
   for (int job = int(item0 / blocks); job <= last_job; ++job) {
@@ -311,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     }
     const ExpertRows r = expert_rows(a, low);
     const int t0 = (job - first_job[low]) * kTokens;
-    const int tiles = min((r.n - t0 + 7) / 8, NT);
     int p = -1;
     if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < r.n) {
       p = a.order[r.first + t0 + threadIdx.x];
@@ -323,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     __syncthreads();  // (every team is done with the last job's)
     if (threadIdx.x < kTokens) pair_of[threadIdx.x] = p;
     __syncthreads();
-    for (int i = threadIdx.x; i < n_groups * tiles * 32; i += kThreads) {
-      const int q = i & 3, tok8 = (i >> 2) & 7, t = (i >> 5) % tiles, gr = (i >> 5) / tiles;
-      const int tok = t * 8 + tok8, pair = pair_of[tok];
+    for (int i = threadIdx.x; i < n_groups * 32; i += kThreads) {
+      const int q = i & 3, tok = (i >> 2) & 7, gr = i >> 5;
+      const int pair = pair_of[tok];
       uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
       if (pair >= 0) {
         const uint4* x = reinterpret_cast<const uint4*>(
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
       }
       const TokenGroup tg = token_quarter<AT>(v0, v1);  // (i runs in whole warps)
       if (q == 0) xsum[gr * kTokens + tok] = tg;
-      uint4* to = xs + ((gr * NT + t) * 2) * 32 + tok8 * 4 + q;
+      uint4* to = xs + gr * 64 + tok * 4 + q;
       to[0] = in_order<BITS>(v0);
       to[32] = in_order<BITS>(v1);
     }
@@ -344,10 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     while (now.left > 0 && now.job == job) {
       __syncwarp();  // every lane is done with the stage whose place is filled next
       fetch();
-      if (now.stage == 0) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = make_float2(0.f, 0.f);
-      }
+      if (now.stage == 0) acc[0] = acc[1] = make_float2(0.f, 0.f);
       // (scale, bias - 1024 * scale) of group c, for the warp
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -377,28 +378,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
         }
         // (past the warp's last group its tokens again: what is finite times 0)
         const int gr = max(min(s0 + i, g1 - 1), 0);
-        const uint4* xg = xs + gr * NT * 64 + lane;
-        const float4* xt = reinterpret_cast<const float4*>(xsum + gr * kTokens + 2 * c);
+        const uint4 b0 = xs[gr * 64 + lane], b1 = xs[gr * 64 + 32 + lane];
+        // of tokens 2c and 2c + 1
+        const float4 tg = *reinterpret_cast<const float4*>(xsum + gr * kTokens + 2 * c);
+        float p0[4] = {0.f, 0.f, 0.f, 0.f}, p1[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(p0, code[0], b0.x, b0.y);
+        mma(p1, code[2], b1.x, b1.y);
+        mma(p0, code[1], b0.z, b0.w);
+        mma(p1, code[3], b1.z, b1.w);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t >= tiles) break;
-          const uint4 b0 = xg[t * 64], b1 = xg[t * 64 + 32];
-          const float4 tg = xt[4 * t];  // of tokens 2c and 2c + 1
-          float p0[4] = {0.f, 0.f, 0.f, 0.f}, p1[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(p0, code[0], b0.x, b0.y);
-          mma(p1, code[2], b1.x, b1.y);
-          mma(p0, code[1], b0.z, b0.w);
-          mma(p1, code[3], b1.z, b1.w);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float2 v = __fadd2_rn(make_float2(p0[2 * half], p0[2 * half + 1]),
-                                  make_float2(p1[2 * half], p1[2 * half + 1]));
-            if constexpr (!std::is_same<AT, __half>::value)
-              v = __fmul2_rn(v, make_float2(tg.y, tg.w));
-            acc[t][half] = __ffma2_rn(make_float2(sz[half].y, sz[half].y),
-                                      make_float2(tg.x, tg.z), acc[t][half]);
-            acc[t][half] = __ffma2_rn(make_float2(sz[half].x, sz[half].x), v, acc[t][half]);
-          }
+        for (int half = 0; half < 2; ++half) {
+          float2 v = __fadd2_rn(make_float2(p0[2 * half], p0[2 * half + 1]),
+                                make_float2(p1[2 * half], p1[2 * half + 1]));
+          if constexpr (!std::is_same<AT, __half>::value)
+            v = __fmul2_rn(v, make_float2(tg.y, tg.w));
+          acc[half] = __ffma2_rn(make_float2(sz[half].y, sz[half].y), make_float2(tg.x, tg.z),
+                                 acc[half]);
+          acc[half] = __ffma2_rn(make_float2(sz[half].x, sz[half].x), v, acc[half]);
         }
       }
       const int block = now.block;
@@ -408,35 +404,27 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
         now.block += kTeams;
         settle(now);
       }
-      // the item's sums: rows g, g + 8 and tokens 2c, 2c + 1 of each tile from every warp
-      // of the team
-      float* mine = sums + team * WK * kTokens * kSumStride;
-      if constexpr (WK > 1)  // the team has read the last item's
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(WK * 32) : "memory");
-      else
-        __syncwarp();
+      // the item's sums: rows g, g + 8 and tokens 2c, 2c + 1 from every warp of the team
+      float* mine = sums + team * kTeam * kTokens * kSumStride;
+      auto team_sync = [&] {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(kTeam * 32) : "memory");
+      };
+      team_sync();  // the team has read the last item's
       float* part = mine + wk * kTokens * kSumStride;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t >= tiles) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          part[(8 * t + 2 * c) * kSumStride + 8 * half + g] = acc[t][half].x;
-          part[(8 * t + 2 * c + 1) * kSumStride + 8 * half + g] = acc[t][half].y;
-        }
+      for (int half = 0; half < 2; ++half) {
+        part[2 * c * kSumStride + 8 * half + g] = acc[half].x;
+        part[(2 * c + 1) * kSumStride + 8 * half + g] = acc[half].y;
       }
-      if constexpr (WK > 1)
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(WK * 32) : "memory");
-      else
-        __syncwarp();
-      for (int i = wk * 32 + lane; i < tiles * 8 * kRows; i += WK * 32) {
+      team_sync();
+      for (int i = wk * 32 + lane; i < kTokens * kRows; i += kTeam * 32) {
         const int tok = i / kRows, row = block * kRows + i % kRows;
         const int pair = pair_of[tok];
         if (pair < 0 || row >= N) continue;
         const float* sum = mine + tok * kSumStride + i % kRows;
         float v = sum[0];
 #pragma unroll
-        for (int k = 1; k < WK; ++k) v += sum[k * kTokens * kSumStride];
+        for (int k = 1; k < kTeam; ++k) v += sum[k * kTokens * kSumStride];
         if (a.y_f32)
           static_cast<float*>(a.y)[int64_t(pair) * N + row] = v;
         else
@@ -447,28 +435,27 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   copies_wait<0>();
 }
 
-size_t shared_bytes(int nt, int64_t K) {
-  const size_t tokens = 8 * size_t(nt);
-  return size_t(kWarps) * (kRingBytes + kGroups * kScaleStride * 8 + tokens * kSumStride * 4) +
-         size_t(K / kGroup) * tokens * (sizeof(TokenGroup) + kGroup * 2);
+size_t shared_bytes(int64_t K) {
+  return size_t(kWarps) * (kRingBytes + kGroups * kScaleStride * 8 + kTokens * kSumStride * 4) +
+         size_t(K / kGroup) * kTokens * (sizeof(TokenGroup) + kGroup * 2);
 }
 
 constexpr size_t kMostShared = 227 * 1024 - 2560;  // beside first_job and pair_of
 
-template <int BITS, typename AT, int NT, int WK>
+template <int BITS, typename AT>
 qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
-  auto kern = stream_kernel<BITS, AT, NT, WK>;
+  auto kern = stream_kernel<BITS, AT>;
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), int(kMostShared), &done))
     return check_launch("qlin_expert_linear: shared memory");
   // tiles of tokens: at most one more than full ones for each expert that has any
   const int64_t used = std::min<int64_t>(a.E, a.n_pairs);
-  const int64_t jobs = a.n_pairs / (8 * NT) + used;
+  const int64_t jobs = a.n_pairs / kTokens + used;
   const int64_t items = jobs * ((a.N + kRows - 1) / kRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(items, sm_count())));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = shared_bytes(NT, a.K);
+  cfg.dynamicSmemBytes = shared_bytes(a.K);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -479,39 +466,16 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   return check_launch("qlin_expert_linear");
 }
 
-template <int BITS, typename AT, int NT>
-qlin_status with_warps(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
-  const int64_t groups = a.K / kGroup;
-  int wk = 2;
-  if (const char* env = std::getenv("QLIN_EXPERT_WK")) wk = std::atoi(env);
-  if (wk >= 8) return launch_t<BITS, AT, NT, 8>(a, flags, st);
-  if (wk >= 4) return launch_t<BITS, AT, NT, 4>(a, flags, st);
-  return launch_t<BITS, AT, NT, 2>(a, flags, st);
-}
-
-template <int BITS, typename AT>
-qlin_status with_tiles(const ExpertArgs& a, int tiles, unsigned flags, cudaStream_t st) {
-  if (tiles == 1) return with_warps<BITS, AT, 1>(a, flags, st);
-  if (tiles == 2) return with_warps<BITS, AT, 2>(a, flags, st);
-  return with_warps<BITS, AT, 4>(a, flags, st);
-}
-
 }  // namespace
 
-int expert_stream_tiles(int64_t K, double rows) {
-  int tiles = rows <= 2.0 ? 1 : rows <= 8.0 ? 2 : 4;
-  if (const char* env = std::getenv("QLIN_EXPERT_NT")) tiles = std::atoi(env);
-  while (tiles && shared_bytes(tiles, K) > kMostShared) tiles /= 2;
-  return tiles;
-}
+bool expert_stream_fits(int64_t K) { return shared_bytes(K) <= kMostShared; }
 
-qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, int tiles,
-                                 unsigned flags, cudaStream_t st) {
+qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
+                                 cudaStream_t st) {
   if (dtype == QLIN_F16)
-    return bits == 4 ? with_tiles<4, __half>(a, tiles, flags, st)
-                     : with_tiles<8, __half>(a, tiles, flags, st);
-  return bits == 4 ? with_tiles<4, __nv_bfloat16>(a, tiles, flags, st)
-                   : with_tiles<8, __nv_bfloat16>(a, tiles, flags, st);
+    return bits == 4 ? launch_t<4, __half>(a, flags, st) : launch_t<8, __half>(a, flags, st);
+  return bits == 4 ? launch_t<4, __nv_bfloat16>(a, flags, st)
+                   : launch_t<8, __nv_bfloat16>(a, flags, st);
 }
 
 cudaError_t expert_stream_take_status(unsigned* flags) {
