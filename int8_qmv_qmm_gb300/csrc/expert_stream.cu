@@ -46,18 +46,20 @@ constexpr int kTeams = kWarps / kTeam;
 // an expert that has more than 8 tokens finds its weights in L2.)
 constexpr int kTokens = 8;
 constexpr int kRows = 16;  // of an item
-constexpr int kGroups = 4;               // of a stage
-constexpr int kRingBytes = 8 * 1024;     // of a warp
+// Groups of a stage: 4, or 2 where that makes room for the tokens of a longer K.
+constexpr int kManyGroups = 4, kFewGroups = 2;
+template <int G>
+constexpr int kRingBytes = 2048 * G;  // of a warp
 constexpr int kScaleStride = kRows + 4;  // of a group's (scale, rest): spreads the banks
 constexpr int kSumStride = kRows + 4;  // of a token's sums: spreads the banks
 constexpr int kMaxExperts = 512;
 constexpr int kCtasForJob = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
+template <int BITS, int G>
+constexpr int kStageBytes = G * kRows * 8 * BITS;
 template <int BITS>
-constexpr int kStageBytes = kGroups * kRows * 8 * BITS;
-template <int BITS>
-constexpr int kStages = kRingBytes / kStageBytes<BITS>;  // 4 (4-bit) or 2
+constexpr int kStages = 64 / (4 * BITS);  // 4 (4-bit) or 2
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -157,9 +159,10 @@ __device__ __forceinline__ TokenGroup token_quarter(uint4& v0, uint4& v1) {
   return TokenGroup{sum, back};
 }
 
-template <int BITS, typename AT>
+template <int BITS, typename AT, int kGroups>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a) {
   constexpr int kAhead = kStages<BITS> - 1;
+  static_assert(kStages<BITS> * kStageBytes<BITS, kGroups> == kRingBytes<kGroups>, "");
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int first_job[kMaxExperts + 1];  // the tiles of the experts before each
   __shared__ int pair_of[kTokens];            // of the tile's tokens (-1: none)
@@ -169,12 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   const int n_groups = int(a.K) / kGroup, N = int(a.N);
   // rings | scales [kWarps][kGroups][kScaleStride] | sums [kWarps][kTokens][kSumStride] |
   // X and factors [n_groups][kTokens] | tokens
-  float2* scales = reinterpret_cast<float2*>(shared + kWarps * kRingBytes) +
+  float2* scales = reinterpret_cast<float2*>(shared + kWarps * kRingBytes<kGroups>) +
                    warp * kGroups * kScaleStride;
-  float* sums = reinterpret_cast<float*>(shared + kWarps * (kRingBytes + kGroups * kScaleStride * 8));
+  float* sums = reinterpret_cast<float*>(shared + kWarps * (kRingBytes<kGroups> + kGroups * kScaleStride * 8));
   TokenGroup* xsum = reinterpret_cast<TokenGroup*>(sums + kWarps * kTokens * kSumStride);
   uint4* xs = reinterpret_cast<uint4*>(xsum + n_groups * kTokens);
-  const uint8_t* ring = shared + warp * kRingBytes;
+  const uint8_t* ring = shared + warp * kRingBytes<kGroups>;
   // where this lane's copies go (4-bit: two groups of a row are 64 bytes, chunk c of row g
   // at chunk c ^ 2 * (g / 2 % 2), so that the reads below meet no bank twice)
   const uint32_t ring_to =
@@ -268,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
       for (int half = 0; half < 2; ++half) coming[i][half] = coming[i + 1][half];
     coming[kAhead][0] = coming[kAhead][1] = 0u;
     if (ahead.left > 0) {
-      const int n = g1 - g0 - ahead.stage * kGroups;  // groups from here on
-      const uint32_t to = ring_to + uint32_t(slot_in * kStageBytes<BITS>);
+      const int n = min(g1 - g0 - ahead.stage * kGroups, kGroups);  // groups
+      const uint32_t to = ring_to + uint32_t(slot_in * kStageBytes<BITS, kGroups>);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if constexpr (BITS == 8) {
@@ -353,11 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const float2 v = widen2<AT>(coming[0][half]);
-        scales[c * kScaleStride + 8 * half + g] = make_float2(v.x, fmaf(-1024.f, v.x, v.y));
+        if (c < kGroups)
+          scales[c * kScaleStride + 8 * half + g] = make_float2(v.x, fmaf(-1024.f, v.x, v.y));
       }
       copies_wait<kAhead>();
       __syncwarp();
-      const uint8_t* st = ring + slot * kStageBytes<BITS>;
+      const uint8_t* st = ring + slot * kStageBytes<BITS, kGroups>;
       if (++slot == kStages<BITS>) slot = 0;
       const int s0 = g0 + now.stage * kGroups;
 #pragma unroll
@@ -435,16 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   copies_wait<0>();
 }
 
-size_t shared_bytes(int64_t K) {
-  return size_t(kWarps) * (kRingBytes + kGroups * kScaleStride * 8 + kTokens * kSumStride * 4) +
+size_t shared_bytes(int64_t K, int groups) {
+  return size_t(kWarps) * (2048 * groups + groups * kScaleStride * 8 + kTokens * kSumStride * 4) +
          size_t(K / kGroup) * kTokens * (sizeof(TokenGroup) + kGroup * 2);
 }
 
 constexpr size_t kMostShared = 227 * 1024 - 2560;  // beside first_job and pair_of
 
-template <int BITS, typename AT>
-qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
-  auto kern = stream_kernel<BITS, AT>;
+template <int BITS, typename AT, int G>
+qlin_status launch_g(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
+  auto kern = stream_kernel<BITS, AT, G>;
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), int(kMostShared), &done))
     return check_launch("qlin_expert_linear: shared memory");
@@ -455,7 +459,7 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(items, sm_count())));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = shared_bytes(a.K);
+  cfg.dynamicSmemBytes = shared_bytes(a.K, G);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -466,9 +470,16 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   return check_launch("qlin_expert_linear");
 }
 
+template <int BITS, typename AT>
+qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
+  return shared_bytes(a.K, kManyGroups) <= kMostShared
+             ? launch_g<BITS, AT, kManyGroups>(a, flags, st)
+             : launch_g<BITS, AT, kFewGroups>(a, flags, st);
+}
+
 }  // namespace
 
-bool expert_stream_fits(int64_t K) { return shared_bytes(K) <= kMostShared; }
+bool expert_stream_fits(int64_t K) { return shared_bytes(K, kFewGroups) <= kMostShared; }
 
 qlin_status launch_expert_stream(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
                                  cudaStream_t st) {

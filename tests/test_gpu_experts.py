@@ -564,3 +564,29 @@ def test_logprobs_binding_refusals(dev):
             q.token_logprobs(*args)
     out = q.token_logprobs(x[:0], t[:0], 4)
     assert [o.shape for o in out] == [(0,), (0,), (0, 4), (0, 4)]
+
+
+# ------------------------------------------------------- a K of any length
+@pytest.mark.parametrize("bits,dt", [(4, F16), (8, BF16)])
+@pytest.mark.parametrize("k", [4544, 4608, 8384, 8512, 12800])
+def test_expert_linear_long_rows(dev, bits, dt, k):
+    """Around the lengths whose tokens still fit beside the weights on their way."""
+    layer = Layer(dev, 3, 48, k, bits, dt, seed=k)
+    for tokens in (1, 11):
+        layer.check(normal(1, tokens, k).to(dt).to(dev),
+                    routing_of(random_experts(3, tokens, 2, 3), 3, dev))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1e4, 1e30])
+def test_expert_linear_bfloat16_of_any_size(dev, scale):
+    """Tokens and weights far from 1, and a token whose elements are far apart: the powers
+    of two that bring them to f16 have to be undone."""
+    for tokens in (4, 200):
+        layer = Layer(dev, 3, 72, 192, 8, BF16)
+        layer.scales.mul_(2.0 ** -20)
+        layer.biases.mul_(2.0 ** -20)
+        layer.w *= 2.0 ** -20
+        layer.step = layer.step * 2.0 ** -20
+        x = (normal(1, tokens, 192) * scale).to(BF16)
+        x[1, :64] *= 2.0 ** -12
+        layer.check(x.to(dev), routing_of(random_experts(3, tokens, 1, 3), 3, dev), out_dtype=F32)
