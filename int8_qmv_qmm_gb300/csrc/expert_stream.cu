@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   static_assert(kStages<BITS> * kStageBytes<BITS, kGroups> == kRingBytes<kGroups>, "");
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ int first_job[kMaxExperts + 1];  // the tiles of the experts before each
+  __shared__ int first_row[kMaxExperts], row_count[kMaxExperts];  // of each expert in order
+  __shared__ int order[kThreads];             // where that holds all of it
   __shared__ int pair_of[kTokens];            // of the tile's tokens (-1: none)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wk = warp % kTeam, team = warp / kTeam;
@@ -189,7 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     const ExpertRows r = expert_rows(a, e);
     if (r.bad && blockIdx.x == 0) report(kStatusPlan);
     first_job[e + 1] = (r.n + kTokens - 1) / kTokens;
+    first_row[e] = r.first;
+    row_count[e] = r.n;
   }
+  // (a small plan is fetched whole beside its offsets, not after them)
+  const bool small = a.n_pairs <= kThreads;
+  if (small && int(threadIdx.x) < a.n_pairs) order[threadIdx.x] = a.order[threadIdx.x];
   if (threadIdx.x == 0) first_job[0] = 0;
   __syncthreads();
   if (warp == 0) {
@@ -245,7 +252,19 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   // Where the copies are, ahead of the products: this lane's chunk of rows g and g + 8,
   // and the scale and bias of its group (c) there.
   Place ahead = now;
-  int expert = 0;  // ahead's
+  // the expert of a job: first_job[expert] <= job < first_job[expert + 1]
+  auto expert_of = [&](int job) {
+    int low = 0, high = a.E;
+    while (high - low > 1) {
+      const int mid = (low + high) / 2;
+      if (first_job[mid] <= job)
+        low = mid;
+      else
+        high = mid;
+    }
+    return low;
+  };
+  int expert = ahead.left > 0 ? expert_of(ahead.job) : 0;  // ahead's
   const uint8_t* from[2];
   const uint16_t *scale_from[2], *bias_from[2];
   auto at_item = [&] {
@@ -309,19 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   const int last_job = int((item0 + n_items - 1) / blocks);
   for (int job = int(item0 / blocks); job <= last_job; ++job) {
     // the job's tokens
-    int low = 0, high = a.E;  // first_job[low] <= job < first_job[high]
-    while (high - low > 1) {
-      const int mid = (low + high) / 2;
-      if (first_job[mid] <= job)
-        low = mid;
-      else
-        high = mid;
-    }
-    const ExpertRows r = expert_rows(a, low);
-    const int t0 = (job - first_job[low]) * kTokens;
+    const int of = expert_of(job), t0 = (job - first_job[of]) * kTokens;
     int p = -1;
-    if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < r.n) {
-      p = a.order[r.first + t0 + threadIdx.x];
+    if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < row_count[of]) {
+      const int at = first_row[of] + t0 + threadIdx.x;
+      p = small ? order[at] : a.order[at];
       if (p < 0 || p >= a.n_pairs) {
         report(kStatusPlan);
         p = -1;
@@ -444,7 +455,7 @@ size_t shared_bytes(int64_t K, int groups) {
          size_t(K / kGroup) * kTokens * (sizeof(TokenGroup) + kGroup * 2);
 }
 
-constexpr size_t kMostShared = 227 * 1024 - 2560;  // beside first_job and pair_of
+constexpr size_t kMostShared = 227 * 1024 - 8704;  // beside the plan
 
 template <int BITS, typename AT, int G>
 qlin_status launch_g(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
