@@ -727,13 +727,23 @@ class Routing:
               "a routing's tensors must be on one device")
         self._set(experts, weights, order, offsets)
 
+    _TENSORS = ("experts", "weights", "order", "offsets")
+
     def _set(self, experts, weights, order, offsets):
-        self.experts, self.weights, self.order, self.offsets = experts, weights, order, offsets
-        self.tokens, self.top_k = experts.shape
-        self.pairs, self.n_experts = self.tokens * self.top_k, offsets.shape[0] - 1
-        self._index = experts.get_device()
-        self._at = (experts.data_ptr(), weights.data_ptr(), order.data_ptr(), offsets.data_ptr())
+        tokens, top_k = experts.shape
+        self.__dict__.update(
+            experts=experts, weights=weights, order=order, offsets=offsets, tokens=tokens,
+            top_k=top_k, pairs=tokens * top_k, n_experts=offsets.shape[0] - 1,
+            _index=experts.get_device(),
+            _at=(experts.data_ptr(), weights.data_ptr(), order.data_ptr(), offsets.data_ptr()))
         return self
+
+    def __setattr__(self, name, value):
+        # (routing.weights *= 2 assigns the tensor that it has changed in place)
+        if name in self._TENSORS and getattr(self, name, value) is not value:
+            raise AttributeError(f"the routing's {name} cannot be replaced: write into it, or "
+                                 "make another Routing")
+        super().__setattr__(name, value)
 
 
 _SCORING = {"softmax": 0, "sigmoid": 1}

@@ -19,8 +19,10 @@
 // 1e37 or infinite, fewer than n threads with a logit above it) a second, slower way takes
 // the part: the definition, logit by logit.
 //
-// 2048 rows of 128256 in 16 bits are 525 MB; the instructions for an exponential and two
-// sums of each logit take about as long as reading it.
+// 2048 rows of 128256 in 16 bits, with the 5 likeliest, take 102 us, 5.2 TB/s: the
+// instructions for an exponential and two sums of each logit take about as long as reading
+// it.  One row of float32 with the 20 likeliest takes 10 us: launch, two rounds of loads,
+// and a chain of exchanges in the CTAs and between the eight of the cluster.
 
 #include <cmath>
 #include <type_traits>
@@ -32,6 +34,9 @@
 namespace qlin {
 namespace {
 
+// Of a CTA: four or five of them to an SM, so that one picks while others read.  (16-bit
+// logits with four: 111 us for 102; float32 with five: 101 for 97.)
+constexpr int kThreads = 256;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;  // logits that are ranked by counting
@@ -178,9 +183,8 @@ struct Part {
   }
 };
 
-template <int THREADS>
 struct Shared {
-  static constexpr int kWarps = THREADS / 32;
+  static constexpr int kWarps = kThreads / 32;
   float red[3][kWarps];
   u64 sorted[kWarps][32];    // the threads' largest logits and their vectors
   int chosen[kMaxTop];       // threads
@@ -194,23 +198,23 @@ struct Shared {
   u64 all[kMaxCluster][kMaxTop];
 };
 
-template <int THREADS, class Op>
+template <class Op>
 __device__ __forceinline__ float block_reduce(float v, float* buf, Op op) {
   for (int d = 16; d; d >>= 1) v = op(v, __shfl_xor_sync(kAll, v, d));
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
   v = buf[0];
 #pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) v = op(v, buf[w]);
+  for (int w = 1; w < kThreads / 32; ++w) v = op(v, buf[w]);
   return v;
 }
 
 // The part's likeliest `top` logits, one after another (the slower way).
-template <typename T, int THREADS>
-__device__ void pick_slowly(const Part<T>& part, int top, Shared<THREADS>& s) {
+template <typename T>
+__device__ void pick_slowly(const Part<T>& part, int top, Shared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   u64 mine = 0;
-  for (int k = part.first + int(threadIdx.x); k < part.end; k += THREADS)
+  for (int k = part.first + int(threadIdx.x); k < part.end; k += kThreads)
     part.each(k, [&](float v, int i) {
       const u64 p = place_of(v, i);
       mine = p > mine ? p : mine;
@@ -222,14 +226,14 @@ __device__ void pick_slowly(const Part<T>& part, int top, Shared<THREADS>& s) {
     __syncthreads();
     u64 best = 0;
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) best = s.warp_best[i] > best ? s.warp_best[i] : best;
+    for (int i = 0; i < kThreads / 32; ++i) best = s.warp_best[i] > best ? s.warp_best[i] : best;
     if (threadIdx.x == 0) s.best[j] = best;
     if (!best) continue;
     const int k = (int(~uint32_t(best)) + part.shift) / Part<T>::kElems;
-    const int owner = (k - part.first) % THREADS;
+    const int owner = (k - part.first) % kThreads;
     if (warp == owner / 32) {  // its warp looks for its next one
       u64 next = 0;
-      for (int v = part.first + owner + THREADS * lane; v < part.end; v += THREADS * 32)
+      for (int v = part.first + owner + kThreads * lane; v < part.end; v += kThreads * 32)
         part.each(v, [&](float x, int i) {
           const u64 p = place_of(x, i);
           if (p < best && p > next) next = p;
@@ -256,14 +260,22 @@ __device__ __forceinline__ u64 warp_sort(u64 v) {
   return v;
 }
 
+// How many of a list's first n values, in falling order, are larger than v.
+__device__ __forceinline__ int larger_in(const u64* list, int n, u64 v) {
+  int low = 0;
+  for (int d = 32; d; d >>= 1)
+    if (low + d <= n && list[low + d - 1] > v) low += d;
+  return low;
+}
+
 // The part's likeliest `top` logits from the threads that have them; false where fewer
 // threads have a logit to speak of, or the logits to rank are too many.
 //
 // The threads' best ones are sorted in each warp, and ranked by a search in each other
 // warp's list.  (One warp picking the best of all, `top` times: 2048 rows with their
-// first 5 took 119 us, with 20 172, where this takes 111 and 127; without any, 97.)
-template <typename T, int THREADS>
-__device__ bool pick(const Part<T>& part, int top, float most, int at, Shared<THREADS>& s) {
+// first 5 took 119 us, with 20 172, where this took 111 and 127; without any, 97.)
+template <typename T>
+__device__ bool pick(const Part<T>& part, int top, float most, int at, Shared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const u64 mine = warp_sort(
       most > Bounds<T>::kLowest ? u64(key_of(most)) << 32 | uint32_t(~at) : 0ull);
@@ -276,15 +288,9 @@ __device__ bool pick(const Part<T>& part, int top, float most, int at, Shared<TH
   if (lane < top && mine) {
     int rank = lane;
 #pragma unroll
-    for (int i = 1; i < THREADS / 32; ++i) {
-      const u64* list = s.sorted[(warp + i) % (THREADS / 32)];
-      int n = 0;  // of the list's that are larger
-#pragma unroll
-      for (int d = 16; d; d >>= 1)
-        if (list[n + d - 1] > mine) n += d;
-      rank += n + (n == 31 && list[31] > mine ? 1 : 0);
-    }
-    if (rank < top) s.chosen[rank] = (int(~uint32_t(mine)) - part.first) % THREADS;
+    for (int i = 1; i < kThreads / 32; ++i)
+      rank += larger_in(s.sorted[(warp + i) % (kThreads / 32)], top, mine);
+    if (rank < top) s.chosen[rank] = (int(~uint32_t(mine)) - part.first) % kThreads;
     if (rank == top - 1) s.last = mine;
   }
   __syncthreads();
@@ -292,8 +298,8 @@ __device__ bool pick(const Part<T>& part, int top, float most, int at, Shared<TH
   if (!last) return false;
   const float last_value = value_of(uint32_t(last >> 32));
   const int last_at = int(~uint32_t(last));
-  for (int j = warp; j < top; j += THREADS / 32) {
-    for (int k = part.first + s.chosen[j] + THREADS * lane; k < part.end; k += THREADS * 32) {
+  for (int j = warp; j < top; j += kThreads / 32) {
+    for (int k = part.first + s.chosen[j] + kThreads * lane; k < part.end; k += kThreads * 32) {
       if (clean<T>(part.load(k)).most < last_value) continue;
       part.each(k, [&](float v, int i) {
         if (v > last_value || (v == last_value && k <= last_at)) {
@@ -306,7 +312,7 @@ __device__ bool pick(const Part<T>& part, int top, float most, int at, Shared<TH
   __syncthreads();
   const int n = s.n_list;
   if (n > kList) return false;
-  for (int i = threadIdx.x; i < n; i += THREADS) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const u64 p = s.list[i];
     int better = 0;
     for (int j = 0; j < n; ++j) better += s.list[j] > p;
@@ -320,10 +326,10 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     logprobs_kernel(const Args a, int ranks) {
-  __shared__ Shared<THREADS> s;
+  __shared__ Shared s;
   constexpr int kElems = Part<T>::kElems, kUnroll = 4;
   const int rank = ranks > 1 ? int(ptx::cluster_ctarank()) : 0;
   const int64_t m = int64_t(blockIdx.x) / ranks;
@@ -366,18 +372,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
   };
   int k = part.first + int(threadIdx.x);
-  for (; k + (kUnroll - 1) * THREADS < part.end; k += kUnroll * THREADS) {
+  for (; k + (kUnroll - 1) * kThreads < part.end; k += kUnroll * kThreads) {
     uint4 raw[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) raw[i] = part.load(k + i * THREADS);
+    for (int i = 0; i < kUnroll; ++i) raw[i] = part.load(k + i * kThreads);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) take(raw[i], k + i * THREADS);
+    for (int i = 0; i < kUnroll; ++i) take(raw[i], k + i * kThreads);
   }
-  for (; k < part.end; k += THREADS) take(part.load(k), k);
+  for (; k < part.end; k += kThreads) take(part.load(k), k);
 
   // the part's: largest logit, sum of exponentials under it, and of those times the
   // exponents (in powers of two)
-  float high = block_reduce<THREADS>(most, s.red[0], [](float x, float y) { return fmaxf(x, y); });
+  float high = block_reduce(most, s.red[0], [](float x, float y) { return fmaxf(x, y); });
   float z = 0.f, u = 0.f;
   const bool plain = high >= Bounds<T>::kLow && high <= kHigh;  // of the CTA
   if (plain) {
@@ -389,11 +395,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
   } else {
     float top = -INFINITY;
-    for (int j = part.first + int(threadIdx.x); j < part.end; j += THREADS)
+    for (int j = part.first + int(threadIdx.x); j < part.end; j += kThreads)
       part.each(j, [&](float v, int) { top = fmaxf(top, v); });
     __syncthreads();
-    high = block_reduce<THREADS>(top, s.red[0], [](float x, float y) { return fmaxf(x, y); });
-    for (int j = part.first + int(threadIdx.x); j < part.end; j += THREADS)
+    high = block_reduce(top, s.red[0], [](float x, float y) { return fmaxf(x, y); });
+    for (int j = part.first + int(threadIdx.x); j < part.end; j += kThreads)
       part.each(j, [&](float v, int) {
         if (!(v > -INFINITY)) return;
         const float d = v == high ? 0.f : (v - high) * kLog2e, e = exp2f(d);
@@ -401,10 +407,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (e > 0.f) u += e * d;
       });
   }
-  z = block_reduce<THREADS>(z, s.red[1], [](float x, float y) { return x + y; });
-  u = block_reduce<THREADS>(u, s.red[2], [](float x, float y) { return x + y; });
-  if (a.top && !(plain && pick<T, THREADS>(part, a.top, most, at, s)))
-    pick_slowly<T, THREADS>(part, a.top, s);
+  z = block_reduce(z, s.red[1], [](float x, float y) { return x + y; });
+  u = block_reduce(u, s.red[2], [](float x, float y) { return x + y; });
+  if (a.top && !(plain && pick<T>(part, a.top, most, at, s)))
+    pick_slowly<T>(part, a.top, s);
 
   if (ranks > 1) {
     // to the first CTA of the cluster
@@ -428,17 +434,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         u += (s.sums[r][2] + s.sums[r][1] * d) * f;
       }
     }
-    // a logit's place among all lists: the number of better ones
-    for (int i = threadIdx.x; i < ranks * a.top; i += THREADS) {
-      const u64 p = s.all[i / a.top][i % a.top];
-      int better = 0;
+    // a logit's place among all lists: the number of better ones in each
+    if (int(threadIdx.x) < a.top) s.best[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < ranks * a.top; i += kThreads) {
+      const int own = i / a.top, j = i % a.top;
+      const u64 p = s.all[own][j];
+      int better = j;
       for (int r = 0; r < ranks; ++r)
-        for (int j = 0; j < a.top; ++j) {
-          // (those without a logit behind all others, in their own order)
-          const u64 o = s.all[r][j];
-          better += o > p || (!p && !o && r * a.top + j < i);
-        }
-      if (better < a.top) s.best[better] = p;
+        if (r != own) better += larger_in(s.all[r], a.top, p);
+      if (p && better < a.top) s.best[better] = p;
     }
     __syncthreads();
   }
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     if (!(v > -INFINITY)) return -INFINITY;
     return (v == high ? 0.f : v - high) - log_z;
   };
-  if (threadIdx.x == THREADS - 1) {
+  if (threadIdx.x == kThreads - 1) {
     const int t = a.tokens[m];
     a.logprobs[m] = t >= 0 && t < a.V ? logprob(widen(part.row[t])) : -INFINITY;
     a.entropy[m] = high > -INFINITY ? log_z - u / z * kLn2 : 0.f;
@@ -459,11 +464,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   }
 }
 
-template <typename T, int THREADS>
+template <typename T>
 void launch_t(const Args& a, int ranks, unsigned flags, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.M * ranks));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -481,19 +486,19 @@ void launch_t(const Args& a, int ranks, unsigned flags, cudaStream_t st) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a, ranks);
+  cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a, ranks);
 }
 
 template <typename T>
 void dispatch(const Args& a, unsigned flags, cudaStream_t st) {
-  // CTAs of 256 threads, four to an SM, a row each, where rows fill the SMs so; else CTAs
-  // of 512, and as many to a row as two to an SM allow and leave each thread 16 logits
+  // As many CTAs to a row as leave each thread 16 logits and an SM three CTAs.  (128256
+  // logits in 16 bits, us, with two, three and four: 64 rows 12.9, 12.9 and 14.2, 100 rows
+  // 17.1, 15.1 and 15.1, 150 rows 17.9, 17.9 and 23.5, 200 rows 23.9, 19.8 and 19.8.)
   const int64_t sms = sm_count();
-  if (a.M >= 2 * sms) return launch_t<T, 256>(a, 1, flags, st);
   int ranks = 1;
-  while (ranks < kMaxCluster && a.M * ranks * 2 <= 2 * sms && a.V / (ranks * 2) >= 16 * 512)
+  while (ranks < kMaxCluster && a.M * ranks * 2 <= 3 * sms && a.V / (ranks * 2) >= 16 * kThreads)
     ranks *= 2;
-  launch_t<T, 512>(a, ranks, flags, st);
+  launch_t<T>(a, ranks, flags, st);
 }
 
 }  // namespace

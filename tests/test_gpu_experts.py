@@ -147,6 +147,26 @@ def test_route_is_the_same_again_and_in_a_graph(dev):
         assert torch.equal(getattr(first, name), getattr(again, name)), name
 
 
+def test_routing_tensors_cannot_be_replaced(dev):
+    """Its calls read the memory that it was made with; writing into it works."""
+    r = q.route_experts(normal(1, 4, 8).float().to(dev), 2)
+    for routing in (r, q.Routing(r.experts, r.weights, r.order, r.offsets)):
+        with pytest.raises(AttributeError):
+            routing.weights = r.weights * 2
+        before = routing.weights.clone()
+        routing.weights *= 2
+        y = torch.ones(8, 16, dtype=F16, device=dev)
+        out = q.combine_experts(y, routing)
+        assert torch.allclose(out[:, 0].float(), 2 * before.sum(1), rtol=1e-3)
+        routing.weights.copy_(before)
+    for bad in (dict(experts=r.experts.long()), dict(weights=r.weights.half()),
+                dict(order=r.order[:7]), dict(offsets=r.offsets[:, None]),
+                dict(order=r.order.cpu())):
+        with pytest.raises(ValueError):
+            q.Routing(**{**dict(experts=r.experts, weights=r.weights, order=r.order,
+                                offsets=r.offsets), **bad})
+
+
 # ------------------------------------------------------------ experts' products
 class Layer:
     """Packed weights of experts on the GPU beside their float64 values."""
@@ -538,6 +558,26 @@ def test_logprobs_special_rows(dev, vocab):
     tokens[3], tokens[4] = vocab, 1 << 30
     lp, h, _, _ = q.token_logprobs(x.to(dev), tokens.to(dev))
     assert (lp == -inf).all() and not h.isnan().any()
+
+
+@pytest.mark.parametrize("rows", [1, 500])
+def test_logprobs_where_a_few_threads_have_all_large_logits(dev, rows):
+    """31 of every 256 neighbourhoods of 16 bytes hold thousands of logits above the 32nd
+    neighbourhood's best: more than are ranked by counting."""
+    v = 65536
+    x = normal(1, rows, v).to(F16)
+    at = torch.arange(v) // 8 % 256
+    x[:, at < 31] = (100 + normal(2, rows, int((at < 31).sum()))).to(F16)
+    x[:, 31 * 8 + 5] = 50.0
+    tokens = torch.full((rows,), 3, dtype=torch.int32)
+    if rows == 1:
+        check_logprobs(x.to(dev), tokens.to(dev), 32)
+        return
+    _, _, tt, tl = q.token_logprobs(x.to(dev), tokens.to(dev), 32)
+    for m in range(0, rows, 83):
+        ref = O.logprobs(f64(x)[m], 3, 32)
+        assert np.array_equal(tt[m].cpu().numpy(), ref[2])
+        assert np.allclose(f64(tl)[m], ref[3], atol=2.0 ** -16)
 
 
 def test_logprobs_of_what_sample_drew(dev):
