@@ -279,16 +279,19 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     }
   };
   if (ahead.left > 0) at_item();
-  // scale and bias (low and high half) of the stages on their way; 0 for a group past the
-  // warp's last, which then adds nothing
-  uint32_t coming[kAhead + 1][2];
+  // scales and biases of the stages on their way (as loaded: nothing may touch them, and
+  // so wait for them, before their stage); 0 for a group past the warp's last, which then
+  // adds nothing
+  uint16_t coming[kAhead + 1][2][2];
   int slot_in = 0;  // of the ring
   auto fetch = [&] {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) coming[i][half] = coming[i + 1][half];
-    coming[kAhead][0] = coming[kAhead][1] = 0u;
+      for (int half = 0; half < 2; ++half) {
+        coming[i][half][0] = coming[i + 1][half][0];
+        coming[i][half][1] = coming[i + 1][half][1];
+      }
     if (ahead.left > 0) {
       const int n = min(g1 - g0 - ahead.stage * kGroups, kGroups);  // groups
       const uint32_t to = ring_to + uint32_t(slot_in * kStageBytes<BITS, kGroups>);
@@ -303,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
           for (int i = 0; i < kGroups; i += 2)
             if (i + c / 2 < n) copy16(to + uint32_t((i + half) * 512), from[half] + i * 32);
         }
-        if (c < n) coming[kAhead][half] = uint32_t(*scale_from[half]) | uint32_t(*bias_from[half]) << 16;
+        coming[kAhead][half][0] = c < n ? *scale_from[half] : uint16_t(0);
+        coming[kAhead][half][1] = c < n ? *bias_from[half] : uint16_t(0);
         from[half] += kGroups * 8 * BITS;
         scale_from[half] += kGroups;
         bias_from[half] += kGroups;
@@ -366,9 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
       // (scale, bias - 1024 * scale) of group c, for the warp
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float2 v = widen2<AT>(coming[0][half]);
+        const float scale = Act<AT>::to_f32(*reinterpret_cast<const AT*>(&coming[0][half][0]));
+        const float bias = Act<AT>::to_f32(*reinterpret_cast<const AT*>(&coming[0][half][1]));
         if (c < kGroups)
-          scales[c * kScaleStride + 8 * half + g] = make_float2(v.x, fmaf(-1024.f, v.x, v.y));
+          scales[c * kScaleStride + 8 * half + g] = make_float2(scale, fmaf(-1024.f, scale, bias));
       }
       copies_wait<kAhead>();
       __syncwarp();
