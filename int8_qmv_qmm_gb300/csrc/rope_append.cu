@@ -93,8 +93,16 @@ __device__ __forceinline__ Unit unit_of(int u, int rot, bool interleaved) {
 
 // Products and their difference are rounded one by one, as the definition's
 // float32 operations are: a fused multiply-add would round differently and
-// could change a code.
+// could change a code.  (After a norm, which no definition rounds in one way, it does
+// one rounding less.)
+template <bool NORM>
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  if constexpr (NORM) {
+    const float na = fmaf(a, c, -(b * s));
+    b = fmaf(b, c, a * s);
+    a = na;
+    return;
+  }
   const float na = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
   const float nb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
   a = na;
@@ -121,7 +129,8 @@ struct Norm {
 };
 
 // 1/rms of the head that a lane's unit is part of: kUnits lanes share it, each calls.
-// (rsqrtf, 2 ulp: a division and a root bring calls of their slow paths, which spill.)
+// (A division and a root bring calls of their slow paths, which spill; so rsqrtf, and a
+// Newton step that brings its 2 ulp down to rounding.)
 template <typename T, int D>
 __device__ __forceinline__ float inverse_rms(const Vec8& x, const Vec8& y, float eps) {
   constexpr int kUnits = D / 16;
@@ -134,7 +143,9 @@ __device__ __forceinline__ float inverse_rms(const Vec8& x, const Vec8& y, float
   }
 #pragma unroll
   for (int d = 1; d < kUnits; d <<= 1) sum += __shfl_xor_sync(mask, sum, d);
-  return rsqrtf(sum * (1.0f / D) + eps);
+  const float a = sum * (1.0f / D) + eps, r = rsqrtf(a);
+  const float better = fmaf(0.5f * r, fmaf(-a * r, r, 1.0f), r);
+  return a > 0.f && a < INFINITY ? better : r;
 }
 
 template <typename T, bool NORM>
@@ -146,19 +157,20 @@ __device__ __forceinline__ void rotate_unit(Vec8& x, Vec8& y, int u, int rot, bo
     float2 a = unpack<T>(x.w[i]), b = unpack<T>(y.w[i]);
     if constexpr (NORM) {
       const float2 p = unpack<T>(norm.x.w[i]), q = unpack<T>(norm.y.w[i]);
-      a = make_float2(a.x * norm.inv * p.x, a.y * norm.inv * p.y);
-      b = make_float2(b.x * norm.inv * q.x, b.y * norm.inv * q.y);
+      // (a product of two 16-bit numbers is exact in float32)
+      a = make_float2(a.x * p.x * norm.inv, a.y * p.y * norm.inv);
+      b = make_float2(b.x * q.x * norm.inv, b.y * q.y * norm.inv);
     }
     if (NORM && 16 * u >= rot) {
       // (normed only)
     } else if (interleaved) {
       const float4 t = angles.v[i / 2], z = angles.v[2 + i / 2];
-      turn(a.x, a.y, i % 2 ? t.z : t.x, i % 2 ? t.w : t.y);
-      turn(b.x, b.y, i % 2 ? z.z : z.x, i % 2 ? z.w : z.y);
+      turn<NORM>(a.x, a.y, i % 2 ? t.z : t.x, i % 2 ? t.w : t.y);
+      turn<NORM>(b.x, b.y, i % 2 ? z.z : z.x, i % 2 ? z.w : z.y);
     } else {
       const float4 t = angles.v[i];
-      turn(a.x, b.x, t.x, t.y);
-      turn(a.y, b.y, t.z, t.w);
+      turn<NORM>(a.x, b.x, t.x, t.y);
+      turn<NORM>(a.y, b.y, t.z, t.w);
     }
     x.w[i] = pack<T>(a);
     y.w[i] = pack<T>(b);
