@@ -10,7 +10,7 @@
 // below the output's rounding.)  Tokens in bfloat16 become f16 after a power of two for
 // each group, which brings its largest element to 2^14: exact down to 2^-31 of that
 // element, below which 2^-38 of it is lost at most.  (bfloat16 products on 8-bit codes
-// need two halves of each code, and took 70 us where f16 codes take 60.)
+// would need two halves of each code: twice the products and masks.)
 //
 // A CTA, one on an SM, takes a run of items, each 16 rows for a tile of an expert's
 // tokens.  Its 16 warps form teams that take items in turn, the warps of a team a share
@@ -19,6 +19,11 @@
 // warp keeps a ring of stages in flight by its own cp.async, on through items and
 // experts, so that the stream does not stop where a tile of tokens is fetched or sums
 // are joined.
+//
+// 32 tokens of 8 of 64 experts of 2048 x 1024 at 8 bits, 135 MB, take 29 us, 4.6 TB/s; at
+// 4 bits 31 us: about 100 instructions for 16 rows of a group, and 16 warps an SM to hide
+// their latency, are what bounds it.  One token of 8 experts of 2048 x 2048 at 4 bits, 19
+// MB, takes 12 us, of which 7.5 are launch, plan, tokens and the way of the first weights.
 
 #include <algorithm>
 #include <type_traits>

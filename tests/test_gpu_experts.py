@@ -630,3 +630,36 @@ def test_expert_linear_bfloat16_of_any_size(dev, scale):
         x = (normal(1, tokens, 192) * scale).to(BF16)
         x[1, :64] *= 2.0 ** -12
         layer.check(x.to(dev), routing_of(random_experts(3, tokens, 1, 3), 3, dev), out_dtype=F32)
+
+
+# ------------------------------------------------- more elements than 32 bits count
+def test_expert_linear_past_32_bits(dev):
+    """Outputs of 2.3e9 elements: the last pairs' rows are where they belong."""
+    n, pairs = 70000, 33000
+    layer = Layer(dev, 1, n, 64, 4, F16)
+    x = normal(1, pairs, 64).to(F16).to(dev)
+    y = q.expert_linear(x, routing_of(np.zeros((pairs, 1)), 1, dev), layer.wq, layer.scales,
+                        layer.biases, 4)
+    for p in (0, 30679, pairs - 1):  # (30679 * n passes 2^31)
+        ref, size = layer.w[0] @ f64(x)[p], np.abs(layer.w[0]) @ np.abs(f64(x)[p])
+        close(y[p], ref, 2.0 ** -11 * np.abs(ref) + 2.0 ** -10 * size + TINY[F16])
+
+
+def test_logprobs_and_sums_past_32_bits(dev):
+    rows, v = 18000, 120000
+    x = torch.zeros(rows, v, dtype=F16, device=dev)
+    x[-1] = normal(1, v).to(F16).to(dev)
+    x[-2, 7] = 20.0
+    tokens = torch.full((rows,), 7, dtype=torch.int32, device=dev)
+    lp, h, tt, _ = q.token_logprobs(x, tokens, 3)
+    for m in (0, rows - 2, rows - 1):
+        ref = O.logprobs(f64(x[m]), 7, 3)
+        assert abs(float(lp[m]) - ref[0]) < 1e-4 and abs(float(h[m]) - ref[1]) < 1e-3
+        assert tt[m].tolist() == ref[2].tolist()
+    # the same memory as rows of 15 experts' outputs
+    tokens_, k = 1200, 15
+    routing = routing_of(np.tile(np.arange(k), (tokens_, 1)), k, dev)
+    out = q.combine_experts(x, routing)
+    ref = (f64(routing.weights)[-1][:, None] * f64(x[-k:])).sum(0)
+    size = (f64(routing.weights)[-1][:, None] * np.abs(f64(x[-k:]))).sum(0)
+    close(out[-1], ref, U[F16] * np.abs(ref) + 16 * 2.0 ** -24 * size + TINY[F16])
