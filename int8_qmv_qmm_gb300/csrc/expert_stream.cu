@@ -169,10 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   constexpr int kAhead = kStages<BITS> - 1;
   static_assert(kStages<BITS> * kStageBytes<BITS, kGroups> == kRingBytes<kGroups>, "");
   extern __shared__ __align__(128) uint8_t shared[];
-  __shared__ int first_job[kMaxExperts + 1];  // the tiles of the experts before each
-  __shared__ int first_row[kMaxExperts], row_count[kMaxExperts];  // of each expert in order
-  __shared__ int order[kThreads];             // where that holds all of it
-  __shared__ int pair_of[kTokens];            // of the tile's tokens (-1: none)
+  __shared__ Jobs<kMaxExperts> plan;
+  const int (&first_job)[kMaxExperts + 1] = plan.first;
+  __shared__ int order[kThreads];  // where that holds all of it
+  __shared__ int pair_of[kTokens];  // of the tile's tokens (-1: none)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wk = warp % kTeam, team = warp / kTeam;
   const int g = lane >> 2, c = lane & 3;
@@ -190,39 +190,27 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
   const uint32_t ring_to =
       ptx::smem_u32(ring) + uint32_t(BITS == 8 ? lane * 16 : g * 64 + (c ^ (g & 2)) * 16);
 
+  const int ctas = int(gridDim.x), cta = int(blockIdx.x);
   grid_launch_dependents();
   grid_dependency_wait();
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    const ExpertRows r = expert_rows(a, e);
-    if (r.bad && blockIdx.x == 0) report(kStatusPlan);
-    first_job[e + 1] = (r.n + kTokens - 1) / kTokens;
-    first_row[e] = r.first;
-    row_count[e] = r.n;
-  }
   // (a small plan is fetched whole beside its offsets, not after them)
   const bool small = a.n_pairs <= kThreads;
   if (small && int(threadIdx.x) < a.n_pairs) order[threadIdx.x] = a.order[threadIdx.x];
-  if (threadIdx.x == 0) first_job[0] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    int before = 0;
-    for (int e0 = 1; e0 <= a.E; e0 += 32) {
-      int v = e0 + lane <= a.E ? first_job[e0 + lane] : 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kAll, v, d);
-        if (lane >= d) v += o;
-      }
-      if (e0 + lane <= a.E) first_job[e0 + lane] = before + v;
-      before += __shfl_sync(kAll, v, 31);
-    }
-  }
-  __syncthreads();
+  if (fill_jobs(a, kTokens, plan) && cta == 0) report(kStatusPlan);
   const int blocks = (N + kRows - 1) / kRows;
   // The CTA's run of items: an equal share of all; where there are CTAs enough for each
   // job, one of a single job, whose tokens are then all that it fetches.
-  const int jobs = first_job[a.E], ctas = int(gridDim.x), cta = int(blockIdx.x);
-  int64_t item0 = int64_t(jobs) * blocks * cta / ctas;
-  int64_t item1 = int64_t(jobs) * blocks * (cta + 1) / ctas;
+  const int jobs = first_job[a.E];
+  const int64_t items = int64_t(jobs) * blocks;
+  int64_t item0, item1;
+  if (items <= 0x7fffffff) {  // (64-bit divisions take a good part of a microsecond)
+    const unsigned each = unsigned(items) / ctas, more = unsigned(items) % ctas;
+    item0 = each * cta + min(unsigned(cta), more);
+    item1 = item0 + each + (unsigned(cta) < more ? 1 : 0);
+  } else {
+    item0 = items * cta / ctas;
+    item1 = items * (cta + 1) / ctas;
+  }
   if (jobs > 0 && kCtasForJob * jobs <= ctas) {
     const int job = cta * jobs / ctas;
     const int first = (job * ctas + jobs - 1) / jobs;  // of the job's CTAs
@@ -243,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
     int job, block, stage, left;  // left: items to come, this one too
   };
   Place now;
-  now.job = int(item0 / blocks);
-  now.block = int(item0 % blocks) + team;
+  now.job = items <= 0x7fffffff ? int(unsigned(item0) / unsigned(blocks)) : int(item0 / blocks);
+  const int first = now.job;
+  now.block = int(item0 - int64_t(first) * blocks) + team;
   now.stage = 0;
   now.left = (n_items - team + kTeams - 1) / kTeams;
   auto settle = [&](Place& q) {
@@ -334,13 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const ExpertArgs a)
 
   float2 acc[2];
   int slot = 0;
-  const int last_job = int((item0 + n_items - 1) / blocks);
-  for (int job = int(item0 / blocks); job <= last_job; ++job) {
+  const int64_t past = item0 + n_items;
+  for (int job = first; int64_t(job) * blocks < past; ++job) {
     // the job's tokens
     const int of = expert_of(job), t0 = (job - first_job[of]) * kTokens;
     int p = -1;
-    if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < row_count[of]) {
-      const int at = first_row[of] + t0 + threadIdx.x;
+    if (threadIdx.x < kTokens && t0 + int(threadIdx.x) < plan.count[of]) {
+      const int at = plan.row[of] + t0 + threadIdx.x;
       p = small ? order[at] : a.order[at];
       if (p < 0 || p >= a.n_pairs) {
         report(kStatusPlan);

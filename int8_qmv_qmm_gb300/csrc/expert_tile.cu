@@ -83,7 +83,7 @@ struct Layout {
   static constexpr int kRings = kX * kXBytes + kW * kWBytes;
   // barriers and the tensor memory's address, the epilogue's tiles, the plan, the tiles'
   // pairs and factors
-  static constexpr int kRestBytes = 512 + kOutBytes + (3 * kMaxExperts + 4) * 4 + 2 * BN * 8;
+  static constexpr int kRestBytes = 512 + kOutBytes + int(sizeof(Jobs<kMaxExperts>)) + 2 * BN * 8;
   static constexpr int kTmemCols = 512;
   static_assert(kACol0 + kA * kACols <= kTmemCols, "");
   // (a barrier of the A ring tells the other two how far the MMAs are; the groups take
@@ -170,10 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const rest = gbase + L::kRings;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rest + 508);
   uint16_t* turned = reinterpret_cast<uint16_t*>(rest + 512);  // [2][2][kOutTokens][kBM]
-  int* first_job = reinterpret_cast<int*>(rest + 512 + kOutBytes);  // the jobs of the experts before each
-  int* first_row = first_job + kMaxExperts + 4;         // of each expert in order
-  int* row_count = first_row + kMaxExperts;
-  int* pairs = row_count + kMaxExperts;                 // [2][BN], of the tile's tokens
+  Jobs<kMaxExperts>& plan = *reinterpret_cast<Jobs<kMaxExperts>*>(rest + 512 + kOutBytes);
+  const int (&first_job)[kMaxExperts + 1] = plan.first;
+  int* pairs = reinterpret_cast<int*>(&plan + 1);             // [2][BN], of the tile's tokens
   float* factors = reinterpret_cast<float*>(pairs + 2 * BN);  // [2][BN] (bfloat16)
 
   if (threadIdx.x == 0) {
@@ -199,30 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   grid_dependency_wait();  // the plan, x and y are the preceding kernels'
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    const ExpertRows r = expert_rows(a, e);
-    if (r.bad && blockIdx.x == 0) report(kStatusPlan);
-    first_job[e + 1] = (r.n + BN - 1) / BN;
-    first_row[e] = r.first;
-    row_count[e] = r.n;
-  }
-  if (threadIdx.x == 0) first_job[0] = 0;
+  static_assert(kThreads >= kMaxExperts && kThreads / 32 <= 32, "a thread for each expert");
   ptx::tc_fence_before();
-  __syncthreads();
+  if (fill_jobs(a, BN, plan) && blockIdx.x == 0) report(kStatusPlan);
   ptx::tc_fence_after();
-  if (warp == 0) {
-    int before = 0;
-    for (int e0 = 1; e0 <= a.E; e0 += 32) {
-      int v = e0 + lane <= a.E ? first_job[e0 + lane] : 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kAll, v, d);
-        if (lane >= d) v += o;
-      }
-      if (e0 + lane <= a.E) first_job[e0 + lane] = before + v;
-      before += __shfl_sync(kAll, v, 31);
-    }
-  }
-  __syncthreads();
   const uint32_t tmem_base = __shfl_sync(kAll, *tmem_slot, 0);
   // (a kernel that starts from here on finds this one's tensor memory taken already)
   grid_launch_dependents();
@@ -234,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (first_job[q.expert + 1] <= q.job) ++q.expert;
     const int t0 = (q.job - first_job[q.expert]) * BN;
     q.n0 = q.n_tile * kBM;
-    q.at = first_row[q.expert] + t0;
-    q.count = min(row_count[q.expert] - t0, BN);
+    q.at = plan.row[q.expert] + t0;
+    q.count = min(plan.count[q.expert] - t0, BN);
   };
   auto first_tile = [&] {
     Tile q;
