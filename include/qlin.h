@@ -565,11 +565,17 @@ size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int6
  *            for a row for each token, 1 for a row for each pair
  *   y        y_dtype [n_pairs][N] (dtype, one rounding, or QLIN_F32); rows of
  *            pairs without an expert are not written
- * float32 sums; accuracy as qlin_linear.  x and wq 16-byte aligned, x_stride a
- * multiple of 8; y apart from all else.  workspace:
- * qlin_expert_linear_workspace_size bytes, 16-byte aligned, with anything in them
- * (NULL where that is 0); calls that can overlap need one each.  Experts whose offsets are not a plan's
- * and pairs outside n_pairs are left out and set a device status bit.
+ * float32 sums.  Where experts have few rows no weight is rounded.  Where they have
+ * more a weight is rounded to f16: by 2^-11 of it (one past f16's range is infinite),
+ * and with QLIN_BF16, where it is taken in a unit for its row, by no less than 2^-38 of
+ * the row's largest.  With QLIN_BF16 x is taken in a unit for its row too: exact down to
+ * 2^-28 of the row's largest element, below that to 2^-38 of it.  A row of x with NaN or
+ * an infinity gives outputs that are not finite (NaN also where the sum is infinite), and
+ * no other row's change.  x and wq 16-byte aligned, x_stride a multiple of 8; y apart
+ * from all else.  workspace: qlin_expert_linear_workspace_size bytes, 16-byte aligned,
+ * with anything in them (NULL where that is 0); calls that can overlap need one each.
+ * Experts whose offsets are not a plan's and pairs outside n_pairs are left out and set
+ * a device status bit.
  * QLIN_OVERLAP_PREVIOUS: as for qlin_qmv_ex (weights may be read before the
  * preceding kernel has completed; x, order and offsets are not).
  */
