@@ -571,8 +571,9 @@ size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int6
  * the row's largest.  With QLIN_BF16 x is taken in a unit for its row too: exact down to
  * 2^-28 of the row's largest element, below that to 2^-38 of it.  A row of x with NaN or
  * an infinity gives outputs that are not finite (NaN also where the sum is infinite), and
- * no other row's change.  x and wq 16-byte aligned, x_stride a multiple of 8; y apart
- * from all else.  workspace: qlin_expert_linear_workspace_size bytes, 16-byte aligned,
+ * no other row's change; with QLIN_BF16 elements of x or weights past 2^56 may do so
+ * too.  x and wq 16-byte aligned, x_stride a multiple of 8; y apart from all else.
+ * workspace: qlin_expert_linear_workspace_size bytes, 16-byte aligned,
  * with anything in them (NULL where that is 0); calls that can overlap need one each.
  * Experts whose offsets are not a plan's and pairs outside n_pairs are left out and set
  * a device status bit.
