@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && leads) ptx::mma_commit(accf_bar + 8u * buf);
       __syncwarp();
     }
-    // before tensor memory is freed every MMA issued here must have completed
-    if (leads) ptx::mma_commit(done_bar);
+    // before tensor memory is freed every MMA issued here must have completed (a CTA that
+    // issued none commits nothing: nobody would wait for that arrival, and it could come
+    // after the CTA has left, in the barriers of the next one)
+    if (any && leads) ptx::mma_commit(done_bar);
     __syncwarp();
     if (any && !ptx::mbar_wait(done_bar, 0)) report(kStatusWait);
     __syncwarp();

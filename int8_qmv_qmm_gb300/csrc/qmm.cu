@@ -295,9 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) ptx::mma_commit(accf_bar + 8u * buf);
       }
-      // before TMEM is freed every MMA issued here must have completed
-      ptx::mma_commit(done_bar);
-      if (any && !ptx::mbar_wait(done_bar, 0)) report(kStatusTeardown);
+      // before TMEM is freed every MMA issued here must have completed (no commit that
+      // nobody waits for: its arrival could outlive the CTA)
+      if (any) {
+        ptx::mma_commit(done_bar);
+        if (!ptx::mbar_wait(done_bar, 0)) report(kStatusTeardown);
+      }
     }
   } else if (warp < 2 + kDequantWarps) {
     // -------------------------------- dequantise (warpgroups take uses in turn)
