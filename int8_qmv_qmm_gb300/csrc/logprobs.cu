@@ -351,9 +351,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   auto take = [&](uint4 raw, int k) {
     const Pack<T> p = clean<T>(raw);
     if (p.most > c + 60.f) {
+      // (where f is 0 what there was is gone: its product with d could have overflown)
       const float d = (c - p.most) * kLog2e, f = exp2_fast(d);
-      mean.x = (mean.x + sum.x * d) * f;
-      mean.y = (mean.y + sum.y * d) * f;
+      mean.x = f > 0.f ? (mean.x + sum.x * d) * f : 0.f;
+      mean.y = f > 0.f ? (mean.y + sum.y * d) * f : 0.f;
       sum.x *= f;
       sum.y *= f;
       c = p.most;
@@ -390,8 +391,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     if (most > Bounds<T>::kLowest) {
       const float d = (c - high) * kLog2e, f = exp2_fast(d);
       const float own = sum.x + sum.y;
-      z = own * f;
-      u = (mean.x + mean.y + own * d) * f;
+      if (f > 0.f) {
+        z = own * f;
+        u = (mean.x + mean.y + own * d) * f;
+      }
     }
   } else {
     float top = -INFINITY;

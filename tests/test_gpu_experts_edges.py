@@ -30,3 +30,25 @@ def test_expert_linear_launches_that_are_mostly_idle(dev, bits, dt):  # noqa: F8
     outs = [q.expert_linear(*args, overlap_previous=True) for _ in range(40)]
     assert all(torch.equal(o, ref) for o in outs)
     assert q.device_status() == 0
+
+
+# ------------------------------------------------------------ log probabilities
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rows", [1, 240])  # (a cluster to a row, and a CTA)
+@pytest.mark.parametrize("rest,high", [(0.0, 5e35), (0.0, 1e37), (59.0, 1e13), (59.0, 1e30)])
+def test_logprobs_of_a_logit_far_above_all_others(dev, dt, rows, rest, high):  # noqa: F811
+    """The others' exponentials are 0, whatever number of them, or sum under a lower reference
+    (threads begin at 0, then meet `rest`), stands before them: the entropy is 0 and the log
+    probabilities are differences of logits."""
+    v, at = 128256, 77777
+    x = torch.zeros(rows, v, dtype=dt, device=dev)
+    x.view(rows, 8, -1)[:, :, v // 16:] = rest
+    x[:, at] = high
+    tokens = torch.full((rows,), at, dtype=torch.int32, device=dev)
+    tokens[::2] = 4
+    lp, entropy, top, top_lp = q.token_logprobs(x, tokens, 3)
+    assert (entropy == 0).all()
+    assert torch.equal(lp, torch.where(tokens == at, 0.0, -x[:, at].float()))
+    assert (top[:, 0] == at).all() and (top_lp[:, 0] == 0).all()
+    assert (top[:, 1:] == (x[0] == rest).nonzero()[:2, 0]).all()
+    assert torch.equal(top_lp[:, 1], rest - x[:, at].float())
