@@ -497,7 +497,8 @@ qlin_status qlin_sample(const void* logits, int64_t logits_stride, const float* 
  * NaN logits count as -infinity; a row of nothing else has logprob -infinity
  * and entropy 0; with +infinity among the logits only those have a share, equal
  * ones.  Where fewer than top logits are above -infinity the rest of top_tokens
- * is -1, of top_logprobs -infinity.  1 <= V <= 262144.
+ * is -1, of top_logprobs -infinity.  No log probability is above 0 and no
+ * entropy below.  1 <= V <= 262144.
  */
 qlin_status qlin_token_logprobs(const void* logits, int64_t logits_stride, const int32_t* tokens,
                                 float* logprobs, float* entropy, int top, int32_t* top_tokens,

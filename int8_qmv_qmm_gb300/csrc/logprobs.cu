@@ -450,6 +450,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     }
     __syncthreads();
   }
+  // (the largest logit's own share makes z at least 1, and no term of u is above 0: what
+  // rounding takes from there would make a log probability positive, an entropy negative)
+  z = fmaxf(z, 1.f);
+  u = fminf(u, 0.f);
   const float log_z = logf(z);
   auto logprob = [&](float v) {
     if (!(v > -INFINITY)) return -INFINITY;

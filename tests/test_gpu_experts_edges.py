@@ -52,3 +52,27 @@ def test_logprobs_of_a_logit_far_above_all_others(dev, dt, rows, rest, high):  #
     assert (top[:, 0] == at).all() and (top_lp[:, 0] == 0).all()
     assert (top[:, 1:] == (x[0] == rest).nonzero()[:2, 0]).all()
     assert torch.equal(top_lp[:, 1], rest - x[:, at].float())
+
+
+def test_logprobs_are_not_positive(dev):  # noqa: F811
+    """A probability is at most 1: no log probability is above 0, and no entropy below, also
+    where one token has all but nothing of the share and its exponential is 1 by way of a
+    product of two (the reference that a thread began with, 0, and the largest logit, in
+    vectors of the same thread)."""
+    rows, v = 600, 4096
+    high = torch.linspace(1.0, 59.9, rows, dtype=torch.float64)
+    x = torch.full((rows, v), -float("inf"))
+    x[:, 0] = 0.0
+    x[:, 2048] = high.float()
+    for dt in (F32, F16, BF16):
+        y = x.to(dt)
+        h = y[:, 2048].double()
+        tokens = torch.full((rows,), 2048, dtype=torch.int32, device=dev)
+        lp, entropy, _, top_lp = q.token_logprobs(y.to(dev), tokens, 2)
+        assert (lp <= 0).all() and (entropy >= 0).all() and (top_lp <= 0).all()
+        ref = -torch.log1p(torch.exp(-h))
+        # exponentials are 2 ulp off, as is their product's argument: 2^-20 of z; the entropy's
+        # mean is a difference of two numbers up to 60 * log2(e), off by 2^-22 of them
+        assert (lp.double().cpu() - ref).abs().max() <= 2.0 ** -20
+        ref = -ref + h / (1 + torch.exp(h))
+        assert (entropy.double().cpu() - ref).abs().max() <= 2.0 ** -15
