@@ -567,11 +567,13 @@ size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int6
  *   y        y_dtype [n_pairs][N] (dtype, one rounding, or QLIN_F32); rows of
  *            pairs without an expert are not written
  * float32 sums.  Where experts have few rows no weight is rounded.  Where they have
- * more a weight is rounded to f16: by 2^-11 of it (one past f16's range is infinite),
- * and with QLIN_BF16, where it is taken in a unit for its row, by no less than 2^-38 of
- * the row's largest.  With QLIN_BF16 x is taken in a unit for its row too: exact down to
- * 2^-28 of the row's largest element, below that to 2^-38 of it.  A row of x with NaN or
- * an infinity gives outputs that are not finite (NaN also where the sum is infinite), and
+ * more a weight is rounded to f16: by 2^-11 of it at most, or 2^-25 (one past f16's
+ * range is infinite).  With QLIN_BF16 that is done in a unit for its row: by 2^-11 of it
+ * and 2^-31 (8 bits) or 2^-35 (4 bits) of the row's largest at most, so that a group
+ * whose scale is below 2^-39 of that may lose its codes.  With QLIN_BF16 x is taken in a
+ * unit for its row too: exact down to 2^-28 of the row's largest element, below that to
+ * 2^-38 of it.  (A row's largest below 2^-100 counts as that.)  A row of x with NaN or an
+ * infinity gives outputs that are not finite (NaN also where the sum is infinite), and
  * no other row's change; with QLIN_BF16 elements of x or weights past 2^56 may do so
  * too.  x and wq 16-byte aligned, x_stride a multiple of 8; y apart from all else.
  * workspace: qlin_expert_linear_workspace_size bytes, 16-byte aligned,

@@ -14,9 +14,11 @@
 //
 // Both types multiply in f16.  bfloat16 is brought there by powers of two, which the
 // outputs are multiplied back by: one for each token (its largest element to 2^14, exact
-// down to 2^-28 of it) and one for each weight row (found from its scales and biases; a
-// weight is then rounded to f16's 11 bits, or to 2^-38 of the row's largest).  The first
-// kernel finds them.  (Two bfloat16 products for the high and low part of a weight, as
+// down to 2^-28 of it) and one for each weight row, found from its scales and biases, which
+// brings the row's largest to 2^14 or more.  Scale and bias are rounded to f16 there, to a
+// multiple of 2^-24, and code * scale + bias once more: a weight is off by 2^-11 of it and
+// (largest code + 1) * 2^-25 at most, 2^-31 of the row's largest at 8 bits and 2^-35 at 4.
+// The first kernel finds the powers.  (Two bfloat16 products for the high and low part of a weight, as
 // qmm.cu has them, took 361 us where f16 took 241.)
 //
 //   warps 0, 2   load the tokens' rows and the packed tiles (TMA, one thread each)

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import int8_qmv_qmm_gb300 as q
-from tests.test_gpu_decoder import normal
+from tests.test_gpu_decoder import f64, normal
 from tests.test_gpu_experts import BF16, F16, F32, Layer, dev, routing_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +76,54 @@ def test_logprobs_are_not_positive(dev):  # noqa: F811
         assert (lp.double().cpu() - ref).abs().max() <= 2.0 ** -20
         ref = -ref + h / (1 + torch.exp(h))
         assert (entropy.double().cpu() - ref).abs().max() <= 2.0 ** -15
+
+
+# ---------------------------------------------------- what a weight is rounded to
+def spread_layer(dev, bits, dt, spread):  # noqa: F811
+    """A layer in which half of each row's groups are 2^spread smaller than the others, and its
+    scales and biases in float64, for each weight."""
+    layer = Layer(dev, 3, 72, 256, bits, dt, seed=11)
+    for t in (layer.scales, layer.biases):
+        t[..., 1:3] *= 2.0 ** -spread
+    s, b = (np.repeat(f64(t), 64, -1) for t in (layer.scales, layer.biases))
+    codes = layer.wq.cpu().numpy().view(np.uint32)[..., None] >> np.arange(0, 32, bits,
+                                                                           dtype=np.uint32)
+    layer.w = (codes & (2 ** bits - 1)).reshape(s.shape).astype(np.float64) * s + b
+    return layer, s, b
+
+
+def one_hot(dev, layer, tokens, bound, first=0):  # noqa: F811
+    """Rows of x that hold one element each, at first and on, times every weight of their
+    expert, in float32: the largest error in units of `bound` (of each weight) times x."""
+    e, n, k = layer.w.shape
+    rng = np.random.default_rng(5)
+    at = rng.permutation((first + np.arange(tokens)) % k)
+    value = torch.from_numpy(rng.uniform(1, 2, tokens)).to(layer.dt)
+    x = torch.zeros(tokens, k, dtype=layer.dt)
+    x[torch.arange(tokens), torch.from_numpy(at)] = value
+    which = rng.integers(0, e, tokens)
+    y = q.expert_linear(x.to(dev), routing_of(which[:, None], e, dev), layer.wq, layer.scales,
+                        layer.biases, layer.bits, out_dtype=F32)
+    v = value.double().numpy()[:, None]
+    return (np.abs(f64(y) - v * layer.w[which, :, at]) / (v * bound[which, :, at])).max()
+
+
+SPREADS = [(F16, 0), (F16, 12), (BF16, 0), (BF16, 20), (BF16, 32), (BF16, 40)]
+
+
+@pytest.mark.parametrize("dt,spread", SPREADS)
+@pytest.mark.parametrize("bits", [4, 8])
+def test_expert_linear_rounds_weights_as_it_says(dev, bits, dt, spread):  # noqa: F811
+    """With one element of x at a time an output is one weight.  Of many rows' products a weight
+    is one rounding to f16: off by 2^-11 of it at most, or by 2^-25 (f16's least numbers).
+
+    bfloat16 weights are in a unit that puts the row's largest at 2^14 or more.  Scale, bias
+    and weight are multiples of 2^-24 there, the first two off by 2^-25 at most, so that the
+    weight is off by (largest code + 1) * 2^-25 before its own rounding, which is exact where
+    it is below f16's normal numbers: 2^-31 of the row's largest at 8 bits, 2^-35 at 4."""
+    layer, s, b = spread_layer(dev, bits, dt, spread)
+    largest = np.maximum(np.abs(b), np.abs(b + (2 ** bits - 1) * s)).max(-1, keepdims=True)
+    least = 2.0 ** -25 if dt is F16 else 2.0 ** (bits - 39) * largest
+    # (the rounding of a weight that is off already: 2^-11 more of that)
+    worst = one_hot(dev, layer, 768, np.abs(layer.w) * 2.0 ** -11 + least)
+    assert worst <= 1 + 2.0 ** -10, worst
