@@ -566,7 +566,8 @@ size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int6
  *            for a row for each token, 1 for a row for each pair
  *   y        y_dtype [n_pairs][N] (dtype, one rounding, or QLIN_F32); rows of
  *            pairs without an expert are not written
- * float32 sums.  Where experts have few rows no weight is rounded.  Where they have
+ * float32 sums.  Where experts have few rows no weight is rounded (the sums of a group are
+ * of (1024 + code) * x, and of x times its bias - 1024 * scale).  Where they have
  * more a weight is rounded to f16: by 2^-11 of it at most, or 2^-25 (one past f16's
  * range is infinite).  With QLIN_BF16 that is done in a unit for its row: by 2^-11 of it
  * and 2^-31 (8 bits) or 2^-35 (4 bits) of the row's largest at most, so that a group

@@ -127,3 +127,18 @@ def test_expert_linear_rounds_weights_as_it_says(dev, bits, dt, spread):  # noqa
     # (the rounding of a weight that is off already: 2^-11 more of that)
     worst = one_hot(dev, layer, 768, np.abs(layer.w) * 2.0 ** -11 + least)
     assert worst <= 1 + 2.0 ** -10, worst
+
+
+@pytest.mark.parametrize("dt,spread", SPREADS)
+@pytest.mark.parametrize("bits", [4, 8])
+def test_expert_linear_of_few_rows_rounds_no_weight(dev, bits, dt, spread):  # noqa: F811
+    """x and (1024 + code) * x are exact.  bias - 1024 * scale is rounded once, its product with
+    x once more, their sum with scale times the other once more, all in float32: a weight that
+    was rounded to f16 (2^-12 of it off, on the whole) would be far outside."""
+    layer, s, b = spread_layer(dev, bits, dt, spread)
+    bound = np.abs(b - 1024 * s) * 2.0 ** -23 + np.abs(layer.w) * 2.0 ** -24
+    rounded = np.abs(layer.w - layer.w.astype(np.float16)) if dt is F16 or not spread else None
+    assert rounded is None or (rounded / bound).max() > 4
+    for first in range(0, 256, 12):  # (12 rows of 3 experts: few)
+        worst = one_hot(dev, layer, 12, bound, first)
+        assert worst <= 1 + 2.0 ** -10, (first, worst)
