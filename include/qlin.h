@@ -553,8 +553,9 @@ qlin_status qlin_route_experts(const void* logits, int64_t logits_stride, const 
                                qlin_dtype ldtype, void* workspace, size_t workspace_bytes,
                                unsigned flags, void* stream);
 
-/* Bytes of device scratch that qlin_expert_linear needs (0 where experts have few
- * rows; else the rows of x in the plan's order). */
+/* Bytes of device scratch that qlin_expert_linear needs: 0 where experts have few rows,
+ * which is up to 5 pairs for each expert that could have any (n_pairs / min(E, n_pairs))
+ * and K up to 8384; else the rows of x in the plan's order. */
 size_t qlin_expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K);
 
 /*

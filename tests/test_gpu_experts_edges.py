@@ -11,7 +11,8 @@ import torch
 
 import int8_qmv_qmm_gb300 as q
 from tests.test_gpu_decoder import f64, normal
-from tests.test_gpu_experts import BF16, F16, F32, Layer, dev, routing_of  # noqa: F401
+from tests.test_gpu_experts import (BF16, F16, F32, Layer, dev, random_experts,  # noqa: F401
+                                    routing_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +143,16 @@ def test_expert_linear_of_few_rows_rounds_no_weight(dev, bits, dt, spread):  # n
     for first in range(0, 256, 12):  # (12 rows of 3 experts: few)
         worst = one_hot(dev, layer, 12, bound, first)
         assert worst <= 1 + 2.0 ** -10, (first, worst)
+
+
+# ---------------------------------------------------------------- lengths at a border
+@pytest.mark.parametrize("bits,dt", [(4, F16), (8, BF16)])
+@pytest.mark.parametrize("k", [8384, 8448])
+def test_expert_linear_at_the_longest_streamed_row(dev, bits, dt, k):  # noqa: F811
+    """The last length whose tokens fit beside the weights on their way, and the first that
+    goes to the tensor cores."""
+    layer = Layer(dev, 3, 40, k, bits, dt, seed=k)
+    for tokens in (1, 7):
+        layer.check(normal(1, tokens, k).to(dt).to(dev),
+                    routing_of(random_experts(3, tokens, 2, 3), 3, dev))
+    assert q.device_status() == 0
