@@ -46,7 +46,7 @@ class Decoder:
 
     experts and top_experts make the layers mixtures of experts, qk_norm adds the norms of
     query and key heads.  With logprobs = n, logprobs, entropy, top_tokens and top_logprobs are
-    those of the last call's tokens (token_logprobs with the n likeliest; the whole
+    those of each slot's last token (token_logprobs with the n likeliest; the whole
     distribution's, whatever the sampling settings leave out of it).
 
     A slot whose logits have no token (all NaN or -infinity, as after an overflow) gets -1,
@@ -159,7 +159,8 @@ class Decoder:
             self.logprobs, self.entropy, self.top_tokens, self.top_logprobs = token_logprobs(
                 logits, tokens, self._top, overlap_previous=True)
 
-    _ANSWERS = ("logits", "logprobs", "entropy", "top_tokens", "top_logprobs")
+    _OF_TOKENS = ("logprobs", "entropy", "top_tokens", "top_logprobs")
+    _ANSWERS = ("logits",) + _OF_TOKENS
 
     def _answers(self):
         return [getattr(self, name) for name in self._ANSWERS]
@@ -189,9 +190,14 @@ class Decoder:
         starts = starts.to(self.device)
         self.u.uniform_()
         self.logits = self._forward(flat.to(self.device), starts, max(new))
-        tokens = torch.empty_like(self.tokens)
+        tokens, got = torch.empty_like(self.tokens), starts.diff() > 0
+        before = [getattr(self, name) for name in self._OF_TOKENS]
         self._sample(self.logits, tokens)
-        self.tokens.copy_(torch.where(starts.diff() > 0, tokens, self.tokens))
+        self.tokens.copy_(torch.where(got, tokens, self.tokens))
+        for name, old in zip(self._OF_TOKENS, before):
+            if old is not None:  # (a slot that got none keeps its last token's)
+                new = getattr(self, name)
+                setattr(self, name, torch.where(got.view(-1, *[1] * (new.dim() - 1)), new, old))
         self.held = [h + n for h, n in zip(self.held, new)]
         return self.tokens
 

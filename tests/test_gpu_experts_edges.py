@@ -10,9 +10,13 @@ import pytest
 import torch
 
 import int8_qmv_qmm_gb300 as q
+from int8_qmv_qmm_gb300.decoder import Decoder
+from oracle import experts_oracle as O
+from tests.test_gpu_decode_loop import prompts
 from tests.test_gpu_decoder import f64, normal
 from tests.test_gpu_experts import (BF16, F16, F32, Layer, dev, random_experts,  # noqa: F401
                                     routing_of)
+from tests.test_gpu_experts_together import MIXED
 
 pytestmark = pytest.mark.gpu
 
@@ -155,4 +159,30 @@ def test_expert_linear_at_the_longest_streamed_row(dev, bits, dt, k):  # noqa: F
     for tokens in (1, 7):
         layer.check(normal(1, tokens, k).to(dt).to(dev),
                     routing_of(random_experts(3, tokens, 2, 3), 3, dev))
+    assert q.device_status() == 0
+
+
+# --------------------------------------------------------------------- the decoder
+def test_decoder_log_probabilities_stay_with_their_tokens(dev):  # noqa: F811
+    """A call that gives a slot no tokens leaves its last token, and that token's log
+    probabilities with it: the next slot's prompt does not take their place."""
+    d = Decoder(dev, **MIXED)
+    d.temperature.fill_(0.8)
+    torch.manual_seed(3)
+    d.prefill(prompts((5, 70, 9)))
+    names = ("logprobs", "entropy", "top_tokens", "top_logprobs")
+    for captured in (False, True):
+        if captured:
+            d.capture()
+        d.decode()
+        before = {name: getattr(d, name).clone() for name in names}
+        token = d.tokens.clone()
+        d.prefill([[], [1, 2, 3], []])
+        for name in names:
+            now = getattr(d, name)
+            assert torch.equal(now[[0, 2]], before[name][[0, 2]]), name
+        assert torch.equal(d.tokens[[0, 2]], token[[0, 2]])
+        ref = O.logprobs(f64(d.logits)[1], int(d.tokens[1]), 5)
+        assert abs(float(d.logprobs[1]) - ref[0]) <= 2.0 ** -16
+        assert np.array_equal(d.top_tokens[1].cpu().numpy(), ref[2])
     assert q.device_status() == 0
