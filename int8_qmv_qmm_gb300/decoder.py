@@ -196,8 +196,8 @@ class Decoder:
         self.tokens.copy_(torch.where(got, tokens, self.tokens))
         for name, old in zip(self._OF_TOKENS, before):
             if old is not None:  # (a slot that got none keeps its last token's)
-                new = getattr(self, name)
-                setattr(self, name, torch.where(got.view(-1, *[1] * (new.dim() - 1)), new, old))
+                own = got if old.dim() == 1 else got[:, None]
+                setattr(self, name, torch.where(own, getattr(self, name), old))
         self.held = [h + n for h, n in zip(self.held, new)]
         return self.tokens
 
