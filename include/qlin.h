@@ -43,7 +43,8 @@
  * ("track(upstream-iree): ...", section "What is already in-tree").  A launch failure
  * reported by the CUDA runtime returns QLIN_ERR_CUDA.  Calls are asynchronous
  * on the given stream (a cudaStream_t passed as void*; NULL = legacy default
- * stream) and never synchronise the device.
+ * stream) and never synchronise the device.  Stream and pointers are those of the
+ * current device, which the library does not change.
  *
  * Device-side waits in the kernels are bounded; if one gives up it sets a
  * device status word that qlin_device_status() reads (and clears).

@@ -4,7 +4,7 @@ GB300 (sm_103a).
 This package is a thin ctypes binding over the C ABI of ``libqlin.so``
 (declared in ``include/qlin.h``): it checks tensor placement and shape,
 allocates outputs with PyTorch and passes raw device pointers and the current
-CUDA stream.  Every step of the computation runs in the library's CUDA
+CUDA stream.  Tensors are on the current CUDA device.  Every step of the computation runs in the library's CUDA
 kernels; there is no CPU or PyTorch fallback -- if the library is missing the
 calls raise.
 
@@ -143,8 +143,20 @@ def _check(status: int):
                                 f"{L.qlin_last_error().decode()}")
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _current_raw_stream(index: int) -> int:
+    """The current stream of device `index`, which has to be the current device: a kernel is
+    launched there, and would be handed another device's pointers."""
+    if index != _current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device: "
+                         "make the call under torch.cuda.device")
+    return _raw_stream(index)
+
+
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return ctypes.c_void_p(_current_raw_stream(t.get_device()))
 
 
 def _ptr(t: torch.Tensor | None):
@@ -293,11 +305,10 @@ def qmv_chain(x0, link_array, n_links, bits, dtype, workspace, group_size=GROUP_
 
     x0: device tensor (or None); link_array: from make_links; workspace: from
     chain_workspace.  Outputs are written into each link's y."""
-    dev = workspace.device
     _check(lib().qlin_qmv_chain(_ptr(x0) if x0 is not None else None, link_array, n_links,
                                 bits, group_size, _DTYPE_CODE[dtype], _ptr(workspace),
                                 workspace.numel() * 4,
-                                ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+                                _stream(workspace)))
 
 
 class _KVCacheStruct(ctypes.Structure):
@@ -387,9 +398,6 @@ class KVCache:
 # These calls run between a decoder's linears, some microseconds each, so each
 # looks its arguments over in one expression and goes into what is wrong only
 # where something is.
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _refuse(*checks):
     """Raises for the first check (ok, what) that does not hold."""
     for ok, what in checks:

@@ -186,3 +186,39 @@ def test_decoder_log_probabilities_stay_with_their_tokens(dev):  # noqa: F811
         assert abs(float(d.logprobs[1]) - ref[0]) <= 2.0 ** -16
         assert np.array_equal(d.top_tokens[1].cpu().numpy(), ref[2])
     assert q.device_status() == 0
+
+
+# --------------------------------------------------- a device that is not the current one
+def test_every_call_is_refused_where_its_device_is_not_current(dev, monkeypatch):  # noqa: F811
+    layer = Layer(dev, 2, 8, 64, 8, F16)
+    w = normal(1, 8, 64).float().to(dev)
+    packed = q.quantize_affine(w, 8)
+    x, z = normal(2, 3, 64).to(F16).to(dev), torch.zeros(3, 10, device=dev)
+    qkv = normal(3, 3, 3 * 64).to(F16).to(dev)
+    norm = torch.ones(64, dtype=F16, device=dev)
+    routing = q.route_experts(z, 2)
+    row, none = torch.ones(3, device=dev), torch.zeros(3, dtype=torch.int32, device=dev)
+    cache = q.KVCache.empty(1, 128, 1, 64, device=dev)
+    starts = torch.tensor([0, 3], dtype=torch.int32, device=dev)
+    ws = q.attention_workspace(64)
+    expert = (routing_of([[0], [1], [1]], 2, dev), layer.wq, layer.scales, layer.biases, 8)
+    calls = [lambda: q.quantize_affine(w, 8), lambda: q.dequant(*packed, 8),
+             lambda: q.qmv(x[:1], *packed, 8), lambda: q.qmm(x, *packed, 8),
+             lambda: q.linear(x, *packed, 8), lambda: q.add_rms_norm(x, norm),
+             lambda: q.rope_table(8, 64), lambda: q.rope_append(qkv, None, cache, starts, 1),
+             lambda: q.rope_append(qkv, None, cache, starts, 1, q_norm=norm, k_norm=norm),
+             lambda: q.cache_attention(x.view(3, 1, 64), cache, starts, 3, ws),
+             lambda: q.cache_dequant(cache, none[:1]),
+             lambda: q.sample(z, row, row, none, row, 0 * row),
+             lambda: q.token_logprobs(z, none, 2), lambda: q.route_experts(z, 2),
+             lambda: q.expert_linear(x, *expert),
+             lambda: q.combine_experts(normal(4, 6, 64).to(F16).to(dev), routing)]
+    for call in calls:
+        call()
+    assert q.device_status() == 0
+    monkeypatch.setattr(q, "_current_device", lambda: 1)
+    for i, call in enumerate(calls):
+        if i == 6:
+            continue  # (it makes its table on the current device)
+        with pytest.raises(ValueError, match="not the current device"):
+            call()
