@@ -32,6 +32,24 @@ qlin_status qlin_testing_qmv_chain_stalled(const void* x0, const qlin_link* link
                                            void* stream);
 
 /*
+ * qlin_expert_linear (4 bits, QLIN_F16) by the tensor-core kernel, where in each CTA the
+ * copies of packed weights stop before its stage `stalled_stage` (a group of 64 of K of
+ * a tile; the CTA's tiles one after another): every wait behind them runs out after
+ * `wait_limit_us` microseconds (1000 .. 2,000,000).  The kernel then records its status
+ * (qlin_device_status reports 1 << 30), lets its copies and products in flight end,
+ * frees its tensor memory and exits; outputs of tiles that were not complete are not
+ * written, and the context stays usable.  A CTA with no more stages than that runs as
+ * ever.  Arguments otherwise as qlin_expert_linear.  Errors: QLIN_ERR_INVALID_ARG where
+ * the call needs no workspace (it would not take that kernel), stalled_stage is negative
+ * or wait_limit_us out of range; else as qlin_expert_linear.
+ */
+qlin_status qlin_testing_expert_linear_stalled(
+    const void* x, int64_t x_stride, int pairs_per_row, const int32_t* order,
+    const int32_t* offsets, int64_t n_pairs, const uint32_t* wq, const void* scales,
+    const void* biases, void* y, int E, int64_t N, int64_t K, void* workspace,
+    size_t workspace_bytes, int stalled_stage, unsigned wait_limit_us, void* stream);
+
+/*
  * The split of K that qlin_qmv (and qlin_linear's qmv path) would use for an
  * N x K matrix of `bits`-bit codes on a device with `sm_count` SMs: the
  * number of CTAs (a thread-block cluster) that share each row block, each

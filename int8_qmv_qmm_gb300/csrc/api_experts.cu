@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "qlin_internal.h"
+#include "qlin_testing.h"
 
 namespace qlin {
 namespace {
@@ -26,6 +27,47 @@ qlin_status check_routing(const char* name, int64_t T, int top_k, int E) {
     return fail(QLIN_ERR_UNSUPPORTED, "%s: E=%d (at most 512), top_k=%d (at most 32)", name, E,
                 top_k);
   if (T > kMaxPairs / top_k) return fail(QLIN_ERR_UNSUPPORTED, "%s: T too large", name);
+  return QLIN_OK;
+}
+
+// What qlin_expert_linear takes (with no pairs, whatever the pointers).
+qlin_status check_expert_linear(const char* name, const ExpertArgs& a, int bits, int group_size,
+                                qlin_dtype dtype, qlin_dtype y_dtype, size_t workspace_bytes,
+                                unsigned flags) {
+  qlin_status s = check_flags(name, flags);
+  if (s != QLIN_OK) return s;
+  if (bits != 4 && bits != 8)
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: bits=%d (supported: 4, 8)", name, bits);
+  if (group_size != kGroup)
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: group_size=%d (supported: 64)", name, group_size);
+  if (dtype != QLIN_F16 && dtype != QLIN_BF16)
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: dtype %d (supported: QLIN_F16, QLIN_BF16)", name,
+                int(dtype));
+  if (y_dtype != dtype && y_dtype != QLIN_F32)
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: y dtype %d must be float32 or the activation dtype",
+                name, int(y_dtype));
+  if (a.n_pairs < 0 || a.pairs_per_row < 1 || a.n_pairs % a.pairs_per_row || a.E < 1 || a.N < 1 ||
+      a.K < 1 || a.K % kGroup)
+    return fail(QLIN_ERR_INVALID_ARG,
+                "%s: n_pairs=%lld pairs_per_row=%d E=%d N=%lld K=%lld (K a multiple of %d)", name,
+                (long long)a.n_pairs, a.pairs_per_row, a.E, (long long)a.N, (long long)a.K, kGroup);
+  if (a.E > 512 || a.n_pairs > kMaxPairs || a.N > (int64_t(1) << 20) || a.K > 65536 ||
+      int64_t(a.E) * a.N > (int64_t(1) << 30))
+    return fail(QLIN_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", name);
+  if (a.n_pairs == 0) return QLIN_OK;
+  if (!a.x || !a.order || !a.offsets || !a.wq || !a.scales || !a.biases || !a.y)
+    return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (a.x_stride < a.K)
+    return fail(QLIN_ERR_INVALID_ARG, "%s: x_stride is shorter than K", name);
+  const size_t need = expert_linear_workspace_size(a.n_pairs, a.E, a.N, a.K);
+  if (need && (!a.workspace || workspace_bytes < need))
+    return fail(QLIN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, need);
+  if (!aligned(a.x, 16) || a.x_stride % 8 || !aligned(a.wq, 16) || !aligned(a.workspace, 16) ||
+      !aligned(a.scales, 2) || !aligned(a.biases, 2) || !aligned(a.y, a.y_f32 ? 4 : 2) ||
+      !aligned(a.order, 4) || !aligned(a.offsets, 4))
+    return fail(QLIN_ERR_MISALIGNED,
+                "%s: x, wq and workspace must be 16-byte aligned, x_stride a multiple of 8, the "
+                "rest aligned to its elements", name);
   return QLIN_OK;
 }
 
@@ -90,45 +132,35 @@ qlin_status qlin_expert_linear(const void* x, int64_t x_stride, int pairs_per_ro
                                int E, int64_t N, int64_t K, int bits, int group_size,
                                qlin_dtype dtype, qlin_dtype y_dtype, void* workspace,
                                size_t workspace_bytes, unsigned flags, void* stream) {
-  const char* name = "qlin_expert_linear";
-  clear_error();
-  qlin_status s = check_flags(name, flags);
-  if (s != QLIN_OK) return s;
-  if (bits != 4 && bits != 8)
-    return fail(QLIN_ERR_UNSUPPORTED, "%s: bits=%d (supported: 4, 8)", name, bits);
-  if (group_size != kGroup)
-    return fail(QLIN_ERR_UNSUPPORTED, "%s: group_size=%d (supported: 64)", name, group_size);
-  if (dtype != QLIN_F16 && dtype != QLIN_BF16)
-    return fail(QLIN_ERR_UNSUPPORTED, "%s: dtype %d (supported: QLIN_F16, QLIN_BF16)", name,
-                int(dtype));
-  if (y_dtype != dtype && y_dtype != QLIN_F32)
-    return fail(QLIN_ERR_UNSUPPORTED, "%s: y dtype %d must be float32 or the activation dtype",
-                name, int(y_dtype));
-  if (n_pairs < 0 || pairs_per_row < 1 || n_pairs % pairs_per_row || E < 1 || N < 1 || K < 1 ||
-      K % kGroup)
-    return fail(QLIN_ERR_INVALID_ARG,
-                "%s: n_pairs=%lld pairs_per_row=%d E=%d N=%lld K=%lld (K a multiple of %d)", name,
-                (long long)n_pairs, pairs_per_row, E, (long long)N, (long long)K, kGroup);
-  if (E > 512 || n_pairs > kMaxPairs || N > (int64_t(1) << 20) || K > 65536 ||
-      int64_t(E) * N > (int64_t(1) << 30))
-    return fail(QLIN_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", name);
-  if (n_pairs == 0) return QLIN_OK;
-  if (!x || !order || !offsets || !wq || !scales || !biases || !y)
-    return fail(QLIN_ERR_INVALID_ARG, "%s: null pointer argument", name);
-  if (x_stride < K) return fail(QLIN_ERR_INVALID_ARG, "%s: x_stride is shorter than K", name);
-  const size_t need = expert_linear_workspace_size(n_pairs, E, N, K);
-  if (need && (!workspace || workspace_bytes < need))
-    return fail(QLIN_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed", name, need);
-  if (!aligned(x, 16) || x_stride % 8 || !aligned(wq, 16) || !aligned(workspace, 16) || !aligned(scales, 2) ||
-      !aligned(biases, 2) || !aligned(y, y_dtype == QLIN_F32 ? 4 : 2) || !aligned(order, 4) ||
-      !aligned(offsets, 4))
-    return fail(QLIN_ERR_MISALIGNED,
-                "%s: x, wq and workspace must be 16-byte aligned, x_stride a multiple of 8, the rest aligned "
-                "to its elements", name);
-  const ExpertArgs a = {x,      x_stride, pairs_per_row, order, offsets,
-                        n_pairs, wq,      scales,        biases, y,
+  const ExpertArgs a = {x,       x_stride, pairs_per_row, order,  offsets,
+                        n_pairs, wq,       scales,        biases, y,
                         y_dtype == QLIN_F32 ? 1 : 0, E, N, K, workspace};
+  clear_error();
+  const qlin_status s = check_expert_linear("qlin_expert_linear", a, bits, group_size, dtype,
+                                            y_dtype, workspace_bytes, flags);
+  if (s != QLIN_OK || n_pairs == 0) return s;
   return launch_expert_linear(a, bits, dtype, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status qlin_testing_expert_linear_stalled(
+    const void* x, int64_t x_stride, int pairs_per_row, const int32_t* order,
+    const int32_t* offsets, int64_t n_pairs, const uint32_t* wq, const void* scales,
+    const void* biases, void* y, int E, int64_t N, int64_t K, void* workspace,
+    size_t workspace_bytes, int stalled_stage, unsigned wait_limit_us, void* stream) {
+  const char* name = "qlin_testing_expert_linear_stalled";
+  const ExpertArgs a = {x,  x_stride, pairs_per_row, order, offsets, n_pairs, wq,       scales,
+                        biases, y,    0,             E,     N,       K,       workspace};
+  clear_error();
+  const qlin_status s = check_expert_linear(name, a, 4, kGroup, QLIN_F16, QLIN_F16,
+                                            workspace_bytes, 0);
+  if (s != QLIN_OK) return s;
+  if (stalled_stage < 0 || wait_limit_us < 1000 || wait_limit_us > 2000000)
+    return fail(QLIN_ERR_INVALID_ARG, "%s: stalled_stage=%d wait_limit_us=%u (1000 .. 2000000)",
+                name, stalled_stage, wait_limit_us);
+  if (expert_linear_workspace_size(n_pairs, E, N, K) == 0)
+    return fail(QLIN_ERR_INVALID_ARG, "%s: a call that waits for nothing", name);
+  return launch_expert_stalled(a, stalled_stage, wait_limit_us,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlin_status qlin_combine_experts(const void* y, const int32_t* experts, const float* weights,

@@ -121,13 +121,15 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 // mbar_wait of a whole warp, converged.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   if (__all_sync(kAll, ptx::mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (__all_sync(kAll, ptx::mbar_try_wait(bar, parity))) return true;
-    if ((i & 63u) == 0 && __any_sync(kAll, ptx::globaltimer_ns() - t0 > 2000000000ull))
+    if ((i & 63u) == 0 && __any_sync(kAll, ptx::globaltimer_ns() - t0 > limit_ns))
       return false;
   }
 }
@@ -139,10 +141,20 @@ struct Tile {
   int n0, at, count;  // the first weight row, the first token's place in order, tokens
 };
 
-template <int BITS, typename AT, int BN>
+// For tests: the producer of packed tiles stops before its stage `stage`, and waits are
+// shorter.
+struct Stall {
+  int stage;
+  uint64_t limit_ns;
+};
+
+template <int BITS, typename AT, int BN, bool STALL>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                const ExpertArgs a, const Sorted sorted) {
+                const ExpertArgs a, const Sorted sorted, const Stall stall) {
+  const uint64_t limit = STALL ? stall.limit_ns : kWaitNs;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, limit); };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) { return wait_warp(bar, parity, limit); };
   constexpr bool kHalf = std::is_same<AT, __half>::value;
   using L = Layout<BITS, BN>;
   using G = Geo<BITS>;
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < kb_count; ++kb, ++u) {
           const int before = u - L::kX;  // the use that had the place
           if (before >= 0 &&
-              !ptx::mbar_wait(done(before % L::kA), uint32_t(before / L::kA) & 1u)) {
+              !wait(done(before % L::kA), uint32_t(before / L::kA) & 1u)) {
             report(kStatusWait);
             ok = false;
             break;
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (after a wait that gave up: the last loads, one for each place, may be in flight)
       if (!ok)
         for (int v = u > L::kX ? u - L::kX : 0; v < u; ++v)
-          if (!ptx::mbar_wait(ready(v % L::kA), uint32_t(v / L::kA) & 1u)) report(kStatusWait);
+          if (!wait(ready(v % L::kA), uint32_t(v / L::kA) & 1u)) report(kStatusWait);
     }
   } else if (warp == 2) {
     // ------------------------------------------------- producer of packed tiles
@@ -271,7 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Tile q = first_tile(); q.job < jobs && ok; next_tile(q)) {
         const int row = q.expert * N + q.n0;
         for (int kb = 0; kb < kb_count; ++kb, ++u) {
-          if (u >= L::kW && !ptx::mbar_wait(w_empty(s), phase ^ 1u)) {
+          if (STALL && u == stall.stage) {
+            ok = false;
+            break;
+          }
+          if (u >= L::kW && !wait(w_empty(s), phase ^ 1u)) {
             report(kStatusWait);
             ok = false;
             break;
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s = L::kW - 1;
             phase ^= 1u;
           }
-          if (!ptx::mbar_wait(w_full(s), phase)) report(kStatusWait);
+          if (!wait(w_full(s), phase)) report(kStatusWait);
         }
     }
   } else if (warp == 1) {
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = ptx::idesc_f16(0u, kBM, columns);
       const int buf = i % L::kDBufs;
       if (i >= L::kDBufs &&
-          !wait_warp(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u)) {
+          !warp_wait(acce_bar + 8u * buf, uint32_t(i / L::kDBufs - 1) & 1u)) {
         report(kStatusWait);
         ok = false;
         break;
@@ -314,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_tmem = tmem_base + uint32_t(buf * BN);
       uint32_t more = 0;
       for (int kb = 0; kb < kb_count; ++kb) {
-        if (!wait_warp(ready(s), phase)) {
+        if (!warp_wait(ready(s), phase)) {
           report(kStatusWait);
           ok = false;
           break;
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after the CTA has left, in the barriers of the next one)
     if (any && leads) ptx::mma_commit(done_bar);
     __syncwarp();
-    if (any && !ptx::mbar_wait(done_bar, 0)) report(kStatusWait);
+    if (any && !wait(done_bar, 0)) report(kStatusWait);
     __syncwarp();
   } else if (warp < kFirstEpilogue) {
     // -------------------------------- reconstruct (the warpgroups in turn)
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_sc = srow[kb + kDequantGroups];
           next_bc = brow[kb + kDequantGroups];
         }
-        if (!wait_warp(w_full(ws), w_phase)) {
+        if (!warp_wait(w_full(ws), w_phase)) {
           report(kStatusWait);
           ok = false;
           break;
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(w_empty(ws));
         // the A slot's last products
-        if (u >= L::kA && !wait_warp(done(as), a_phase ^ 1u)) {
+        if (u >= L::kA && !warp_wait(done(as), a_phase ^ 1u)) {
           report(kStatusWait);
           ok = false;
           break;
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = i % L::kDBufs;
       // (a warp whose wait gave up stores nothing from there on, but comes to every barrier:
       // the other warps of its half wait there without a limit)
-      if (live && !wait_warp(accf_bar + 8u * buf, uint32_t(i / L::kDBufs) & 1u)) {
+      if (live && !warp_wait(accf_bar + 8u * buf, uint32_t(i / L::kDBufs) & 1u)) {
         report(kStatusWait);
         live = false;
       }
@@ -654,11 +670,11 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   }
 }
 
-template <int BITS, typename AT, int BN>
-qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
+template <int BITS, typename AT, int BN, bool STALL = false>
+qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st, Stall stall = {}) {
   using L = Layout<BITS, BN>;
   constexpr int kBytes = 1024 + L::kRings + L::kRestBytes;
-  auto kern = tile_kernel<BITS, AT, BN>;
+  auto kern = tile_kernel<BITS, AT, BN, STALL>;
   static std::atomic<unsigned long long> done{0};
   if (!allow_shared(reinterpret_cast<const void*>(kern), kBytes, &done))
     return check_launch("qlin_expert_linear: shared memory");
@@ -696,7 +712,7 @@ qlin_status launch_t(const ExpertArgs& a, unsigned flags, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a, sorted);
+  cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, a, sorted, stall);
   return check_launch("qlin_expert_linear");
 }
 
@@ -716,6 +732,11 @@ qlin_status launch_expert_tile(const ExpertArgs& a, int bits, qlin_dtype dtype, 
                      : dispatch<8, __half>(a, rows, flags, st);
   return bits == 4 ? dispatch<4, __nv_bfloat16>(a, rows, flags, st)
                    : dispatch<8, __nv_bfloat16>(a, rows, flags, st);
+}
+
+qlin_status launch_expert_stalled(const ExpertArgs& a, int stage, unsigned wait_limit_us,
+                                  cudaStream_t st) {
+  return launch_t<4, __half, 64, true>(a, 0, st, Stall{stage, uint64_t(wait_limit_us) * 1000});
 }
 
 size_t expert_tile_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K) {

@@ -152,6 +152,9 @@ struct ExpertArgs {
 size_t expert_linear_workspace_size(int64_t n_pairs, int E, int64_t N, int64_t K);
 qlin_status launch_expert_linear(const ExpertArgs& a, int bits, qlin_dtype dtype, unsigned flags,
                                  cudaStream_t st);
+// The tensor-core kernel with a producer that stops before stage `stage` (for tests).
+qlin_status launch_expert_stalled(const ExpertArgs& a, int stage, unsigned wait_limit_us,
+                                  cudaStream_t st);
 qlin_status launch_combine_experts(const void* y, const int32_t* experts, const float* weights,
                                    const void* add, int64_t add_stride, void* out, int64_t T,
                                    int top_k, int64_t N, qlin_dtype dtype, qlin_dtype y_dtype,

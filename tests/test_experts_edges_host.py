@@ -54,3 +54,20 @@ def test_calls_are_refused_where_their_device_is_not_current(monkeypatch):
                 else:
                     with pytest.raises(ValueError, match=f"cuda:{index}, which is not the current"):
                         call()
+
+
+def test_stalled_expert_linear_refusals(L):
+    """The test-only entry refuses what qlin_expert_linear does, calls that take the streaming
+    kernel, and limits out of range."""
+    FAKE, INVALID, MISALIGNED = 0x10000, 1, 3
+    need = L.qlin_expert_linear_workspace_size(320, 8, 256, 128)
+
+    def call(x=FAKE, P=320, K=128, ws=FAKE, size=need, stage=3, limit=2000):
+        return L.qlin_testing_expert_linear_stalled(x, 128, 1, FAKE, FAKE, P, FAKE, FAKE, FAKE,
+                                                    FAKE, 8, 256, K, ws, size, stage, limit, None)
+
+    assert call(x=None) == INVALID and call(x=FAKE + 8) == MISALIGNED
+    assert call(K=100) == INVALID and call(ws=None) == INVALID and call(size=need - 1) == INVALID
+    assert call(P=8) == INVALID and call(P=0) == INVALID
+    assert call(stage=-1) == INVALID
+    assert call(limit=999) == INVALID and call(limit=2000001) == INVALID

@@ -222,3 +222,36 @@ def test_every_call_is_refused_where_its_device_is_not_current(dev, monkeypatch)
             continue  # (it makes its table on the current device)
         with pytest.raises(ValueError, match="not the current device"):
             call()
+
+
+# ---------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("n,k,stages", [(4096, 256, (0, 2, 5, 8)), (200, 1536, (1, 7, 8, 19, 24))])
+def test_expert_linear_whose_copies_stop(dev, n, k, stages):  # noqa: F811
+    """The packed weights of each CTA stop at some stage of its tiles: every role's wait runs
+    out, the call ends with its status bit, tiles that were complete are right and others not
+    written, and the next call finds everything as ever."""
+    experts, tokens = 8, 320
+    layer = Layer(dev, experts, n, k, 4, F16, seed=k)
+    x = normal(1, tokens, k).to(F16).to(dev)
+    which = np.arange(tokens) % experts
+    routing = routing_of(which[:, None], experts, dev)
+    args = (x, routing, layer.wq, layer.scales, layer.biases, 4)
+    ref = q.expert_linear(*args)
+    size = q.lib().qlin_expert_linear_workspace_size(tokens, experts, n, k)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    blocks = (n + 127) // 128
+    tile = which[:, None] * blocks + np.arange(n)[None, :] // 128  # of each output
+    for stage in stages:
+        out = torch.full_like(ref, 5.0)
+        status = q.lib().qlin_testing_expert_linear_stalled(
+            x.data_ptr(), k, 1, routing.order.data_ptr(), routing.offsets.data_ptr(), tokens,
+            layer.wq.data_ptr(), layer.scales.data_ptr(), layer.biases.data_ptr(), out.data_ptr(),
+            experts, n, k, ws.data_ptr(), size, stage, 2000,
+            torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        complete = torch.from_numpy(tile < sms * (stage * 64 // k)).to(dev)
+        assert q.device_status() == (0 if complete.all() else 1 << 30)
+        assert torch.equal(out[complete], ref[complete]) and (out[~complete] == 5).all()
+        assert torch.equal(q.expert_linear(*args, overlap_previous=True), ref)
+        assert q.device_status() == 0
