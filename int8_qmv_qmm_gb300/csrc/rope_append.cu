@@ -302,23 +302,29 @@ __device__ void token_warp(const Args& a, int64_t t, int part) {
   // two heads' loads before the first store (which could be to the same memory,
   // for all that the compiler knows); with norms one, for want of registers
   for (int h = a.q_heads * part / kParts + lane / kUnits; h < q1; h += (NORM ? 1 : 2) * kHeads) {
-    const bool two = !NORM && h + kHeads < q1;
     const T* from = row + h * D;
     T* to = out + h * D;
-    Vec8 x0 = load8(from + un.at0), y0 = load8(from + un.at1), x1 = x0, y1 = y0;
-    if (two) {
-      x1 = load8(from + kHeads * D + un.at0);
-      y1 = load8(from + kHeads * D + un.at1);
-    }
-    if constexpr (NORM) norm.inv = inverse_rms<T, D>(x0, y0, a.eps);
-    rotate_unit<T, NORM>(x0, y0, u, a.rot, a.interleaved, angles, norm);
-    store8(to + un.at0, x0);
-    store8(to + un.at1, y0);
-    if (two) {
-      if constexpr (NORM) norm.inv = inverse_rms<T, D>(x1, y1, a.eps);
-      rotate_unit<T, NORM>(x1, y1, u, a.rot, a.interleaved, angles, norm);
-      store8(to + kHeads * D + un.at0, x1);
-      store8(to + kHeads * D + un.at1, y1);
+    Vec8 x0 = load8(from + un.at0), y0 = load8(from + un.at1);
+    if constexpr (NORM) {
+      norm.inv = inverse_rms<T, D>(x0, y0, a.eps);
+      rotate_unit<T, NORM>(x0, y0, u, a.rot, a.interleaved, angles, norm);
+      store8(to + un.at0, x0);
+      store8(to + un.at1, y0);
+    } else {
+      const bool two = h + kHeads < q1;
+      Vec8 x1 = x0, y1 = y0;
+      if (two) {
+        x1 = load8(from + kHeads * D + un.at0);
+        y1 = load8(from + kHeads * D + un.at1);
+      }
+      rotate_unit<T, NORM>(x0, y0, u, a.rot, a.interleaved, angles, norm);
+      store8(to + un.at0, x0);
+      store8(to + un.at1, y0);
+      if (two) {
+        rotate_unit<T, NORM>(x1, y1, u, a.rot, a.interleaved, angles, norm);
+        store8(to + kHeads * D + un.at0, x1);
+        store8(to + kHeads * D + un.at1, y1);
+      }
     }
   }
   const int total = r.held + r.n;

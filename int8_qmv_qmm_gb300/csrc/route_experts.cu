@@ -297,7 +297,6 @@ __device__ void offsets_of(const Args& a, int* base, int* buf, bool write) {
 // Counts of a CTA in the workspace: whole vectors of four.
 __host__ __device__ constexpr int stride_of(int E) { return (E + 4) / 4 * 4; }
 
-template <int NE>
 __host__ __device__ constexpr int scratch_words(int E) {
   const int words = spot(E - 1) + 1;
   return words > E + 1 ? words : E + 1;
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(kWarpsFor<NE> * 32) route_kernel(const Args a)
   extern __shared__ int shared[];
   __shared__ int buf[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int width = a.E + 1, words = scratch_words<NE>(a.E);
+  const int width = a.E + 1, words = scratch_words(a.E);
   int* base = shared + kWarps * words;
   for (int i = threadIdx.x; i < width; i += kThreads) base[i] = 0;
   Lane<NE> own;
@@ -403,15 +402,15 @@ qlin_status launch_t(Args a, unsigned flags, cudaStream_t st) {
   }
   a.per = (a.T + ctas - 1) / ctas;
   if (ctas > 1) ctas = (a.T + a.per - 1) / a.per;
-  static_assert((kWarpsFor<16> * scratch_words<16>(512) + 513) * 4 <= 48 * 1024 - 256 &&
-                    (kWarpsFor<8> * scratch_words<8>(256) + 257) * 4 <= 48 * 1024 - 256 &&
+  static_assert((kWarpsFor<16> * scratch_words(512) + 513) * 4 <= 48 * 1024 - 256 &&
+                    (kWarpsFor<8> * scratch_words(256) + 257) * 4 <= 48 * 1024 - 256 &&
                     (kWarpsFor<16> * 513 + 2 * 516) * 4 <= 48 * 1024 - 256 &&
                     (kWarpsFor<8> * 257 + 2 * 260) * 4 <= 48 * 1024 - 256,
                 "without asking for more");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = size_t(kWarps * scratch_words<NE>(a.E) + a.E + 1) * 4;
+  cfg.dynamicSmemBytes = size_t(kWarps * scratch_words(a.E) + a.E + 1) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
