@@ -411,8 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t w[32], none[1];
         dequant_row<BITS, __half, 1>(wrow, r, scale, bias, row_ok, w, none);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(w_empty(ws));
         // the A slot's last products
         if (u >= L::kA && !warp_wait(done(as), a_phase ^ 1u)) {
           report(kStatusWait);
@@ -424,7 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ready(as));
+        // (the packed tile's place is free only here, where what was read from it has been
+        // stored: an arrival straight after the loads can come before they are done, while
+        // scattered loads of scales hold them up, and the next tile be read in their place)
+        if (lane == 0) {
+          ptx::mbar_arrive(w_empty(ws));
+          ptx::mbar_arrive(ready(as));
+        }
         if ((ws += kDequantGroups) >= L::kW) {
           ws = grp;
           w_phase ^= 1u;

@@ -13,7 +13,7 @@ import int8_qmv_qmm_gb300 as q
 from int8_qmv_qmm_gb300.decoder import Decoder
 from oracle import experts_oracle as O
 from tests.test_gpu_decode_loop import prompts
-from tests.test_gpu_decoder import f64, normal
+from tests.test_gpu_decoder import TINY, U, f64, normal
 from tests.test_gpu_experts import (BF16, F16, F32, Layer, dev, random_experts,  # noqa: F401
                                     routing_of)
 from tests.test_gpu_experts_together import MIXED
@@ -255,3 +255,33 @@ def test_expert_linear_whose_copies_stop(dev, n, k, stages):  # noqa: F811
         assert torch.equal(out[complete], ref[complete]) and (out[~complete] == 5).all()
         assert torch.equal(q.expert_linear(*args, overlap_previous=True), ref)
         assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("dt,experts,rows,n,k", [(F16, 64, 11800, 680, 3712), (BF16, 16, 1688, 3000, 3392),
+                                                 (F16, 8, 545, 4078, 3520), (BF16, 128, 8388, 310, 3712)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_expert_linear_of_long_rows_at_full_speed(dev, bits, dt, experts, rows, n, k):  # noqa: F811
+    """Many tiles of long rows, whose scales no longer stay in L1: no packed tile is overwritten
+    before it was read.  Ten calls, every output against products in 32 bits."""
+    gen = torch.Generator(device=dev).manual_seed(k)
+    w = torch.randn(experts * n, k, generator=gen, device=dev) / k ** 0.5
+    wq, sc, bi = q.quantize_affine(w, bits, sdtype=dt)
+    del w
+    which = torch.randint(0, experts, (rows,), generator=gen, device=dev)
+    routing = routing_of(which[:, None].cpu().numpy(), experts, dev)
+    x = torch.randn(rows, k, generator=gen, device=dev).to(dt)
+    hat = q.dequant(wq, sc, bi, bits, out_dtype=F32).view(experts, n, k)
+    ref, size = torch.empty(rows, n, device=dev), torch.empty(rows, n, device=dev)
+    for e in range(experts):
+        at = which == e
+        ref[at], size[at] = x[at].float() @ hat[e].T, x[at].float().abs() @ hat[e].abs().T
+    # the weight's rounding to f16 (bf16: and 2^-31 of its row's largest, nothing here), float32
+    # sums of k products in each of two (an outer bound: each addition off by 2^-24 of the sum
+    # of magnitudes), the output's rounding
+    bound = (2.0 ** -11 + 2 * k * 2.0 ** -24) * size + U[dt] * ref.abs() + TINY[dt]
+    packed = [t.view(experts, n, -1) for t in (wq, sc, bi)]
+    for call in range(10):
+        out = q.expert_linear(x, routing, *packed, bits).float()
+        bad = ~((out - ref).abs() <= bound)
+        assert not bad.any(), (call, int(bad.sum()), bad.nonzero()[:3].tolist())
+    assert q.device_status() == 0
