@@ -52,11 +52,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// This thread's shared-memory writes, to the asynchronous proxy (MMA operands).
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // D (TMEM, f32) += A (TMEM: row i in lane i, K along columns, two 16-bit
 // elements per 32-bit column, element k in the low half) * B (shared memory
 // descriptor); accumulate = 0 overwrites D.

@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                first_pos + 1 - j * kBlock, lane);
       ++done;
     }
+    ptx::fence_async_shared();
     __syncwarp();  // every lane has read the chunk and the info
   }
   if (lane == 0 && split.last >= 0) splits[me] = split;

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmv_kernel(
         accumulate_stage<BITS, MT, R, AT>(stage, kRB, warp * R, kt, kt - kt_lo, geom, kScaleCopy,
                                           scales, biases, rb0, xs, xsum, lane, acc);
       }
+      ptx::fence_async_shared();  // the stage has been read before a copy fills it again
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty0 + 8u * s);
       if (++s == sh.stages) {

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2) qmv_chain_kernel(const __grid_con
           accumulate_stage<BITS, 1, kR, AT>(stage, kRB, warp * kR, kt, kt, geom, L.scale_copy != 0,
                                             sc, bi, row0, xs, xsum, lane, acc);
         }
+        ptx::fence_async_shared();  // the stage has been read before a copy fills it again
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty0 + 8u * s);
         if (++s == p.stages) {

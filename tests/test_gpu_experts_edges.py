@@ -285,3 +285,40 @@ def test_expert_linear_of_long_rows_at_full_speed(dev, bits, dt, experts, rows, 
         bad = ~((out - ref).abs() <= bound)
         assert not bad.any(), (call, int(bad.sum()), bad.nonzero()[:3].tolist())
     assert q.device_status() == 0
+
+
+# ------------------------------------- rings that bulk copies fill while warps read them
+@pytest.mark.parametrize("bits,dt", [(4, BF16), (8, F16)])
+@pytest.mark.parametrize("n,k,m", [(20000, 8256, 1), (9000, 3712, 3), (30000, 2048, 2)])
+def test_linear_is_the_same_at_full_speed(dev, bits, dt, n, k, m):  # noqa: F811
+    """Rows with and without a tile's scales beside them: thirty calls in a row, one result, and
+    that within float32 sums of the dequantised product."""
+    gen = torch.Generator(device=dev).manual_seed(k)
+    packed = q.quantize_affine(torch.randn(n, k, generator=gen, device=dev) / k ** 0.5, bits,
+                               sdtype=dt)
+    x = torch.randn(m, k, generator=gen, device=dev).to(dt)
+    outs = [q.linear(x, *packed, bits) for _ in range(30)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    hat, xf = q.dequant(*packed, bits, out_dtype=F32).double(), x.double()
+    ref, size = xf @ hat.T, xf.abs() @ hat.abs().T
+    # sums of (magic + code) * x: up to 2^9 steps of the group's scale beside the code, k float32
+    # additions of what is at most that; the output's rounding
+    step = xf.abs() @ packed[1].double().abs().repeat_interleave(64, 1).T
+    bound = U[dt] * ref.abs() + k * 2.0 ** -24 * size + 2.0 ** 9 * 2.0 ** -18 * step + TINY[dt]
+    assert ((outs[0].double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("context,slots", [(30000, 2), (900, 24)])
+def test_cache_attention_is_the_same_at_full_speed(dev, context, slots):  # noqa: F811
+    cache = q.KVCache.empty(slots, context + 64, 8, 64, device=dev)
+    ws = q.attention_workspace(64)
+    starts = torch.arange(slots + 1, dtype=torch.int32, device=dev)
+    filled = starts * context
+    qkv = normal(3, slots * context, 48 * 64).to(F16).to(dev)
+    q.rope_append(qkv, None, cache, filled, 32)
+    cache.lens += context
+    new = normal(4, slots, 48 * 64).to(F16).to(dev)
+    query = q.rope_append(new, None, cache, starts, 32)
+    outs = [q.cache_attention(query, cache, starts, 1, ws) for _ in range(30)]
+    assert all(torch.equal(o, outs[0]) for o in outs) and outs[0].isfinite().all()
+    assert q.device_status() == 0
