@@ -21,9 +21,11 @@
 // are joined.
 //
 // 32 tokens of 8 of 64 experts of 2048 x 1024 at 8 bits, 135 MB, take 29 us, 4.6 TB/s; at
-// 4 bits 31 us: about 100 instructions for 16 rows of a group, and 16 warps an SM to hide
-// their latency, are what bounds it.  One token of 8 experts of 2048 x 2048 at 4 bits, 19
-// MB, takes 11.7 us, of which 7 are launch, plan, tokens and the way of the first weights.
+// 4 bits 31 us.  Neither memory (56% busy) nor the issue slots (50%, about 110 instructions
+// for 16 rows of a group) are full: it waits for latencies between dependent instructions,
+// fixed ones, shared memory's and the matrix products', which 16 warps an SM do not cover.
+// One token of 8 experts of 2048 x 2048 at 4 bits, 19 MB, takes 11.7 us, of which 7 are
+// launch, plan, tokens and the way of the first weights.
 
 #include <algorithm>
 #include <type_traits>

@@ -32,11 +32,11 @@
 //                stores 16 bytes a lane by way of shared memory while the next tile runs
 //                (2 bytes a lane, 64 a warp, took 304 us where this took 271)
 //
-// 4096 tokens of 8 of 64 experts of 2048 x 2048 at 4 bits (275 GFLOP) take 213 us, 1290
-// TFLOP/s: a stage takes 545 cycles, where the MMAs of a full tile take 538 and the
+// 4096 tokens of 8 of 64 experts of 2048 x 2048 at 4 bits (275 GFLOP) take 213 to 221 us by
+// machine, 1245 to 1290 TFLOP/s; the same at 8 bits in bfloat16 235.  A stage takes 545 cycles, where the MMAs of a full tile take 538 and the
 // reconstructing warps about as long, whatever its columns, of which a fifth is empty;
 // 1500 cycles pass between tiles; the copy takes 23 us.  500 tokens of 6
-// of 60 experts of 2501 x 1408 at 8 bits (241 MB) take 63 us: a stage of few tokens takes
+// of 60 experts of 2501 x 1408 at 8 bits (241 MB) take 64 us: a stage of few tokens takes
 // the reconstructing warps 410 cycles, where memory would take 180.
 //
 // Every wait is bounded (about 2 s); one that gives up sets a status bit, and the CTA

@@ -19,6 +19,9 @@
 // 1e37 or infinite, fewer than n threads with a logit above it) a second, slower way takes
 // the part: the definition, logit by logit.
 //
+// Exponentials are the hardware's (2 ulp): outputs are off by 3e-8 to 1.1e-7 of their size,
+// over a set of rows.
+//
 // 2048 rows of 128256 in 16 bits, with the 5 likeliest, take 102 us, 5.2 TB/s: the
 // instructions for an exponential and two sums of each logit take about as long as reading
 // it.  One row of float32 with the 20 likeliest takes 10 us: launch, two rounds of loads,

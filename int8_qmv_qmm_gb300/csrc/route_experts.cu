@@ -8,10 +8,11 @@
 // stretch of tokens, a second launch (the same one, where one CTA has all tokens) adds
 // up what lies before each stretch and expert and places the pairs.
 //
-// 8192 tokens, 8 of 256 experts by sigmoids with a bias out of 4 of 8 groups, take 24.6 us:
-// 15 for the scores (about 900 instructions a token, of which the rounds and the groups
-// are half), 4 for the second launch's sums over the other CTAs' counts, 1 for its scan
-// and 4 for placing.  One token takes 4.7, the latency of its rounds.
+// 8192 tokens, 8 of 256 experts by sigmoids with a bias out of 4 of 8 groups, take 24.8 us:
+// 15 for the scores, 4 for the second launch's sums over the other CTAs' counts, 1 for its
+// scan and 4 for placing.  The scores are bound by their instructions, about 1580 a token,
+// which take 74% of the issue slots.  The second launch waits for what it loads (its warps
+// issue a quarter of the time).  One token takes 4.8, the latency of its rounds.
 //
 // Scores and choices are float32, one rounding an operation, so that near ties fall
 // the same way wherever the same operations are done.
