@@ -21,12 +21,12 @@ struct alignas(sizeof(T) * VEC > 16 ? 16 : sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 
-// T: of out and add, Y: of the experts' rows.
+// T: of out and add, Y: of the experts' rows.  (Nothing is __restrict__: what the preceding
+// kernel writes while this one has started must not be taken for constant.)
 template <typename T, typename Y, int VEC>
 __global__ void __launch_bounds__(kThreads)
-    combine_kernel(const Y* __restrict__ y, const int32_t* __restrict__ experts,
-                   const float* __restrict__ weights, const T* add, int64_t add_stride, T* out,
-                   int64_t packs, int top_k, int64_t N) {
+    combine_kernel(const Y* y, const int32_t* experts, const float* weights, const T* add,
+                   int64_t add_stride, T* out, int64_t packs, int top_k, int64_t N) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t per_row = N / VEC;

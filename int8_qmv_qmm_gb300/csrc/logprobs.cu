@@ -156,7 +156,8 @@ struct Part {
     return k * kElems >= shift && (k + 1) * kElems - shift <= n;
   }
   __device__ __forceinline__ uint4 load(int k) const {
-    if (whole(k)) return __ldg(reinterpret_cast<const uint4*>(row + (k * kElems - shift)));
+    // (not by the read-only path: the preceding kernel may have written them since the start)
+    if (whole(k)) return *reinterpret_cast<const uint4*>(row + (k * kElems - shift));
     // an edge: what is not the row's counts as -infinity
     constexpr uint32_t kNone = std::is_same<T, float>::value    ? 0xff800000u
                                : std::is_same<T, __half>::value ? 0xfc00fc00u

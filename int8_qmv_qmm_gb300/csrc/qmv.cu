@@ -83,8 +83,9 @@ struct Shape {
 // untouched.
 template <int BITS, int MT, int R, typename AT, int MODE, bool EPI>
 __global__ void __launch_bounds__(kThreads, 2) qmv_kernel(
-    const AT* __restrict__ x, const uint32_t* __restrict__ wq, const AT* __restrict__ scales,
-    const AT* __restrict__ biases, AT* __restrict__ y, const Shape sh) {
+    // (x is the preceding kernel's, and not constant from this one's start: not __restrict__)
+    const AT* x, const uint32_t* __restrict__ wq, const AT* __restrict__ scales,
+    const AT* __restrict__ biases, AT* y, const Shape sh) {
   constexpr bool kScaleCopy = MODE != 0;
   constexpr bool kKH = MODE == 3;
   static_assert(!kKH || (MT == 1 && (R == 2 || R == 4) &&
